@@ -64,6 +64,7 @@ typedef enum {
 #define PKV_ERR_BLOCK_RANGE 0x2   /* block table entry that must be read lies outside [0, num_blocks) */
 #define PKV_ERR_CONTEXT_RANGE 0x4 /* context_len < 0 or above min(max_context_len, max_blocks*block_size) */
 #define PKV_ERR_WAIT_TIMEOUT 0x8  /* a bounded wait on an asynchronous copy gave up                    */
+#define PKV_ERR_AXIS_RANGE 0x20   /* rotary frequency whose axis lies outside [0, num_axes)              */
 #define PKV_ERR_WORKSPACE 0x10    /* decode workspace control block not in a state this library left   */
 
 /* Version of this ABI (bumped on any incompatible change). */
@@ -428,6 +429,151 @@ PKV_API pkv_status pkv_paged_decode_store_fp8(const uint16_t *q, const uint16_t 
                                               int32_t max_context_len, float scale, uint16_t *out,
                                               int32_t *slot_mapping, void *workspace, size_t workspace_bytes,
                                               int32_t num_workers, int32_t *err_word, pkv_stream_t stream);
+
+/*
+ * int8 KV cache with a scale per block of tokens and kv head.  Caches hold
+ * one signed byte per element, k_cache / v_cache [num_blocks, block_size,
+ * num_kv_heads, head_dim] int8, and one array of scales
+ *     scales  [num_blocks, block_size / PKV_I8_BLOCK, num_kv_heads, 2] float32
+ * (8-byte aligned): the K scale and the V scale of each run of PKV_I8_BLOCK
+ * tokens of a page, per kv head.  An element stands for code * scale.  Unlike
+ * the E4M3 caches there is nothing to calibrate: the store derives the scales
+ * from the rows it writes.  block_size: a power of two in [16, 1024].
+ * (The pages have no counterpart; the mini-vLLM README names quantised KV
+ * among its gaps, § "与 production vLLM 的关键差距".)
+ */
+#define PKV_I8_BLOCK 16
+
+/*
+ * pkv_kv_store_i8 -- quantise new K and V rows and store them at their
+ * sequences' last positions: sequence b's n new rows (rows cu_seqlens[b] ..
+ * cu_seqlens[b + 1] - 1 of k and v, or b * n .. b * n + n - 1 with
+ * new_per_seq = n > 0; cu_seqlens may then be NULL) go to positions
+ * context_lens[b] - n .. context_lens[b] - 1, which already count them
+ * (n = 1: the position of pkv_decode_slot_mapping), through the block table.
+ *
+ * Per scale block (16 consecutive positions from a multiple of 16), kv head
+ * and K or V, with a = the largest magnitude among the block's new rows:
+ *     s' = a / 127 (the binary32 product of a and 1 / 127) if the call writes the
+ *          block's first position, else the larger of that and the block's scale s so far;
+ *     a new element's code is x / s' rounded to the nearest integer, ties to even;
+ *     where s' > s the block's earlier rows are requantised: code * s / s', rounded
+ *     the same way.  Quotients are rounded once, as if exact.
+ * So a block is restarted by the row at its first position (whatever its page
+ * held before does not matter), and rows appended later never saturate.  A
+ * block whose rows are all zero has scale 0.  An infinity or NaN among the new
+ * rows makes the scale NaN, and codes of 0: every read of the block gives NaN
+ * until it restarts.  Rows behind a sequence's last position are not written,
+ * but share their block's scale: they hold nothing.
+ *
+ *   k, v          [num_tokens][num_kv_heads, head_dim] bf16, rows k_stride /
+ *                 v_stride elements apart (multiples of 8, at least
+ *                 num_kv_heads * head_dim: parts of a wider projection's rows)
+ *   block_tables  [num_seqs, max_blocks_per_seq] int32; context_lens [num_seqs]
+ *   cu_seqlens    [num_seqs + 1] int32, non-decreasing from 0, ending at num_tokens
+ * The scale blocks written must not be shared with another sequence of the
+ * call (copy-on-write gives every sequence its own last block).  With
+ * new_per_seq, a sequence of context_lens 0 is a padding row: nothing is
+ * written.  Sequences with 0 <= context_lens[b] < n, lengths beyond the table
+ * and offsets out of order set PKV_ERR_CONTEXT_RANGE, block ids outside the
+ * cache PKV_ERR_BLOCK_RANGE; what they name is not written.  head_dim 64 or 128.
+ */
+PKV_API pkv_status pkv_kv_store_i8(const uint16_t *k, const uint16_t *v, int64_t k_stride, int64_t v_stride,
+                                   const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t *cu_seqlens, const int32_t *context_lens, int32_t num_seqs,
+                                   int32_t num_tokens, int32_t new_per_seq, int8_t *k_cache, int8_t *v_cache,
+                                   float *scales, int32_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t *err_word, pkv_stream_t stream);
+
+/*
+ * pkv_paged_decode_i8 -- pkv_paged_decode over int8 caches: K_j and V_j are
+ * code * scale of their scale block and kv head; block_size from 16 on,
+ * num_q_heads / num_kv_heads in 1..16, everything else (shapes, workspace,
+ * num_workers, errors) as pkv_paged_decode.  Products run in f16 with fp32
+ * accumulators: codes are exact, a query row is scaled by a power of two that
+ * keeps elements of at least 2^-28 of its largest exact, softmax weights round
+ * by at most 2^-11 of themselves; scales multiply in fp32.
+ */
+PKV_API pkv_status pkv_paged_decode_i8(const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache,
+                                       const float *scales, const int32_t *block_tables,
+                                       int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                                       int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale,
+                                       uint16_t *out, void *workspace, size_t workspace_bytes, int32_t num_workers,
+                                       int32_t *err_word, pkv_stream_t stream);
+
+/*
+ * pkv_paged_attention_i8 -- pkv_paged_attention over int8 caches (chunks of a
+ * prefill over a cached prefix, mixed batches, verify steps); the chunk's K/V
+ * already stored by pkv_kv_store_i8.  Workspace:
+ * pkv_paged_attention_workspace_size.  Limits as pkv_paged_decode_i8,
+ * everything else as pkv_paged_attention.
+ */
+PKV_API pkv_status pkv_paged_attention_i8(const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache,
+                                          const float *scales, const int32_t *block_tables,
+                                          int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
+                                          const int32_t *context_lens, int32_t num_seqs, int32_t num_rows,
+                                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                          int32_t block_size, int32_t num_blocks, int32_t max_context_len,
+                                          float scale, uint16_t *out, int32_t new_per_seq, void *workspace,
+                                          size_t workspace_bytes, int32_t num_workers, int32_t *err_word,
+                                          pkv_stream_t stream);
+
+/*
+ * pkv_copy_blocks_i8 -- pkv_copy_blocks for int8 caches: block dst of both
+ * code arrays and of the scales becomes a copy of block src, for every pair.
+ * Pairs, ids and errors as pkv_copy_blocks; block_size a multiple of 16.
+ */
+PKV_API pkv_status pkv_copy_blocks_i8(int8_t *k_cache, int8_t *v_cache, float *scales, const int32_t *pairs,
+                                      int32_t num_pairs, int32_t num_blocks, int32_t block_size,
+                                      int32_t num_kv_heads, int32_t head_dim, int32_t *err_word,
+                                      pkv_stream_t stream);
+
+/*
+ * pkv_rope -- rotary positions for q and k, with one position a token or
+ * several (time, height and width of an image or video token, say).  Pair i of
+ * a head (i < rot_dim / 2; dims i and i + rot_dim / 2, or with interleaved != 0
+ * dims 2i and 2i + 1) is turned by the angle
+ *     t = positions[freq_axis[i]][token] * inv_freq[i]:
+ *     (x, y) -> (x cos t - y sin t, y cos t + x sin t),
+ * in fp32, rounded to bf16 once; dims from rot_dim on are copied.  The angle is
+ * reduced to one turn exactly, in 64-bit fixed point, so far positions lose
+ * nothing.  (The pages apply rotary positions to q and k before the store; see
+ * the nano-vllm KV-cache post, §3.1, for the store that follows.)
+ *
+ *   q, q_out      [num_tokens][num_q_heads, head_dim] bf16, rows q_stride /
+ *                 q_out_stride elements apart (multiples of 8)
+ *   k, k_out      [num_tokens][num_kv_heads, head_dim] bf16, likewise
+ *   positions     [num_axes, num_tokens] int32 (any value)
+ *   inv_freq      [rot_dim / 2] float32, finite
+ *   freq_axis     [rot_dim / 2] int32 in [0, num_axes), or NULL (axis 0); an entry
+ *                 outside sets PKV_ERR_AXIS_RANGE and is taken as 0
+ * An output may be its input (the same pointer and stride); it must not
+ * overlap an input in any other way.  head_dim a multiple of 16 up to 256,
+ * rot_dim a multiple of 16 up to head_dim; num_tokens == 0 is a no-op.
+ */
+PKV_API pkv_status pkv_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                            const int32_t *positions, int32_t num_axes, const float *inv_freq,
+                            const int32_t *freq_axis, int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                            int32_t head_dim, int32_t rot_dim, int32_t interleaved, uint16_t *q_out,
+                            int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride, int32_t *err_word,
+                            pkv_stream_t stream);
+
+/*
+ * pkv_rope_store -- pkv_rope with the store fused in: q is turned into q_out,
+ * and the turned row k[t] and the row v[t] (rows v_stride elements apart) go to
+ * cache slot slot_mapping[t] of bf16 caches, as pkv_kv_store places them: the
+ * turned keys make no round trip through memory.  Slot -1 skips a token's K and
+ * V (its q is still turned); other slots outside the cache too, and set
+ * PKV_ERR_SLOT_RANGE.  Two rows with the same slot are not allowed.
+ */
+PKV_API pkv_status pkv_rope_store(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                                  const uint16_t *v, int64_t v_stride, const int32_t *positions, int32_t num_axes,
+                                  const float *inv_freq, const int32_t *freq_axis, const int32_t *slot_mapping,
+                                  int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                  int32_t rot_dim, int32_t interleaved, uint16_t *q_out, int64_t q_out_stride,
+                                  uint16_t *k_cache, uint16_t *v_cache, int32_t num_blocks, int32_t block_size,
+                                  int32_t *err_word, pkv_stream_t stream);
 
 /*
  * pkv_copy_blocks -- batched copy-on-write block copies.

@@ -14,14 +14,14 @@ extern "C" size_t pkv_paged_decode_workspace_size(int32_t num_seqs, int32_t num_
     return ws_layout(num_seqs, num_q_heads / num_kv_heads, num_kv_heads, head_dim).total;
 }
 
-// Shared by the bf16 and the E4M3 entry points (k_scale / v_scale: the
-// latter's per-kv-head scales, device arrays).  qn > 1: entry b holds up to qn
+// Shared by the entry points of all cache types (ct; k_scale / v_scale: the
+// per-kv-head scales of E4M3 caches, scales: those of int8 ones, device arrays).  qn > 1: entry b holds up to qn
 // queries that share its K/V stream as qn * G virtual heads of a kv head --
 // with row_cnt null, every entry is a sequence with qn new tokens (q / out rows
 // b * qn + i; context_lens the sequences' whole lengths); otherwise entry b
 // holds row_cnt[b] queries at rows b + i (row_seq[b]: its sequence,
 // context_lens[b]: the length its last query sees).
-static pkv_status decode_call(bool fp8, bool qs, int32_t qn, const uint16_t *q, const void *k_cache, const void *v_cache,
+static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, const void *k_cache, const void *v_cache,
                               const float *k_scale, const float *v_scale, const int32_t *row_seq,
                               const int32_t *row_cnt, const int32_t *block_tables,
                               int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
@@ -29,8 +29,9 @@ static pkv_status decode_call(bool fp8, bool qs, int32_t qn, const uint16_t *q, 
                               int32_t num_blocks, int32_t max_context_len, float scale, uint16_t *out,
                               void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word,
                               pkv_stream_t stream, const uint16_t *k_new = nullptr, const uint16_t *v_new = nullptr,
-                              int32_t *slot_out = nullptr)
+                              int32_t *slot_out = nullptr, const float *scales = nullptr)
 {
+    const bool fp8 = ct != kBf16;  // one byte per cached element
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
         head_dim <= 0 || block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0 ||
         num_workers < 0 || !std::isfinite(scale))
@@ -40,19 +41,20 @@ static pkv_status decode_call(bool fp8, bool qs, int32_t qn, const uint16_t *q, 
     if (qn < 1) return PKV_EINVAL;
     const int gq = num_q_heads / num_kv_heads;  // query heads per kv head
     const int G = gq * qn;                      // virtual heads per kv head sharing one K/V stream
-    if (G > (fp8 ? 8 : 16)) return PKV_EUNSUPPORTED;  // virtual heads per warp: the MMA tile's rows
-    if (!is_pow2(block_size) || block_size < 8 || block_size > 1024) return PKV_EUNSUPPORTED;
+    if (G > (ct == kE4m3 ? 8 : 16)) return PKV_EUNSUPPORTED;  // virtual heads per warp: the MMA tile's rows
+    if (!is_pow2(block_size) || block_size < (ct == kI8 ? kScaleToks : 8) || block_size > 1024) return PKV_EUNSUPPORTED;
     if (int64_t(num_blocks) * block_size > INT32_MAX) return PKV_EBOUNDS;
     if (num_seqs == 0) return PKV_OK;
     if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out) return PKV_EINVAL;
-    if (fp8 && (!k_scale || !v_scale)) return PKV_EINVAL;
+    if (ct == kE4m3 && (!k_scale || !v_scale)) return PKV_EINVAL;
+    if (ct == kI8 && (!scales || (reinterpret_cast<uintptr_t>(scales) & 7u))) return PKV_EINVAL;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return PKV_EINVAL;
     const int64_t len_limit = std::min<int64_t>(max_context_len, int64_t(max_blocks_per_seq) * block_size);
     // unit counts (and positions in the unit list) are kept in 32 bits
     const int64_t max_units = int64_t(num_kv_heads) * num_seqs * ((len_limit + 7) / 8);
     if (max_units > INT32_MAX) return PKV_EBOUNDS;
-    if (qs && (fp8 || !row_cnt)) return PKV_EINVAL;  // query-split entries are chunks of bf16 calls
-    if ((k_new || v_new) && (qs || qn != 1 || row_seq || !k_new || !v_new || !aligned16(k_new) ||
+    if (qs && (ct == kE4m3 || !row_cnt)) return PKV_EINVAL;  // query-split entries are chunks of bf16 or int8 calls
+    if ((k_new || v_new) && (qs || ct == kI8 || qn != 1 || row_seq || !k_new || !v_new || !aligned16(k_new) ||
                              !aligned16(v_new)))
         return PKV_EINVAL;  // the fused store goes with a decode
     const WsLayout ws = ws_layout(num_seqs, G, num_kv_heads, head_dim, qs);
@@ -97,6 +99,7 @@ static pkv_status decode_call(bool fp8, bool qs, int32_t qn, const uint16_t *q, 
     p.scale_log2 = float(double(scale) * 1.4426950408889634);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
+    p.scales = reinterpret_cast<const float2 *>(scales);
     p.row_seq = row_seq;
     p.qn = qn;
     p.gq = gq;
@@ -133,11 +136,13 @@ static pkv_status decode_call(bool fp8, bool qs, int32_t qn, const uint16_t *q, 
     }
     a.stream = reinterpret_cast<cudaStream_t>(stream);
 
-    LaunchFn fn = fp8    ? pick_decode_fp8(head_dim, G)
+    LaunchFn fn = ct == kE4m3 ? pick_decode_fp8(head_dim, G)
+                  : ct == kI8 ? (qs ? pick_decode_i8_qs(head_dim, G)
+                                    : G > 8 ? pick_decode_i8_wide(head_dim, G) : pick_decode_i8(head_dim, G))
                   : tc5  ? pick_decode_tc5(head_dim)
                   : qs   ? pick_decode_qs(head_dim, G)
                   : G > 8 ? pick_decode_wide(head_dim, G)
-                         : (head_dim == 64 ? pick_group<64, false, false>(G) : pick_group<128, false, false>(G));
+                         : (head_dim == 64 ? pick_group<64, kBf16, false>(G) : pick_group<128, kBf16, false>(G));
     if (!fn) return PKV_EUNSUPPORTED;
     if (ws.count_clear) {  // counters outside the fixed region start at zero (see WsLayout)
         const cudaError_t ce = cudaMemsetAsync(p.ws_count, 0, ws.count_bytes, a.stream);
@@ -157,7 +162,7 @@ extern "C" pkv_status pkv_paged_decode(const uint16_t *q, const uint16_t *k_cach
                                        void *workspace, size_t workspace_bytes, int32_t num_workers,
                                        int32_t *err_word, pkv_stream_t stream)
 {
-    return decode_call(false, false, 1, q, k_cache, v_cache, nullptr, nullptr, nullptr, nullptr, block_tables,
+    return decode_call(kBf16, false, 1, q, k_cache, v_cache, nullptr, nullptr, nullptr, nullptr, block_tables,
                        max_blocks_per_seq, context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                        num_blocks, max_context_len, scale, out, workspace, workspace_bytes, num_workers, err_word,
                        stream);
@@ -173,7 +178,7 @@ extern "C" pkv_status pkv_paged_decode_store(const uint16_t *q, const uint16_t *
                                              int32_t num_workers, int32_t *err_word, pkv_stream_t stream)
 {
     if (num_seqs > 0 && (!k_new || !v_new)) return PKV_EINVAL;
-    return decode_call(false, false, 1, q, k_cache, v_cache, nullptr, nullptr, nullptr, nullptr, block_tables,
+    return decode_call(kBf16, false, 1, q, k_cache, v_cache, nullptr, nullptr, nullptr, nullptr, block_tables,
                        max_blocks_per_seq, context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                        num_blocks, max_context_len, scale, out, workspace, workspace_bytes, num_workers, err_word,
                        stream, k_new, v_new, slot_mapping);
@@ -190,7 +195,7 @@ extern "C" pkv_status pkv_paged_decode_store_fp8(const uint16_t *q, const uint16
                                                  int32_t num_workers, int32_t *err_word, pkv_stream_t stream)
 {
     if (num_seqs > 0 && (!k_new || !v_new)) return PKV_EINVAL;
-    return decode_call(true, false, 1, q, k_cache, v_cache, k_scale, v_scale, nullptr, nullptr, block_tables,
+    return decode_call(kE4m3, false, 1, q, k_cache, v_cache, k_scale, v_scale, nullptr, nullptr, block_tables,
                        max_blocks_per_seq, context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                        num_blocks, max_context_len, scale, out, workspace, workspace_bytes, num_workers, err_word,
                        stream, k_new, v_new, slot_mapping);
@@ -205,10 +210,24 @@ extern "C" pkv_status pkv_paged_decode_fp8(const uint16_t *q, const uint8_t *k_c
                                            size_t workspace_bytes, int32_t num_workers, int32_t *err_word,
                                            pkv_stream_t stream)
 {
-    return decode_call(true, false, 1, q, k_cache, v_cache, k_scale, v_scale, nullptr, nullptr, block_tables,
+    return decode_call(kE4m3, false, 1, q, k_cache, v_cache, k_scale, v_scale, nullptr, nullptr, block_tables,
                        max_blocks_per_seq, context_lens,
                        num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, max_context_len, scale,
                        out, workspace, workspace_bytes, num_workers, err_word, stream);
+}
+
+extern "C" pkv_status pkv_paged_decode_i8(const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache,
+                                          const float *scales, const int32_t *block_tables,
+                                          int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                          int32_t block_size, int32_t num_blocks, int32_t max_context_len,
+                                          float scale, uint16_t *out, void *workspace, size_t workspace_bytes,
+                                          int32_t num_workers, int32_t *err_word, pkv_stream_t stream)
+{
+    return decode_call(kI8, false, 1, q, k_cache, v_cache, nullptr, nullptr, nullptr, nullptr, block_tables,
+                       max_blocks_per_seq, context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                       num_blocks, max_context_len, scale, out, workspace, workspace_bytes, num_workers, err_word,
+                       stream, nullptr, nullptr, nullptr, scales);
 }
 
 // ------------------------------------------------------------------ several query rows per sequence
@@ -308,14 +327,14 @@ extern "C" size_t pkv_paged_attention_workspace_size(int32_t num_rows, int32_t n
     return align256(dec) + 3 * rows_bytes(num_rows);
 }
 
-extern "C" pkv_status pkv_paged_attention(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
-                                          const int32_t *block_tables, int32_t max_blocks_per_seq,
-                                          const int32_t *cu_seqlens_q, const int32_t *context_lens, int32_t num_seqs,
-                                          int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
-                                          int32_t head_dim, int32_t block_size, int32_t num_blocks,
-                                          int32_t max_context_len, float scale, uint16_t *out, int32_t new_per_seq,
-                                          void *workspace, size_t workspace_bytes, int32_t num_workers,
-                                          int32_t *err_word, pkv_stream_t stream)
+// Shared by the bf16 and the int8 entry points (scales: the latter's).
+static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache, const void *v_cache,
+                                 const float *scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                 const int32_t *cu_seqlens_q, const int32_t *context_lens, int32_t num_seqs,
+                                 int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                 int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale,
+                                 uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes,
+                                 int32_t num_workers, int32_t *err_word, pkv_stream_t stream)
 {
     if (num_seqs < 0 || num_rows < 0 || new_per_seq < 0) return PKV_EINVAL;
     if (num_rows == 0) return PKV_OK;
@@ -331,10 +350,10 @@ extern "C" pkv_status pkv_paged_attention(const uint16_t *q, const uint16_t *k_c
     const int32_t qg = qs_queries(num_q_heads, num_kv_heads);
     if (new_per_seq > 1 && new_per_seq <= qg)
         // every sequence's n new tokens share its K/V stream: read once, n * G virtual heads
-        return decode_call(false, false, new_per_seq, q, k_cache, v_cache, nullptr, nullptr, nullptr, nullptr,
+        return decode_call(ct, false, new_per_seq, q, k_cache, v_cache, nullptr, nullptr, nullptr, nullptr,
                            block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads, num_kv_heads,
                            head_dim, block_size, num_blocks, max_context_len, scale, out, workspace,
-                           workspace_bytes, num_workers, err_word, stream);
+                           workspace_bytes, num_workers, err_word, stream, nullptr, nullptr, nullptr, scales);
     // chunks of a sequence's queries, one entry per row; few new tokens per sequence on average (at
     // most two regular chunks): chunks of qg on regular CTAs, else chunks of 8 * qg on query-split ones.
     // The row arrays sit after the decode workspace.
@@ -355,7 +374,39 @@ extern "C" pkv_status pkv_paged_attention(const uint16_t *q, const uint16_t *k_c
     }
     const pkv_status st = launch_status("expand_rows_kernel launch");
     if (st != PKV_OK) return st;
-    return decode_call(false, qs, qg, q, k_cache, v_cache, nullptr, nullptr, row_seq, row_cnt, block_tables,
+    return decode_call(ct, qs, qg, q, k_cache, v_cache, nullptr, nullptr, row_seq, row_cnt, block_tables,
                        max_blocks_per_seq, row_len, num_rows, num_q_heads, num_kv_heads, head_dim, block_size,
-                       num_blocks, max_context_len, scale, out, workspace, dec_bytes, num_workers, err_word, stream);
+                       num_blocks, max_context_len, scale, out, workspace, dec_bytes, num_workers, err_word, stream,
+                       nullptr, nullptr, nullptr, scales);
+}
+
+extern "C" pkv_status pkv_paged_attention(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
+                                          const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                          const int32_t *cu_seqlens_q, const int32_t *context_lens, int32_t num_seqs,
+                                          int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
+                                          int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                          int32_t max_context_len, float scale, uint16_t *out, int32_t new_per_seq,
+                                          void *workspace, size_t workspace_bytes, int32_t num_workers,
+                                          int32_t *err_word, pkv_stream_t stream)
+{
+    return attention_call(kBf16, q, k_cache, v_cache, nullptr, block_tables, max_blocks_per_seq, cu_seqlens_q,
+                          context_lens, num_seqs, num_rows, num_q_heads, num_kv_heads, head_dim, block_size,
+                          num_blocks, max_context_len, scale, out, new_per_seq, workspace, workspace_bytes,
+                          num_workers, err_word, stream);
+}
+
+extern "C" pkv_status pkv_paged_attention_i8(const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache,
+                                             const float *scales, const int32_t *block_tables,
+                                             int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
+                                             const int32_t *context_lens, int32_t num_seqs, int32_t num_rows,
+                                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                             int32_t block_size, int32_t num_blocks, int32_t max_context_len,
+                                             float scale, uint16_t *out, int32_t new_per_seq, void *workspace,
+                                             size_t workspace_bytes, int32_t num_workers, int32_t *err_word,
+                                             pkv_stream_t stream)
+{
+    return attention_call(kI8, q, k_cache, v_cache, scales, block_tables, max_blocks_per_seq, cu_seqlens_q,
+                          context_lens, num_seqs, num_rows, num_q_heads, num_kv_heads, head_dim, block_size,
+                          num_blocks, max_context_len, scale, out, new_per_seq, workspace, workspace_bytes,
+                          num_workers, err_word, stream);
 }

@@ -70,6 +70,11 @@
 
 namespace pkv {
 
+// Cache element types (CT): bf16; E4M3 codes with a scale per kv head; int8 codes with a scale per block of
+// kScaleToks tokens and kv head (see attend_tile_i8).
+constexpr int kBf16 = 0, kE4m3 = 1, kI8 = 2;
+constexpr int kScaleToks = PKV_I8_BLOCK;
+
 constexpr int kMaxStages = 16;    // ring depth (as many as fit: 3 of 64 KiB, 12 of 16 KiB)
 constexpr int kMaxSlots = 512;    // slices: SM ids (adaptive) or CTAs (fixed split)
 constexpr int kSegmentUnits = 8;  // small calls: one CTA per segment when no segment has more units
@@ -163,7 +168,8 @@ struct DecodeParams {
     int32_t qslots;              // Q row buffers: 2 (the next segment's rows load during this one), or 1
                                  // where that buys the ring another stage
     float scale_log2;            // scale * log2(e)
-    const float *k_scale, *v_scale;  // E4M3 caches: per-kv-head scales (unused for bf16 caches)
+    const float *k_scale, *v_scale;  // E4M3 caches: per-kv-head scales (unused for other caches)
+    const float2 *scales;            // int8 caches: [NB * bs / kScaleToks][Hkv] (K scale, V scale)
     const int32_t *row_seq;          // several query rows per sequence: row -> the sequence whose table it
                                      // reads (null: row b reads table row b)
     // Several new tokens per sequence sharing one K/V stream: the kernel's G "heads" of a kv head are
@@ -197,10 +203,10 @@ constexpr int kSliceEnd = 4;  // last unit of the slice
 // Shared-memory layout, computed the same way on the host (size) and device (offsets).
 struct CtaLayout {
     uint32_t kv_bytes, stage_bytes, q_bytes, comb_bytes;
-    uint32_t off_v, off_q, off_comb, off_meta, off_bar, off_bound, off_wts, off_red, off_sh, off_scan, total;
+    uint32_t off_v, off_q, off_comb, off_meta, off_sc, off_bar, off_bound, off_wts, off_red, off_sh, off_scan, total;
 };
 
-__host__ __device__ inline uint32_t align_up(uint32_t x, uint32_t a) { return (x + a - 1) / a * a; }
+__host__ __device__ constexpr uint32_t align_up(uint32_t x, uint32_t a) { return (x + a - 1) / a * a; }
 
 // Floats per state in the combine buffer: G * (D + 2) rounded up to a
 // multiple of 4, so every block (and its float4 rows) is 16-byte aligned.
@@ -215,12 +221,19 @@ __host__ __device__ constexpr bool one_q_buffer_ok(int G, bool fp8, bool qs, boo
     return G == 8 && !fp8 && !qs && !tc5;
 }
 
+// Bytes a stage's scales take (int8 caches; a multiple of 16).
+__host__ __device__ constexpr uint32_t scale_bytes(int toks, int hg)
+{
+    return align_up(uint32_t(toks / kScaleToks * hg * 8), 16);
+}
+
 // es: bytes per cached element (2 for bf16, 1 for E4M3); qs: query-split
 // CTA (all sub warps of a kv head on the same tokens, each with its own G
 // virtual heads); tc5: its tensor-memory variant (Q slots hold the 128-row
 // tile as 128-byte-swizzled 64-dim slabs).
 __host__ __device__ inline CtaLayout cta_layout(int D, int G, int es, int hg, int sub, int nst, int B,
-                                                bool qs = false, bool tc5 = false, int qslots = 2)
+                                                bool qs = false, bool tc5 = false, int qslots = 2,
+                                                bool i8 = false)
 {
     CtaLayout l;
     const int toks = warp_tokens(G, es == 1, qs, tc5) * (qs ? 1 : sub);
@@ -241,6 +254,8 @@ __host__ __device__ inline CtaLayout cta_layout(int D, int G, int es, int hg, in
     o += l.comb_bytes;
     l.off_meta = o;
     o += uint32_t(nst) * uint32_t(sizeof(UnitMeta));
+    l.off_sc = o;  // int8 caches: a stage's scales, [scale block of the unit][kv head of the group]
+    if (i8) o += uint32_t(nst) * scale_bytes(toks, hg);
     l.off_bar = o;
     // full / empty per stage, q full / empty x2, combine full / free; tc5: scores full x2, scores read x2,
     // weights full x2, output product done x2, drain, a row's two halves met (one per lane quarter) x4,
@@ -452,16 +467,16 @@ constexpr float kRescaleSlack = 8.0f;
 // groups, and one ldmatrix reads them without a conflict.
 // HR: 8-row halves of the MMA tile that hold a warp's virtual heads (2 when
 // a warp has more than 8).
-template <int D, bool FP8, bool QS = false, int HR_ = 1>
+template <int D, int CT, bool QS = false, int HR_ = 1>
 struct Tc {
-    static constexpr int ES = FP8 ? 1 : 2;              // bytes per cached element
+    static constexpr int ES = CT != kBf16 ? 1 : 2;              // bytes per cached element
     static constexpr int ROWB = D * ES;                 // bytes per cached row
     static constexpr int RB = ROWB >= 128 ? 128 : 64;   // bytes per shared-memory row
     static constexpr int NP = ROWB / RB;                // parts per cached row
     static constexpr int NCP = ROWB / 32;               // 16-byte chunk pairs per row (one ldmatrix.x4 each)
     static constexpr int KS = D / 16;                   // k-steps of the score product
     static constexpr int MT = D / 16;                   // m-tiles of the output product
-    static constexpr int NT = FP8 || QS ? 2 : 1;        // 16-token sub-tiles of a warp's tile
+    static constexpr int NT = CT != kBf16 || QS ? 2 : 1;        // 16-token sub-tiles of a warp's tile
     static constexpr int TW = 16 * NT;                  // tokens of a warp's tile (warp_tokens)
     static constexpr int HR = HR_;                      // 8-row halves of the MMA tile holding virtual heads
 };
@@ -484,9 +499,9 @@ __device__ __forceinline__ uint32_t swizzled_chunk(uint32_t c, uint32_t R)
 // row part i / (RB / 32) (part stride boxtok RB bytes), and since boxtok is a
 // multiple of 8 the swizzle key of its row is that of the token alone, so the
 // piece's chunk is ((i % (RB / 32)) << 5) ^ kx.
-template <int D, bool FP8, bool QS>
+template <int D, int CT, bool QS>
 struct LaneOffsets {
-    using T = Tc<D, FP8, QS>;
+    using T = Tc<D, CT, QS>;
     uint32_t base[T::NT];  // row of the sub-tile's token, part 0, chunk 0
     uint32_t part;         // bytes between a row's parts
     uint32_t kx;           // the lane's chunk bit and the row's swizzle key, as a byte offset
@@ -497,10 +512,10 @@ struct LaneOffsets {
     }
 };
 
-template <int D, bool FP8, bool QS>
-__device__ __forceinline__ void lane_offsets(LaneOffsets<D, FP8, QS> &off, int lane, int j, int h, int hg, int boxtok)
+template <int D, int CT, bool QS>
+__device__ __forceinline__ void lane_offsets(LaneOffsets<D, CT, QS> &off, int lane, int j, int h, int hg, int boxtok)
 {
-    using T = Tc<D, FP8, QS>;
+    using T = Tc<D, CT, QS>;
     const int tl = ((lane >> 4) << 3) | (lane & 7), e = (lane >> 3) & 1;
     const int lg = __ffs(boxtok) - 1;
     const uint32_t box_bytes = uint32_t(boxtok * hg * T::ROWB);
@@ -519,10 +534,10 @@ __device__ __forceinline__ void lane_offsets(LaneOffsets<D, FP8, QS> &off, int l
 // transposed V tile puts dim 16 mt + g in rows g and 16 mt + 8 + g in rows
 // g + 8; E4M3 caches: dims 16 mt + 2g and 16 mt + 2g + 1 (the byte pairs of
 // a 16-bit transpose, split by a byte permute).
-template <bool FP8>
+template <int CT>
 __device__ __forceinline__ int dim_of(int mt, int half, int g)
 {
-    return FP8 ? 16 * mt + 2 * g + half : 16 * mt + 8 * half + g;
+    return CT != kBf16 ? 16 * mt + 2 * g + half : 16 * mt + 8 * half + g;
 }
 
 __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi)
@@ -560,15 +575,15 @@ __device__ __forceinline__ uint32_t f16x2_sat(float lo, float hi)
 // 2^-14 .. 65504; smaller ones keep f16's subnormal steps of 2^-24, larger
 // ones saturate at 65504); the kv head's K scale is in ksc, its V scale is
 // applied by the caller.
-template <int D, bool FP8, bool QS, int HR_, bool TAIL>
+template <int D, int CT, bool QS, int HR_, bool TAIL>
 __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb,
-                                            const LaneOffsets<D, FP8, QS> &off,
-                                            const uint32_t (&qa)[Tc<D, FP8, QS, HR_>::KS][2 * Tc<D, FP8, QS, HR_>::HR],
-                                            float ksc, const int (&lim)[Tc<D, FP8, QS, HR_>::HR], int valid,
-                                            float (&m)[Tc<D, FP8, QS, HR_>::HR], float (&l)[Tc<D, FP8, QS, HR_>::HR],
-                                            float (&o)[Tc<D, FP8, QS, HR_>::MT][Tc<D, FP8, QS, HR_>::HR][4], int lane)
+                                            const LaneOffsets<D, CT, QS> &off,
+                                            const uint32_t (&qa)[Tc<D, CT, QS, HR_>::KS][2 * Tc<D, CT, QS, HR_>::HR],
+                                            float ksc, const int (&lim)[Tc<D, CT, QS, HR_>::HR], int valid,
+                                            float (&m)[Tc<D, CT, QS, HR_>::HR], float (&l)[Tc<D, CT, QS, HR_>::HR],
+                                            float (&o)[Tc<D, CT, QS, HR_>::MT][Tc<D, CT, QS, HR_>::HR][4], int lane)
 {
-    using T = Tc<D, FP8, QS, HR_>;
+    using T = Tc<D, CT, QS, HR_>;
     constexpr int NT = T::NT, HR = T::HR;
     // accumulation chains per n-tile (bf16: halves the MMA dependency depth; not with 16 rows, whose
     // registers would spill at D = 128)
@@ -592,7 +607,7 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb,
         for (int st = 0; st < NT; ++st) {
             uint32_t r0, r1, r2, r3;
             ldsm_x4(kb + off.at(st, i), r0, r1, r2, r3);
-            if constexpr (!FP8) {
+            if constexpr (CT == kBf16) {
                 // chunks 2i, 2i+1 = dims 16i..16i+15 = k-step i; r0/r1 tokens 0-7, r2/r3 tokens 8-15
                 mma_bf16_16816(sa[st][i % CH][0], qa[i][0], a1(i), qa[i][1], a3(i), r0, r1);
                 mma_bf16_16816(sa[st][i % CH][1], qa[i][0], a1(i), qa[i][1], a3(i), r2, r3);
@@ -682,7 +697,7 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb,
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const float p0 = pr[4 * st + 2 * c], p1 = pr[4 * st + 2 * c + 1];
-                if constexpr (FP8) {
+                if constexpr (CT != kBf16) {
                     pb[hr][st][c] = f16x2_of(p0, p1);
                     pl[hr][st][c] = 0u;
                 } else {
@@ -713,7 +728,7 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb,
                 r2 &= keep1;
                 r3 &= keep1;
             }
-            if constexpr (!FP8) {
+            if constexpr (CT == kBf16) {
                 // m-tile i: dims 16i + g (r0: tokens 0-7, r2: tokens 8-15) and 16i + 8 + g (r1, r3)
 #pragma unroll
                 for (int hr = 0; hr < HR; ++hr) {
@@ -738,6 +753,17 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb,
         }
     }
 }
+
+// int8 caches: one warp tile, with each 16-token sub-tile's (K scale, V scale) in sc and the rows' score
+// factors in rowf (defined in pkv_i8_tile.cuh, which the translation units of the int8 kernels include).
+template <int D, bool QS, int HR_, bool TAIL>
+__device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const LaneOffsets<D, kI8, QS> &off,
+                                               const uint32_t (&qa)[Tc<D, kI8, QS, HR_>::KS][2 * HR_],
+                                               const float (&rowf)[HR_], const float2 (&sc)[2],
+                                               const int (&lim)[HR_], int valid, float (&m)[HR_], float (&l)[HR_],
+                                               float (&o)[Tc<D, kI8, QS, HR_>::MT][HR_][4], int lane);
+template <int D>
+__device__ __forceinline__ float q_row_scale(const uint16_t *qr, bool live, int r4, float &mul);
 
 // ------------------------------------------------------------------ load balance
 __device__ __forceinline__ unsigned smid()
@@ -1014,7 +1040,7 @@ __device__ __forceinline__ int slice_of(const long long *bound, int nslots, long
 // (the online-softmax algebra; m in log2 units).  The pieces were written by
 // other SMs, so they are read through L2 (ld.global.cg), BATCH pieces at a
 // time with independent loads, folded into a running (M, l, acc).
-template <int D, int G, bool FP8, bool QS>
+template <int D, int G, int CT, bool QS>
 __device__ __forceinline__ void merge_pieces(const DecodeParams &p, const long long *bound, int sf, int sl,
                                              long long x0, int g, int h, int jq, int b, int kvh, int nvh, int lane)
 {
@@ -1078,7 +1104,7 @@ __device__ __forceinline__ void merge_pieces(const DecodeParams &p, const long l
         for (int i = 0; i < HB; ++i) {
             const int hh = h0 + i;
             if (hh >= nvh) break;
-            const float inv = (FP8 ? __ldg(p.v_scale + kvh) : 1.0f) / lsum[i];
+            const float inv = (CT == kE4m3 ? __ldg(p.v_scale + kvh) : 1.0f) / lsum[i];
             uint16_t *o = p.out + ((int64_t(b) * p.qstride + jq * p.qn + hh / p.gq) * p.Hq + int64_t(kvh) * p.gq +
                                    hh % p.gq) * D + lane * PER;
             if constexpr (PER == 4)
@@ -1615,16 +1641,16 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
 // CTA for long runs of new tokens, where the entry's up to sub * qn queries
 // share every K/V tile).  TC5 (with QS): the same entries on the tensor-memory
 // consumers (see tc5_softmax_warps).
-template <int D, int G, bool FP8, bool QS, bool TC5 = false>
+template <int D, int G, int CT, bool QS, bool TC5 = false>
 __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G) + 1) * 32, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                         const DecodeParams p)
 {
-    static_assert(!TC5 || (QS && !FP8 && G == 16 && (D == 64 || D == 128)), "tensor-memory CTAs: bf16 query-split");
+    static_assert(!TC5 || (QS && CT == kBf16 && G == 16 && (D == 64 || D == 128)), "tensor-memory CTAs: bf16 query-split");
     extern __shared__ __align__(1024) uint8_t smem[];
-    constexpr int ES = FP8 ? 1 : 2;  // bytes per cached element
-    const int qslots = one_q_buffer_ok(G, FP8, QS, TC5) ? p.qslots : 2;
-    const CtaLayout lay = cta_layout(D, G, ES, p.hg, p.sub, p.nst, p.B, QS, TC5, qslots);
+    constexpr int ES = CT != kBf16 ? 1 : 2;  // bytes per cached element
+    const int qslots = one_q_buffer_ok(G, CT != kBf16, QS, TC5) ? p.qslots : 2;
+    const CtaLayout lay = cta_layout(D, G, ES, p.hg, p.sub, p.nst, p.B, QS, TC5, qslots, CT == kI8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     uint8_t *stage0 = smem;
@@ -1655,7 +1681,7 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
         // TC5: a stage and a Q slot are released by one tcgen05.commit of the MMA warp
         const uint32_t releases = TC5 ? 1u : uint32_t(p.cons);
         for (int i = 0; i < p.nst; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], CT == kI8 ? 33 : 1);  // int8 caches: and the lanes' copies of the scales
             mbar_init(&empty[i], releases);
         }
         for (int i = 0; i < 2; ++i) {
@@ -1975,6 +2001,17 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
                     tma_load_4d(st + lay.kv_bytes + lane * box_bytes, &vmap, 0, row, 0, iw.g * p.hg, &full[s],
                                 policy);
                 }
+                if constexpr (CT == kI8) {
+                    // the unit's scales, one (scale block, kv head) pair a lane (at most 16 of them); every
+                    // lane's copies count on the stage's barrier
+                    const int sb = lane / p.hg, t = sb * kScaleToks;
+                    const int32_t rb = __shfl_sync(kFull, row, min(t, p.toks - 1) >> (__ffs(p.boxtok) - 1));
+                    if (t < p.toks && rb >= 0)
+                        copy_async8(smem + lay.off_sc + uint32_t(s) * scale_bytes(p.toks, p.hg) + uint32_t(lane) * 8u,
+                                    p.scales + ((long long)(rb + (t & (p.boxtok - 1))) / kScaleToks * p.Hkv +
+                                                iw.g * p.hg + (lane - sb * p.hg)));
+                    copy_async_arrive(&full[s]);
+                }
                 ++kk;
                 if (++rs == p.nst) {
                     rs = 0;
@@ -1999,6 +2036,7 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
                     if constexpr (TC5) mbar_arrive(&mready[rs]);
                     mbar_arrive(&full[rs]);
                 }
+                if constexpr (CT == kI8) mbar_arrive(&full[rs]);  // no copies of scales
                 ++kk;
             } else {
                 dead = true;
@@ -2058,14 +2096,14 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
         }
         return;
     } else {
-    using TC = Tc<D, FP8, QS, (G > 8 ? 2 : 1)>;
+    using TC = Tc<D, CT, QS, (G > 8 ? 2 : 1)>;
     const int h = warp / p.sub, j = warp - h * p.sub;  // kv head in the group, slice of the unit or queries
     const int jt = QS ? 0 : j;                         // token slice of the unit
     const int jq = QS ? j : 0;                         // block of qn queries of the entry
     const int g8 = lane >> 2, r4 = lane & 3;           // fragment row group and column pair of the thread
     const int home = sh[0];
-    LaneOffsets<D, FP8, QS> off;
-    lane_offsets<D, FP8, QS>(off, lane, jt, h, p.hg, p.boxtok);
+    LaneOffsets<D, CT, QS> off;
+    lane_offsets<D, CT, QS>(off, lane, jt, h, p.hg, p.boxtok);
     const uint32_t stage_addr = smem_u32(stage0);
     constexpr int HR = TC::HR;  // halves of the MMA tile's rows that hold virtual heads
     // several queries per stream: the query of row g8 + 8 hr sees shift[hr] fewer of the entry's last
@@ -2085,6 +2123,7 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
         l[hr] = 0.f;
     }
     float ksc = p.scale_log2;
+    float rowf[HR];    // int8 caches: score factor of the thread's rows (scale_log2 and the power of two taken out of q)
     float vsc = 1.0f;  // E4M3 caches: the kv head's V scale, applied in the final division
     // fused store: this lane's 8 bytes of the new K / V row (4 bf16 elements, or 8 E4M3 codes)
     uint2 kn = make_uint2(0u, 0u), vn = make_uint2(0u, 0u);
@@ -2094,7 +2133,7 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
     constexpr bool kLateNewRow = TC::HR == 2;
     auto load_new_row = [&](const UnitMeta &m_, uint2 &k2, uint2 &v2) {
         const long long row0 = ((long long)m_.b * p.Hkv + m_.g * p.hg + h) * D;
-        if constexpr (!FP8) {
+        if constexpr (CT == kBf16) {
             k2 = __ldg(reinterpret_cast<const uint2 *>(p.k_new + row0 + lane * 4));
             v2 = __ldg(reinterpret_cast<const uint2 *>(p.v_new + row0 + lane * 4));
         } else {  // quantised as pkv_kv_store_fp8 does
@@ -2117,7 +2156,7 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
             const int qs = int(segs & uint32_t(qslots - 1));
             const uint32_t quse = segs >> (qslots - 1);
             ksc = p.scale_log2;  // E4M3 caches: the kv head's K scale joins the score scale
-            if constexpr (FP8) {
+            if constexpr (CT == kE4m3) {
                 ksc *= __ldg(p.k_scale + mt.g * p.hg + h);
                 vsc = __ldg(p.v_scale + mt.g * p.hg + h);
             }
@@ -2125,7 +2164,7 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
                 if (lane == 0) flag_error(p.err, PKV_ERR_WAIT_TIMEOUT);
                 break;
             }
-            if constexpr (!QS && !kLateNewRow) {
+            if constexpr (!QS && !kLateNewRow && CT != kI8) {
                 // the segment's new K/V row, used at its last tile (its load's latency hides until then)
                 if (p.k_new && lane < TC::ROWB / 8) load_new_row(mt, kn, vn);
             }
@@ -2140,13 +2179,21 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
                 const int row = g8 + 8 * hr;
                 shift[hr] = (mt.cnt - 1) - (jq * p.qn + row / p.gq);
                 const uint16_t *qr = qw + row * D;
+                float qs2 = 1.0f;  // int8 caches: power of two that brings the row's largest |q| to [2^14, 2^15)
+                if constexpr (CT == kI8) rowf[hr] = p.scale_log2 * q_row_scale<D>(qr, row < nvh, r4, qs2);
 #pragma unroll
                 for (int ks = 0; ks < TC::KS; ++ks) {
                     qa[ks][2 * hr] = qa[ks][2 * hr + 1] = 0u;
                     if (row < nvh) {
-                        if constexpr (!FP8) {
+                        if constexpr (CT == kBf16) {
                             qa[ks][2 * hr] = *reinterpret_cast<const uint32_t *>(qr + 16 * ks + 2 * r4);
                             qa[ks][2 * hr + 1] = *reinterpret_cast<const uint32_t *>(qr + 16 * ks + 8 + 2 * r4);
+                        } else if constexpr (CT == kI8) {
+                            const uint2 w = *reinterpret_cast<const uint2 *>(qr + 16 * ks + 4 * r4);
+                            qa[ks][2 * hr] = f16x2_of(__uint_as_float(w.x << 16) * qs2,
+                                                      __uint_as_float(w.x & 0xffff0000u) * qs2);
+                            qa[ks][2 * hr + 1] = f16x2_of(__uint_as_float(w.y << 16) * qs2,
+                                                          __uint_as_float(w.y & 0xffff0000u) * qs2);
                         } else {
                             const uint2 w = *reinterpret_cast<const uint2 *>(qr + 16 * ks + 4 * r4);
                             qa[ks][2 * hr] = f16x2_sat(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u));
@@ -2171,7 +2218,7 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
         const int valid = min(TC::TW, mt.L - tok0);
         if (valid > 0 && nvh > 0) {
             const uint32_t kb = stage_addr + uint32_t(s) * lay.stage_bytes;
-            if constexpr (!QS) {
+            if constexpr (!QS && CT != kI8) {
                 // fused store: the tile holding the new token takes its K/V row from k_new / v_new (the
                 // cache row the copy brought is the previous content) and writes it to the cache; no
                 // other CTA reads that row in this kernel (the block of a sequence's last token is its own)
@@ -2199,10 +2246,22 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
             int lim[HR];
 #pragma unroll
             for (int hr = 0; hr < HR; ++hr) lim[hr] = min(valid, mt.L - tok0 - shift[hr]);
-            if (valid == TC::TW)
-                attend_tile<D, FP8, QS, TC::HR, false>(kb, kb + lay.kv_bytes, off, qa, ksc, lim, valid, m, l, o, lane);
+            if constexpr (CT == kI8) {
+                const float2 *sc = reinterpret_cast<const float2 *>(smem + lay.off_sc +
+                                                                    uint32_t(s) * scale_bytes(p.toks, p.hg));
+                float2 sct[TC::NT];
+#pragma unroll
+                for (int st = 0; st < TC::NT; ++st) sct[st] = sc[(jt * TC::NT + st) * p.hg + h];
+                if (valid == TC::TW)
+                    attend_tile_i8<D, QS, TC::HR, false>(kb, kb + lay.kv_bytes, off, qa, rowf, sct, lim, valid, m, l, o,
+                                                         lane);
+                else
+                    attend_tile_i8<D, QS, TC::HR, true>(kb, kb + lay.kv_bytes, off, qa, rowf, sct, lim, valid, m, l, o,
+                                                        lane);
+            } else if (valid == TC::TW)
+                attend_tile<D, CT, QS, TC::HR, false>(kb, kb + lay.kv_bytes, off, qa, ksc, lim, valid, m, l, o, lane);
             else
-                attend_tile<D, FP8, QS, TC::HR, true>(kb, kb + lay.kv_bytes, off, qa, ksc, lim, valid, m, l, o, lane);
+                attend_tile<D, CT, QS, TC::HR, true>(kb, kb + lay.kv_bytes, off, qa, ksc, lim, valid, m, l, o, lane);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[s]);
@@ -2248,7 +2307,7 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
                                     for (int mi = 0; mi < TC::MT; ++mi)
 #pragma unroll
                                         for (int half = 0; half < 2; ++half)
-                                            mine[hh * D + dim_of<FP8>(mi, half, g8)] = o[mi][hr][2 * half + e];
+                                            mine[hh * D + dim_of<CT>(mi, half, g8)] = o[mi][hr][2 * half + e];
                                     if (g8 == 0) {
                                         mine[G * D + hh] = mc[hr][e];
                                         mine[G * D + G + hh] = lc[hr][e];
@@ -2289,7 +2348,7 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
 #pragma unroll
                                             for (int half = 0; half < 2; ++half)
                                                 o[mi][hr][2 * half + e] =
-                                                    fmaf(f, st2[hh * D + dim_of<FP8>(mi, half, g8)],
+                                                    fmaf(f, st2[hh * D + dim_of<CT>(mi, half, g8)],
                                                          o[mi][hr][2 * half + e]);
                                     }
                                     mc[hr][e] = M;
@@ -2316,12 +2375,12 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
                                                           (long long)kvh * p.gq + hh % p.gq) * D;
 #pragma unroll
                                 for (int mi = 0; mi < TC::MT; ++mi) {
-                                    if constexpr (FP8) {
-                                        *reinterpret_cast<uint32_t *>(orow + dim_of<FP8>(mi, 0, g8)) =
+                                    if constexpr (CT != kBf16) {
+                                        *reinterpret_cast<uint32_t *>(orow + dim_of<CT>(mi, 0, g8)) =
                                             pack_bf16x2(o[mi][hr][e] * inv, o[mi][hr][2 + e] * inv);
                                     } else {
-                                        orow[dim_of<FP8>(mi, 0, g8)] = uint16_t(pack_bf16x2(o[mi][hr][e] * inv, 0.f));
-                                        orow[dim_of<FP8>(mi, 1, g8)] =
+                                        orow[dim_of<CT>(mi, 0, g8)] = uint16_t(pack_bf16x2(o[mi][hr][e] * inv, 0.f));
+                                        orow[dim_of<CT>(mi, 1, g8)] =
                                             uint16_t(pack_bf16x2(o[mi][hr][2 + e] * inv, 0.f));
                                     }
                                 }
@@ -2345,12 +2404,12 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
                                 float *dst = p.ws_acc + (slot * G + hh) * D;
 #pragma unroll
                                 for (int mi = 0; mi < TC::MT; ++mi) {
-                                    if constexpr (FP8) {
-                                        *reinterpret_cast<float2 *>(dst + dim_of<FP8>(mi, 0, g8)) =
+                                    if constexpr (CT != kBf16) {
+                                        *reinterpret_cast<float2 *>(dst + dim_of<CT>(mi, 0, g8)) =
                                             make_float2(o[mi][hr][e], o[mi][hr][2 + e]);
                                     } else {
-                                        dst[dim_of<FP8>(mi, 0, g8)] = o[mi][hr][e];
-                                        dst[dim_of<FP8>(mi, 1, g8)] = o[mi][hr][2 + e];
+                                        dst[dim_of<CT>(mi, 0, g8)] = o[mi][hr][e];
+                                        dst[dim_of<CT>(mi, 1, g8)] = o[mi][hr][2 + e];
                                     }
                                 }
                                 if (g8 == 0)
@@ -2367,7 +2426,7 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
                                            gen, uint32_t(piece), uint32_t(mt.n), p.err);
                     if (__shfl_sync(kFull, last, 0)) {
                         __threadfence();
-                        merge_pieces<D, G, FP8, QS>(p, bound, slice_of(bound, nslots, x0),
+                        merge_pieces<D, G, CT, QS>(p, bound, slice_of(bound, nslots, x0),
                                                     slice_of(bound, nslots, x0 + mt.n - 1), x0, mt.g, h, jq, mt.b,
                                                     kvh, nvh, lane);
                     }
@@ -2478,9 +2537,9 @@ inline bool cached_cache_map(CUtensorMap *map, int dev, const void *base, bool f
 
 // cudaFuncSetAttribute once per device and kernel variant (it is a host-side
 // driver call; repeating it on every launch costs microseconds).  Keyed on
-// <D, G, FP8, QS, TC5>: every variant has the same function-pointer type, so
+// <D, G, CT, QS, TC5>: every variant has the same function-pointer type, so
 // the memo must be per instantiation.
-template <int D, int G, bool FP8, bool QS, bool TC5, typename Kernel>
+template <int D, int G, int CT, bool QS, bool TC5, typename Kernel>
 inline bool ensure_smem_attribute(Kernel kern, int dev, size_t smem)
 {
     static std::mutex mu;
@@ -2498,26 +2557,28 @@ inline bool ensure_smem_attribute(Kernel kern, int dev, size_t smem)
     return true;
 }
 
-template <int D, int G, bool FP8, bool QS, bool TC5 = false>
+template <int D, int G, int CT, bool QS, bool TC5 = false>
 pkv_status launch_decode(LaunchArgs &a)
 {
     DecodeParams &p = a.p;
     // ring depth: as many stages (up to kMaxStages) as the shared memory holds, beside two Q row
     // buffers, or beside one where that fits more stages (a segment's Q rows go into registers at its
     // first tile, so one buffer is free again long before the next segment needs it)
-    constexpr int ES = FP8 ? 1 : 2;
+    constexpr int ES = CT != kBf16 ? 1 : 2;
     auto depth = [&](int qslots) {
         int n = kMaxStages;
-        while (n > 2 && cta_layout(D, G, ES, p.hg, p.sub, n, p.B, QS, TC5, qslots).total > uint32_t(a.max_smem)) --n;
+        while (n > 2 &&
+               cta_layout(D, G, ES, p.hg, p.sub, n, p.B, QS, TC5, qslots, CT == kI8).total > uint32_t(a.max_smem))
+            --n;
         return n;
     };
     int nst = depth(2);
     p.qslots = 2;
-    if (one_q_buffer_ok(G, FP8, QS, TC5) && depth(1) > nst) {
+    if (one_q_buffer_ok(G, CT != kBf16, QS, TC5) && depth(1) > nst) {
         nst = depth(1);
         p.qslots = 1;
     }
-    const CtaLayout lay = cta_layout(D, G, ES, p.hg, p.sub, nst, p.B, QS, TC5, p.qslots);
+    const CtaLayout lay = cta_layout(D, G, ES, p.hg, p.sub, nst, p.B, QS, TC5, p.qslots, CT == kI8);
     if (lay.total > uint32_t(a.max_smem)) return PKV_EUNSUPPORTED;
     p.nst = nst;
 
@@ -2534,12 +2595,12 @@ pkv_status launch_decode(LaunchArgs &a)
 
     CUtensorMap kmap, vmap;
     const int64_t rows = int64_t(p.NB) * p.bs;
-    if (!cached_cache_map(&kmap, a.device, a.k_cache, FP8, D, p.Hkv, rows, p.hg, p.boxtok) ||
-        !cached_cache_map(&vmap, a.device, a.v_cache, FP8, D, p.Hkv, rows, p.hg, p.boxtok))
+    if (!cached_cache_map(&kmap, a.device, a.k_cache, CT != kBf16, D, p.Hkv, rows, p.hg, p.boxtok) ||
+        !cached_cache_map(&vmap, a.device, a.v_cache, CT != kBf16, D, p.Hkv, rows, p.hg, p.boxtok))
         return PKV_ECUDA;
 
-    auto kern = paged_decode_kernel<D, G, FP8, QS, TC5>;
-    if (!ensure_smem_attribute<D, G, FP8, QS, TC5>(kern, a.device, lay.total)) return PKV_ECUDA;
+    auto kern = paged_decode_kernel<D, G, CT, QS, TC5>;
+    if (!ensure_smem_attribute<D, G, CT, QS, TC5>(kern, a.device, lay.total)) return PKV_ECUDA;
     const cudaError_t e =
         launch_pdl(kern, dim3(grid), dim3((p.cons + 1) * 32), lay.total, a.stream, kmap, vmap, p);
     if (e != cudaSuccess) {
@@ -2551,18 +2612,18 @@ pkv_status launch_decode(LaunchArgs &a)
 
 using LaunchFn = pkv_status (*)(LaunchArgs &);
 
-template <int D, bool FP8, bool QS>
+template <int D, int CT, bool QS>
 LaunchFn pick_group(int G)
 {
     switch (G) {
-    case 1: return launch_decode<D, 1, FP8, QS>;
-    case 2: return launch_decode<D, 2, FP8, QS>;
-    case 3: return launch_decode<D, 3, FP8, QS>;
-    case 4: return launch_decode<D, 4, FP8, QS>;
-    case 5: return launch_decode<D, 5, FP8, QS>;
-    case 6: return launch_decode<D, 6, FP8, QS>;
-    case 7: return launch_decode<D, 7, FP8, QS>;
-    case 8: return launch_decode<D, 8, FP8, QS>;
+    case 1: return launch_decode<D, 1, CT, QS>;
+    case 2: return launch_decode<D, 2, CT, QS>;
+    case 3: return launch_decode<D, 3, CT, QS>;
+    case 4: return launch_decode<D, 4, CT, QS>;
+    case 5: return launch_decode<D, 5, CT, QS>;
+    case 6: return launch_decode<D, 6, CT, QS>;
+    case 7: return launch_decode<D, 7, CT, QS>;
+    case 8: return launch_decode<D, 8, CT, QS>;
     default: return nullptr;
     }
 }
@@ -2574,6 +2635,9 @@ LaunchFn pick_group(int G)
 LaunchFn pick_decode_fp8(int D, int G);
 LaunchFn pick_decode_qs(int D, int G);
 LaunchFn pick_decode_wide(int D, int G);  // regular bf16 CTAs, 9 to 16 virtual heads (pkv_decode_wide.cu)
+LaunchFn pick_decode_i8(int D, int G);        // int8 caches, 1 to 8 virtual heads (pkv_decode_i8.cu)
+LaunchFn pick_decode_i8_wide(int D, int G);   // int8 caches, 9 to 16 virtual heads (pkv_decode_i8_wide.cu)
+LaunchFn pick_decode_i8_qs(int D, int G);     // int8 caches, query-split CTAs (pkv_decode_i8_wide.cu)
 LaunchFn pick_decode_tc5(int D);          // tensor-memory query-split CTAs, 16 virtual heads (pkv_decode_tc5.cu)
 
 // Whether a query-split call can run on the tensor-memory CTAs: bf16 caches, entries of 128 rows

@@ -12,10 +12,10 @@ template <int D>
 static LaunchFn pick_qs(int G)
 {
     switch (G) {
-    case 12: return launch_decode<D, 12, false, true>;
-    case 14: return launch_decode<D, 14, false, true>;
-    case 15: return launch_decode<D, 15, false, true>;
-    case 16: return launch_decode<D, 16, false, true>;
+    case 12: return launch_decode<D, 12, kBf16, true>;
+    case 14: return launch_decode<D, 14, kBf16, true>;
+    case 15: return launch_decode<D, 15, kBf16, true>;
+    case 16: return launch_decode<D, 16, kBf16, true>;
     default: return nullptr;
     }
 }

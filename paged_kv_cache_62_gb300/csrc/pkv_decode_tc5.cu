@@ -9,8 +9,8 @@ namespace pkv {
 
 LaunchFn pick_decode_tc5(int D)
 {
-    if (D == 64) return launch_decode<64, 16, false, true, true>;
-    if (D == 128) return launch_decode<128, 16, false, true, true>;
+    if (D == 64) return launch_decode<64, 16, kBf16, true, true>;
+    if (D == 128) return launch_decode<128, 16, kBf16, true, true>;
     return nullptr;
 }
 

@@ -11,14 +11,14 @@ template <int D>
 static LaunchFn pick_wide(int G)
 {
     switch (G) {
-    case 9: return launch_decode<D, 9, false, false>;
-    case 10: return launch_decode<D, 10, false, false>;
-    case 11: return launch_decode<D, 11, false, false>;
-    case 12: return launch_decode<D, 12, false, false>;
-    case 13: return launch_decode<D, 13, false, false>;
-    case 14: return launch_decode<D, 14, false, false>;
-    case 15: return launch_decode<D, 15, false, false>;
-    case 16: return launch_decode<D, 16, false, false>;
+    case 9: return launch_decode<D, 9, kBf16, false>;
+    case 10: return launch_decode<D, 10, kBf16, false>;
+    case 11: return launch_decode<D, 11, kBf16, false>;
+    case 12: return launch_decode<D, 12, kBf16, false>;
+    case 13: return launch_decode<D, 13, kBf16, false>;
+    case 14: return launch_decode<D, 14, kBf16, false>;
+    case 15: return launch_decode<D, 15, kBf16, false>;
+    case 16: return launch_decode<D, 16, kBf16, false>;
     default: return nullptr;
     }
 }

@@ -103,6 +103,19 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     return __all_sync(kFull, ok);
 }
 
+// 8-byte asynchronous copy global -> shared by this thread, and an arrival on `bar` once all of the
+// thread's copies so far have landed (one of the arrivals the barrier was initialised with).
+__device__ __forceinline__ void copy_async8(void *dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(__cvta_generic_to_global(src))
+                 : "memory");
+}
+
+__device__ __forceinline__ void copy_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // ---------------------------------------------------------------- programmatic dependent launch
 // Every pkv kernel is launched with programmatic stream serialization: it may
 // start while the previous kernel in the stream is still running, so it calls

@@ -1,0 +1,211 @@
+// One warp tile of the decode kernel over int8 caches.  Included by the translation units that
+// instantiate the kernel for them, after pkv_decode_kernel.cuh.
+//
+// A cached value is code * scale with one scale per kScaleToks = 16 tokens and kv head, one for K and one
+// for V, so a 16-token sub-tile of the MMA tile has one (K scale s_k, V scale s_v) pair:
+//   x_j = (q . code_j) * (scale * s_k),   o += s_v * sum_j 2^(x_j - m) codeV_j.
+// The products run in f16 with fp32 accumulators: an int8 code is exact in f16 (one byte permute builds
+// 1024 + (code + 128), one subtraction of 1152 takes the rest off), a bf16 query element too once its row
+// is brought to one power of two (see q_row_scale), and a weight rounds by at most 2^-11 of itself.  The V scale
+// multiplies the sub-tile's fp32 product, not the f16 weights: s_v may be any size without moving the
+// weights out of the f16 range, and costs one fp32 FMA per 16 weights.
+#pragma once
+
+#include "pkv_decode_kernel.cuh"
+
+namespace pkv {
+
+// Head room of the weights: they stay <= 2^(kI8Head + kRescaleSlack) = 2^14 (f16 holds up to 65504), and the
+// largest of a row is at least 2^kI8Head when its max last moved, so the f16 subnormal step of 2^-24 is
+// 2^-30 of it.
+constexpr float kI8Head = 6.0f;
+
+// Four int8 codes (byte e is element e) as f16 pairs picked by the two permute selectors: K operands take
+// elements (0, 1) and (2, 3), V operands (0, 2) and (1, 3).
+template <uint32_t SEL0, uint32_t SEL1>
+__device__ __forceinline__ void i8x4_to_f16x2x2(uint32_t codes, uint32_t &a, uint32_t &b)
+{
+    const uint32_t u = codes ^ 0x80808080u;  // code + 128
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const uint32_t x = __byte_perm(u, 0x64646464u, SEL0), y = __byte_perm(u, 0x64646464u, SEL1);
+    const __half2 hx = __hsub2(*reinterpret_cast<const __half2 *>(&x), off);
+    const __half2 hy = __hsub2(*reinterpret_cast<const __half2 *>(&y), off);
+    a = *reinterpret_cast<const uint32_t *>(&hx);
+    b = *reinterpret_cast<const uint32_t *>(&hy);
+}
+
+// The power of two 2^k that brings the row's largest |q| to [2^14, 2^15) (mul), so that every element of at
+// least 2^-28 of it stays a normal f16; returns 2^-k.  A row of zeros, or one holding an infinity or NaN, is
+// left as it is.  The row's four threads (r4 = 0..3) look at their own dims.
+template <int D>
+__device__ __forceinline__ float q_row_scale(const uint16_t *qr, bool live, int r4, float &mul)
+{
+    uint32_t mx = 0u;
+    if (live) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(qr + 16 * ks + 4 * r4);
+            mx = max(max(mx, max(w.x & 0x7fffu, (w.x >> 16) & 0x7fffu)), max(w.y & 0x7fffu, (w.y >> 16) & 0x7fffu));
+        }
+    }
+    mx = max(mx, __shfl_xor_sync(kFull, mx, 1));
+    mx = max(mx, __shfl_xor_sync(kFull, mx, 2));
+    const int e = int(mx >> 7);  // biased exponent
+    const int k = mx == 0u || e == 255 ? 0 : 141 - max(e, 15);
+    mul = __uint_as_float(uint32_t(127 + k) << 23);
+    return __uint_as_float(uint32_t(127 - k) << 23);
+}
+
+template <int D, bool QS, int HR_, bool TAIL>
+__device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const LaneOffsets<D, kI8, QS> &off,
+                                               const uint32_t (&qa)[Tc<D, kI8, QS, HR_>::KS][2 * HR_],
+                                               const float (&rowf)[HR_], const float2 (&sc)[2],
+                                               const int (&lim)[HR_], int valid, float (&m)[HR_], float (&l)[HR_],
+                                               float (&o)[Tc<D, kI8, QS, HR_>::MT][HR_][4], int lane)
+{
+    using T = Tc<D, kI8, QS, HR_>;
+    constexpr int NT = T::NT, HR = T::HR;
+    static_assert(NT == 2, "two 16-token sub-tiles, one pair of scales each");
+    const int r4 = lane & 3;
+    auto a1 = [&](int ks) { return HR == 2 ? qa[ks][2 % (2 * HR)] : 0u; };
+    auto a3 = [&](int ks) { return HR == 2 ? qa[ks][3 % (2 * HR)] : 0u; };
+    float sa[NT][2][4];  // [sub-tile][n-tile][fragment]
+#pragma unroll
+    for (int st = 0; st < NT; ++st)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sa[st][nt][e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < T::NCP; ++i) {
+#pragma unroll
+        for (int st = 0; st < NT; ++st) {
+            uint32_t r0, r1, r2, r3;
+            ldsm_x4(kb + off.at(st, i), r0, r1, r2, r3);
+            // chunk 2i (r0, r2) is k-step 2i, chunk 2i + 1 (r1, r3) k-step 2i + 1; a register holds codes
+            // 4 r4 .. 4 r4 + 3 of a token (tokens 0-7 in r0, r1; 8-15 in r2, r3)
+            uint32_t b[4][2];
+            i8x4_to_f16x2x2<0x4140, 0x4342>(r0, b[0][0], b[0][1]);
+            i8x4_to_f16x2x2<0x4140, 0x4342>(r1, b[1][0], b[1][1]);
+            i8x4_to_f16x2x2<0x4140, 0x4342>(r2, b[2][0], b[2][1]);
+            i8x4_to_f16x2x2<0x4140, 0x4342>(r3, b[3][0], b[3][1]);
+            mma_f16_16816(sa[st][0], qa[2 * i][0], a1(2 * i), qa[2 * i][1], a3(2 * i), b[0][0], b[0][1]);
+            mma_f16_16816(sa[st][1], qa[2 * i][0], a1(2 * i), qa[2 * i][1], a3(2 * i), b[2][0], b[2][1]);
+            mma_f16_16816(sa[st][0], qa[2 * i + 1][0], a1(2 * i + 1), qa[2 * i + 1][1], a3(2 * i + 1), b[1][0],
+                          b[1][1]);
+            mma_f16_16816(sa[st][1], qa[2 * i + 1][0], a1(2 * i + 1), qa[2 * i + 1][1], a3(2 * i + 1), b[3][0],
+                          b[3][1]);
+        }
+    }
+    // the thread's scores (see attend_tile); a sub-tile without a token has no scale, its scores are masked
+    float x[HR][NT * 4];
+#pragma unroll
+    for (int hr = 0; hr < HR; ++hr)
+#pragma unroll
+        for (int st = 0; st < NT; ++st) {
+            const float f = rowf[hr] * sc[st].x;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    x[hr][4 * st + 2 * nt + e] =
+                        16 * st + 8 * nt + 2 * r4 + e < lim[hr] ? sa[st][nt][2 * hr + e] * f : -INFINITY;
+        }
+    float mx[HR];
+    bool grow = false;
+#pragma unroll
+    for (int hr = 0; hr < HR; ++hr) {
+        mx[hr] = x[hr][0];
+#pragma unroll
+        for (int k = 1; k < NT * 4; ++k) mx[hr] = fmaxf(mx[hr], x[hr][k]);
+        mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(kFull, mx[hr], 1));
+        mx[hr] = fmaxf(mx[hr], __shfl_xor_sync(kFull, mx[hr], 2)) - kI8Head;
+        grow |= mx[hr] > m[hr] + kRescaleSlack;
+    }
+    if (__any_sync(kFull, grow)) {
+#pragma unroll
+        for (int hr = 0; hr < HR; ++hr) {
+            const float mn = fmaxf(m[hr], mx[hr]);
+            const float alpha = mn == -INFINITY ? 1.0f : ex2(m[hr] - mn);
+            l[hr] *= alpha;
+            m[hr] = mn;
+            const float a0 = __shfl_sync(kFull, alpha, 8 * r4), a1v = __shfl_sync(kFull, alpha, 8 * r4 + 4);
+#pragma unroll
+            for (int mt = 0; mt < T::MT; ++mt) {
+                o[mt][hr][0] *= a0;
+                o[mt][hr][1] *= a1v;
+                o[mt][hr][2] *= a0;
+                o[mt][hr][3] *= a1v;
+            }
+        }
+    }
+    uint32_t pb[HR][NT][2];
+#pragma unroll
+    for (int hr = 0; hr < HR; ++hr) {
+        const float mr = m[hr] == -INFINITY ? 0.f : m[hr];
+        float pr[NT * 4];
+#pragma unroll
+        for (int k = 0; k < NT * 4; ++k) pr[k] = ex2(x[hr][k] - mr);
+        float ps = 0.f;
+#pragma unroll
+        for (int k = 0; k < NT * 4; ++k) ps += pr[k];
+        l[hr] += ps;
+#pragma unroll
+        for (int st = 0; st < NT; ++st)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) pb[hr][st][c] = f16x2_of(pr[4 * st + 2 * c], pr[4 * st + 2 * c + 1]);
+    }
+#pragma unroll
+    for (int st = 0; st < NT; ++st) {
+        if (TAIL && 16 * st >= valid) break;  // no token, and no scale
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if constexpr (TAIL) {
+            const int v0 = valid - 16 * st;
+            keep0 = (2 * r4 < v0 ? 0x0000ffffu : 0u) | (2 * r4 + 1 < v0 ? 0xffff0000u : 0u);
+            keep1 = (2 * r4 + 8 < v0 ? 0x0000ffffu : 0u) | (2 * r4 + 9 < v0 ? 0xffff0000u : 0u);
+        }
+        // s_v for the thread's output columns; a block whose scale is NaN or infinite reaches only the
+        // queries that see one of its tokens (0 * NaN would reach them all)
+        float vs[HR][2];
+#pragma unroll
+        for (int hr = 0; hr < HR; ++hr) vs[hr][0] = vs[hr][1] = sc[st].y;
+        if (!(fabsf(sc[st].y) < INFINITY)) {
+#pragma unroll
+            for (int hr = 0; hr < HR; ++hr)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (__shfl_sync(kFull, lim[hr], 8 * r4 + 4 * e) <= 16 * st) vs[hr][e] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < T::NCP; ++i) {
+            uint32_t r0, r1, r2, r3;
+            ldsm_x4_t(vb + off.at(st, i), r0, r1, r2, r3);
+            if constexpr (TAIL) {
+                r0 &= keep0;
+                r1 &= keep0;
+                r2 &= keep1;
+                r3 &= keep1;
+            }
+            // a register holds (token 2 r4: dims 2g, 2g + 1 | token 2 r4 + 1: the same) of a 16-dim chunk: the
+            // permute pairs the two tokens of a dim
+            uint32_t a[4][2];
+            i8x4_to_f16x2x2<0x4240, 0x4341>(r0, a[0][0], a[0][1]);
+            i8x4_to_f16x2x2<0x4240, 0x4341>(r1, a[1][0], a[1][1]);
+            i8x4_to_f16x2x2<0x4240, 0x4341>(r2, a[2][0], a[2][1]);
+            i8x4_to_f16x2x2<0x4240, 0x4341>(r3, a[3][0], a[3][1]);
+#pragma unroll
+            for (int hr = 0; hr < HR; ++hr) {
+                float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16_16816(c0, a[0][0], a[0][1], a[2][0], a[2][1], pb[hr][st][0], pb[hr][st][1]);
+                mma_f16_16816(c1, a[1][0], a[1][1], a[3][0], a[3][1], pb[hr][st][0], pb[hr][st][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    o[2 * i][hr][e] = fmaf(vs[hr][e & 1], c0[e], o[2 * i][hr][e]);
+                    o[2 * i + 1][hr][e] = fmaf(vs[hr][e & 1], c1[e], o[2 * i + 1][hr][e]);
+                }
+            }
+        }
+    }
+}
+
+}  // namespace pkv

@@ -18,10 +18,12 @@ LIB_PATH = os.path.join(_HERE, "libpkv.so")
 
 OK, EINVAL, EUNSUPPORTED, ECUDA, EWORKSPACE, EBOUNDS, EFULL = 0, -1, -2, -3, -4, -5, -6
 ERR_SLOT_RANGE, ERR_BLOCK_RANGE, ERR_CONTEXT_RANGE, ERR_WAIT_TIMEOUT, ERR_WORKSPACE = 0x1, 0x2, 0x4, 0x8, 0x10
+ERR_AXIS_RANGE = 0x20
+I8_BLOCK = 16  # tokens that share a scale in an int8 cache (PKV_I8_BLOCK)
 MAX_SEQS, MAX_WORKERS = 16384, 4096
 
 # name -> (restype, argtypes), mirroring include/pkv.h
-_P, _I32, _SZ, _F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
+_P, _I32, _I64, _SZ, _F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 SIGNATURES = {
     "pkv_abi_version": (ctypes.c_int, []),
     "pkv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -46,6 +48,17 @@ SIGNATURES = {
     "pkv_kv_store_fp8": (ctypes.c_int, [_P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P]),
     "pkv_paged_decode_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32,
                                             _I32, _F32, _P, _P, _SZ, _I32, _P, _P]),
+    "pkv_kv_store_i8": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _I32, _P, _P, _I32, _I32, _I32, _P, _P, _P, _I32, _I32,
+                                       _I32, _I32, _P, _P]),
+    "pkv_paged_decode_i8": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                                           _F32, _P, _P, _SZ, _I32, _P, _P]),
+    "pkv_paged_attention_i8": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32,
+                                              _I32, _I32, _F32, _P, _I32, _P, _SZ, _I32, _P, _P]),
+    "pkv_copy_blocks_i8": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P]),
+    "pkv_rope": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _P, _I64,
+                                _P, _I64, _P, _P]),
+    "pkv_rope_store": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _I32, _P, _P, _P, _I32, _I32, _I32, _I32,
+                                      _I32, _I32, _P, _I64, _P, _P, _I32, _I32, _P, _P]),
     "pkv_allocator_create": (_P, [_I32, _I32]),
     "pkv_allocator_destroy": (None, [_P]),
     "pkv_allocator_add": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32]),
@@ -113,8 +126,9 @@ def _opt(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is None:  # the current stream's handle, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def decode_slot_mapping(block_tables: torch.Tensor, context_lens: torch.Tensor, block_size: int, num_blocks: int,
@@ -472,3 +486,184 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         _dev(out, torch.bfloat16, "out", 3), int(new_per_seq), _dev(workspace, torch.uint8, "workspace"),
         workspace.numel(),
         int(num_workers), _opt(err_word), _stream(stream)), "pkv_paged_attention")
+
+
+def _arg(t: torch.Tensor, dtype, name: str, ndim: int, dev: int) -> int:
+    """Pointer of a dense tensor on device `dev`; the checks of _dev in one expression (a call's host time is spent
+    here)."""
+    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous() or t.dim() != ndim:
+        _dev(t, dtype, name, ndim)
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, dev: int) -> tuple[int, int]:
+    """Pointer and row stride of a bf16 [T, H, D] tensor whose rows ([H, D]) are dense and may lie apart (a part of
+    a wider projection's rows)."""
+    if t.get_device() != dev or t.dtype is not torch.bfloat16 or t.dim() != 3:
+        _dev(t.contiguous(), torch.bfloat16, name, 3)
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"{name}: the heads of a row must be dense")
+    return t.data_ptr(), (st if T > 1 else H * D)
+
+
+def _device(t: torch.Tensor, name: str) -> int:
+    """The device of a call's tensors: the current one, where the library launches."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _err(err_word, dev: int) -> int | None:
+    return None if err_word is None else _arg(err_word, torch.int32, "err_word", err_word.dim(), dev)
+
+
+def _i8_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor, dev: int, what: str):
+    """Pointers and shape of an int8 cache; scales [NB, bs / 16, Hkv, 2]."""
+    kp, vp = _arg(k_cache, torch.int8, "k_cache", 4, dev), _arg(v_cache, torch.int8, "v_cache", 4, dev)
+    NB, bs, Hkv, D = k_cache.shape
+    if v_cache.shape != k_cache.shape or scales.shape != (NB, bs // I8_BLOCK, Hkv, 2):
+        raise ValueError(f"{what}: shape mismatch")
+    return kp, vp, _arg(scales, torch.float32, "scales", 4, dev), NB, bs, Hkv, D
+
+
+def alloc_i8_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int, device=None):
+    """(k_cache, v_cache, scales) of an int8 cache, zero-filled."""
+    if block_size % I8_BLOCK:
+        raise ValueError(f"int8 caches need a block_size that is a multiple of {I8_BLOCK}")
+    shape = (num_blocks, block_size, num_kv_heads, head_dim)
+    kc, vc = (torch.zeros(shape, dtype=torch.int8, device=device or "cuda") for _ in range(2))
+    return kc, vc, torch.zeros(num_blocks, block_size // I8_BLOCK, num_kv_heads, 2, device=device or "cuda")
+
+
+def kv_store_i8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor,
+                block_tables: torch.Tensor, context_lens: torch.Tensor, cu_seqlens: torch.Tensor | None = None,
+                new_per_seq: int = 0, err_word: torch.Tensor | None = None, stream=None) -> None:
+    """Quantise each sequence's new rows (cu_seqlens[b]..cu_seqlens[b+1], or b*n..b*n+n-1 with new_per_seq = n) and
+    store them at its last positions of an int8 cache with a scale per 16 tokens and kv head.  k and v may be
+    parts of wider rows."""
+    dev = _device(k, "k")
+    (kp, ks), (vp, vs) = _rows(k, "k", dev), _rows(v, "v", dev)
+    kc, vc, sc, NB, bs, Hkv, D = _i8_cache(k_cache, v_cache, scales, dev, "kv_store_i8")
+    T, Hk, Dk = k.shape
+    B, mb = block_tables.shape
+    if v.shape != k.shape or Hk != Hkv or Dk != D or context_lens.numel() != B \
+            or (cu_seqlens is None and new_per_seq <= 0) or (cu_seqlens is not None and cu_seqlens.numel() != B + 1):
+        raise ValueError("kv_store_i8: shape mismatch")
+    _check(load().pkv_kv_store_i8(
+        kp, vp, ks, vs, _arg(block_tables, torch.int32, "block_tables", 2, dev), mb,
+        None if cu_seqlens is None else _arg(cu_seqlens, torch.int32, "cu_seqlens", 1, dev),
+        _arg(context_lens, torch.int32, "context_lens", 1, dev), B, T, int(new_per_seq), kc, vc, sc, NB, bs, Hkv, D,
+        _err(err_word, dev), _stream(stream)), "pkv_kv_store_i8")
+
+
+def paged_decode_i8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor,
+                    block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, out: torch.Tensor,
+                    workspace: torch.Tensor, max_context_len: int | None = None, num_workers: int = 0,
+                    err_word: torch.Tensor | None = None, stream=None) -> None:
+    """paged_decode over an int8 cache (int8 [NB, bs, Hkv, D]) with scales [NB, bs / 16, Hkv, 2]."""
+    dev = _device(q, "q")
+    kc, vc, sc, NB, bs, Hkv, D = _i8_cache(k_cache, v_cache, scales, dev, "paged_decode_i8")
+    B, Hq, Dq = q.shape
+    Bt, mb = block_tables.shape
+    if Dq != D or Bt != B or context_lens.numel() != B or out.shape != q.shape:
+        raise ValueError("paged_decode_i8: shape mismatch")
+    _check(load().pkv_paged_decode_i8(
+        _arg(q, torch.bfloat16, "q", 3, dev), kc, vc, sc, _arg(block_tables, torch.int32, "block_tables", 2, dev), mb,
+        _arg(context_lens, torch.int32, "context_lens", 1, dev), B, Hq, Hkv, D, bs, NB,
+        mb * bs if max_context_len is None else int(max_context_len), float(scale),
+        _arg(out, torch.bfloat16, "out", 3, dev),
+        _arg(workspace, torch.uint8, "workspace", 1, dev), workspace.numel(), int(num_workers), _err(err_word, dev),
+        _stream(stream)), "pkv_paged_decode_i8")
+
+
+def paged_attention_i8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor,
+                       block_tables: torch.Tensor, cu_seqlens_q: torch.Tensor | None, context_lens: torch.Tensor,
+                       scale: float, out: torch.Tensor, workspace: torch.Tensor, max_context_len: int | None = None,
+                       num_workers: int = 0, err_word: torch.Tensor | None = None, stream=None,
+                       new_per_seq: int = 0) -> None:
+    """paged_attention over an int8 cache (int8 [NB, bs, Hkv, D]) with scales [NB, bs / 16, Hkv, 2]; workspace from
+    alloc_attention_workspace."""
+    dev = _device(q, "q")
+    kc, vc, sc, NB, bs, Hkv, D = _i8_cache(k_cache, v_cache, scales, dev, "paged_attention_i8")
+    T, Hq, Dq = q.shape
+    B, mb = block_tables.shape
+    if Dq != D or context_lens.numel() != B or out.shape != q.shape or (cu_seqlens_q is None and new_per_seq <= 0) \
+            or (cu_seqlens_q is not None and cu_seqlens_q.numel() != B + 1):
+        raise ValueError("paged_attention_i8: shape mismatch")
+    _check(load().pkv_paged_attention_i8(
+        _arg(q, torch.bfloat16, "q", 3, dev), kc, vc, sc, _arg(block_tables, torch.int32, "block_tables", 2, dev), mb,
+        None if cu_seqlens_q is None else _arg(cu_seqlens_q, torch.int32, "cu_seqlens_q", 1, dev),
+        _arg(context_lens, torch.int32, "context_lens", 1, dev), B, T, Hq, Hkv, D, bs, NB,
+        mb * bs if max_context_len is None else int(max_context_len), float(scale),
+        _arg(out, torch.bfloat16, "out", 3, dev),
+        int(new_per_seq), _arg(workspace, torch.uint8, "workspace", 1, dev), workspace.numel(), int(num_workers),
+        _err(err_word, dev), _stream(stream)), "pkv_paged_attention_i8")
+
+
+def copy_blocks_i8(k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor, pairs: torch.Tensor,
+                   err_word: torch.Tensor | None = None, stream=None) -> None:
+    """copy_blocks for an int8 cache: codes and scales of block dst become those of block src."""
+    dev = _device(k_cache, "k_cache")
+    kc, vc, sc, NB, bs, Hkv, D = _i8_cache(k_cache, v_cache, scales, dev, "copy_blocks_i8")
+    n, two = pairs.shape
+    if two != 2:
+        raise ValueError("copy_blocks_i8: shape mismatch")
+    _check(load().pkv_copy_blocks_i8(kc, vc, sc, _arg(pairs, torch.int32, "pairs", 2, dev), n, NB, bs, Hkv, D,
+                                     _err(err_word, dev), _stream(stream)), "pkv_copy_blocks_i8")
+
+
+def _rope_args(q, k, positions, inv_freq, freq_axis, q_out, dev, what):
+    """The arguments the rotary calls share: rows of q and k, positions and frequencies, sizes, rows of q_out."""
+    (qp, qs), (kp, ks), (op, os_) = _rows(q, "q", dev), _rows(k, "k", dev), _rows(q_out, "q_out", dev)
+    T, Hq, D = q.shape
+    Tk, Hkv, Dk = k.shape
+    pos = positions if positions.dim() == 2 else positions.view(1, -1)
+    axes, Tp = pos.shape
+    half = inv_freq.numel()
+    if Tk != T or Dk != D or q_out.shape != q.shape or Tp != T \
+            or (freq_axis is not None and freq_axis.numel() != half):
+        raise ValueError(f"{what}: shape mismatch")
+    return (qp, qs, kp, ks), (_arg(pos, torch.int32, "positions", 2, dev), axes,
+                              _arg(inv_freq, torch.float32, "inv_freq", 1, dev),
+                              None if freq_axis is None else _arg(freq_axis, torch.int32, "freq_axis", 1, dev)), \
+        (T, Hq, Hkv, D, 2 * half), (op, os_)
+
+
+def rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, q_out: torch.Tensor,
+         k_out: torch.Tensor, freq_axis: torch.Tensor | None = None, interleaved: bool = False,
+         err_word: torch.Tensor | None = None, stream=None) -> None:
+    """Rotary positions for q and k (bf16 [T, H, D], parts of wider rows allowed): positions int32 [T] or
+    [axes, T], inv_freq float32 [rot / 2], freq_axis int32 [rot / 2] (the axis each frequency follows).  q_out /
+    k_out may be q / k."""
+    dev = _device(q, "q")
+    rows, pos, sizes, out = _rope_args(q, k, positions, inv_freq, freq_axis, q_out, dev, "rope")
+    if k_out.shape != k.shape:
+        raise ValueError("rope: shape mismatch")
+    _check(load().pkv_rope(*rows, *pos, *sizes, int(interleaved), *out, *_rows(k_out, "k_out", dev),
+                           _err(err_word, dev), _stream(stream)), "pkv_rope")
+
+
+def rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
+               slot_mapping: torch.Tensor, q_out: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+               freq_axis: torch.Tensor | None = None, interleaved: bool = False,
+               err_word: torch.Tensor | None = None, stream=None) -> None:
+    """rope and kv_store in one launch: q turned into q_out, turned k and v stored at slot_mapping of bf16 caches
+    (-1: not stored)."""
+    dev = _device(q, "q")
+    rows, pos, sizes, out = _rope_args(q, k, positions, inv_freq, freq_axis, q_out, dev, "rope_store")
+    NB, bs, Hkv, D = k_cache.shape
+    if v.shape != k.shape or sizes[2] != Hkv or sizes[3] != D or v_cache.shape != k_cache.shape \
+            or slot_mapping.numel() != sizes[0]:
+        raise ValueError("rope_store: shape mismatch")
+    _check(load().pkv_rope_store(
+        *rows, *_rows(v, "v", dev), *pos, _arg(slot_mapping, torch.int32, "slot_mapping", 1, dev), *sizes,
+        int(interleaved), *out, _arg(k_cache, torch.bfloat16, "k_cache", 4, dev),
+        _arg(v_cache, torch.bfloat16, "v_cache", 4, dev), NB, bs, _err(err_word, dev), _stream(stream)),
+        "pkv_rope_store")

@@ -1,0 +1,482 @@
+"""GPU tests of the int8 cache with a scale per block of 16 tokens and kv head: the quantising store, decode and
+several-token attention over it, its page copies, and a serving run of them together.
+
+Store and copies must match the 64-bit reference bit for bit.  Attention must stay within
+    2^-8 |out| + 2^-10 A,    A = the softmax-weighted mean of |v|,
+of the 64-bit result over the same codes and scales: the bf16 output rounds by at most 2^-8 of itself; each
+weight rounds to f16 by at most 2^-11 of itself, which moves the output by at most 2^-11 A; the fp32 scores,
+exponentials, sums and merges have another 2^-11 A (a score error of 2^-12 at the sizes below: scores stay
+under 2^6, their fp32 sums of at most 128 products err by less than 2^-14 of that).
+"""
+import numpy as np
+import pytest
+import torch
+
+from i8_reference import SB, attend_i8, store_i8
+from paged_kv_cache_62_gb300 import pkv
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(0)
+
+
+def tables(lens, bs, rng, extra=3):
+    nblk = [-(-int(x) // bs) for x in lens]
+    NB = sum(nblk) + extra
+    perm = rng.permutation(NB)
+    bt = np.full((len(lens), max(max(nblk), 1)), -1, np.int32)
+    cur = 0
+    for b, n in enumerate(nblk):
+        bt[b, :n] = perm[cur:cur + n]
+        cur += n
+    return bt, NB
+
+
+def garbage_cache(NB, bs, Hkv, D, seed):
+    """What earlier owners left: any codes, NaN scales."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    kc, vc = (torch.randint(-128, 128, (NB, bs, Hkv, D), generator=g, device="cuda").to(torch.int8) for _ in range(2))
+    return kc, vc, torch.full((NB, bs // SB, Hkv, 2), float("nan"), device="cuda")
+
+
+def synth(lens, Hq, Hkv, D, bs, seed, new=None, spread=1.0):
+    """A cache whose valid blocks hold random codes under random scales, NaN scales elsewhere, and queries."""
+    rng = np.random.default_rng(seed)
+    bt, NB = tables(lens, bs, rng)
+    kc, vc, sc = garbage_cache(NB, bs, Hkv, D, seed)
+    kc.clamp_(-127)
+    vc.clamp_(-127)
+    for b, L in enumerate(lens):
+        for u in range(-(-int(L) // SB)):
+            s = np.exp(rng.uniform(-spread, spread, (Hkv, 2))) * np.array([0.01, 0.015])
+            sc[int(bt[b, u * SB // bs]), (u * SB % bs) // SB] = torch.as_tensor(s, dtype=torch.float32)
+    T = len(lens) if new is None else sum(new)
+    q = torch.randn(T, Hq, D, generator=torch.Generator(device="cuda").manual_seed(seed + 1), device="cuda").bfloat16()
+    return q, kc, vc, sc, bt, torch.from_numpy(bt).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+def check(out, q, kc, vc, sc, bt, lens, new, scale, what):
+    want, mag = attend_i8(q.cpu(), kc.cpu(), vc.cpu(), sc.cpu(), bt, lens, new, scale)
+    got = out.cpu().double()
+    assert torch.isfinite(got).all(), what
+    off = (got - want).abs() - (2.0 ** -8 * want.abs() + 2.0 ** -10 * mag)
+    assert off.max() <= 0, f"{what}: over the bound by {off.max():.3g}"
+
+
+def decode(q, kc, vc, sc, bt_d, lens_d, scale, workers=0, ws=None, err=None, **kw):
+    out = torch.full_like(q, float("nan"))
+    ws = pkv.alloc_workspace(q.shape[0], q.shape[1], kc.shape[2], q.shape[2]) if ws is None else ws
+    pkv.paged_decode_i8(q, kc, vc, sc, bt_d, lens_d, scale, out, ws, num_workers=workers, err_word=err, **kw)
+    return out
+
+
+def attend(q, kc, vc, sc, bt_d, cu, lens_d, scale, n=0, workers=0, ws=None, err=None):
+    out = torch.full_like(q, float("nan"))
+    ws = pkv.alloc_attention_workspace(q.shape[0], q.shape[1], kc.shape[2], q.shape[2]) if ws is None else ws
+    pkv.paged_attention_i8(q, kc, vc, sc, bt_d, cu, lens_d, scale, out, ws, num_workers=workers, err_word=err,
+                           new_per_seq=n)
+    return out
+
+
+# ------------------------------------------------------------------------------------------ the store
+def run_store(lens, new, Hkv, D, bs, seed, magnitude=1.0, uniform=0, stride=False, cache=None, bt=None):
+    rng = np.random.default_rng(seed)
+    if bt is None:
+        bt, NB = tables(lens, bs, rng)
+    if cache is None:
+        cache = garbage_cache(NB, bs, Hkv, D, seed)
+    kc, vc, sc = cache
+    T = sum(new)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    wide = torch.randn(T, 2 * Hkv * D + 64, generator=g, device="cuda") * magnitude
+    wide *= torch.exp(torch.randn(T, 1, generator=g, device="cuda"))
+    wide = wide.bfloat16()
+    k, v = wide[:, 8:8 + Hkv * D].view(T, Hkv, D), wide[:, 64 + Hkv * D:].view(T, Hkv, D)
+    if not stride:
+        k, v = k.contiguous(), v.contiguous()
+    ref = [t.cpu().numpy().copy() for t in (kc, vc, sc)]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    pkv.kv_store_i8(k, v, kc, vc, sc, torch.from_numpy(bt).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                    None if uniform else cu, new_per_seq=uniform, err_word=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    store_i8(k.double().cpu().numpy(), v.double().cpu().numpy(), *ref, bt, lens, new)
+    for got, want, name in zip((kc, vc, sc), ref, ("K codes", "V codes", "scales")):
+        assert np.array_equal(got.cpu().numpy(), want, equal_nan=name == "scales"), name
+    return cache, bt
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hkv", [1, 2, 3, 8, 20])
+@pytest.mark.parametrize("bs", [16, 64, 256])
+def test_store_prompts(D, Hkv, bs):
+    lens = [1, 15, 16, 17, 31, 32, 33, 100, 0, 5]
+    run_store(lens, lens, Hkv, D, bs, seed=D + Hkv + bs, stride=Hkv % 2 == 0)
+
+
+@pytest.mark.parametrize("uniform", [0, 1])
+def test_store_steps_grow_the_scales(uniform):
+    """Forty decode steps on top of prompts: blocks restart at their first position, grow and requantise."""
+    lens, Hkv, D, bs = [3, 16, 30, 47, 64], 4, 128, 32
+    total = [x + 40 for x in lens]
+    bt, NB = tables(total, bs, np.random.default_rng(0))
+    cache, _ = run_store(lens, lens, Hkv, D, bs, 1, cache=garbage_cache(NB, bs, Hkv, D, 2), bt=bt)
+    for step in range(40):
+        lens = [x + 1 for x in lens]
+        run_store(lens, [1] * 5, Hkv, D, bs, 10 + step, magnitude=1.0 + 0.3 * (step % 7), uniform=uniform, cache=cache,
+                  bt=bt)
+
+
+@pytest.mark.parametrize("n", [2, 15, 16, 17, 40])
+def test_store_chunks_of_one_length(n):
+    lens = [n, n + 1, n + 7, n + 15, n + 16, 3 * n + 5]
+    bt, NB = tables(lens, 64, np.random.default_rng(n))
+    cache, _ = run_store([x - n for x in lens], [x - n for x in lens], 2, 64, 64, n,
+                         cache=garbage_cache(NB, 64, 2, 64, n), bt=bt)
+    run_store(lens, [n] * len(lens), 2, 64, 64, n + 1, magnitude=3.0, uniform=n, stride=True, cache=cache, bt=bt)
+
+
+def test_store_many_sequences_of_ragged_lengths():
+    rng = np.random.default_rng(4)
+    lens = rng.integers(0, 70, 1200)
+    lens[::7] = 0
+    run_store(lens.tolist(), lens.tolist(), 2, 64, 16, 5)
+
+
+def store_one_block(x, kept=0, prev=None):
+    """K and V = x [n, 1, 64] at positions kept .. of one block; returns codes and scales of the block."""
+    kc, vc, sc = garbage_cache(1, 16, 1, 64, 0) if prev is None else prev
+    n = x.shape[0]
+    pkv.kv_store_i8(x, x, kc, vc, sc, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                    torch.tensor([kept + n], dtype=torch.int32, device="cuda"), new_per_seq=n)
+    torch.cuda.synchronize()
+    return kc, vc, sc
+
+
+def test_store_ties_zeros_and_extremes():
+    x = torch.zeros(4, 1, 64, device="cuda")
+    x[0, 0, 0] = 127.0                                   # scale exactly 1
+    x[0, 0, 1:9] = torch.tensor([0.5, 1.5, 2.5, -0.5, -1.5, -2.5, 63.5, 62.5])
+    # 0.5 - 2^-9 and 0.5 + 2^-8 are bf16 values; 0.5 + 2^-9 lies halfway between two and becomes 0.5
+    x[1, 0, :5] = torch.tensor([0.498046875, 0.501953125, -0.0, 126.5, 0.50390625])
+    kc, vc, sc = store_one_block(x.bfloat16())
+    assert sc[0, 0, 0].tolist() == [1.0, 1.0]
+    assert kc[0, 0, 0, :9].tolist() == [127, 0, 2, 2, 0, -2, -2, 64, 62]
+    assert kc[0, 1, 0, :5].tolist() == [0, 0, 0, 126, 1]
+    zero = torch.zeros(16, 1, 64, device="cuda").bfloat16()
+    kc, vc, sc = store_one_block(zero)
+    assert torch.all(sc == 0) and torch.all(kc == 0) and torch.all(vc == 0)
+    for size in (3.0e38, 1e-36, 2.0 ** -130):             # large, small, subnormal
+        x = (torch.randn(16, 1, 64, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+             .clamp(-1, 1) * size).bfloat16()
+        kc, vc, sc = store_one_block(x)
+        ref = [np.zeros((1, 16, 1, 64), np.int8), np.zeros((1, 16, 1, 64), np.int8), np.zeros((1, 1, 1, 2), np.float32)]
+        store_i8(x.double().cpu().numpy(), x.double().cpu().numpy(), *ref, np.zeros((1, 1), np.int32), [16], [16])
+        assert np.array_equal(kc.cpu().numpy(), ref[0]) and np.array_equal(sc.cpu().numpy(), ref[2])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_store_marks_a_block_with_a_bad_value_until_it_restarts(bad):
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(5, 1, 64, generator=g, device="cuda").bfloat16()
+    cache = store_one_block(x)
+    before = cache[0][0, :5].clone()
+    y = x[:1].clone()
+    y[0, 0, 7] = bad
+    kc, vc, sc = store_one_block(y, kept=5, prev=cache)
+    assert torch.isnan(sc).all() and torch.all(kc[0, 5] == 0) and torch.equal(kc[0, :5], before)
+    kc, vc, sc = store_one_block(x[:1], kept=6, prev=cache)   # still marked
+    assert torch.isnan(sc).all()
+    kc, vc, sc = store_one_block(x, prev=cache)               # restarted
+    assert torch.isfinite(sc).all() and torch.equal(kc[0, :5], before)
+
+
+def test_store_leaves_what_it_must_not_touch():
+    """Padding sequences, rejected lengths, tables and offsets: flagged, nothing of them written."""
+    Hkv, D, bs, NB = 2, 64, 32, 8
+    kc, vc, sc = garbage_cache(NB, bs, Hkv, D, 3)
+    sc.fill_(0.5)
+    keep = [t.clone() for t in (kc, vc, sc)]
+    x = torch.randn(6, Hkv, D, device="cuda").bfloat16()
+    bt = torch.tensor([[0, 1], [2, NB], [-1, 3], [4, 5], [6, 7], [6, 7]], dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call(lens, cu=None, n=0):
+        err.zero_()
+        pkv.kv_store_i8(x, x, kc, vc, sc, bt, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                        None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda"), new_per_seq=n,
+                        err_word=err)
+        torch.cuda.synchronize()
+        return err.item()
+
+    same = lambda: all(torch.equal(a, b) for a, b in zip((kc, vc, sc), keep))
+    assert call([0] * 6, n=1) == 0 and same()                                   # all padding
+    assert call([0, 40, 0, 0, 0, 0], n=1) == pkv.ERR_BLOCK_RANGE and same()     # id NB
+    assert call([0, 0, 5, 0, 0, 0], n=1) == pkv.ERR_BLOCK_RANGE and same()      # id -1
+    assert call([0, 0, 0, 65, 0, 0], n=1) == pkv.ERR_CONTEXT_RANGE and same()   # beyond its table row
+    assert call([-3, 0, 0, 0, 0, 0], n=1) == pkv.ERR_CONTEXT_RANGE and same()
+    assert call([2, 2, 2, 2, 2, 2], cu=[0, 3, 3, 3, 3, 3, 3]) == pkv.ERR_CONTEXT_RANGE and same()  # 3 rows, length 2
+    assert call([9] * 6, cu=[0, 7, 7, 7, 7, 7, 7]) == pkv.ERR_CONTEXT_RANGE and same()             # past the rows
+    # a good sequence beside bad ones is stored, rows behind it are left
+    assert call([0, 40, 0, 40, 0, 0], n=1) == pkv.ERR_BLOCK_RANGE
+    changed = (kc != keep[0]).any(dim=(2, 3)).nonzero().tolist()
+    assert [5, 7] in changed and all(c == 5 and r <= 7 for c, r in changed)
+
+
+# ------------------------------------------------------------------------------------------ decode
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads", [(8, 2), (16, 4), (16, 8)])
+@pytest.mark.parametrize("bs", [16, 32, 256])
+def test_decode_matrix(D, heads, bs):
+    Hq, Hkv = heads
+    lens = [1, 15, 16, 17, 128, 511, 1024, 40]
+    q, kc, vc, sc, bt, btd, ld = synth(lens, Hq, Hkv, D, bs, seed=D + bs + Hq)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = decode(q, kc, vc, sc, btd, ld, D ** -0.5, err=err)
+    assert err.item() == 0
+    check(out, q, kc, vc, sc, bt, lens, [1] * len(lens), D ** -0.5, f"D{D} {heads} bs{bs}")
+
+
+@pytest.mark.parametrize("G", range(1, 17))
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_every_group_size(G, D):
+    lens = [300, 1, 77, 0, 1500]
+    q, kc, vc, sc, bt, btd, ld = synth(lens, G * 2, 2, D, 16, seed=G * 3 + D)
+    out = decode(q, kc, vc, sc, btd, ld, D ** -0.5)
+    assert torch.all(out[3] == 0)
+    check(out, q, kc, vc, sc, bt, lens, [1] * 5, D ** -0.5, f"G{G} D{D}")
+
+
+@pytest.mark.parametrize("Hkv", [1, 3, 5, 7, 12])
+def test_decode_head_groups_and_repeated_calls(Hkv):
+    lens = [700, 1, 33, 250, 96]
+    q, kc, vc, sc, bt, btd, ld = synth(lens, 2 * Hkv, Hkv, 128, 16, seed=Hkv)
+    ws = pkv.alloc_workspace(len(lens), 2 * Hkv, Hkv, 128)
+    for call in range(3):
+        out = decode(q, kc, vc, sc, btd, ld, 128 ** -0.5, ws=ws)
+        check(out, q, kc, vc, sc, bt, lens, [1] * 5, 128 ** -0.5, f"Hkv{Hkv} call{call}")
+
+
+@pytest.mark.parametrize("workers", [0, 1, 7, 333, 4096])
+def test_decode_splits(workers):
+    lens = [1, 15, 17, 40, 300, 0, 3000, 2, 513]
+    q, kc, vc, sc, bt, btd, ld = synth(lens, 16, 8, 128, 64, seed=workers)
+    out = decode(q, kc, vc, sc, btd, ld, 128 ** -0.5, workers=workers)
+    check(out, q, kc, vc, sc, bt, lens, [1] * len(lens), 128 ** -0.5, f"workers {workers}")
+    if workers:
+        assert torch.equal(out, decode(q, kc, vc, sc, btd, ld, 128 ** -0.5, workers=workers))
+
+
+def test_decode_scales_of_any_size():
+    """V scales from 2^-80 to 2^80 and K scales against them; queries from 2^-60 to 2^60 in size."""
+    lens = [200, 77, 16, 1000]
+    q, kc, vc, sc, bt, btd, ld = synth(lens, 8, 4, 128, 32, seed=9)
+    size = torch.tensor([2.0 ** -60, 2.0 ** 60, 1.0, 2.0 ** 20], device="cuda")
+    q = (q.float() * size.view(-1, 1, 1)).bfloat16()
+    own = torch.zeros(sc.shape[0], dtype=torch.long, device="cuda")
+    for b in range(4):
+        own[torch.from_numpy(bt[b][bt[b] >= 0].astype(np.int64)).cuda()] = b
+    sc[..., 0] /= size[own].view(-1, 1, 1)                    # the scores keep their size
+    e = torch.arange(sc.shape[0], device="cuda") % 4
+    sc[..., 1] *= (2.0 ** (40.0 * (own.float() - 2))).view(-1, 1, 1)  # per sequence
+    sc[..., 1] *= torch.where(e == 0, 1e-4, 1.0).view(-1, 1, 1)       # and within one
+    out = decode(q, kc, vc, sc, btd, ld, 128 ** -0.5)
+    check(out, q, kc, vc, sc, bt, lens, [1] * 4, 128 ** -0.5, "scales of any size")
+
+
+def test_decode_zero_scales_and_marked_blocks():
+    lens = [100, 100, 100]
+    q, kc, vc, sc, bt, btd, ld = synth(lens, 4, 2, 64, 16, seed=10)
+    sc[int(bt[1, 2])] = 0.0
+    out = decode(q, kc, vc, sc, btd, ld, 0.125)
+    check(out, q, kc, vc, sc, bt, lens, [1] * 3, 0.125, "a block of zeros")
+    sc[int(bt[1, 2])] = float("nan")                          # a block the store marked
+    out = decode(q, kc, vc, sc, btd, ld, 0.125)
+    assert torch.isnan(out[1]).all()
+    good = torch.tensor([0, 2], device="cuda")
+    assert torch.isfinite(out[good]).all()
+
+
+def test_decode_flags_bad_blocks_and_lengths():
+    lens = [40, 40]
+    q, kc, vc, sc, bt, btd, ld = synth(lens, 4, 2, 64, 16, seed=11)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    btd[0, 1] = kc.shape[0]
+    decode(q, kc, vc, sc, btd, ld, 0.125, err=err)
+    assert err.item() == pkv.ERR_BLOCK_RANGE
+    btd[0, 1] = int(bt[0, 1])
+    err.zero_()
+    ld[1] = 49
+    out = decode(q, kc, vc, sc, btd, ld, 0.125, err=err)
+    assert err.item() == pkv.ERR_CONTEXT_RANGE and torch.all(out[1] == 0)
+
+
+# ------------------------------------------------------------------------------------------ several tokens
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 8, 16, 40])
+@pytest.mark.parametrize("heads,D,bs", [((16, 8), 128, 256), ((14, 2), 64, 16), ((16, 1), 128, 128), ((6, 2), 64, 32)])
+def test_attention_of_one_length(n, heads, D, bs):
+    Hq, Hkv = heads
+    lens = [n, n + 1, 40 + n, 300, 513]
+    q, kc, vc, sc, bt, btd, ld = synth(lens, Hq, Hkv, D, bs, seed=n + Hq + D, new=[n] * 5)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = attend(q, kc, vc, sc, btd, None, ld, D ** -0.5, n=n, err=err)
+    assert err.item() == 0
+    check(out, q, kc, vc, sc, bt, lens, [n] * 5, D ** -0.5, f"n{n} {heads} D{D} bs{bs}")
+
+
+@pytest.mark.parametrize("workers", [0, 5, 1000])
+@pytest.mark.parametrize("heads,D,bs", [((16, 8), 128, 256), ((14, 2), 64, 16), ((8, 8), 128, 64), ((8, 2), 64, 128),
+                                        ((15, 5), 128, 32)])
+def test_attention_ragged(workers, heads, D, bs):
+    Hq, Hkv = heads
+    lens = [700, 1, 64, 0, 333, 130, 2000]
+    new = [130, 1, 64, 0, 7, 1, 70]
+    q, kc, vc, sc, bt, btd, ld = synth(lens, Hq, Hkv, D, bs, seed=workers + Hq + bs, new=new)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = pkv.alloc_attention_workspace(q.shape[0], Hq, Hkv, D)
+    for call in range(2):
+        out = attend(q, kc, vc, sc, btd, cu, ld, D ** -0.5, workers=workers, err=err, ws=ws)
+        assert err.item() == 0
+        check(out, q, kc, vc, sc, bt, lens, new, D ** -0.5, f"{heads} D{D} bs{bs} call{call}")
+
+
+@pytest.mark.parametrize("heads,D,bs,n", [((16, 8), 128, 256, 4), ((16, 8), 128, 256, 64), ((6, 2), 64, 16, 40)])
+def test_marked_blocks_reach_only_queries_that_see_them(heads, D, bs, n):
+    """A NaN scale in the block of the last tokens: queries before that block are as without it."""
+    Hq, Hkv = heads
+    L = 208 + n
+    lens, new = [L, L], [n, n]
+    q, kc, vc, sc, bt, btd, ld = synth(lens, Hq, Hkv, D, bs, seed=5, new=new)
+    last = (L - 1) // SB * SB
+    sc[int(bt[0, last // bs]), (last % bs) // SB, :, :] = float("nan")
+    out = attend(q, kc, vc, sc, btd, None, ld, D ** -0.5, n=n)
+    blind = max(0, last - (L - n))                             # queries of sequence 0 that do not see it
+    assert torch.isnan(out[blind:n]).all()
+    rows = list(range(blind)) + list(range(n, 2 * n))
+    clean = sc.clone()
+    clean[torch.isnan(sc)] = 0.01
+    want, mag = attend_i8(q.cpu(), kc.cpu(), vc.cpu(), clean.cpu(), bt, lens, new, D ** -0.5)
+    off = (out.cpu().double() - want).abs() - (2.0 ** -8 * want.abs() + 2.0 ** -10 * mag)
+    assert off[rows].max() <= 0
+
+
+# ------------------------------------------------------------------------------------------ copies
+@pytest.mark.parametrize("NB,bs,Hkv,D,n", [(64, 16, 8, 128, 20), (24, 256, 8, 128, 9), (40, 16, 1, 64, 13),
+                                           (10, 32, 3, 64, 1), (300, 16, 2, 64, 140), (6, 1024, 5, 128, 3)])
+def test_copy_blocks(NB, bs, Hkv, D, n):
+    rng = np.random.default_rng(n)
+    kc, vc, sc = garbage_cache(NB, bs, Hkv, D, n)
+    sc.copy_(torch.randn(sc.shape, device="cuda"))
+    ids = rng.permutation(NB)[:2 * n]
+    pairs = np.stack([ids[:n], ids[n:]], 1).astype(np.int32)
+    if n > 2:
+        pairs[0, 1] = pairs[0, 0]
+        pairs[1] = [NB, 0]
+        pairs[2] = [0, -1]
+    ref = [t.clone() for t in (kc, vc, sc)]
+    for s, d in pairs:
+        if 0 <= s < NB and 0 <= d < NB:
+            for t in ref:
+                t[int(d)] = t[int(s)]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkv.copy_blocks_i8(kc, vc, sc, torch.from_numpy(pairs).cuda(), err)
+    torch.cuda.synchronize()
+    assert err.item() == (pkv.ERR_BLOCK_RANGE if n > 2 else 0)
+    assert all(torch.equal(a, b) for a, b in zip((kc, vc, sc), ref))
+    pkv.copy_blocks_i8(kc, vc, sc, torch.zeros(0, 2, dtype=torch.int32, device="cuda"))
+    assert torch.equal(kc, ref[0])
+
+
+# ------------------------------------------------------------------------------------------ together
+def test_prompt_chunk_fork_and_steps():
+    """A serving run: two prompts stored and attended in chunks, a fork with copy-on-write, decode steps of the
+    three sequences, all against the reference run on the same operations."""
+    NB, bs, Hq, Hkv, D = 40, 32, 8, 2, 128
+    a = pkv.BlockAllocator(NB, bs)
+    kc, vc, sc = garbage_cache(NB, bs, Hkv, D, 1)
+    ref = [t.cpu().numpy().copy() for t in (kc, vc, sc)]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a.add(0, 90)
+    a.add(1, 41)
+    full, _ = a.tables([0, 1], 8)
+    for lens, new in (([50, 41], [50, 41]), ([90, 41], [40, 0])):     # sequence 0 in two chunks
+        T = sum(new)
+        k, v, q = rand(T, Hkv, D), rand(T, Hkv, D), rand(T, Hq, D)
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+        ld = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        pkv.kv_store_i8(k, v, kc, vc, sc, full.cuda(), ld, cu, err_word=err)
+        out = attend(q, kc, vc, sc, full.cuda(), cu, ld, D ** -0.5, err=err)
+        store_i8(k.double().cpu().numpy(), v.double().cpu().numpy(), *ref, full.numpy(), lens, new)
+        check(out, q, torch.from_numpy(ref[0]), torch.from_numpy(ref[1]), torch.from_numpy(ref[2]), full.numpy(), lens,
+              new, D ** -0.5, "chunk")
+    a.fork(0, 2)
+    ws = pkv.alloc_workspace(3, Hq, Hkv, D)
+    for step in range(10):
+        cow = [c for c in (a.append(s) for s in (0, 1, 2)) if c != (-1, -1)]
+        if cow:
+            pkv.copy_blocks_i8(kc, vc, sc, torch.tensor(cow, dtype=torch.int32, device="cuda"), err)
+            for s, d in cow:
+                for t in ref:
+                    t[d] = t[s]
+        assert (step == 0) == bool(cow)
+        bt, lens = a.tables([0, 1, 2], 8)
+        k, v, q = rand(3, Hkv, D), rand(3, Hkv, D), rand(3, Hq, D)
+        pkv.kv_store_i8(k, v, kc, vc, sc, bt.cuda(), lens.cuda(), new_per_seq=1, err_word=err)
+        out = decode(q, kc, vc, sc, bt.cuda(), lens.cuda(), D ** -0.5, ws=ws, err=err)
+        store_i8(k.double().cpu().numpy(), v.double().cpu().numpy(), *ref, bt.numpy(), lens.tolist(), [1] * 3)
+        check(out, q, torch.from_numpy(ref[0]), torch.from_numpy(ref[1]), torch.from_numpy(ref[2]), bt.numpy(),
+              lens.tolist(), [1] * 3, D ** -0.5, f"step {step}")
+    assert err.item() == 0
+    for got, want in zip((kc, vc, sc), ref):
+        assert np.array_equal(got.cpu().numpy(), want, equal_nan=True)
+
+
+def test_captured_step_replays():
+    """Store and decode captured once on a side stream, replayed with other contents of the same buffers."""
+    Hq, Hkv, D, bs = 16, 8, 128, 64
+    lens0 = [100, 31, 480, 64]
+    q, kc, vc, sc, bt, btd, ld = synth([x + 8 for x in lens0], Hq, Hkv, D, bs, seed=1)
+    ref = None
+    k, v = (torch.zeros(4, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    out = torch.empty_like(q)
+    ws = pkv.alloc_workspace(4, Hq, Hkv, D)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ld.copy_(torch.tensor(lens0, dtype=torch.int32))
+    side = torch.cuda.Stream()
+
+    def step():
+        pkv.kv_store_i8(k, v, kc, vc, sc, btd, ld, new_per_seq=1, err_word=err)
+        pkv.paged_decode_i8(q, kc, vc, sc, btd, ld, D ** -0.5, out, ws, max_context_len=512, err_word=err)
+
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()                                                # warm-up outside the capture
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    torch.cuda.synchronize()
+    ref = [t.cpu().numpy().copy() for t in (kc, vc, sc)]
+    g = torch.Generator(device="cuda").manual_seed(6)
+    for i in range(1, 9):
+        lens = [x + i for x in lens0]
+        ld.copy_(torch.tensor(lens, dtype=torch.int32))
+        for t in (k, v, q):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert err.item() == 0
+        store_i8(k.double().cpu().numpy(), v.double().cpu().numpy(), *ref, bt, lens, [1] * 4)
+        check(out, q, torch.from_numpy(ref[0]), torch.from_numpy(ref[1]), torch.from_numpy(ref[2]), bt, lens, [1] * 4,
+              D ** -0.5, f"replay {i}")

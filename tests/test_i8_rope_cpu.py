@@ -1,0 +1,122 @@
+"""Refusals of the int8-cache and rotary entry points, on the host before any CUDA call (FAKE is never
+dereferenced), and of their bindings."""
+import pytest
+import torch
+
+from paged_kv_cache_62_gb300 import build as pkv_build
+from paged_kv_cache_62_gb300 import pkv
+
+NULL, FAKE = None, 0x10000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    pkv_build.build()
+    return pkv.load()
+
+
+def swap(names, base, **kw):
+    assert set(kw) <= set(names)
+    return [kw.get(n, b) for n, b in zip(names, base)]
+
+
+STORE = "k v ks vs bt mb cu lens B T n kc vc sc NB bs Hkv D err st".split()
+STORE_OK = [FAKE, FAKE, 1024, 1024, FAKE, 4, FAKE, FAKE, 2, 5, 0, FAKE, FAKE, FAKE, 10, 16, 8, 128, NULL, NULL]
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(k=NULL), pkv.EINVAL), (dict(v=FAKE + 8), pkv.EINVAL), (dict(cu=NULL), pkv.EINVAL),
+    (dict(sc=NULL), pkv.EINVAL), (dict(sc=FAKE + 4), pkv.EINVAL), (dict(kc=FAKE + 8), pkv.EINVAL),
+    (dict(ks=1016), pkv.EINVAL), (dict(vs=1028), pkv.EINVAL), (dict(n=2), pkv.EINVAL), (dict(T=-1), pkv.EINVAL),
+    (dict(B=0), pkv.EINVAL), (dict(D=96), pkv.EUNSUPPORTED), (dict(bs=8), pkv.EUNSUPPORTED),
+    (dict(bs=48), pkv.EUNSUPPORTED), (dict(bs=2048), pkv.EUNSUPPORTED), (dict(NB=1 << 28), pkv.EBOUNDS),
+    (dict(T=0, k=NULL, cu=NULL), pkv.OK),
+])
+def test_store_i8(lib, kw, status):
+    assert lib.pkv_kv_store_i8(*swap(STORE, STORE_OK, **kw)) == status
+
+
+DEC = "q kc vc sc bt mb lens B Hq Hkv D bs NB mx scale out ws wsb workers err st".split()
+DEC_OK = [FAKE, FAKE, FAKE, FAKE, FAKE, 4, FAKE, 2, 16, 8, 128, 16, 10, 64, 0.1, FAKE, FAKE, 1 << 30, 0, NULL, NULL]
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(sc=NULL), pkv.EINVAL), (dict(sc=FAKE + 4), pkv.EINVAL), (dict(q=FAKE + 2), pkv.EINVAL),
+    (dict(D=96), pkv.EUNSUPPORTED), (dict(Hq=136), pkv.EUNSUPPORTED), (dict(bs=8), pkv.EUNSUPPORTED),
+    (dict(Hq=12), pkv.EINVAL), (dict(scale=float("inf")), pkv.EINVAL), (dict(wsb=64), pkv.EWORKSPACE),
+    (dict(ws=NULL), pkv.EWORKSPACE), (dict(workers=pkv.MAX_WORKERS + 1), pkv.EBOUNDS),
+    (dict(B=pkv.MAX_SEQS + 1), pkv.EBOUNDS), (dict(B=0, q=NULL), pkv.OK),
+])
+def test_decode_i8(lib, kw, status):
+    assert lib.pkv_paged_decode_i8(*swap(DEC, DEC_OK, **kw)) == status
+
+
+ATT = "q kc vc sc bt mb cu lens B T Hq Hkv D bs NB mx scale out n ws wsb workers err st".split()
+ATT_OK = [FAKE, FAKE, FAKE, FAKE, FAKE, 4, FAKE, FAKE, 2, 5, 16, 8, 128, 16, 10, 64, 0.1, FAKE, 0, FAKE, 1 << 30, 0,
+          NULL, NULL]
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(cu=NULL), pkv.EINVAL), (dict(n=3), pkv.EINVAL), (dict(lens=NULL), pkv.EINVAL), (dict(B=0), pkv.EINVAL),
+    (dict(T=pkv.MAX_SEQS + 1), pkv.EBOUNDS), (dict(wsb=64), pkv.EWORKSPACE), (dict(Hq=12), pkv.EINVAL),
+    (dict(T=0, q=NULL), pkv.OK),
+])
+def test_attention_i8(lib, kw, status):
+    assert lib.pkv_paged_attention_i8(*swap(ATT, ATT_OK, **kw)) == status
+
+
+COPY = "kc vc sc pairs n NB bs Hkv D err st".split()
+COPY_OK = [FAKE, FAKE, FAKE, FAKE, 3, 10, 16, 8, 128, NULL, NULL]
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(sc=NULL), pkv.EINVAL), (dict(pairs=NULL), pkv.EINVAL), (dict(n=-1), pkv.EINVAL),
+    (dict(bs=24), pkv.EUNSUPPORTED), (dict(vc=FAKE + 8), pkv.EINVAL), (dict(NB=1 << 30), pkv.EBOUNDS),
+    (dict(n=0, kc=NULL), pkv.OK),
+])
+def test_copy_i8(lib, kw, status):
+    assert lib.pkv_copy_blocks_i8(*swap(COPY, COPY_OK, **kw)) == status
+
+
+ROPE = "q qs k ks pos axes inv ax T Hq Hkv D rot inter qo qos ko kos err st".split()
+ROPE_OK = [FAKE, 2048, FAKE, 1024, FAKE, 3, FAKE, NULL, 5, 16, 8, 128, 128, 0, FAKE, 2048, FAKE, 1024, NULL, NULL]
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=NULL), pkv.EINVAL), (dict(ko=NULL), pkv.EINVAL), (dict(pos=NULL), pkv.EINVAL), (dict(inv=NULL), pkv.EINVAL),
+    (dict(qs=2040), pkv.EINVAL), (dict(kos=1020), pkv.EINVAL), (dict(ks=1026), pkv.EINVAL), (dict(axes=0), pkv.EINVAL),
+    (dict(rot=144), pkv.EINVAL), (dict(rot=40), pkv.EUNSUPPORTED), (dict(D=136, qs=4096, qos=4096), pkv.EUNSUPPORTED),
+    (dict(D=512, qs=1 << 14, qos=1 << 14, ks=1 << 14), pkv.EUNSUPPORTED), (dict(qo=FAKE + 8), pkv.EINVAL),
+    (dict(T=-1), pkv.EINVAL), (dict(T=0, q=NULL), pkv.OK),
+])
+def test_rope(lib, kw, status):
+    assert lib.pkv_rope(*swap(ROPE, ROPE_OK, **kw)) == status
+
+
+RS = "q qs k ks v vs pos axes inv ax slots T Hq Hkv D rot inter qo qos kc vc NB bs err st".split()
+RS_OK = [FAKE, 2048, FAKE, 1024, FAKE, 1024, FAKE, 1, FAKE, NULL, FAKE, 5, 16, 8, 128, 128, 0, FAKE, 2048, FAKE, FAKE,
+         10, 16, NULL, NULL]
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(v=NULL), pkv.EINVAL), (dict(vs=1000), pkv.EINVAL), (dict(slots=NULL), pkv.EINVAL), (dict(kc=NULL), pkv.EINVAL),
+    (dict(vc=FAKE + 8), pkv.EINVAL), (dict(NB=0), pkv.EINVAL), (dict(T=0, v=NULL), pkv.OK),
+])
+def test_rope_store(lib, kw, status):
+    assert lib.pkv_rope_store(*swap(RS, RS_OK, **kw)) == status
+
+
+def test_bindings_refuse_cpu_tensors_and_bad_shapes(lib):
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt)
+    kc, sc, i32 = z(4, 16, 2, 64, dt=torch.int8), z(4, 1, 2, 2, dt=torch.float32), torch.int32
+    with pytest.raises(ValueError):
+        pkv.kv_store_i8(z(2, 2, 64), z(2, 2, 64), kc, kc, sc, z(2, 3, dt=i32), z(2, dt=i32), new_per_seq=1)
+    with pytest.raises(ValueError):
+        pkv.paged_decode_i8(z(2, 4, 64), kc, kc, sc, z(2, 3, dt=i32), z(2, dt=i32), 0.1, z(2, 4, 64),
+                            z(64, dt=torch.uint8))
+    with pytest.raises(ValueError):
+        pkv.copy_blocks_i8(kc, kc, sc, z(1, 2, dt=i32))
+    with pytest.raises(ValueError):
+        pkv.rope(z(2, 4, 64), z(2, 2, 64), z(2, dt=i32), z(32, dt=torch.float32), z(2, 4, 64), z(2, 2, 64))
+    with pytest.raises(ValueError):
+        pkv.alloc_i8_cache(4, 8, 2, 64)
