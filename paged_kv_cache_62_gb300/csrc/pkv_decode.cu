@@ -31,7 +31,7 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
                               pkv_stream_t stream, const uint16_t *k_new = nullptr, const uint16_t *v_new = nullptr,
                               int32_t *slot_out = nullptr, const float *scales = nullptr)
 {
-    const bool fp8 = ct != kBf16;  // one byte per cached element
+    const bool fp8 = ct != kBf16, i8 = ct == kI8;  // fp8: one byte per cached element
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
         head_dim <= 0 || block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0 ||
         num_workers < 0 || !std::isfinite(scale))
@@ -57,7 +57,8 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
     if ((k_new || v_new) && (qs || ct == kI8 || qn != 1 || row_seq || !k_new || !v_new || !aligned16(k_new) ||
                              !aligned16(v_new)))
         return PKV_EINVAL;  // the fused store goes with a decode
-    const WsLayout ws = ws_layout(num_seqs, G, num_kv_heads, head_dim, qs);
+    // (query-split entries of int8 calls leave pieces of 16-row blocks whatever their group)
+    const WsLayout ws = ws_layout(num_seqs, i8 && qs ? 16 : G, num_kv_heads, head_dim, qs);
     if (!workspace || workspace_bytes < ws.total || !aligned16(workspace)) return PKV_EWORKSPACE;
 
     DeviceInfo dev;
@@ -84,7 +85,7 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
     p.max_blocks = max_blocks_per_seq;
     p.len_limit = int32_t(len_limit);
     // query-split entries of 128 rows run on the tensor-memory CTAs where they can
-    const bool tc5 = qs && !fp8 && tc5_eligible(head_dim, G, gq, block_size, num_seqs, dev.max_smem_optin);
+    const bool tc5 = qs && (i8 || tc5_eligible(head_dim, G, gq, block_size, num_seqs, dev.max_smem_optin));
     p.hg = qs ? 1 : head_group(num_kv_heads, G);
     p.nhg = num_kv_heads / p.hg;
     p.sub = qs ? team_warps(G) : warp_slices(G, p.hg);
@@ -92,7 +93,7 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
     p.boxtok = std::min(p.toks, block_size);
     p.nbox = p.toks / p.boxtok;
     p.lg_nbox = ilog2(p.nbox);
-    p.cons = tc5 ? kTc5Consumers : p.hg * p.sub;
+    p.cons = tc5 ? tc5_consumers(ct) : p.hg * p.sub;
     p.nst = 2;
     p.num_workers = 0;
     p.per_segment = 0;
@@ -137,7 +138,7 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
     a.stream = reinterpret_cast<cudaStream_t>(stream);
 
     LaunchFn fn = ct == kE4m3 ? pick_decode_fp8(head_dim, G)
-                  : ct == kI8 ? (qs ? pick_decode_i8_qs(head_dim, G)
+                  : ct == kI8 ? (qs ? pick_decode_i8_tc5(head_dim)
                                     : G > 8 ? pick_decode_i8_wide(head_dim, G) : pick_decode_i8(head_dim, G))
                   : tc5  ? pick_decode_tc5(head_dim)
                   : qs   ? pick_decode_qs(head_dim, G)
@@ -321,7 +322,8 @@ extern "C" size_t pkv_paged_attention_workspace_size(int32_t num_rows, int32_t n
     // chunk entry per row (qg * G virtual heads a warp, on a regular or a query-split CTA); then the
     // three row arrays
     const int32_t gq = num_q_heads / num_kv_heads, qg = qs_queries(num_q_heads, num_kv_heads);
-    size_t dec = std::max(base, ws_layout(num_rows, gq * qg, num_kv_heads, head_dim, true).total);
+    // (int8 calls: 16-row blocks whatever the group)
+    size_t dec = std::max(base, ws_layout(num_rows, gq <= 16 ? 16 : gq * qg, num_kv_heads, head_dim, true).total);
     for (int32_t qn = 2; qn <= qg; ++qn)
         dec = std::max(dec, ws_layout(num_rows, gq * qn, num_kv_heads, head_dim).total);
     return align256(dec) + 3 * rows_bytes(num_rows);
@@ -358,7 +360,9 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     // most two regular chunks): chunks of qg on regular CTAs, else chunks of 8 * qg on query-split ones.
     // The row arrays sit after the decode workspace.
     const bool qs = int64_t(num_rows) > 2 * int64_t(qg) * num_seqs;
-    const int32_t chunk = qs ? entry_queries(num_q_heads, num_kv_heads) : qg;
+    // (query-split int8 entries fill the tensor-memory tile: as many whole queries as 128 rows hold)
+    const int32_t chunk = !qs ? qg : ct == kI8 ? 128 / (num_q_heads / num_kv_heads)
+                                              : entry_queries(num_q_heads, num_kv_heads);
     uint8_t *wsb = static_cast<uint8_t *>(workspace);
     const size_t dec_bytes = need - 3 * rows_bytes(num_rows);
     int32_t *row_seq = reinterpret_cast<int32_t *>(wsb + dec_bytes);

@@ -1,6 +1,5 @@
 // Instantiations of the decode kernel for int8 caches with 9 to 16 virtual heads (both 8-row halves of the MMA
-// tile) and of its query-split variant, in a translation unit of their own so that they compile in parallel
-// with the other kernel families.
+// tile), in a translation unit of their own so that they compile in parallel with the other kernel families.
 #include "pkv_decode_kernel.cuh"
 #include "pkv_i8_tile.cuh"
 
@@ -22,29 +21,10 @@ static LaunchFn pick_wide(int G)
     }
 }
 
-template <int D>
-static LaunchFn pick_qs(int G)
-{
-    switch (G) {
-    case 12: return launch_decode<D, 12, kI8, true>;
-    case 14: return launch_decode<D, 14, kI8, true>;
-    case 15: return launch_decode<D, 15, kI8, true>;
-    case 16: return launch_decode<D, 16, kI8, true>;
-    default: return nullptr;
-    }
-}
-
 LaunchFn pick_decode_i8_wide(int D, int G)
 {
     if (D == 64) return pick_wide<64>(G);
     if (D == 128) return pick_wide<128>(G);
-    return nullptr;
-}
-
-LaunchFn pick_decode_i8_qs(int D, int G)
-{
-    if (D == 64) return pick_qs<64>(G);
-    if (D == 128) return pick_qs<128>(G);
     return nullptr;
 }
 

@@ -115,6 +115,14 @@ constexpr uint32_t kTc5SlabBytes = 128u * 128u;  // one 64-dim slab of 128 rows 
 // tiles through a ring of kTc5VSlots (free again once their output product is done).
 constexpr int kTc5VSlots = 3;
 static_assert(kTc5Keys * 128 == int(kTc5SlabBytes), "a stage's K or V slab holds one tile of 128-byte rows");
+// int8 caches: more warps turn each tile's codes into f16 operands (see tc5_convert_warps), one buffer
+// for K and one for V; the ring's stages hold the codes of a K and a V tile.
+constexpr int kTc5ConvertWarps = 2;
+// Head room of their f16 weights (see kI8Head in pkv_i8_tile.cuh: largest 2^14, a row's max at 2^6 or more).
+constexpr float kTc5Head = 6.0f;
+constexpr int kTc5KConv = 1, kTc5VConv = 1;
+static_assert(kTc5KConv + kTc5VConv <= kTc5VSlots, "their barriers take the places of the V slots'");
+__host__ __device__ constexpr int tc5_consumers(int ct) { return kTc5Consumers + (ct == kI8 ? kTc5ConvertWarps : 0); }
 
 // Query-split CTAs (qs; long runs of new tokens, see paged_decode_kernel)
 // take 32-token tiles too: one kv head's stage is small, and every warp
@@ -239,7 +247,7 @@ __host__ __device__ inline CtaLayout cta_layout(int D, int G, int es, int hg, in
     const int toks = warp_tokens(G, es == 1, qs, tc5) * (qs ? 1 : sub);
     l.kv_bytes = uint32_t(toks * hg * D * es);
     // stages start on the 1024-byte swizzle period; tc5: a stage is a K slot, the V slots follow the ring
-    l.stage_bytes = align_up((tc5 ? 1 : 2) * l.kv_bytes, 1024);
+    l.stage_bytes = align_up((tc5 && !i8 ? 1 : 2) * l.kv_bytes, 1024);
     l.q_bytes = tc5 ? 0u : align_up(uint32_t(hg * (qs ? sub : 1) * G * D * 2), 128);  // tc5: Q in tensor memory
     // states of the non-leading warps of every head (the leader keeps its own in registers); tc5: the
     // values each row's two key halves exchange ([2 tile parities][2 halves][128 rows] floats)
@@ -247,7 +255,10 @@ __host__ __device__ inline CtaLayout cta_layout(int D, int G, int es, int hg, in
                        : (sub > 1 && !qs ? align_up(uint32_t(hg * (sub - 1) * comb_stride(D, G) * 4), 128) : 0u);
     uint32_t o = uint32_t(nst) * l.stage_bytes;
     l.off_v = o;
-    if (tc5) o += uint32_t(kTc5VSlots) * align_up(l.kv_bytes, 1024);
+    if (tc5 && i8)
+        o += uint32_t(kTc5KConv + kTc5VConv) * 2u * l.kv_bytes;  // f16 operands
+    else if (tc5)
+        o += uint32_t(kTc5VSlots) * align_up(l.kv_bytes, 1024);
     l.off_q = o;
     o += uint32_t(qslots) * l.q_bytes;
     l.off_comb = o;
@@ -255,13 +266,14 @@ __host__ __device__ inline CtaLayout cta_layout(int D, int G, int es, int hg, in
     l.off_meta = o;
     o += uint32_t(nst) * uint32_t(sizeof(UnitMeta));
     l.off_sc = o;  // int8 caches: a stage's scales, [scale block of the unit][kv head of the group]
-    if (i8) o += uint32_t(nst) * scale_bytes(toks, hg);
+    if (i8) o += uint32_t(nst) * scale_bytes(toks, hg) * (tc5 ? 3 : 1);  // tc5: and what the softmax makes of them
     l.off_bar = o;
     // full / empty per stage, q full / empty x2, combine full / free; tc5: scores full x2, scores read x2,
     // weights full x2, output product done x2, drain, a row's two halves met (one per lane quarter) x4,
     // all softmax warps met, a Q tile written, full / empty per V slot (the stages' pair then covers the
-    // K slots), and per K slot its meta written
-    o += uint32_t(2 * nst + 6 + (tc5 ? 15 + 2 * kTc5VSlots + nst : 0)) * 8;
+    // K slots), and per K slot its meta written; int8 caches: K and V operands written / read in place of
+    // the V slots' pair, and per stage its scales prepared
+    o += uint32_t(2 * nst + 6 + (tc5 ? 15 + 2 * kTc5VSlots + (i8 ? 2 : 1) * nst : 0)) * 8;
     l.off_bound = align_up(o, 16);
     o = l.off_bound + (kMaxSlots + 1) * 8;
     l.off_wts = o;
@@ -765,6 +777,17 @@ __device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const L
 template <int D>
 __device__ __forceinline__ float q_row_scale(const uint16_t *qr, bool live, int r4, float &mul);
 
+// The power of two 2^k (mul) that brings a row whose largest |q| has these bf16 bits to [2^14, 2^15), so that
+// every element of at least 2^-28 of it is a normal f16; returns 2^-k.  A row of zeros, or one holding an
+// infinity or NaN, is left as it is.
+__device__ __forceinline__ float q_pow2(uint32_t max_bits, float &mul)
+{
+    const int e = int(max_bits >> 7);  // biased exponent
+    const int k = max_bits == 0u || e == 255 ? 0 : 141 - max(e, 15);
+    mul = __uint_as_float(uint32_t(127 + k) << 23);
+    return __uint_as_float(uint32_t(127 - k) << 23);
+}
+
 // ------------------------------------------------------------------ load balance
 __device__ __forceinline__ unsigned smid()
 {
@@ -1149,6 +1172,11 @@ struct Tc5Smem {
     // full / empty: a K slot (and its unit's meta); vfull / vempty: a V slot
     uint64_t *full, *empty, *vfull, *vempty, *qready, *sfull, *sfree, *pfull, *odone, *drain, *pair, *team;
     uint64_t *mready;  // [nst] a K slot's meta written (its copy may still be on the way)
+    // int8 caches: K / V operands written (by the converting warps) and read (by the tensor core), a stage's
+    // scales prepared; the stages' scales, and what the softmax takes of them
+    uint64_t *kready, *kfree, *vready, *vfree, *dready;
+    const float2 *scales;
+    float4 *prep;
     uint8_t *vbase;                  // V slot 0
     uint32_t stage_addr, v_addr;     // shared addresses of K slot 0 and V slot 0
 };
@@ -1348,11 +1376,23 @@ __device__ void tc5_merge(const DecodeParams &p, const long long *bound, int sf,
 
 static_assert(team_warps(16) * 16 == 128, "a tensor-memory piece tile is 8 slots of 16 rows");
 
+// int8 caches: the warp that issues the products and the warps that turn codes into f16 operands (defined in
+// pkv_i8_tc5.cuh, which the translation unit of these kernels includes).
+template <int D>
+__device__ void tc5_mma_warp_i8(const DecodeParams &p, const Tc5Smem &m, uint32_t tmem);
+template <int D>
+__device__ void tc5_convert_warps(const DecodeParams &p, const CtaLayout &lay, const Tc5Smem &m, uint8_t *stage0,
+                                  int t);
+
 // The softmax warps: thread t of the 256 takes row r = 32 (w % 4) + lane (TMEM lane r; w = t / 32) and
 // keys 64 h .. 64 h + 63 of every tile, h = w / 4.  The two threads of a row (warps w and w + 4) hold the
 // same running max: they exchange their tile max each tile; each keeps the sum of its own keys' weights.
 // When a segment starts they write its Q tile (dims 64 h .. 64 h + 63 of row r) into tensor memory.
-template <int D, int G>
+// int8 caches: the scores are of code rows, so a group of 16 keys (a scale block) has a factor kc = s_k times
+// the row's; the weights take the V scale along, P = 2^(kc s + lv - m) with lv = log2 s_v and m the running
+// max of kc s + lv (less kTc5Head), and the row's sum divides it out again group by group: both products then
+// see plain codes, at no cost per key.
+template <int D, int G, int CT>
 __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, const Tc5Smem &m, uint32_t tmem,
                                   float *xch, const long long *bound, const int32_t *scan, int *sh,
                                   const float *wts, int nslots, uint32_t gen, int wp, bool adaptive)
@@ -1369,6 +1409,7 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
     int s = 0;
     uint32_t ph = 0, j = 0, segs = 0;
     float mrun = -INFINITY, lrun = 0.f;
+    float crow = c, cnext = c;  // int8 caches: the row's score factor, and that of the Q tile written last
     bool row_ok = false;
     int shift = 0, u_first = 0;
     uint32_t meets = 0;  // exchanges with the row's other half so far (the same in both warps)
@@ -1398,6 +1439,8 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
     // A segment's Q tile into tensor memory (tile segs % 2: the tile before it was last read by the
     // segment before the previous one's scores, all of which were read back): this thread's 64 dims of
     // its row, zeros for rows that are not queries of the entry.
+    // int8 caches: as f16, times the power of two that brings the row's largest |q| to [2^14, 2^15) (found by
+    // its two threads together); false if a wait gave up.
     auto write_q = [&](const UnitMeta &sg) {
         uint32_t w[32];
         if (qi < sg.cnt) {
@@ -1415,6 +1458,21 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
 #pragma unroll
             for (int k = 0; k < DH / 2; ++k) w[k] = 0u;
         }
+        if constexpr (CT == kI8) {
+            uint32_t mx = 0u;
+#pragma unroll
+            for (int k = 0; k < DH / 2; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+            float other;
+            if (!exchange(__uint_as_float(mx), other)) return false;
+            float mul;
+            // the row's factor stays positive, whatever the scale's sign (the max of a masked tile depends on it)
+            cnext = fabsf(c) * q_pow2(max(mx, __float_as_uint(other)), mul);
+            if (c <= 0.f) mul = c < 0.f ? -mul : 0.f;
+            if (c == 0.f) cnext = 1.f;
+#pragma unroll
+            for (int k = 0; k < DH / 2; ++k)
+                w[k] = f16x2_of(__uint_as_float(w[k] << 16) * mul, __uint_as_float(w[k] & 0xffff0000u) * mul);
+        }
         const uint32_t qa = tlane + kTc5QCol + (segs & 1u) * 64u + uint32_t(half * DH / 2);
         if constexpr (DH / 2 == 32) {
             tmem_st32(qa, w);
@@ -1429,18 +1487,19 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
         __syncwarp();
         if (lane == 0) mbar_arrive(m.qready);
         ++segs;
+        return true;
     };
     // the next segment's Q tile is already written: the first one before the loop, each later one at the
     // end of the segment before it
-    bool q_early = false;
+    bool q_early = false, alive = true;
     if (wait(&m.mready[0], 0u)) {
         const UnitMeta f0 = m.metas[0];
         if (f0.b >= 0 && (f0.flags & kFirst)) {
-            write_q(f0);
+            alive = write_q(f0);
             q_early = true;
         }
     }
-    for (;;) {
+    while (alive) {
         if (!wait(&m.full[s], ph)) break;
         const UnitMeta mt = m.metas[s];
         if (mt.b < 0) break;
@@ -1452,13 +1511,14 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
             mrun = -INFINITY;
             lrun = 0.f;
             u_first = mt.u;
-            if (!q_early) write_q(mt);
+            if (!q_early && !write_q(mt)) break;
             q_early = false;
+            crow = cnext;
         }
         const int tok0 = mt.u * kTc5Keys;
         const int valid = min(kTc5Keys, mt.L - tok0);
         const int lim = row_ok ? min(valid, mt.L - tok0 - shift) - KH * half : 0;  // keys of this half
-        if (valid < kTc5Keys) {
+        if (CT == kBf16 && valid < kTc5Keys) {
             // V rows past the sequence's end hold anything (NaN included) and 0 * NaN is NaN: zero them,
             // once the V copy has landed
             if (!wait(&m.vfull[j % kTc5VSlots], (j / kTc5VSlots) & 1u)) break;
@@ -1475,8 +1535,8 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
         tc_fence_after();
         const uint32_t sbuf = tlane + (j & 1u) * 128u;  // the unit's score buffer (and then its weights)
         // raw scores s of the half's keys (at or past the row's bound: -inf); weights 2^(s c - m)
-        float x[KH];
-        {
+        float x[CT == kI8 ? 1 : KH];
+        if constexpr (CT == kBf16) {
             uint32_t r[KH];
             tmem_ld64(sbuf + uint32_t(KH * half), r);
             if (lim >= KH) {
@@ -1487,13 +1547,48 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
                 for (int i = 0; i < KH; ++i) x[i] = i < lim ? __uint_as_float(r[i]) : -INFINITY;
             }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&m.sfree[j & 1u]);  // the unit's K slot (and meta) may be reused
-        float mx4[4] = {x[0], x[1], x[2], x[3]};
+        // int8 caches: the scores are read twice, a scale block's 16 keys at a time (for the max, then for the
+        // weights), in rolled loops: the softmax, converting and issuing warps share the instruction
+        // caches
+        const float4 *prep = m.prep + s * (kTc5Keys / kScaleToks) + half * (KH / kScaleToks);
+        auto scores16 = [&](int g, float (&y)[kScaleToks]) {
+            uint32_t r[kScaleToks];
+            tmem_ld16(sbuf + uint32_t(KH * half + kScaleToks * g), r);
 #pragma unroll
-        for (int i = 4; i < KH; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], x[i]);
-        float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;  // c > 0
+            for (int i = 0; i < kScaleToks; ++i) y[i] = __uint_as_float(r[i]);
+            const int left = lim - kScaleToks * g;
+            if (left < kScaleToks) {
+#pragma unroll
+                for (int i = 0; i < kScaleToks; ++i) y[i] = i < left ? y[i] : -INFINITY;
+            }
+        };
+        float mx;
+        if constexpr (CT == kI8) {
+            if (!wait(&m.dready[s], ph)) break;
+            mx = -INFINITY;
+#pragma unroll 1
+            for (int g = 0; g < KH / kScaleToks; ++g) {
+                float y[kScaleToks];
+                scores16(g, y);
+                const float4 sc = prep[g];
+                float m2[2] = {y[0], y[1]};
+#pragma unroll
+                for (int i = 2; i < kScaleToks; ++i) m2[i & 1] = fmaxf(m2[i & 1], y[i]);
+                mx = fmaxf(mx, fmaf(fmaxf(m2[0], m2[1]), fmaxf(sc.x * crow, 0x1p-126f), sc.y));
+            }
+            mx -= kTc5Head;
+            // fmaxf passes NaN over: a row that has seen a key of a marked block takes some max all the same (a
+            // piece whose max is -inf counts as empty)
+            if (mx == -INFINITY && lim > 0) mx = 0.f;
+        } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m.sfree[j & 1u]);  // the unit's K slot (and meta) may be reused
+            float mx4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int i = 4; i < KH; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], x[i]);
+            mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;  // c > 0
+        }
         float other;
         if (!exchange(mx, other)) break;
         mx = fmaxf(mx, other);  // the row's tile max: the same in both halves
@@ -1526,16 +1621,41 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
         // weights (2^-inf = 0 for the masked keys; a row without any key so far takes m = 0 and gets zeros)
         {
             const float mneg = mrun == -INFINITY ? 0.f : -mrun;
-            float ps[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t w[32];
+            if constexpr (CT == kI8) {
+                // (the weights of group g, 8 columns, go over the scores of group g / 2: this thread's own, read
+                // already; so half h's are columns 64 h .. + 31 of the buffer)
+#pragma unroll 1
+                for (int g = 0; g < KH / kScaleToks; ++g) {
+                    float y[kScaleToks];
+                    scores16(g, y);
+                    const float4 sc = prep[g];
+                    // kc is never zero: a masked key is -inf times it
+                    const float kc = fmaxf(sc.x * crow, 0x1p-126f), bias = sc.y + mneg;
+                    float ps[2] = {0.f, 0.f};
+                    uint32_t w[kScaleToks / 2];
 #pragma unroll
-            for (int k = 0; k < KH / 2; ++k) {
-                const float p0 = ex2(fmaf(x[2 * k], c, mneg)), p1 = ex2(fmaf(x[2 * k + 1], c, mneg));
-                ps[k & 3] += p0 + p1;
-                w[k] = pack_bf16x2(p0, p1);
+                    for (int k = 0; k < kScaleToks / 2; ++k) {
+                        const float p0 = ex2(fmaf(y[2 * k], kc, bias)), p1 = ex2(fmaf(y[2 * k + 1], kc, bias));
+                        ps[k & 1] += p0 + p1;
+                        w[k] = f16x2_of(p0, p1);
+                    }
+                    lrun = fmaf(ps[0] + ps[1], sc.z, lrun);
+                    tmem_st8(sbuf + uint32_t(KH * half + 8 * g), w);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m.empty[s]);  // the unit's meta and scales are read
+            } else {
+                uint32_t w[32];
+                float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < KH / 2; ++k) {
+                    const float p0 = ex2(fmaf(x[2 * k], c, mneg)), p1 = ex2(fmaf(x[2 * k + 1], c, mneg));
+                    ps[k & 3] += p0 + p1;
+                    w[k] = pack_bf16x2(p0, p1);
+                }
+                lrun += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                tmem_st32(sbuf + 32u * half, w);
             }
-            lrun += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-            tmem_st32(sbuf + 32u * half, w);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -1551,7 +1671,7 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
                 if (!wait(&m.mready[sn], s + 1 == p.nst ? ph ^ 1u : ph)) break;
                 const UnitMeta nx = m.metas[sn];
                 if (nx.b >= 0 && (nx.flags & kFirst)) {
-                    write_q(nx);
+                    if (!write_q(nx)) break;
                     q_early = true;
                 }
             }
@@ -1642,11 +1762,12 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
 // share every K/V tile).  TC5 (with QS): the same entries on the tensor-memory
 // consumers (see tc5_softmax_warps).
 template <int D, int G, int CT, bool QS, bool TC5 = false>
-__global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G) + 1) * 32, 1)
+__global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_warps(G) + 1) * 32, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                         const DecodeParams p)
 {
-    static_assert(!TC5 || (QS && CT == kBf16 && G == 16 && (D == 64 || D == 128)), "tensor-memory CTAs: bf16 query-split");
+    static_assert(!TC5 || (QS && CT != kE4m3 && G == 16 && (D == 64 || D == 128)),
+                  "tensor-memory CTAs: query-split, bf16 or int8 caches");
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr int ES = CT != kBf16 ? 1 : 2;  // bytes per cached element
     const int qslots = one_q_buffer_ok(G, CT != kBf16, QS, TC5) ? p.qslots : 2;
@@ -1674,12 +1795,14 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
     uint64_t *vfull = tc5_bar + 15;        // TC5: [kTc5VSlots] a V slot loaded
     uint64_t *vempty = vfull + kTc5VSlots;  // TC5: [kTc5VSlots] a V slot released
     uint64_t *mready = vempty + kTc5VSlots;  // TC5: [nst] a K slot's meta written (before its copy lands)
+    uint64_t *dready = mready + p.nst;       // TC5, int8 caches: [nst] a stage's scales prepared
 
     if (threadIdx.x == 32 * p.cons) {  // none of this reads what the previous kernel writes
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
-        // TC5: a stage and a Q slot are released by one tcgen05.commit of the MMA warp
-        const uint32_t releases = TC5 ? 1u : uint32_t(p.cons);
+        // TC5: a stage and a Q slot are released by one tcgen05.commit of the MMA warp (int8 caches: by the
+        // softmax warps and the converting warps)
+        const uint32_t releases = TC5 ? (CT == kI8 ? uint32_t(kTc5SoftmaxWarps + kTc5ConvertWarps) : 1u) : uint32_t(p.cons);
         for (int i = 0; i < p.nst; ++i) {
             mbar_init(&full[i], CT == kI8 ? 33 : 1);  // int8 caches: and the lanes' copies of the scales
             mbar_init(&empty[i], releases);
@@ -1701,9 +1824,18 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
             for (int i = 0; i < 4; ++i) mbar_init(&tc5_bar[9 + i], 2);  // the two warps of lane quarter i met
             mbar_init(&tc5_bar[13], kTc5SoftmaxWarps);      // all softmax warps met
             mbar_init(&tc5_bar[14], kTc5SoftmaxWarps);      // a segment's Q tile written
-            for (int i = 0; i < kTc5VSlots; ++i) {
-                mbar_init(&vfull[i], 1);
-                mbar_init(&vempty[i], 1);
+            if constexpr (CT == kI8) {  // in this order: kready, kfree, vready, vfree
+                constexpr int n = kTc5KConv + kTc5VConv;
+                for (int i = 0; i < 2 * n; ++i) {
+                    const bool ready = i < kTc5KConv || (i >= 2 * kTc5KConv && i < 2 * kTc5KConv + kTc5VConv);
+                    mbar_init(&vfull[i], ready ? uint32_t(kTc5ConvertWarps) : 1u);
+                }
+                for (int i = 0; i < p.nst; ++i) mbar_init(&dready[i], 1);
+            } else {
+                for (int i = 0; i < kTc5VSlots; ++i) {
+                    mbar_init(&vfull[i], 1);
+                    mbar_init(&vempty[i], 1);
+                }
             }
             for (int i = 0; i < p.nst; ++i) mbar_init(&mready[i], 1);
         }
@@ -1865,7 +1997,7 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
             // the end of the segment before): 8 qn queries x gq heads of kv head g, D values each, as
             // 128-byte lines, lane-strided (plain prefetches: they do not queue behind the copies)
             auto prefetch_q = [&](const Walker &w) {
-                const int nq = min(team_warps(G) * p.qn, p.B - w.b);
+                const int nq = min(CT == kI8 ? 128 / p.gq : team_warps(G) * p.qn, p.B - w.b);
                 const int lines = p.gq * D * 2 / 128;
                 for (int i = lane; i < nq * lines; i += 32) {
                     const int r = i / lines, c = i - r * lines;
@@ -1972,7 +2104,7 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
                     mt.newrow = newrow;
                     if constexpr (TC5) mbar_arrive(&mready[s]);  // the meta, for a look ahead
                     // TC5: full[s] counts the K half only; the V half has barriers of its own
-                    mbar_arrive_expect_tx(&full[s], (TC5 ? 1u : 2u) * nrows * box_bytes);
+                    mbar_arrive_expect_tx(&full[s], (TC5 && CT == kBf16 ? 1u : 2u) * nrows * box_bytes);
                 }
                 __syncwarp();
                 if (k == 0 && lane == 0 && adaptive && !p.row_seq && slice == sh[0] && row >= 0 &&
@@ -1980,7 +2112,7 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
                     p.ws_bal->hint[my_sm][0] = make_int4(row, iw.g * p.hg, int32_t(gen) ^ kHintMagic, iw.b);
                     p.ws_bal->hint[my_sm][1] = make_int4((iw.u * p.toks) >> p.log2_bs, len, 0, 0);
                 }
-                if constexpr (TC5) {
+                if constexpr (TC5 && CT == kBf16) {
                     // K now (its half of the stage is free once the previous scores of the slot are done);
                     // V once the slot's previous output product is done
                     if (row >= 0) tma_load_4d(st + lane * box_bytes, &kmap, 0, row, 0, iw.g, &full[s], policy);
@@ -2046,7 +2178,7 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
         // let every copy this warp started land before the CTA can retire
         for (uint32_t i = kk > uint32_t(p.nst) ? kk - uint32_t(p.nst) : 0u; i < kk; ++i)
             mbar_wait_bounded(&full[i % uint32_t(p.nst)], (i / uint32_t(p.nst)) & 1u);
-        if constexpr (TC5)
+        if constexpr (TC5 && CT == kBf16)
             for (uint32_t i = vunits > uint32_t(kTc5VSlots) ? vunits - uint32_t(kTc5VSlots) : 0u; i < vunits; ++i)
                 mbar_wait_bounded(&vfull[i % kTc5VSlots], (i / kTc5VSlots) & 1u);
         // Count this CTA in: every thread of it read the control block long ago (the fence orders
@@ -2085,11 +2217,24 @@ __global__ void __launch_bounds__(TC5 ? (kTc5Consumers + 1) * 32 : (team_warps(G
         tm.vbase = smem + lay.off_v;
         tm.stage_addr = smem_u32(stage0);
         tm.v_addr = smem_u32(smem + lay.off_v);
-        if (warp == kTc5SoftmaxWarps)
+        if constexpr (CT == kI8) {
+            tm.kready = vfull;
+            tm.kfree = tm.kready + kTc5KConv;
+            tm.vready = tm.kfree + kTc5KConv;
+            tm.vfree = tm.vready + kTc5VConv;
+            tm.dready = dready;
+            tm.scales = reinterpret_cast<const float2 *>(smem + lay.off_sc);
+            tm.prep = reinterpret_cast<float4 *>(smem + lay.off_sc + uint32_t(p.nst) * scale_bytes(p.toks, p.hg));
+            if (warp == kTc5SoftmaxWarps)
+                tc5_mma_warp_i8<D>(p, tm, tmem);
+            else if (warp > kTc5SoftmaxWarps)
+                tc5_convert_warps<D>(p, lay, tm, stage0, int(threadIdx.x) - 32 * (kTc5SoftmaxWarps + 1));
+        } else if (warp == kTc5SoftmaxWarps) {
             tc5_mma_warp<D>(p, lay, tm, tmem);
-        else
-            tc5_softmax_warps<D, G>(p, lay, tm, tmem, comb, bound, scan, sh, wts, nslots, gen, wp, adaptive);
-        named_barrier(2, 32 * kTc5Consumers);  // every tensor-memory access of the CTA is done
+        }
+        if (warp < kTc5SoftmaxWarps)
+            tc5_softmax_warps<D, G, CT>(p, lay, tm, tmem, comb, bound, scan, sh, wts, nslots, gen, wp, adaptive);
+        named_barrier(2, 32 * tc5_consumers(CT));  // every tensor-memory access of the CTA is done
         if (warp == kTc5SoftmaxWarps) {
             tc_fence_after();
             tmem_dealloc(tmem, kTc5Cols);
@@ -2491,7 +2636,10 @@ inline bool encode_cache_map(CUtensorMap *map, const void *base, bool fp8, int D
     const CUresult r = enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                            const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                           // one kv head of 8-bit codes is 64 or 128 bytes of a token's row: a longer fetch would
+                           // read another head's
+                           fp8 && box_heads == 1 && Hkv > 1 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                            : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         char msg[64];
         std::snprintf(msg, sizeof msg, "CUresult %d", int(r));
@@ -2637,12 +2785,13 @@ LaunchFn pick_decode_qs(int D, int G);
 LaunchFn pick_decode_wide(int D, int G);  // regular bf16 CTAs, 9 to 16 virtual heads (pkv_decode_wide.cu)
 LaunchFn pick_decode_i8(int D, int G);        // int8 caches, 1 to 8 virtual heads (pkv_decode_i8.cu)
 LaunchFn pick_decode_i8_wide(int D, int G);   // int8 caches, 9 to 16 virtual heads (pkv_decode_i8_wide.cu)
-LaunchFn pick_decode_i8_qs(int D, int G);     // int8 caches, query-split CTAs (pkv_decode_i8_wide.cu)
+LaunchFn pick_decode_i8_tc5(int D);           // int8 caches, tensor-memory query-split CTAs (pkv_decode_i8_tc5.cu)
 LaunchFn pick_decode_tc5(int D);          // tensor-memory query-split CTAs, 16 virtual heads (pkv_decode_tc5.cu)
 
 // Whether a query-split call can run on the tensor-memory CTAs: bf16 caches, entries of 128 rows
 // (16 virtual heads per block: the query heads of a kv head a power of two), 128-key tiles within one
 // block (block_size >= 128), and a ring of at least two stages in shared memory.
+// The int8 ones take any block size (a tile is as many boxes as it spans blocks) and any group of up to 16 heads.
 inline bool tc5_eligible(int D, int G, int gq, int block_size, int B, int max_smem)
 {
     if (G != 16 || (D != 64 && D != 128) || block_size < kTc5Keys || (gq & (gq - 1)) != 0) return false;  // one box a tile

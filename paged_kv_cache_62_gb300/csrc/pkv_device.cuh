@@ -88,16 +88,23 @@ __device__ __forceinline__ uint64_t global_ns()
     return t;
 }
 
-// Warp-collective: every lane must call it; the result is the same in all lanes.
+// Warp-collective: every lane must call it; the result is the same in all lanes.  The timer is read only once
+// a wait has failed 256 times: a read takes long enough to delay a wait that was about to end.
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity)
 {
     const uint32_t a = smem_u32(bar);
     bool ok = mbar_try_wait(a, parity);
     if (!ok) {
-        const uint64_t t0 = global_ns();
+        uint64_t t0 = 0;
         for (uint32_t i = 1; !ok; ++i) {
             ok = mbar_try_wait(a, parity);
-            if (!ok && (i & 255u) == 0 && global_ns() - t0 > kWaitLimitNs) break;
+            if (!ok && (i & 255u) == 0) {
+                const uint64_t now = global_ns();
+                if (t0 == 0)
+                    t0 = now;
+                else if (now - t0 > kWaitLimitNs)
+                    break;
+            }
         }
     }
     return __all_sync(kFull, ok);
@@ -320,6 +327,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
         : "r"(taddr));
 }
 
+// 16 columns (as tmem_ld32).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
 // 64 columns of the warp's 32 lanes (register i: column base + i), then wait for the load.
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64])
 {
@@ -352,6 +371,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
         "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])

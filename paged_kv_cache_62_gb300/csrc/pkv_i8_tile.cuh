@@ -6,12 +6,13 @@
 //   x_j = (q . code_j) * (scale * s_k),   o += s_v * sum_j 2^(x_j - m) codeV_j.
 // The products run in f16 with fp32 accumulators: an int8 code is exact in f16 (one byte permute builds
 // 1024 + (code + 128), one subtraction of 1152 takes the rest off), a bf16 query element too once its row
-// is brought to one power of two (see q_row_scale), and a weight rounds by at most 2^-11 of itself.  The V scale
+// is brought to one power of two (see q_pow2), and a weight rounds by at most 2^-11 of itself.  The V scale
 // multiplies the sub-tile's fp32 product, not the f16 weights: s_v may be any size without moving the
 // weights out of the f16 range, and costs one fp32 FMA per 16 weights.
 #pragma once
 
 #include "pkv_decode_kernel.cuh"
+#include "pkv_i8_codes.cuh"
 
 namespace pkv {
 
@@ -20,23 +21,7 @@ namespace pkv {
 // 2^-30 of it.
 constexpr float kI8Head = 6.0f;
 
-// Four int8 codes (byte e is element e) as f16 pairs picked by the two permute selectors: K operands take
-// elements (0, 1) and (2, 3), V operands (0, 2) and (1, 3).
-template <uint32_t SEL0, uint32_t SEL1>
-__device__ __forceinline__ void i8x4_to_f16x2x2(uint32_t codes, uint32_t &a, uint32_t &b)
-{
-    const uint32_t u = codes ^ 0x80808080u;  // code + 128
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
-    const uint32_t x = __byte_perm(u, 0x64646464u, SEL0), y = __byte_perm(u, 0x64646464u, SEL1);
-    const __half2 hx = __hsub2(*reinterpret_cast<const __half2 *>(&x), off);
-    const __half2 hy = __hsub2(*reinterpret_cast<const __half2 *>(&y), off);
-    a = *reinterpret_cast<const uint32_t *>(&hx);
-    b = *reinterpret_cast<const uint32_t *>(&hy);
-}
-
-// The power of two 2^k that brings the row's largest |q| to [2^14, 2^15) (mul), so that every element of at
-// least 2^-28 of it stays a normal f16; returns 2^-k.  A row of zeros, or one holding an infinity or NaN, is
-// left as it is.  The row's four threads (r4 = 0..3) look at their own dims.
+// A query row's power of two (see q_pow2): the row's four threads (r4 = 0..3) look at their own dims.
 template <int D>
 __device__ __forceinline__ float q_row_scale(const uint16_t *qr, bool live, int r4, float &mul)
 {
@@ -50,10 +35,7 @@ __device__ __forceinline__ float q_row_scale(const uint16_t *qr, bool live, int 
     }
     mx = max(mx, __shfl_xor_sync(kFull, mx, 1));
     mx = max(mx, __shfl_xor_sync(kFull, mx, 2));
-    const int e = int(mx >> 7);  // biased exponent
-    const int k = mx == 0u || e == 255 ? 0 : 141 - max(e, 15);
-    mul = __uint_as_float(uint32_t(127 + k) << 23);
-    return __uint_as_float(uint32_t(127 - k) << 23);
+    return q_pow2(mx, mul);
 }
 
 template <int D, bool QS, int HR_, bool TAIL>
