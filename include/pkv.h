@@ -492,7 +492,9 @@ PKV_API pkv_status pkv_kv_store_i8(const uint16_t *k, const uint16_t *v, int64_t
  * num_workers, errors) as pkv_paged_decode.  Products run in f16 with fp32
  * accumulators: codes are exact, a query row is scaled by a power of two that
  * keeps elements of at least 2^-28 of its largest exact, softmax weights round
- * by at most 2^-11 of themselves; scales multiply in fp32.
+ * by at most 2^-11 of themselves; scales enter in fp32.  V scales below 2^-104
+ * count as zero, above 2^104 as NaN; within a sequence they may lie 2^90 apart.
+ * A NaN scale (see pkv_kv_store_i8) gives NaN to the queries that see its block.
  */
 PKV_API pkv_status pkv_paged_decode_i8(const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache,
                                        const float *scales, const int32_t *block_tables,

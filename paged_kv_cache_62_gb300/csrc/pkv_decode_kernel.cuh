@@ -766,14 +766,23 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb,
     }
 }
 
-// int8 caches: one warp tile, with each 16-token sub-tile's (K scale, V scale) in sc and the rows' score
-// factors in rowf (defined in pkv_i8_tile.cuh, which the translation units of the int8 kernels include).
-template <int D, bool QS, int HR_, bool TAIL>
-__device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const LaneOffsets<D, kI8, QS> &off,
-                                               const uint32_t (&qa)[Tc<D, kI8, QS, HR_>::KS][2 * HR_],
-                                               const float (&rowf)[HR_], const float2 (&sc)[2],
-                                               const int (&lim)[HR_], int valid, float (&m)[HR_], float (&l)[HR_],
-                                               float (&o)[Tc<D, kI8, QS, HR_>::MT][HR_][4], int lane);
+// int8 caches (defined in pkv_i8_tile.cuh, which the translation units of the int8 kernels include): what a tile
+// takes of a scale block, and one warp tile, with the rows' score factors in rowf and the correction of the
+// biased codes in qb.
+struct I8Scales {
+    float k, lv, iv;  // K scale, log2 of the V scale, its inverse
+    bool plain, vzero;
+};
+__device__ __forceinline__ I8Scales i8_scales(float2 s);
+template <int KS, int HR>
+__device__ __forceinline__ void q_bias(const uint32_t (&qa)[KS][2 * HR], float (&qb)[HR]);
+template <int D, int HR_, bool TAIL>
+__device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const LaneOffsets<D, kI8, false> &off,
+                                               const uint32_t (&qa)[Tc<D, kI8, false, HR_>::KS][2 * HR_],
+                                               const float (&rowf)[HR_], const float (&qb)[HR_],
+                                               const I8Scales (&sc)[2], const int (&lim)[HR_], int valid,
+                                               float (&m)[HR_], float (&l)[HR_],
+                                               float (&o)[Tc<D, kI8, false, HR_>::MT][HR_][4], int lane);
 template <int D>
 __device__ __forceinline__ float q_row_scale(const uint16_t *qr, bool live, int r4, float &mul);
 
@@ -2268,7 +2277,9 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
         l[hr] = 0.f;
     }
     float ksc = p.scale_log2;
-    float rowf[HR];    // int8 caches: score factor of the thread's rows (scale_log2 and the power of two taken out of q)
+    // int8 caches: score factor of the thread's rows (scale_log2 and the power of two taken out of q), and the
+    // biased codes' part of their scores
+    float rowf[HR], qb[HR];
     float vsc = 1.0f;  // E4M3 caches: the kv head's V scale, applied in the final division
     // fused store: this lane's 8 bytes of the new K / V row (4 bf16 elements, or 8 E4M3 codes)
     uint2 kn = make_uint2(0u, 0u), vn = make_uint2(0u, 0u);
@@ -2354,6 +2365,7 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                 m[hr] = -INFINITY;
                 l[hr] = 0.f;
             }
+            if constexpr (CT == kI8) q_bias<TC::KS, HR>(qa, qb);
             __syncwarp();
             if (lane == 0) mbar_arrive(&qempty[qs]);
             ++segs;
@@ -2394,15 +2406,19 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
             if constexpr (CT == kI8) {
                 const float2 *sc = reinterpret_cast<const float2 *>(smem + lay.off_sc +
                                                                     uint32_t(s) * scale_bytes(p.toks, p.hg));
-                float2 sct[TC::NT];
+                I8Scales sct[TC::NT];
+                bool plain = true;
 #pragma unroll
-                for (int st = 0; st < TC::NT; ++st) sct[st] = sc[(jt * TC::NT + st) * p.hg + h];
-                if (valid == TC::TW)
-                    attend_tile_i8<D, QS, TC::HR, false>(kb, kb + lay.kv_bytes, off, qa, rowf, sct, lim, valid, m, l, o,
-                                                         lane);
+                for (int st = 0; st < TC::NT; ++st) {
+                    sct[st] = i8_scales(sc[(jt * TC::NT + st) * p.hg + h]);
+                    plain &= sct[st].plain;
+                }
+                if (valid == TC::TW && plain)
+                    attend_tile_i8<D, TC::HR, false>(kb, kb + lay.kv_bytes, off, qa, rowf, qb, sct, lim, valid, m, l, o,
+                                                     lane);
                 else
-                    attend_tile_i8<D, QS, TC::HR, true>(kb, kb + lay.kv_bytes, off, qa, rowf, sct, lim, valid, m, l, o,
-                                                        lane);
+                    attend_tile_i8<D, TC::HR, true>(kb, kb + lay.kv_bytes, off, qa, rowf, qb, sct, lim, valid, m, l, o,
+                                                    lane);
             } else if (valid == TC::TW)
                 attend_tile<D, CT, QS, TC::HR, false>(kb, kb + lay.kv_bytes, off, qa, ksc, lim, valid, m, l, o, lane);
             else

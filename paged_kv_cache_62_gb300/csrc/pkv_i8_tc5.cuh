@@ -64,7 +64,7 @@ __device__ __forceinline__ void tc5_convert_tile(const uint8_t *raw, uint8_t *ds
 // whose scales are not of ordinary size is dealt with in the operands (tc5_mark_block), with scales of 1 here.
 __device__ __forceinline__ bool tc5_plain(float2 s)
 {
-    return s.x > 0.f && s.x < INFINITY && s.y >= 0x1p-40f && s.y <= 0x1p+40f;
+    return s.x > 0.f && s.x < INFINITY && s.y >= kMinVScale && s.y <= kMaxVScale;
 }
 
 // mode 1: zeros, mode 2: NaN, into the 16 rows of scale block g of an operand (all converting warps).
@@ -109,9 +109,9 @@ __device__ void tc5_convert_warps(const DecodeParams &p, const CtaLayout &lay, c
                 const bool plain = tc5_plain(sc);
                 if (t < 32) {
                     if (lane < kGroups) {
-                        // a K or V scale of zero: zeros there; a V scale below 2^-40 counts as zero; a NaN, an
-                        // infinity or a V scale above 2^40: NaN scores
-                        const bool ko = sc.x > 0.f && sc.x < INFINITY, vo = sc.y >= 0x1p-40f && sc.y <= 0x1p+40f;
+                        // a K or V scale of zero: zeros there; a V scale below kMinVScale counts as zero; a NaN, an
+                        // infinity or a V scale above kMaxVScale: NaN scores
+                        const bool ko = sc.x > 0.f && sc.x < INFINITY, vo = sc.y >= kMinVScale && sc.y <= kMaxVScale;
                         const float lv = vo ? __log2f(sc.y) : 0.f;
                         m.prep[s * kGroups + lane] = make_float4(ko ? sc.x : 1.f, lv, ex2(-lv), 0.f);
                     }
@@ -121,8 +121,8 @@ __device__ void tc5_convert_warps(const DecodeParams &p, const CtaLayout &lay, c
                 uint8_t *kop = kdst + kb * 2u * lay.kv_bytes;
                 tc5_convert_tile<D>(stage0 + uint32_t(s) * lay.stage_bytes, kop, t);
                 // blocks to mark (the same in every warp): bits 0-7 zeros in K, 8-15 zeros in V, 16-23 NaN in K
-                const bool kz = sc.x == 0.f, vz = sc.y >= 0.f && sc.y < 0x1p-40f;
-                const bool bad = !plain && !((kz || (sc.x > 0.f && sc.x < INFINITY)) && (vz || (sc.y >= 0x1p-40f && sc.y <= 0x1p+40f)));
+                const bool kz = sc.x == 0.f, vz = sc.y >= 0.f && sc.y < kMinVScale;
+                const bool bad = !plain && !((kz || (sc.x > 0.f && sc.x < INFINITY)) && (vz || (sc.y >= kMinVScale && sc.y <= kMaxVScale)));
                 const unsigned odd = __ballot_sync(kFull, !plain) & ((1u << kGroups) - 1u);
                 if (odd) {
                     const unsigned mk = __ballot_sync(kFull, kz && !bad), mv = __ballot_sync(kFull, vz && !bad),

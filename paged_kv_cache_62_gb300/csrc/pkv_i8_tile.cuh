@@ -2,13 +2,20 @@
 // instantiate the kernel for them, after pkv_decode_kernel.cuh.
 //
 // A cached value is code * scale with one scale per kScaleToks = 16 tokens and kv head, one for K and one
-// for V, so a 16-token sub-tile of the MMA tile has one (K scale s_k, V scale s_v) pair:
-//   x_j = (q . code_j) * (scale * s_k),   o += s_v * sum_j 2^(x_j - m) codeV_j.
-// The products run in f16 with fp32 accumulators: an int8 code is exact in f16 (one byte permute builds
-// 1024 + (code + 128), one subtraction of 1152 takes the rest off), a bf16 query element too once its row
-// is brought to one power of two (see q_pow2), and a weight rounds by at most 2^-11 of itself.  The V scale
-// multiplies the sub-tile's fp32 product, not the f16 weights: s_v may be any size without moving the
-// weights out of the f16 range, and costs one fp32 FMA per 16 weights.
+// for V, so a 16-token sub-tile of the MMA tile has one (K scale s_k, V scale s_v) pair, and with lv = log2 s_v
+//     x_j = (q . code_j) * (scale * s_k) + lv,   p_j = 2^(x_j - m),
+//     o += sum_j p_j codeV_j,   l += (sum_j p_j) / s_v,   out = o / l:
+// the weights take the V scale along and the sum divides it out, so both products see plain codes and m, the
+// running max of the x_j, keeps the weights in the f16 range whatever the scales.  The products run in f16 with
+// fp32 accumulators: codes are exact, a query row too once it is brought to one power of two (see q_pow2), and a
+// weight rounds by at most 2^-11 of itself.
+//
+// The widening of the codes is what the consumers spend most on.  One byte permute makes 1152 + code in f16 (see
+// i8x4_biased); the 1152 is taken off in the products, not from every pair of codes: the score accumulators start
+// at -1152 sum q (computed once a segment), and a product with -1152 for a matrix takes 1152 sum p off the
+// output of every sub-tile.  Next to a subtraction per pair that saves 128 of about 590 instructions a tile;
+// what the detour costs is fp32 rounding at 1152 times a sub-tile's weights, 2^-13.8 of a code each time.  16-row
+// tiles subtract from V's codes (their two halves would need twice the products).
 #pragma once
 
 #include "pkv_decode_kernel.cuh"
@@ -20,6 +27,34 @@ namespace pkv {
 // largest of a row is at least 2^kI8Head when its max last moved, so the f16 subnormal step of 2^-24 is
 // 2^-30 of it.
 constexpr float kI8Head = 6.0f;
+
+// -1152 times the sum of the thread's rows of Q (f16 fragments; rows g and g + 8), as a product with -1152
+// for every key: what the biased codes add to a score.
+template <int KS, int HR>
+__device__ __forceinline__ void q_bias(const uint32_t (&qa)[KS][2 * HR], float (&qb)[HR])
+{
+    float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+        mma_f16_16816(t, qa[ks][0], HR == 2 ? qa[ks][2 % (2 * HR)] : 0u, qa[ks][1], HR == 2 ? qa[ks][3 % (2 * HR)] : 0u,
+                      0xe480e480u, 0xe480e480u);
+#pragma unroll
+    for (int hr = 0; hr < HR; ++hr) qb[hr] = t[2 * hr];
+}
+
+// What a tile takes of a scale block's pair (s_k, s_v).  Scales of ordinary size (plain) as they are; a V scale of
+// zero or below kMinVScale counts as zero: the block's V codes are taken as zeros (vzero); a NaN, an infinity or a
+// V scale above kMaxVScale makes the block's scores NaN.
+__device__ __forceinline__ I8Scales i8_scales(float2 s)
+{
+    I8Scales r;
+    r.plain = s.y >= kMinVScale && s.y <= kMaxVScale;
+    r.vzero = s.y >= 0.f && s.y < kMinVScale;
+    r.k = r.plain || r.vzero ? s.x : __uint_as_float(0x7fc00000u);
+    r.lv = r.plain ? __log2f(s.y) : 0.f;
+    r.iv = ex2(-r.lv);
+    return r;
+}
 
 // A query row's power of two (see q_pow2): the row's four threads (r4 = 0..3) look at their own dims.
 template <int D>
@@ -38,16 +73,18 @@ __device__ __forceinline__ float q_row_scale(const uint16_t *qr, bool live, int 
     return q_pow2(mx, mul);
 }
 
-template <int D, bool QS, int HR_, bool TAIL>
-__device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const LaneOffsets<D, kI8, QS> &off,
-                                               const uint32_t (&qa)[Tc<D, kI8, QS, HR_>::KS][2 * HR_],
-                                               const float (&rowf)[HR_], const float2 (&sc)[2],
-                                               const int (&lim)[HR_], int valid, float (&m)[HR_], float (&l)[HR_],
-                                               float (&o)[Tc<D, kI8, QS, HR_>::MT][HR_][4], int lane)
+template <int D, int HR_, bool TAIL>
+__device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const LaneOffsets<D, kI8, false> &off,
+                                               const uint32_t (&qa)[Tc<D, kI8, false, HR_>::KS][2 * HR_],
+                                               const float (&rowf)[HR_], const float (&qb)[HR_],
+                                               const I8Scales (&sc)[2], const int (&lim)[HR_], int valid,
+                                               float (&m)[HR_], float (&l)[HR_],
+                                               float (&o)[Tc<D, kI8, false, HR_>::MT][HR_][4], int lane)
 {
-    using T = Tc<D, kI8, QS, HR_>;
+    using T = Tc<D, kI8, false, HR_>;
     constexpr int NT = T::NT, HR = T::HR;
     static_assert(NT == 2, "two 16-token sub-tiles, one pair of scales each");
+    constexpr uint32_t kMinus1152 = 0xe480e480u;  // f16 pair
     const int r4 = lane & 3;
     auto a1 = [&](int ks) { return HR == 2 ? qa[ks][2 % (2 * HR)] : 0u; };
     auto a3 = [&](int ks) { return HR == 2 ? qa[ks][3 % (2 * HR)] : 0u; };
@@ -57,7 +94,7 @@ __device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const L
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sa[st][nt][e] = 0.f;
+            for (int e = 0; e < 4; ++e) sa[st][nt][e] = qb[e >> 1 < HR ? e >> 1 : 0];
 #pragma unroll
     for (int i = 0; i < T::NCP; ++i) {
 #pragma unroll
@@ -67,10 +104,10 @@ __device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const L
             // chunk 2i (r0, r2) is k-step 2i, chunk 2i + 1 (r1, r3) k-step 2i + 1; a register holds codes
             // 4 r4 .. 4 r4 + 3 of a token (tokens 0-7 in r0, r1; 8-15 in r2, r3)
             uint32_t b[4][2];
-            i8x4_to_f16x2x2<0x4140, 0x4342>(r0, b[0][0], b[0][1]);
-            i8x4_to_f16x2x2<0x4140, 0x4342>(r1, b[1][0], b[1][1]);
-            i8x4_to_f16x2x2<0x4140, 0x4342>(r2, b[2][0], b[2][1]);
-            i8x4_to_f16x2x2<0x4140, 0x4342>(r3, b[3][0], b[3][1]);
+            i8x4_biased<0x4140, 0x4342>(r0, b[0][0], b[0][1]);
+            i8x4_biased<0x4140, 0x4342>(r1, b[1][0], b[1][1]);
+            i8x4_biased<0x4140, 0x4342>(r2, b[2][0], b[2][1]);
+            i8x4_biased<0x4140, 0x4342>(r3, b[3][0], b[3][1]);
             mma_f16_16816(sa[st][0], qa[2 * i][0], a1(2 * i), qa[2 * i][1], a3(2 * i), b[0][0], b[0][1]);
             mma_f16_16816(sa[st][1], qa[2 * i][0], a1(2 * i), qa[2 * i][1], a3(2 * i), b[2][0], b[2][1]);
             mma_f16_16816(sa[st][0], qa[2 * i + 1][0], a1(2 * i + 1), qa[2 * i + 1][1], a3(2 * i + 1), b[1][0],
@@ -79,19 +116,21 @@ __device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const L
                           b[3][1]);
         }
     }
-    // the thread's scores (see attend_tile); a sub-tile without a token has no scale, its scores are masked
+    // the thread's scores (see attend_tile), log2 of the V scale added; a sub-tile without a token has no
+    // scales, its scores are masked
     float x[HR][NT * 4];
 #pragma unroll
     for (int hr = 0; hr < HR; ++hr)
 #pragma unroll
         for (int st = 0; st < NT; ++st) {
-            const float f = rowf[hr] * sc[st].x;
+            const float f = rowf[hr] * sc[st].k;
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    x[hr][4 * st + 2 * nt + e] =
-                        16 * st + 8 * nt + 2 * r4 + e < lim[hr] ? sa[st][nt][2 * hr + e] * f : -INFINITY;
+                    x[hr][4 * st + 2 * nt + e] = 16 * st + 8 * nt + 2 * r4 + e < lim[hr]
+                                                     ? fmaf(sa[st][nt][2 * hr + e], f, sc[st].lv)
+                                                     : -INFINITY;
         }
     float mx[HR];
     bool grow = false;
@@ -125,38 +164,25 @@ __device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const L
 #pragma unroll
     for (int hr = 0; hr < HR; ++hr) {
         const float mr = m[hr] == -INFINITY ? 0.f : m[hr];
-        float pr[NT * 4];
 #pragma unroll
-        for (int k = 0; k < NT * 4; ++k) pr[k] = ex2(x[hr][k] - mr);
-        float ps = 0.f;
+        for (int st = 0; st < NT; ++st) {
+            float pr[4];
 #pragma unroll
-        for (int k = 0; k < NT * 4; ++k) ps += pr[k];
-        l[hr] += ps;
+            for (int k = 0; k < 4; ++k) pr[k] = ex2(x[hr][4 * st + k] - mr);
+            // (a sub-tile without a token has no scales either)
+            if (!TAIL || 16 * st < valid) l[hr] = fmaf((pr[0] + pr[1]) + (pr[2] + pr[3]), sc[st].iv, l[hr]);
 #pragma unroll
-        for (int st = 0; st < NT; ++st)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) pb[hr][st][c] = f16x2_of(pr[4 * st + 2 * c], pr[4 * st + 2 * c + 1]);
+            for (int c = 0; c < 2; ++c) pb[hr][st][c] = f16x2_of(pr[2 * c], pr[2 * c + 1]);
+        }
     }
 #pragma unroll
     for (int st = 0; st < NT; ++st) {
-        if (TAIL && 16 * st >= valid) break;  // no token, and no scale
+        if (TAIL && 16 * st >= valid) break;  // no token
         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
         if constexpr (TAIL) {
-            const int v0 = valid - 16 * st;
+            const int v0 = sc[st].vzero ? 0 : valid - 16 * st;
             keep0 = (2 * r4 < v0 ? 0x0000ffffu : 0u) | (2 * r4 + 1 < v0 ? 0xffff0000u : 0u);
             keep1 = (2 * r4 + 8 < v0 ? 0x0000ffffu : 0u) | (2 * r4 + 9 < v0 ? 0xffff0000u : 0u);
-        }
-        // s_v for the thread's output columns; a block whose scale is NaN or infinite reaches only the
-        // queries that see one of its tokens (0 * NaN would reach them all)
-        float vs[HR][2];
-#pragma unroll
-        for (int hr = 0; hr < HR; ++hr) vs[hr][0] = vs[hr][1] = sc[st].y;
-        if (!(fabsf(sc[st].y) < INFINITY)) {
-#pragma unroll
-            for (int hr = 0; hr < HR; ++hr)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (__shfl_sync(kFull, lim[hr], 8 * r4 + 4 * e) <= 16 * st) vs[hr][e] = 0.f;
         }
 #pragma unroll
         for (int i = 0; i < T::NCP; ++i) {
@@ -171,19 +197,26 @@ __device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const L
             // a register holds (token 2 r4: dims 2g, 2g + 1 | token 2 r4 + 1: the same) of a 16-dim chunk: the
             // permute pairs the two tokens of a dim
             uint32_t a[4][2];
-            i8x4_to_f16x2x2<0x4240, 0x4341>(r0, a[0][0], a[0][1]);
-            i8x4_to_f16x2x2<0x4240, 0x4341>(r1, a[1][0], a[1][1]);
-            i8x4_to_f16x2x2<0x4240, 0x4341>(r2, a[2][0], a[2][1]);
-            i8x4_to_f16x2x2<0x4240, 0x4341>(r3, a[3][0], a[3][1]);
+            if constexpr (HR == 1) {
+                i8x4_biased<0x4240, 0x4341>(r0, a[0][0], a[0][1]);
+                i8x4_biased<0x4240, 0x4341>(r1, a[1][0], a[1][1]);
+                i8x4_biased<0x4240, 0x4341>(r2, a[2][0], a[2][1]);
+                i8x4_biased<0x4240, 0x4341>(r3, a[3][0], a[3][1]);
+            } else {
+                i8x4_to_f16x2x2<0x4240, 0x4341>(r0, a[0][0], a[0][1]);
+                i8x4_to_f16x2x2<0x4240, 0x4341>(r1, a[1][0], a[1][1]);
+                i8x4_to_f16x2x2<0x4240, 0x4341>(r2, a[2][0], a[2][1]);
+                i8x4_to_f16x2x2<0x4240, 0x4341>(r3, a[3][0], a[3][1]);
+            }
 #pragma unroll
             for (int hr = 0; hr < HR; ++hr) {
-                float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16_16816(c0, a[0][0], a[0][1], a[2][0], a[2][1], pb[hr][st][0], pb[hr][st][1]);
-                mma_f16_16816(c1, a[1][0], a[1][1], a[3][0], a[3][1], pb[hr][st][0], pb[hr][st][1]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    o[2 * i][hr][e] = fmaf(vs[hr][e & 1], c0[e], o[2 * i][hr][e]);
-                    o[2 * i + 1][hr][e] = fmaf(vs[hr][e & 1], c1[e], o[2 * i + 1][hr][e]);
+                mma_f16_16816(o[2 * i][hr], a[0][0], a[0][1], a[2][0], a[2][1], pb[hr][st][0], pb[hr][st][1]);
+                mma_f16_16816(o[2 * i + 1][hr], a[1][0], a[1][1], a[3][0], a[3][1], pb[hr][st][0], pb[hr][st][1]);
+                if constexpr (HR == 1) {
+                    mma_f16_16816(o[2 * i][hr], kMinus1152, kMinus1152, kMinus1152, kMinus1152, pb[hr][st][0],
+                                  pb[hr][st][1]);
+                    mma_f16_16816(o[2 * i + 1][hr], kMinus1152, kMinus1152, kMinus1152, kMinus1152, pb[hr][st][0],
+                                  pb[hr][st][1]);
                 }
             }
         }
