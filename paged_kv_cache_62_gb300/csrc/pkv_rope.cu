@@ -10,9 +10,11 @@
 // fraction's last place, 2^-64, times 2^31 is 2^-33 turns); its upper 32 bits go to sincospif.  An fp32
 // product would lose the angle's low bits to its whole turns (2^-24 of 32768 radians is 2e-3).
 //
-// Memory-bound: a row is read once and written once.  One CTA takes one token: its first rot / 2 threads
-// make the token's cosines and sines (shared by all its heads) in shared memory while the rows' loads are on
-// their way; each thread then turns 16 dims of one head, two 16-byte loads and stores.
+// Memory-bound: a row is read once and written once.  One warp takes a token (or, when there are few tokens,
+// a part of its heads): it makes the token's rot / 2 cosines and sines, two or so a lane, while the first rows'
+// loads are on their way, passes them through shared memory (no barrier but the warp's own), and then turns 16
+// dims of a head per lane and step, two 16-byte loads and stores.  A lane keeps its place within the head, so
+// its eight cosines and sines stay in registers for all heads.
 #include <algorithm>
 
 #include "pkv_device.cuh"
@@ -28,7 +30,7 @@ struct RopeParams {
     long long q_stride, k_stride, v_stride, qo_stride, ko_stride, vo_stride;
     const int32_t *positions, *freq_axis, *slots;
     const float *inv_freq;
-    int32_t axes, T, Hq, Hkv, D, rot;
+    int32_t axes, T, Hq, Hkv, D, rot, parts;
     long long num_slots;
     int32_t *err;
 };
@@ -93,59 +95,65 @@ __device__ __forceinline__ void turn16(uint4 &a, uint4 &b, const float2 *cs)
     b = make_uint4(ub[0], ub[1], ub[2], ub[3]);
 }
 
+constexpr int kRopeWarps = 4;  // warps (token parts) a CTA
+
 template <bool ADJ>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeParams p)
+__global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams p)
 {
-    __shared__ __align__(16) float2 cs[kRopeMaxHalf];
+    __shared__ __align__(16) float2 cs_all[kRopeWarps][kRopeMaxHalf];
+    constexpr int B = 3;  // pieces of a lane in flight
     griddep_launch_dependents();
     griddep_wait();
-    const int t = blockIdx.x;
+    const int lane = threadIdx.x & 31;
+    const int64_t w = int64_t(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
+    const int t = int(w / p.parts), part = int(w - int64_t(t) * p.parts);
+    if (t >= p.T) return;  // warps do not meet after this
+    float2 *cs = cs_all[threadIdx.x >> 5];
     const int half = p.rot >> 1, per = p.D >> 4, turned = p.rot >> 4;  // 16-dim pieces of a head, those that turn
-    int64_t slot = 0;
-    if (p.slots) {
-        slot = __ldg(p.slots + t);
-        if (slot < -1 || slot >= p.num_slots) {
-            if (threadIdx.x == 0) flag_error(p.err, PKV_ERR_SLOT_RANGE);
-            slot = -1;
-        }
-    }
-    const int64_t out_row = p.slots ? slot : int64_t(t);
-    const int heads = p.Hq + p.Hkv + (p.v ? p.Hkv : 0), items = heads * per;
-    // piece `it`: head it / per of (q heads, k heads, v heads), and its two vectors' places
-    auto place = [&](int it, const uint16_t *&src, uint16_t *&dst, int &c, int &d0, int &d1) {
-        int h = it / per;
-        c = it - h * per;
-        bool turn = c < turned;
+    const int hpw = 32 / per;                                           // heads a step takes
+    const int hl = lane / per, c = lane - hl * per;                     // the lane's head of a step, its piece
+    const int heads = p.Hq + p.Hkv + (p.v ? p.Hkv : 0), turning = p.Hq + p.Hkv;
+    const int64_t slot = p.slots ? int64_t(__ldg(p.slots + t)) : int64_t(t);
+    const bool drop = p.slots && (slot < 0 || slot >= p.num_slots);
+    if (p.slots && (slot < -1 || slot >= p.num_slots) && lane == 0) flag_error(p.err, PKV_ERR_SLOT_RANGE);
+    const bool mine = hl < hpw;
+    // the piece of head h (q heads, k heads, v heads): false where nothing is written
+    auto place = [&](int h, const uint16_t *&src, uint16_t *&dst) {
+        if (!mine || h >= heads) return false;
         if (h < p.Hq) {
             src = p.q + t * p.q_stride + int64_t(h) * p.D;
             dst = p.q_out + t * p.qo_stride + int64_t(h) * p.D;
-        } else if (h < p.Hq + p.Hkv) {
-            h -= p.Hq;
-            src = p.k + t * p.k_stride + int64_t(h) * p.D;
-            dst = out_row < 0 ? nullptr : p.k_out + out_row * p.ko_stride + int64_t(h) * p.D;
+            return true;
+        }
+        if (drop) return false;
+        if (h < turning) {
+            src = p.k + t * p.k_stride + int64_t(h - p.Hq) * p.D;
+            dst = p.k_out + slot * p.ko_stride + int64_t(h - p.Hq) * p.D;
         } else {
-            h -= p.Hq + p.Hkv;
-            src = p.v + t * p.v_stride + int64_t(h) * p.D;
-            dst = out_row < 0 ? nullptr : p.v_out + out_row * p.vo_stride + int64_t(h) * p.D;
-            turn = false;
+            src = p.v + t * p.v_stride + int64_t(h - turning) * p.D;
+            dst = p.v_out + slot * p.vo_stride + int64_t(h - turning) * p.D;
         }
-        d0 = turn && !ADJ ? 8 * c : 16 * c;
-        d1 = turn && !ADJ ? half + 8 * c : 16 * c + 8;
-        if (!turn) c = -1;
+        return true;
     };
-    const uint16_t *src = nullptr;
-    uint16_t *dst = nullptr;
-    int c = -1, d0 = 0, d1 = 0;
-    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-    int it = threadIdx.x;
-    if (it < items) {  // the first piece's loads go out before the angles are made
-        place(it, src, dst, c, d0, d1);
-        if (dst) {
-            a = *reinterpret_cast<const uint4 *>(src + d0);
-            b = *reinterpret_cast<const uint4 *>(src + d1);
+    // a turning piece of pairs of halves lies in two places of the head
+    auto d0 = [&](int h) { return c < turned && !ADJ && h < turning ? 8 * c : 16 * c; };
+    auto d1 = [&](int h) { return c < turned && !ADJ && h < turning ? half + 8 * c : 16 * c + 8; };
+    uint4 a[B], b[B];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const int h = h0 + k * hpw * p.parts;
+            const uint16_t *src;
+            uint16_t *dst;
+            if (place(h, src, dst)) {
+                a[k] = *reinterpret_cast<const uint4 *>(src + d0(h));
+                b[k] = *reinterpret_cast<const uint4 *>(src + d1(h));
+            }
         }
-    }
-    for (int i = threadIdx.x; i < half; i += blockDim.x) {
+    };
+    const int h0 = part * hpw + hl, step = B * hpw * p.parts;
+    load(h0);
+    for (int i = lane; i < half; i += 32) {
         int ax = p.freq_axis ? __ldg(p.freq_axis + i) : 0;
         if (ax < 0 || ax >= p.axes) {
             flag_error(p.err, PKV_ERR_AXIS_RANGE);
@@ -153,30 +161,40 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeParams p)
         }
         cs[i] = turn_cos_sin(turn_fraction(__ldg(p.inv_freq + i)), __ldg(p.positions + int64_t(ax) * p.T + t));
     }
-    __syncthreads();
-    while (it < items) {
-        if (dst) {
-            if (c >= 0) turn16<ADJ>(a, b, cs + 8 * c);
-            *reinterpret_cast<uint4 *>(dst + d0) = a;
-            *reinterpret_cast<uint4 *>(dst + d1) = b;
-        }
-        it += blockDim.x;
-        if (it < items) {
-            place(it, src, dst, c, d0, d1);
-            if (dst) {
-                a = *reinterpret_cast<const uint4 *>(src + d0);
-                b = *reinterpret_cast<const uint4 *>(src + d1);
+    __syncwarp();
+    float2 mycs[8];
+    if (c < turned) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mycs[e] = cs[8 * c + e];
+    }
+    for (int h1 = h0; h1 < heads; h1 += step) {
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const int h = h1 + k * hpw * p.parts;
+            const uint16_t *src;
+            uint16_t *dst;
+            if (place(h, src, dst)) {
+                if (c < turned && h < turning) turn16<ADJ>(a[k], b[k], mycs);
+                *reinterpret_cast<uint4 *>(dst + d0(h)) = a[k];
+                *reinterpret_cast<uint4 *>(dst + d1(h)) = b[k];
             }
         }
+        load(h1 + step);
     }
 }
 
 static pkv_status rope_call(RopeParams &p, int interleaved, pkv_stream_t stream)
 {
-    const int64_t pieces = (int64_t(p.Hq) + p.Hkv + (p.v ? p.Hkv : 0)) * (p.D / 16);
-    const int threads = int(std::min<int64_t>(256, std::max<int64_t>((pieces + 31) / 32 * 32, 64)));
-    const cudaError_t e = launch_pdl(interleaved ? rope_kernel<true> : rope_kernel<false>, dim3(unsigned(p.T)),
-                                     dim3(threads), 0, reinterpret_cast<cudaStream_t>(stream), p);
+    DeviceInfo dev;
+    if (!current_device_info(&dev)) return PKV_ECUDA;
+    // few tokens: several warps a token, each with a part of the heads (as many as leave every lane a piece), until
+    // the SMs have eight warps each
+    const int heads = p.Hq + p.Hkv + (p.v ? p.Hkv : 0), hpw = 32 / (p.D / 16);
+    const int most = (heads + hpw - 1) / hpw;
+    p.parts = int(std::min<int64_t>(most, std::max<int64_t>(1, int64_t(dev.sm_count) * 8 / p.T)));
+    const int64_t grid = (int64_t(p.T) * p.parts + kRopeWarps - 1) / kRopeWarps;
+    const cudaError_t e = launch_pdl(interleaved ? rope_kernel<true> : rope_kernel<false>, dim3(unsigned(grid)),
+                                     dim3(32 * kRopeWarps), 0, reinterpret_cast<cudaStream_t>(stream), p);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return cuda_fail("rope_kernel launch", e);

@@ -21,6 +21,7 @@
 namespace pkv {
 
 constexpr int kSB = PKV_I8_BLOCK;  // tokens a scale block holds
+constexpr int kStoreThreads = 512;
 constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds a small float to an integer, ties to even
 
 struct StoreI8Params {
@@ -55,48 +56,54 @@ __device__ __forceinline__ int exact_code(float hi, float lo, float s)
     return max(-127, min(127, c));
 }
 
-// Eight bf16 values over s as int8 codes (element e in byte e); inv is 1 / s rounded, `tiny` asks for the
-// exact path throughout.
-__device__ __forceinline__ uint2 quantise8_i8(const uint4 w, float s, float inv, bool tiny)
+// Eight bf16 values over s as int8 codes (element e in byte e); inv is 1 / s rounded.  `far` takes the largest
+// distance of a quotient from its integer: x * inv differs from x / s by at most 127.5 * 2^-24 < 2^-17, so
+// codes hold unless it passes 0.5 - 2^-16 (then see exact8_i8).
+__device__ __forceinline__ uint2 quantise8_i8(const uint4 w, float inv, float &far)
 {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-    int c[8];
-    float far = 0.f;  // the largest distance of a quotient from its integer
+    uint32_t c[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float q = x[e] * inv, r = q + kRound;
-        far = fmaxf(far, fabsf(q - (r - kRound)));
-        c[e] = __float_as_int(r);  // its low byte is the code
-    }
-    // q is off by at most 127.5 * 2^-23 < 2^-16
-    if (tiny || far > 0.5f - 0x1p-15f) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = exact_code(x[e], 0.f, s);
+        const float x = __uint_as_float(e & 1 ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16);
+        const float r = __fmaf_rn(x, inv, kRound);  // its low byte is the code
+        far = fmaxf(far, fabsf(__fmaf_rn(x, inv, kRound - r)));
+        c[e] = __float_as_uint(r);
     }
     auto pack = [&](int i) {
-        return __byte_perm(__byte_perm(uint32_t(c[i]), uint32_t(c[i + 1]), 0x0040),
-                           __byte_perm(uint32_t(c[i + 2]), uint32_t(c[i + 3]), 0x0040), 0x5410);
+        return __byte_perm(__byte_perm(c[i], c[i + 1], 0x0040), __byte_perm(c[i + 2], c[i + 3], 0x0040), 0x5410);
     };
     return make_uint2(pack(0), pack(4));
 }
 
-// The earlier rows' eight codes from scale s0 to scale s.
-__device__ __forceinline__ uint2 requantise8_i8(uint2 w, float s0, float s)
+// The same by exact_code (a quotient next to a tie, or a scale too small for 1 / s): rare, kept out of line.
+__device__ __noinline__ uint2 exact8_i8(const uint4 w, float s)
 {
-    uint32_t out[2] = {0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float c = float(int(int8_t(((e < 4 ? w.x : w.y) >> (8 * (e & 3))) & 0xffu)));
-        const float hi = __fmul_rn(c, s0), lo = __fmaf_rn(c, s0, -hi);
-        out[e >> 2] |= (uint32_t(exact_code(hi, lo, s)) & 0xffu) << (8 * (e & 3));
+    uint32_t u[4] = {w.x, w.y, w.z, w.w}, out[2] = {0u, 0u};
+#pragma unroll 1
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = uint32_t(exact_code(__uint_as_float(u[0] << 16), 0.f, s)) & 0xffu;
+        const uint32_t hi = uint32_t(exact_code(__uint_as_float(u[0] & 0xffff0000u), 0.f, s)) & 0xffu;
+        out[0] = (out[0] >> 16) | (out[1] << 16);
+        out[1] = (out[1] >> 16) | ((lo | hi << 8) << 16);
+        u[0] = u[1];
+        u[1] = u[2];
+        u[2] = u[3];
     }
     return make_uint2(out[0], out[1]);
+}
+
+// The earlier rows' eight codes from scale s0 to scale s.
+__device__ __noinline__ uint2 requantise8_i8(uint2 w, float s0, float s)
+{
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+        const float c = float(int(int8_t(w.x & 0xffu)));
+        const float hi = __fmul_rn(c, s0), lo = __fmaf_rn(c, s0, -hi);
+        w.x = (w.x >> 8) | (w.y << 24);
+        w.y = (w.y >> 8) | (uint32_t(exact_code(hi, lo, s)) << 24);
+    }
+    return w;
 }
 
 // One CTA per slot of the block list; its warps take the (kv head, K or V) pairs of the slot's scale block.
@@ -105,7 +112,7 @@ __device__ __forceinline__ uint2 requantise8_i8(uint2 w, float s0, float s)
 // + 1 blocks that n rows can reach, so a slot finds its sequence by a search over the offsets and no prefix
 // over blocks is needed.
 template <int D>
-__global__ void __launch_bounds__(512) kv_store_i8_kernel(const StoreI8Params p)
+__global__ void __launch_bounds__(kStoreThreads, 3) kv_store_i8_kernel(const StoreI8Params p)
 {
     constexpr int LR = D / 8;        // lanes per row (16 bytes of bf16 each)
     constexpr int RPL = 32 / LR;     // rows per load of the warp
@@ -168,27 +175,33 @@ __global__ void __launch_bounds__(512) kv_store_i8_kernel(const StoreI8Params p)
         int8_t *codes = (which ? p.v_cache : p.k_cache) + (crow * p.Hkv + h) * D + col;
         float *sp = p.scales + ((crow / kSB) * p.Hkv + h) * 2 + which;
         const float s0 = first > 0 ? *sp : 0.f;
-        uint4 in[NV];
-        uint32_t mx = 0u;
+        // the block's largest magnitude; two bf16 a lane-word, compared as such (a NaN wins, infinities are seen)
+        __nv_bfloat162 top = __float2bfloat162_rn(0.f);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int r = j * RPL + row;
-            in[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (r >= first && r < last) in[j] = __ldg(reinterpret_cast<const uint4 *>(x + (src0 + r) * stride));
+        for (int j0 = 0; j0 < NV; j0 += 4) {  // four loads in flight: 42 registers a thread, three CTAs an SM
+            uint4 in[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = (j0 + j) * RPL + row;
+                in[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (r >= first && r < last) in[j] = __ldg(reinterpret_cast<const uint4 *>(x + (src0 + r) * stride));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t u[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&u[e])));
+            }
         }
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const uint32_t u[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx = max(mx, max(u[e] & 0x7fffu, (u[e] >> 16) & 0x7fffu));
-        }
-        mx = __reduce_max_sync(kFull, mx);
+        const uint32_t tb = *reinterpret_cast<const uint32_t *>(&top);
+        const uint32_t mx = __reduce_max_sync(kFull, max(tb & 0x7fffu, (tb >> 16) & 0x7fffu));
         // an infinity or NaN makes the block's scale NaN (and a NaN scale stays until the block starts anew)
         float s = mx >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __fmul_rn(__uint_as_float(mx << 16), 1.0f / 127.0f);
         if (first > 0) s = s0 >= s ? s0 : (s0 < s ? s : __uint_as_float(0x7fc00000u));
         const bool fine = s > 0.f;  // not zero, not NaN
-        const float inv = fine ? __fdiv_rn(1.0f, s) : 0.f;
         const bool tiny = fine && s < 0x1p-100f;
+        const float inv = fine && !tiny ? __fdiv_rn(1.0f, s) : 0.f;
         if (first > 0 && s > s0) {  // the scale grew: the earlier rows move to it
 #pragma unroll 1
             for (int r = row; r < first; r += RPL) {
@@ -196,12 +209,15 @@ __global__ void __launch_bounds__(512) kv_store_i8_kernel(const StoreI8Params p)
                 *at = requantise8_i8(*at, s0, s);
             }
         }
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int r = j * RPL + row;
-            if (r >= first && r < last)
-                *reinterpret_cast<uint2 *>(codes + int64_t(r) * p.Hkv * D) =
-                    fine ? quantise8_i8(in[j], s, inv, tiny) : make_uint2(0u, 0u);
+        // the rows once more, from L1: holding them in registers would halve the warps an SM has in flight
+#pragma unroll 2
+        for (int r = first + ((row - first) & (RPL - 1)); r < last; r += RPL) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(x + (src0 + r) * stride));
+            float far = tiny ? 1.0f : 0.f;
+            uint2 q = quantise8_i8(w, inv, far);
+            if (far > 0.5f - 0x1p-16f) q = exact8_i8(w, s);
+            if (!fine) q = make_uint2(0u, 0u);
+            *reinterpret_cast<uint2 *>(codes + int64_t(r) * p.Hkv * D) = q;
         }
         __syncwarp();  // every lane has read the old scale
         if (lane == 0) *sp = s;
