@@ -5,8 +5,8 @@
 //     s' = a * fl(1 / 127)         if the call writes the block's first row, else max(s, a * fl(1 / 127));
 //     code(x) = x / s' rounded to nearest even, for the new rows;
 //     code'   = code * s / s' rounded to nearest even, for the earlier rows, where s' > s.
-//   Every quotient is rounded once, as if it were exact: an approximate quotient decides where it lies
-//   clearly between two ties, the sign of an exact fused residual where it does not (see exact_code).
+//   Every quotient is rounded once, as if it were exact: an approximate quotient gives the integer, or next to
+//   a tie its neighbour, and an exact fused residual tells (see quantise8_i8 and exact_code).
 // pkv_copy_blocks_i8: block dst of the two code arrays and of the scales becomes a copy of block src.
 //
 // Both are memory-bound.  The store gives one warp a (scale block, kv head, K or V): 16 rows of D values are
@@ -21,7 +21,7 @@
 namespace pkv {
 
 constexpr int kSB = PKV_I8_BLOCK;  // tokens a scale block holds
-constexpr int kStoreThreads = 512;
+constexpr int kStoreThreads = 256;
 constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds a small float to an integer, ties to even
 
 struct StoreI8Params {
@@ -36,18 +36,12 @@ struct StoreI8Params {
 };
 
 // (hi + lo) / s rounded to the nearest integer, ties to even, exactly (|lo| <= half an ulp of hi, s > 0, the
-// quotient at most 127.5): t is the rounding of an approximate quotient q, which is wrong only next to a tie
-// b = t +- 1/2, and there the sign of hi + lo - b s decides: b has 8 bits and s 24, so hi - b s is exact
-// where it is small.
-__device__ __forceinline__ int exact_code(float hi, float lo, float s)
+// quotient at most 127.5): t is the rounding of an approximate quotient q (off by less than 2^-16), which is
+// wrong only next to a tie b = t +- 1/2, and there the sign of hi + lo - b s decides: b has 8 bits and s 24, so
+// hi - b s is exact where it is small.
+__device__ __forceinline__ int exact_code(float hi, float lo, float s, float inv)
 {
-    if (s < 0x1p-100f) {  // keep 1 / s and the residual in range
-        hi *= 0x1p+110f;
-        lo *= 0x1p+110f;
-        s *= 0x1p+110f;
-    }
-    const float q = __fdiv_rn(hi, s);
-    const float t = rintf(q);
+    const float q = hi * inv, t = rintf(q);
     const float half = q >= t ? 0.5f : -0.5f;
     const float e = __fadd_rn(__fmaf_rn(-(t + half), s, hi), lo);
     const int ti = int(t), away = half > 0.f ? ti + 1 : ti - 1;
@@ -56,19 +50,30 @@ __device__ __forceinline__ int exact_code(float hi, float lo, float s)
     return max(-127, min(127, c));
 }
 
-// Eight bf16 values over s as int8 codes (element e in byte e); inv is 1 / s rounded.  `far` takes the largest
-// distance of a quotient from its integer: x * inv differs from x / s by at most 127.5 * 2^-24 < 2^-17, so
-// codes hold unless it passes 0.5 - 2^-16 (then see exact8_i8).
-__device__ __forceinline__ uint2 quantise8_i8(const uint4 w, float inv, float &far)
+// Eight bf16 values over s as int8 codes (element e in byte e), exactly: t = x * inv rounded (inv is 1 / s
+// rounded) is the code or, next to a tie, its neighbour, and the residual x - t s, exact in fp32, tells: the code
+// is t where its magnitude stays below s / 2.  (With bf16 rows near-ties are no rarity: 127 x / a has few bits
+// for many x and a.  Checking the residual leaves the corrections to the few that rounded the wrong way.)
+__device__ __forceinline__ uint2 quantise8_i8(const uint4 w, float s, float inv)
 {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
     uint32_t c[8];
+    float far = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float x = __uint_as_float(e & 1 ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16);
         const float r = __fmaf_rn(x, inv, kRound);  // its low byte is the code
-        far = fmaxf(far, fabsf(__fmaf_rn(x, inv, kRound - r)));
+        far = fmaxf(far, fabsf(__fmaf_rn(kRound - r, s, x)));
         c[e] = __float_as_uint(r);
+    }
+    const float half = 0.5f * s;
+    if (far >= half) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float x = __uint_as_float(e & 1 ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16);
+            const float d = __fmaf_rn(kRound - __uint_as_float(c[e]), s, x);
+            if (fabsf(d) > half || (fabsf(d) == half && (c[e] & 1u))) c[e] += d > 0.f ? 1u : ~0u;
+        }
     }
     auto pack = [&](int i) {
         return __byte_perm(__byte_perm(c[i], c[i + 1], 0x0040), __byte_perm(c[i + 2], c[i + 3], 0x0040), 0x5410);
@@ -76,34 +81,30 @@ __device__ __forceinline__ uint2 quantise8_i8(const uint4 w, float inv, float &f
     return make_uint2(pack(0), pack(4));
 }
 
-// The same by exact_code (a quotient next to a tie, or a scale too small for 1 / s): rare, kept out of line.
-__device__ __noinline__ uint2 exact8_i8(const uint4 w, float s)
-{
-    uint32_t u[4] = {w.x, w.y, w.z, w.w}, out[2] = {0u, 0u};
-#pragma unroll 1
-    for (int e = 0; e < 4; ++e) {
-        const uint32_t lo = uint32_t(exact_code(__uint_as_float(u[0] << 16), 0.f, s)) & 0xffu;
-        const uint32_t hi = uint32_t(exact_code(__uint_as_float(u[0] & 0xffff0000u), 0.f, s)) & 0xffu;
-        out[0] = (out[0] >> 16) | (out[1] << 16);
-        out[1] = (out[1] >> 16) | ((lo | hi << 8) << 16);
-        u[0] = u[1];
-        u[1] = u[2];
-        u[2] = u[3];
-    }
-    return make_uint2(out[0], out[1]);
-}
-
 // The earlier rows' eight codes from scale s0 to scale s.
 __device__ __noinline__ uint2 requantise8_i8(uint2 w, float s0, float s)
 {
+    const float lift = s < 0x1p-100f ? 0x1p+110f : 1.0f;  // keeps 1 / s and the residuals in range
+    s *= lift;
+    const float inv = __fdiv_rn(1.0f, s);
 #pragma unroll 1
     for (int e = 0; e < 8; ++e) {
         const float c = float(int(int8_t(w.x & 0xffu)));
         const float hi = __fmul_rn(c, s0), lo = __fmaf_rn(c, s0, -hi);
         w.x = (w.x >> 8) | (w.y << 24);
-        w.y = (w.y >> 8) | (uint32_t(exact_code(hi, lo, s)) << 24);
+        w.y = (w.y >> 8) | (uint32_t(exact_code(hi * lift, lo * lift, s, inv)) << 24);
     }
     return w;
+}
+
+// Eight bf16 values times 2^110 (a block of tiny values, see kv_store_i8_kernel).
+__device__ __forceinline__ uint4 lifted(uint4 w)
+{
+    uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        u[i] = pack_bf16x2(__uint_as_float(u[i] << 16) * 0x1p+110f, __uint_as_float(u[i] & 0xffff0000u) * 0x1p+110f);
+    return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
 // One CTA per slot of the block list; its warps take the (kv head, K or V) pairs of the slot's scale block.
@@ -112,7 +113,7 @@ __device__ __noinline__ uint2 requantise8_i8(uint2 w, float s0, float s)
 // + 1 blocks that n rows can reach, so a slot finds its sequence by a search over the offsets and no prefix
 // over blocks is needed.
 template <int D>
-__global__ void __launch_bounds__(kStoreThreads, 3) kv_store_i8_kernel(const StoreI8Params p)
+__global__ void __launch_bounds__(kStoreThreads, 6) kv_store_i8_kernel(const StoreI8Params p)
 {
     constexpr int LR = D / 8;        // lanes per row (16 bytes of bf16 each)
     constexpr int RPL = 32 / LR;     // rows per load of the warp
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(kStoreThreads, 3) kv_store_i8_kernel(const Sto
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-    int32_t b, i, r0, n;
+    int32_t b, i, r0, n, L;
     if (p.cu_seqlens) {
         // the last b with cu[b] / 16 + 2 b <= slot, by 32-way steps
         int lo = 0, width = p.num_seqs;
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(kStoreThreads, 3) kv_store_i8_kernel(const Sto
         }
         b = lo;
         r0 = __ldg(p.cu_seqlens + b);
+        L = __ldg(p.context_lens + b);
         const int32_t r1 = __ldg(p.cu_seqlens + b + 1);
         i = int32_t(blockIdx.x) - ((max(0, r0) >> 4) + 2 * b);
         n = r1 - r0;
@@ -148,8 +150,8 @@ __global__ void __launch_bounds__(kStoreThreads, 3) kv_store_i8_kernel(const Sto
         i = int32_t(blockIdx.x) - b * p.slots_per_seq;
         n = p.new_per_seq;
         r0 = b * n;
+        L = __ldg(p.context_lens + b);
     }
-    const int32_t L = __ldg(p.context_lens + b);
     if (n == 0 || i < 0 || (L == 0 && !p.cu_seqlens)) return;  // no rows, or a padding sequence
     if (L < n || L > int64_t(p.max_blocks) * p.block_size) {
         if (threadIdx.x == 0 && i == 0) flag_error(p.err, PKV_ERR_CONTEXT_RANGE);
@@ -160,13 +162,13 @@ __global__ void __launch_bounds__(kStoreThreads, 3) kv_store_i8_kernel(const Sto
     if (base >= L) return;
     const int32_t first = max(p0 - base, 0), last = min(L - base, kSB);  // new rows of the block
     const int32_t phys = __ldg(p.block_tables + int64_t(b) * p.max_blocks + (base >> p.log2_bs));
+    const int row = lane / LR, col = (lane - row * LR) * 8;
+    const int64_t src0 = int64_t(r0) + (base - p0);  // input row of the block's row 0 (may lie before the input)
     if (phys < 0 || phys >= p.num_blocks) {
         if (threadIdx.x == 0) flag_error(p.err, PKV_ERR_BLOCK_RANGE);
         return;
     }
     const int64_t crow = int64_t(phys) * p.block_size + (base & (p.block_size - 1));  // cache row of the block
-    const int row = lane / LR, col = (lane - row * LR) * 8;
-    const int64_t src0 = int64_t(r0) + (base - p0);  // input row of the block's row 0 (may lie before the input)
 
     for (int w = warp; w < 2 * p.Hkv; w += nwarps) {
         const int which = w & 1, h = w >> 1;
@@ -200,8 +202,8 @@ __global__ void __launch_bounds__(kStoreThreads, 3) kv_store_i8_kernel(const Sto
         float s = mx >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __fmul_rn(__uint_as_float(mx << 16), 1.0f / 127.0f);
         if (first > 0) s = s0 >= s ? s0 : (s0 < s ? s : __uint_as_float(0x7fc00000u));
         const bool fine = s > 0.f;  // not zero, not NaN
-        const bool tiny = fine && s < 0x1p-100f;
-        const float inv = fine && !tiny ? __fdiv_rn(1.0f, s) : 0.f;
+        const bool tiny = fine && s < 0x1p-100f;  // lifted by 2^110: 1 / s and the residuals stay in range
+        const float sq = !fine ? 1.0f : tiny ? s * 0x1p+110f : s, inv = __fdiv_rn(1.0f, sq);
         if (first > 0 && s > s0) {  // the scale grew: the earlier rows move to it
 #pragma unroll 1
             for (int r = row; r < first; r += RPL) {
@@ -210,14 +212,14 @@ __global__ void __launch_bounds__(kStoreThreads, 3) kv_store_i8_kernel(const Sto
             }
         }
         // the rows once more, from L1: holding them in registers would halve the warps an SM has in flight
+        const int rf = first + ((row - first) & (RPL - 1));
+        const uint16_t *xr = x + (src0 + rf) * stride;
+        int8_t *cr = codes + int64_t(rf) * p.Hkv * D;
 #pragma unroll 2
-        for (int r = first + ((row - first) & (RPL - 1)); r < last; r += RPL) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(x + (src0 + r) * stride));
-            float far = tiny ? 1.0f : 0.f;
-            uint2 q = quantise8_i8(w, inv, far);
-            if (far > 0.5f - 0x1p-16f) q = exact8_i8(w, s);
-            if (!fine) q = make_uint2(0u, 0u);
-            *reinterpret_cast<uint2 *>(codes + int64_t(r) * p.Hkv * D) = q;
+        for (int r = rf; r < last; r += RPL, xr += RPL * stride, cr += int64_t(RPL) * p.Hkv * D) {
+            uint4 w = __ldg(reinterpret_cast<const uint4 *>(xr));
+            if (tiny) w = lifted(w);
+            *reinterpret_cast<uint2 *>(cr) = fine ? quantise8_i8(w, sq, inv) : make_uint2(0u, 0u);
         }
         __syncwarp();  // every lane has read the old scale
         if (lane == 0) *sp = s;
@@ -321,7 +323,7 @@ extern "C" pkv_status pkv_kv_store_i8(const uint16_t *k, const uint16_t *v, int6
     const int64_t grid = new_per_seq > 0 ? int64_t(num_seqs) * p.slots_per_seq
                                          : int64_t(num_tokens) / kSB + 2 * int64_t(num_seqs);
     if (grid > INT32_MAX) return PKV_EBOUNDS;
-    const int threads = 32 * std::min(2 * num_kv_heads, 16);
+    const int threads = std::min(64 * num_kv_heads, kStoreThreads);
     const cudaError_t e = launch_pdl(head_dim == 64 ? kv_store_i8_kernel<64> : kv_store_i8_kernel<128>,
                                      dim3(unsigned(grid)), dim3(threads), 0, reinterpret_cast<cudaStream_t>(stream), p);
     if (e != cudaSuccess) {
