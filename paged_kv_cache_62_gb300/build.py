@@ -3,6 +3,8 @@
 Every translation unit is compiled for sm_103a only, in parallel, then linked
 into one shared library next to this file.  The CUDA runtime is linked
 statically, so the library needs nothing beyond the NVIDIA driver at run time.
+``_pkv_torch.so``, the native argument checks of the int8 and rotary bindings,
+is compiled beside it against the installed torch.
 """
 from __future__ import annotations
 
@@ -11,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libpkv.so")
+TORCH_PATH = os.path.join(HERE, "_pkv_torch.so")
 SOURCES = ["pkv_api.cu", "pkv_store.cu", "pkv_decode.cu", "pkv_decode_fp8.cu", "pkv_decode_qs.cu", "pkv_decode_wide.cu",
            "pkv_decode_tc5.cu", "pkv_decode_i8.cu", "pkv_decode_i8_wide.cu", "pkv_decode_i8_tc5.cu", "pkv_store_i8.cu",
            "pkv_rope.cu", "pkv_noalloc.cu", "pkv_alloc.cpp"]
@@ -43,6 +47,24 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def torch_commands(tmp: str) -> tuple[list[str], list[str]]:
+    """Compile and link commands of _pkv_torch.so (found at run time: torch's own libraries, already loaded, and
+    libpkv.so beside it)."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    obj = os.path.join(BUILD_DIR, "pkv_torch.o")
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                *(x for i in inc for x in ("-isystem", i)), "-c", os.path.join(CSRC, "pkv_torch.cpp"), "-o", obj]
+    libs = os.path.join(root, "lib")
+    link = ["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-lpkv", "-L", libs, "-ltorch_python", "-ltorch_cpu",
+            "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    return compile_, link
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     include = os.path.join(ROOT, "include")
@@ -58,16 +80,21 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append(cmd)
 
+    tsrc, tobj = os.path.join(CSRC, "pkv_torch.cpp"), os.path.join(BUILD_DIR, "pkv_torch.o")
+    ttmp = TORCH_PATH + f".tmp{os.getpid()}"
+    if force or _stale(tobj, [tsrc, os.path.join(include, "pkv.h")]):
+        jobs.insert(0, torch_commands(ttmp)[0])
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         for cmd, r in ex.map(run, jobs):
             if verbose or ptxas_info or r.returncode:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode:
-                raise RuntimeError("nvcc failed: " + " ".join(cmd))
+                raise RuntimeError("compilation failed: " + " ".join(cmd))
     if force or jobs or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + f".tmp{os.getpid()}"
         cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
@@ -76,6 +103,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed: " + " ".join(cmd))
         os.replace(tmp, LIB_PATH)
+    if force or _stale(TORCH_PATH, [tobj, LIB_PATH]):
+        cmd = torch_commands(ttmp)[1]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("link failed: " + " ".join(cmd))
+        os.replace(ttmp, TORCH_PATH)
     return LIB_PATH
 
 

@@ -488,49 +488,21 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         int(num_workers), _opt(err_word), _stream(stream)), "pkv_paged_attention")
 
 
-def _arg(t: torch.Tensor, dtype, name: str, ndim: int, dev: int) -> int:
-    """Pointer of a dense tensor on device `dev`; the checks of _dev in one expression (a call's host time is spent
-    here)."""
-    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous() or t.dim() != ndim:
-        _dev(t, dtype, name, ndim)
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
-    return t.data_ptr()
+_torch_native = None
 
 
-def _rows(t: torch.Tensor, name: str, dev: int) -> tuple[int, int]:
-    """Pointer and row stride of a bf16 [T, H, D] tensor whose rows ([H, D]) are dense and may lie apart (a part of
-    a wider projection's rows)."""
-    if t.get_device() != dev or t.dtype is not torch.bfloat16 or t.dim() != 3:
-        _dev(t.contiguous(), torch.bfloat16, name, 3)
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
-    T, H, D = t.shape
-    st, sh, sd = t.stride()
-    if (sd != 1 and D > 1) or (sh != D and H > 1):
-        raise ValueError(f"{name}: the heads of a row must be dense")
-    return t.data_ptr(), (st if T > 1 else H * D)
-
-
-def _device(t: torch.Tensor, name: str) -> int:
-    """The device of a call's tensors: the current one, where the library launches."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
-    return dev
-
-
-def _err(err_word, dev: int) -> int | None:
-    return None if err_word is None else _arg(err_word, torch.int32, "err_word", err_word.dim(), dev)
-
-
-def _i8_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor, dev: int, what: str):
-    """Pointers and shape of an int8 cache; scales [NB, bs / 16, Hkv, 2]."""
-    kp, vp = _arg(k_cache, torch.int8, "k_cache", 4, dev), _arg(v_cache, torch.int8, "v_cache", 4, dev)
-    NB, bs, Hkv, D = k_cache.shape
-    if v_cache.shape != k_cache.shape or scales.shape != (NB, bs // I8_BLOCK, Hkv, 2):
-        raise ValueError(f"{what}: shape mismatch")
-    return kp, vp, _arg(scales, torch.float32, "scales", 4, dev), NB, bs, Hkv, D
+def _native():
+    """The native argument checks of the calls below (built with the library); raises if they are missing."""
+    global _torch_native
+    if _torch_native is None:
+        load()
+        try:
+            from . import _pkv_torch
+        except ImportError as e:
+            raise RuntimeError("_pkv_torch.so is missing or does not load: build it with "
+                               "`python -m paged_kv_cache_62_gb300.build`") from e
+        _torch_native = _pkv_torch
+    return _torch_native
 
 
 def alloc_i8_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_dim: int, device=None):
@@ -548,19 +520,10 @@ def kv_store_i8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache
     """Quantise each sequence's new rows (cu_seqlens[b]..cu_seqlens[b+1], or b*n..b*n+n-1 with new_per_seq = n) and
     store them at its last positions of an int8 cache with a scale per 16 tokens and kv head.  k and v may be
     parts of wider rows."""
-    dev = _device(k, "k")
-    (kp, ks), (vp, vs) = _rows(k, "k", dev), _rows(v, "v", dev)
-    kc, vc, sc, NB, bs, Hkv, D = _i8_cache(k_cache, v_cache, scales, dev, "kv_store_i8")
-    T, Hk, Dk = k.shape
-    B, mb = block_tables.shape
-    if v.shape != k.shape or Hk != Hkv or Dk != D or context_lens.numel() != B \
-            or (cu_seqlens is None and new_per_seq <= 0) or (cu_seqlens is not None and cu_seqlens.numel() != B + 1):
-        raise ValueError("kv_store_i8: shape mismatch")
-    _check(load().pkv_kv_store_i8(
-        kp, vp, ks, vs, _arg(block_tables, torch.int32, "block_tables", 2, dev), mb,
-        None if cu_seqlens is None else _arg(cu_seqlens, torch.int32, "cu_seqlens", 1, dev),
-        _arg(context_lens, torch.int32, "context_lens", 1, dev), B, T, int(new_per_seq), kc, vc, sc, NB, bs, Hkv, D,
-        _err(err_word, dev), _stream(stream)), "pkv_kv_store_i8")
+    st = _native().kv_store_i8(k, v, k_cache, v_cache, scales, block_tables, context_lens, cu_seqlens, new_per_seq,
+                               err_word, stream)
+    if st != OK:
+        raise PkvError(st, "pkv_kv_store_i8")
 
 
 def paged_decode_i8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor,
@@ -568,19 +531,10 @@ def paged_decode_i8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                     workspace: torch.Tensor, max_context_len: int | None = None, num_workers: int = 0,
                     err_word: torch.Tensor | None = None, stream=None) -> None:
     """paged_decode over an int8 cache (int8 [NB, bs, Hkv, D]) with scales [NB, bs / 16, Hkv, 2]."""
-    dev = _device(q, "q")
-    kc, vc, sc, NB, bs, Hkv, D = _i8_cache(k_cache, v_cache, scales, dev, "paged_decode_i8")
-    B, Hq, Dq = q.shape
-    Bt, mb = block_tables.shape
-    if Dq != D or Bt != B or context_lens.numel() != B or out.shape != q.shape:
-        raise ValueError("paged_decode_i8: shape mismatch")
-    _check(load().pkv_paged_decode_i8(
-        _arg(q, torch.bfloat16, "q", 3, dev), kc, vc, sc, _arg(block_tables, torch.int32, "block_tables", 2, dev), mb,
-        _arg(context_lens, torch.int32, "context_lens", 1, dev), B, Hq, Hkv, D, bs, NB,
-        mb * bs if max_context_len is None else int(max_context_len), float(scale),
-        _arg(out, torch.bfloat16, "out", 3, dev),
-        _arg(workspace, torch.uint8, "workspace", 1, dev), workspace.numel(), int(num_workers), _err(err_word, dev),
-        _stream(stream)), "pkv_paged_decode_i8")
+    st = _native().paged_decode_i8(q, k_cache, v_cache, scales, block_tables, context_lens, scale, out, workspace,
+                                   max_context_len, num_workers, err_word, stream)
+    if st != OK:
+        raise PkvError(st, "pkv_paged_decode_i8")
 
 
 def paged_attention_i8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor,
@@ -590,50 +544,18 @@ def paged_attention_i8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
                        new_per_seq: int = 0) -> None:
     """paged_attention over an int8 cache (int8 [NB, bs, Hkv, D]) with scales [NB, bs / 16, Hkv, 2]; workspace from
     alloc_attention_workspace."""
-    dev = _device(q, "q")
-    kc, vc, sc, NB, bs, Hkv, D = _i8_cache(k_cache, v_cache, scales, dev, "paged_attention_i8")
-    T, Hq, Dq = q.shape
-    B, mb = block_tables.shape
-    if Dq != D or context_lens.numel() != B or out.shape != q.shape or (cu_seqlens_q is None and new_per_seq <= 0) \
-            or (cu_seqlens_q is not None and cu_seqlens_q.numel() != B + 1):
-        raise ValueError("paged_attention_i8: shape mismatch")
-    _check(load().pkv_paged_attention_i8(
-        _arg(q, torch.bfloat16, "q", 3, dev), kc, vc, sc, _arg(block_tables, torch.int32, "block_tables", 2, dev), mb,
-        None if cu_seqlens_q is None else _arg(cu_seqlens_q, torch.int32, "cu_seqlens_q", 1, dev),
-        _arg(context_lens, torch.int32, "context_lens", 1, dev), B, T, Hq, Hkv, D, bs, NB,
-        mb * bs if max_context_len is None else int(max_context_len), float(scale),
-        _arg(out, torch.bfloat16, "out", 3, dev),
-        int(new_per_seq), _arg(workspace, torch.uint8, "workspace", 1, dev), workspace.numel(), int(num_workers),
-        _err(err_word, dev), _stream(stream)), "pkv_paged_attention_i8")
+    st = _native().paged_attention_i8(q, k_cache, v_cache, scales, block_tables, cu_seqlens_q, context_lens, scale, out,
+                                      workspace, max_context_len, num_workers, err_word, stream, new_per_seq)
+    if st != OK:
+        raise PkvError(st, "pkv_paged_attention_i8")
 
 
 def copy_blocks_i8(k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor, pairs: torch.Tensor,
                    err_word: torch.Tensor | None = None, stream=None) -> None:
     """copy_blocks for an int8 cache: codes and scales of block dst become those of block src."""
-    dev = _device(k_cache, "k_cache")
-    kc, vc, sc, NB, bs, Hkv, D = _i8_cache(k_cache, v_cache, scales, dev, "copy_blocks_i8")
-    n, two = pairs.shape
-    if two != 2:
-        raise ValueError("copy_blocks_i8: shape mismatch")
-    _check(load().pkv_copy_blocks_i8(kc, vc, sc, _arg(pairs, torch.int32, "pairs", 2, dev), n, NB, bs, Hkv, D,
-                                     _err(err_word, dev), _stream(stream)), "pkv_copy_blocks_i8")
-
-
-def _rope_args(q, k, positions, inv_freq, freq_axis, q_out, dev, what):
-    """The arguments the rotary calls share: rows of q and k, positions and frequencies, sizes, rows of q_out."""
-    (qp, qs), (kp, ks), (op, os_) = _rows(q, "q", dev), _rows(k, "k", dev), _rows(q_out, "q_out", dev)
-    T, Hq, D = q.shape
-    Tk, Hkv, Dk = k.shape
-    pos = positions if positions.dim() == 2 else positions.view(1, -1)
-    axes, Tp = pos.shape
-    half = inv_freq.numel()
-    if Tk != T or Dk != D or q_out.shape != q.shape or Tp != T \
-            or (freq_axis is not None and freq_axis.numel() != half):
-        raise ValueError(f"{what}: shape mismatch")
-    return (qp, qs, kp, ks), (_arg(pos, torch.int32, "positions", 2, dev), axes,
-                              _arg(inv_freq, torch.float32, "inv_freq", 1, dev),
-                              None if freq_axis is None else _arg(freq_axis, torch.int32, "freq_axis", 1, dev)), \
-        (T, Hq, Hkv, D, 2 * half), (op, os_)
+    st = _native().copy_blocks_i8(k_cache, v_cache, scales, pairs, err_word, stream)
+    if st != OK:
+        raise PkvError(st, "pkv_copy_blocks_i8")
 
 
 def rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, q_out: torch.Tensor,
@@ -642,12 +564,9 @@ def rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: to
     """Rotary positions for q and k (bf16 [T, H, D], parts of wider rows allowed): positions int32 [T] or
     [axes, T], inv_freq float32 [rot / 2], freq_axis int32 [rot / 2] (the axis each frequency follows).  q_out /
     k_out may be q / k."""
-    dev = _device(q, "q")
-    rows, pos, sizes, out = _rope_args(q, k, positions, inv_freq, freq_axis, q_out, dev, "rope")
-    if k_out.shape != k.shape:
-        raise ValueError("rope: shape mismatch")
-    _check(load().pkv_rope(*rows, *pos, *sizes, int(interleaved), *out, *_rows(k_out, "k_out", dev),
-                           _err(err_word, dev), _stream(stream)), "pkv_rope")
+    st = _native().rope(q, k, positions, inv_freq, q_out, k_out, freq_axis, interleaved, err_word, stream)
+    if st != OK:
+        raise PkvError(st, "pkv_rope")
 
 
 def rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
@@ -656,14 +575,7 @@ def rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: tor
                err_word: torch.Tensor | None = None, stream=None) -> None:
     """rope and kv_store in one launch: q turned into q_out, turned k and v stored at slot_mapping of bf16 caches
     (-1: not stored)."""
-    dev = _device(q, "q")
-    rows, pos, sizes, out = _rope_args(q, k, positions, inv_freq, freq_axis, q_out, dev, "rope_store")
-    NB, bs, Hkv, D = k_cache.shape
-    if v.shape != k.shape or sizes[2] != Hkv or sizes[3] != D or v_cache.shape != k_cache.shape \
-            or slot_mapping.numel() != sizes[0]:
-        raise ValueError("rope_store: shape mismatch")
-    _check(load().pkv_rope_store(
-        *rows, *_rows(v, "v", dev), *pos, _arg(slot_mapping, torch.int32, "slot_mapping", 1, dev), *sizes,
-        int(interleaved), *out, _arg(k_cache, torch.bfloat16, "k_cache", 4, dev),
-        _arg(v_cache, torch.bfloat16, "v_cache", 4, dev), NB, bs, _err(err_word, dev), _stream(stream)),
-        "pkv_rope_store")
+    st = _native().rope_store(q, k, v, positions, inv_freq, slot_mapping, q_out, k_cache, v_cache, freq_axis, interleaved,
+                              err_word, stream)
+    if st != OK:
+        raise PkvError(st, "pkv_rope_store")
