@@ -29,7 +29,8 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
                               int32_t num_blocks, int32_t max_context_len, float scale, uint16_t *out,
                               void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word,
                               pkv_stream_t stream, const uint16_t *k_new = nullptr, const uint16_t *v_new = nullptr,
-                              int32_t *slot_out = nullptr, const float *scales = nullptr)
+                              int32_t *slot_out = nullptr, const float *scales = nullptr,
+                              const int32_t *row0 = nullptr)
 {
     const bool fp8 = ct != kBf16, i8 = ct == kI8;  // fp8: one byte per cached element
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
@@ -53,7 +54,7 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
     // unit counts (and positions in the unit list) are kept in 32 bits
     const int64_t max_units = int64_t(num_kv_heads) * num_seqs * ((len_limit + 7) / 8);
     if (max_units > INT32_MAX) return PKV_EBOUNDS;
-    if (qs && (ct == kE4m3 || !row_cnt)) return PKV_EINVAL;  // query-split entries are chunks of bf16 or int8 calls
+    if (qs && (ct == kE4m3 || !row_cnt || (i8 && !row0))) return PKV_EINVAL;  // query-split entries are chunks of bf16 or int8 calls
     if ((k_new || v_new) && (qs || ct == kI8 || qn != 1 || row_seq || !k_new || !v_new || !aligned16(k_new) ||
                              !aligned16(v_new)))
         return PKV_EINVAL;  // the fused store goes with a decode
@@ -105,6 +106,7 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
     p.qn = qn;
     p.gq = gq;
     p.row_cnt = row_cnt;
+    p.row0 = row0;
     p.k_new = k_new;
     p.v_new = v_new;
     p.k_cache_w = static_cast<uint8_t *>(const_cast<void *>(k_cache));
@@ -289,6 +291,60 @@ __global__ void expand_rows_kernel(const int32_t *__restrict__ cu_seqlens_q, int
     row_cnt[r] = cnt;
 }
 
+// The same for query-split int8 calls, whose entries are numbered without gaps to speak of: sequence b's chunks
+// are entries cu_seqlens_q[b] / chunk + b on (room for the ceil(n / chunk) chunks of its n rows; entries that are no
+// chunk have row_cnt = 0), num_rows / chunk + num_seqs of them.  One thread per entry and per row: the entry's
+// thread finds its sequence by binary search and writes the entry (row0: the row of its first query), the row's
+// thread checks that the row lies in a consistent sequence and else writes zeros to its output.
+__global__ void expand_entries_kernel(const int32_t *__restrict__ cu_seqlens_q, int32_t new_per_seq,
+                                      const int32_t *__restrict__ context_lens, int32_t num_seqs, int32_t num_rows,
+                                      int32_t num_entries, int32_t chunk, int32_t row_values,
+                                      int32_t *__restrict__ row_seq, int32_t *__restrict__ row_len,
+                                      int32_t *__restrict__ row_cnt, int32_t *__restrict__ row0,
+                                      uint16_t *__restrict__ out, int32_t *err)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int32_t x = blockIdx.x * blockDim.x + threadIdx.x;
+    auto start = [&](int32_t b) { return cu_seqlens_q ? __ldg(cu_seqlens_q + b) : b * new_per_seq; };
+    // the last b whose key is at most v (keys of consistent offsets are non-decreasing)
+    auto find = [&](int32_t v, bool entries) {
+        int32_t lo = 0, hi = num_seqs;
+        while (hi - lo > 1) {
+            const int32_t mid = (lo + hi) >> 1;
+            if ((entries ? max(start(mid), 0) / chunk + mid : start(mid)) <= v)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        return lo;
+    };
+    auto consistent = [&](int32_t b, int32_t r0, int32_t r1) {
+        return start(0) == 0 && r0 >= 0 && r0 <= r1 && r1 <= num_rows && r1 - r0 <= __ldg(context_lens + b);
+    };
+    if (x < num_entries) {
+        const int32_t b = find(x, true), r0 = start(b), r1 = start(b + 1);
+        const int32_t i = x - (max(r0, 0) / chunk + b);
+        int32_t cnt = 0, len = 0;
+        if (i >= 0 && consistent(b, r0, r1) && int64_t(i) * chunk < r1 - r0) {
+            cnt = min(chunk, r1 - r0 - i * chunk);
+            len = __ldg(context_lens + b) - (r1 - r0) + i * chunk + cnt;
+        }
+        row_seq[x] = b;
+        row_len[x] = len;
+        row_cnt[x] = cnt;
+        row0[x] = cnt > 0 ? r0 + i * chunk : 0;
+    }
+    if (x < num_rows) {
+        const int32_t b = find(x, false), r0 = start(b), r1 = start(b + 1);
+        if (!(r0 <= x && x < r1 && consistent(b, r0, r1))) {
+            flag_error(err, PKV_ERR_CONTEXT_RANGE);
+            uint4 *o = reinterpret_cast<uint4 *>(out + int64_t(x) * row_values);
+            for (int32_t k = 0; k < row_values / 8; ++k) o[k] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+}
+
 inline size_t rows_bytes(int32_t num_rows) { return align256(size_t(num_rows) * 4); }
 
 // Queries per warp: as many as keep its qg * G virtual heads within the rows
@@ -320,13 +376,13 @@ extern "C" size_t pkv_paged_attention_workspace_size(int32_t num_rows, int32_t n
     if (base == 0) return 0;
     // decode workspace: same-n calls (entries of n <= qg queries, n * G virtual heads), or one
     // chunk entry per row (qg * G virtual heads a warp, on a regular or a query-split CTA); then the
-    // three row arrays
+    // four row arrays
     const int32_t gq = num_q_heads / num_kv_heads, qg = qs_queries(num_q_heads, num_kv_heads);
     // (int8 calls: 16-row blocks whatever the group)
     size_t dec = std::max(base, ws_layout(num_rows, gq <= 16 ? 16 : gq * qg, num_kv_heads, head_dim, true).total);
     for (int32_t qn = 2; qn <= qg; ++qn)
         dec = std::max(dec, ws_layout(num_rows, gq * qn, num_kv_heads, head_dim).total);
-    return align256(dec) + 3 * rows_bytes(num_rows);
+    return align256(dec) + 4 * rows_bytes(num_rows);
 }
 
 // Shared by the bf16 and the int8 entry points (scales: the latter's).
@@ -343,6 +399,7 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     if (num_seqs == 0 || !context_lens || (new_per_seq == 0 && !cu_seqlens_q)) return PKV_EINVAL;
     if (new_per_seq > 0 && int64_t(num_seqs) * new_per_seq != num_rows) return PKV_EINVAL;
     if (num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0) return PKV_EINVAL;
+    if (ct == kI8 && ((head_dim != 64 && head_dim != 128) || num_q_heads / num_kv_heads > 16)) return PKV_EUNSUPPORTED;
     const size_t need = pkv_paged_attention_workspace_size(num_rows, num_q_heads, num_kv_heads, head_dim);
     if (need == 0) return num_rows > PKV_MAX_SEQS ? PKV_EBOUNDS : PKV_EINVAL;
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return PKV_EWORKSPACE;
@@ -364,10 +421,31 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     const int32_t chunk = !qs ? qg : ct == kI8 ? 128 / (num_q_heads / num_kv_heads)
                                               : entry_queries(num_q_heads, num_kv_heads);
     uint8_t *wsb = static_cast<uint8_t *>(workspace);
-    const size_t dec_bytes = need - 3 * rows_bytes(num_rows);
+    const size_t dec_bytes = need - 4 * rows_bytes(num_rows);
     int32_t *row_seq = reinterpret_cast<int32_t *>(wsb + dec_bytes);
     int32_t *row_len = reinterpret_cast<int32_t *>(wsb + dec_bytes + rows_bytes(num_rows));
     int32_t *row_cnt = reinterpret_cast<int32_t *>(wsb + dec_bytes + 2 * rows_bytes(num_rows));
+    if (ct == kI8 && qs) {
+        const int32_t entries = num_rows / chunk + num_seqs;
+        if (entries > num_rows) return PKV_EBOUNDS;  // (not with more than 2 qg rows a sequence)
+        if (!out || !q || !aligned16(out)) return PKV_EINVAL;
+        int32_t *row0 = reinterpret_cast<int32_t *>(wsb + dec_bytes + 3 * rows_bytes(num_rows));
+        const cudaError_t e = launch_pdl(expand_entries_kernel, dim3((num_rows + 255) / 256), dim3(256), 0,
+                                         reinterpret_cast<cudaStream_t>(stream),
+                                         new_per_seq > 0 ? nullptr : cu_seqlens_q, new_per_seq, context_lens, num_seqs,
+                                         num_rows, entries, chunk, num_q_heads * head_dim, row_seq, row_len, row_cnt,
+                                         row0, out, err_word);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return cuda_fail("expand_entries_kernel launch", e);
+        }
+        const pkv_status st = launch_status("expand_entries_kernel launch");
+        if (st != PKV_OK) return st;
+        return decode_call(ct, true, qg, q, k_cache, v_cache, nullptr, nullptr, row_seq, row_cnt, block_tables,
+                           max_blocks_per_seq, row_len, entries, num_q_heads, num_kv_heads, head_dim, block_size,
+                           num_blocks, max_context_len, scale, out, workspace, dec_bytes, num_workers, err_word, stream,
+                           nullptr, nullptr, nullptr, scales, row0);
+    }
     const cudaError_t e = launch_pdl(expand_rows_kernel, dim3((num_rows + 255) / 256), dim3(256), 0,
                                      reinterpret_cast<cudaStream_t>(stream), new_per_seq > 0 ? nullptr : cu_seqlens_q,
                                      new_per_seq, context_lens, num_seqs, num_rows, chunk, row_seq, row_len,

@@ -117,12 +117,11 @@ constexpr int kTc5VSlots = 3;
 static_assert(kTc5Keys * 128 == int(kTc5SlabBytes), "a stage's K or V slab holds one tile of 128-byte rows");
 // int8 caches: more warps turn each tile's codes into f16 operands (see tc5_convert_warps), one buffer
 // for K and one for V; the ring's stages hold the codes of a K and a V tile.
-constexpr int kTc5ConvertWarps = 2;
-// Head room of their f16 weights (see kI8Head in pkv_i8_tile.cuh: largest 2^14, a row's max at 2^6 or more).
-constexpr float kTc5Head = 6.0f;
+constexpr int kTc5ConvertWarps = 4;
 constexpr int kTc5KConv = 1, kTc5VConv = 1;
 static_assert(kTc5KConv + kTc5VConv <= kTc5VSlots, "their barriers take the places of the V slots'");
-__host__ __device__ constexpr int tc5_consumers(int ct) { return kTc5Consumers + (ct == kI8 ? kTc5ConvertWarps : 0); }
+// (and a second warp that issues products: one the scores, one the output products)
+__host__ __device__ constexpr int tc5_consumers(int ct) { return kTc5Consumers + (ct == kI8 ? 1 + kTc5ConvertWarps : 0); }
 
 // Query-split CTAs (qs; long runs of new tokens, see paged_decode_kernel)
 // take 32-token tiles too: one kv head's stage is small, and every warp
@@ -187,6 +186,7 @@ struct DecodeParams {
     // Decode: qn = 1, gq = G, qstride = 1.
     int32_t qn, gq, qstride;
     const int32_t *row_cnt;
+    const int32_t *row0;  // int8 query-split calls: entry -> its first q / out row (null: b * qstride)
     // Store fused into a decode (qn = 1): row b of k_new / v_new [B, Hkv, D] (bf16) is the K/V of
     // sequence b's token at position L - 1; the kernel writes it (E4M3 caches: its codes under the kv
     // head's scales) to that token's cache row (k_cache_w / v_cache_w, [NB * bs, Hkv, D] elements) and
@@ -202,7 +202,8 @@ struct alignas(16) UnitMeta {
     int32_t b, g, u, n;            // unit u of the n units of (b, group g); b < 0: no more work
     int32_t L, flags, slice, cnt;  // context length of b, kFirst | kLast | kSliceEnd, slice of the unit,
                                    // queries of entry b
-    int32_t newrow, pad[3];        // fused store: cache row of token L - 1 if the unit holds it, else -1
+    int32_t newrow, row0, pad[2];  // fused store: cache row of token L - 1 if the unit holds it, else -1;
+                                   // query-split int8 calls: first q / out row of the entry
 };
 constexpr int kFirst = 1;     // first unit of (b, g) in this slice
 constexpr int kLast = 2;      // last unit of (b, g) in this slice
@@ -250,13 +251,14 @@ __host__ __device__ inline CtaLayout cta_layout(int D, int G, int es, int hg, in
     l.stage_bytes = align_up((tc5 && !i8 ? 1 : 2) * l.kv_bytes, 1024);
     l.q_bytes = tc5 ? 0u : align_up(uint32_t(hg * (qs ? sub : 1) * G * D * 2), 128);  // tc5: Q in tensor memory
     // states of the non-leading warps of every head (the leader keeps its own in registers); tc5: the
-    // values each row's two key halves exchange ([2 tile parities][2 halves][128 rows] floats)
-    l.comb_bytes = tc5 ? 2u * 2u * 128u * 4u
+    // values each row's two key halves exchange ([2 tile parities][2 halves][128 rows] floats; int8 caches: a
+    // state and a query maximum from each group of warps)
+    l.comb_bytes = tc5 ? 2u * 2u * 128u * 4u + (i8 ? 2u * 128u * 4u : 0u)
                        : (sub > 1 && !qs ? align_up(uint32_t(hg * (sub - 1) * comb_stride(D, G) * 4), 128) : 0u);
     uint32_t o = uint32_t(nst) * l.stage_bytes;
     l.off_v = o;
     if (tc5 && i8)
-        o += uint32_t(kTc5KConv + kTc5VConv) * 2u * l.kv_bytes;  // f16 operands
+        o += uint32_t(kTc5KConv + kTc5VConv + 1) * 2u * l.kv_bytes;  // f16 operands: K, V and Q
     else if (tc5)
         o += uint32_t(kTc5VSlots) * align_up(l.kv_bytes, 1024);
     l.off_q = o;
@@ -1385,10 +1387,14 @@ __device__ void tc5_merge(const DecodeParams &p, const long long *bound, int sf,
 
 static_assert(team_warps(16) * 16 == 128, "a tensor-memory piece tile is 8 slots of 16 rows");
 
-// int8 caches: the warp that issues the products and the warps that turn codes into f16 operands (defined in
-// pkv_i8_tc5.cuh, which the translation unit of these kernels includes).
+// int8 caches: their softmax warps, the warp that issues the products and the warps that turn codes into f16
+// operands (defined in pkv_i8_tc5.cuh, which the translation unit of these kernels includes).
 template <int D>
-__device__ void tc5_mma_warp_i8(const DecodeParams &p, const Tc5Smem &m, uint32_t tmem);
+__device__ void tc5_softmax_warps_i8(const DecodeParams &p, const CtaLayout &lay, const Tc5Smem &m, uint32_t tmem,
+                                     float2 *xch, const long long *bound, const int32_t *scan, int *sh,
+                                     const float *wts, int nslots, uint32_t gen, int wp, bool adaptive);
+template <int D>
+__device__ void tc5_mma_warp_i8(const DecodeParams &p, const Tc5Smem &m, uint32_t tmem, bool output);
 template <int D>
 __device__ void tc5_convert_warps(const DecodeParams &p, const CtaLayout &lay, const Tc5Smem &m, uint8_t *stage0,
                                   int t);
@@ -1397,11 +1403,7 @@ __device__ void tc5_convert_warps(const DecodeParams &p, const CtaLayout &lay, c
 // keys 64 h .. 64 h + 63 of every tile, h = w / 4.  The two threads of a row (warps w and w + 4) hold the
 // same running max: they exchange their tile max each tile; each keeps the sum of its own keys' weights.
 // When a segment starts they write its Q tile (dims 64 h .. 64 h + 63 of row r) into tensor memory.
-// int8 caches: the scores are of code rows, so a group of 16 keys (a scale block) has a factor kc = s_k times
-// the row's; the weights take the V scale along, P = 2^(kc s + lv - m) with lv = log2 s_v and m the running
-// max of kc s + lv (less kTc5Head), and the row's sum divides it out again group by group: both products then
-// see plain codes, at no cost per key.
-template <int D, int G, int CT>
+template <int D, int G>
 __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, const Tc5Smem &m, uint32_t tmem,
                                   float *xch, const long long *bound, const int32_t *scan, int *sh,
                                   const float *wts, int nslots, uint32_t gen, int wp, bool adaptive)
@@ -1418,7 +1420,6 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
     int s = 0;
     uint32_t ph = 0, j = 0, segs = 0;
     float mrun = -INFINITY, lrun = 0.f;
-    float crow = c, cnext = c;  // int8 caches: the row's score factor, and that of the Q tile written last
     bool row_ok = false;
     int shift = 0, u_first = 0;
     uint32_t meets = 0;  // exchanges with the row's other half so far (the same in both warps)
@@ -1448,8 +1449,6 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
     // A segment's Q tile into tensor memory (tile segs % 2: the tile before it was last read by the
     // segment before the previous one's scores, all of which were read back): this thread's 64 dims of
     // its row, zeros for rows that are not queries of the entry.
-    // int8 caches: as f16, times the power of two that brings the row's largest |q| to [2^14, 2^15) (found by
-    // its two threads together); false if a wait gave up.
     auto write_q = [&](const UnitMeta &sg) {
         uint32_t w[32];
         if (qi < sg.cnt) {
@@ -1467,21 +1466,6 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
 #pragma unroll
             for (int k = 0; k < DH / 2; ++k) w[k] = 0u;
         }
-        if constexpr (CT == kI8) {
-            uint32_t mx = 0u;
-#pragma unroll
-            for (int k = 0; k < DH / 2; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-            float other;
-            if (!exchange(__uint_as_float(mx), other)) return false;
-            float mul;
-            // the row's factor stays positive, whatever the scale's sign (the max of a masked tile depends on it)
-            cnext = fabsf(c) * q_pow2(max(mx, __float_as_uint(other)), mul);
-            if (c <= 0.f) mul = c < 0.f ? -mul : 0.f;
-            if (c == 0.f) cnext = 1.f;
-#pragma unroll
-            for (int k = 0; k < DH / 2; ++k)
-                w[k] = f16x2_of(__uint_as_float(w[k] << 16) * mul, __uint_as_float(w[k] & 0xffff0000u) * mul);
-        }
         const uint32_t qa = tlane + kTc5QCol + (segs & 1u) * 64u + uint32_t(half * DH / 2);
         if constexpr (DH / 2 == 32) {
             tmem_st32(qa, w);
@@ -1496,19 +1480,18 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
         __syncwarp();
         if (lane == 0) mbar_arrive(m.qready);
         ++segs;
-        return true;
     };
     // the next segment's Q tile is already written: the first one before the loop, each later one at the
     // end of the segment before it
-    bool q_early = false, alive = true;
+    bool q_early = false;
     if (wait(&m.mready[0], 0u)) {
         const UnitMeta f0 = m.metas[0];
         if (f0.b >= 0 && (f0.flags & kFirst)) {
-            alive = write_q(f0);
+            write_q(f0);
             q_early = true;
         }
     }
-    while (alive) {
+    for (;;) {
         if (!wait(&m.full[s], ph)) break;
         const UnitMeta mt = m.metas[s];
         if (mt.b < 0) break;
@@ -1520,14 +1503,13 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
             mrun = -INFINITY;
             lrun = 0.f;
             u_first = mt.u;
-            if (!q_early && !write_q(mt)) break;
+            if (!q_early) write_q(mt);
             q_early = false;
-            crow = cnext;
         }
         const int tok0 = mt.u * kTc5Keys;
         const int valid = min(kTc5Keys, mt.L - tok0);
         const int lim = row_ok ? min(valid, mt.L - tok0 - shift) - KH * half : 0;  // keys of this half
-        if (CT == kBf16 && valid < kTc5Keys) {
+        if (valid < kTc5Keys) {
             // V rows past the sequence's end hold anything (NaN included) and 0 * NaN is NaN: zero them,
             // once the V copy has landed
             if (!wait(&m.vfull[j % kTc5VSlots], (j / kTc5VSlots) & 1u)) break;
@@ -1544,8 +1526,8 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
         tc_fence_after();
         const uint32_t sbuf = tlane + (j & 1u) * 128u;  // the unit's score buffer (and then its weights)
         // raw scores s of the half's keys (at or past the row's bound: -inf); weights 2^(s c - m)
-        float x[CT == kI8 ? 1 : KH];
-        if constexpr (CT == kBf16) {
+        float x[KH];
+        {
             uint32_t r[KH];
             tmem_ld64(sbuf + uint32_t(KH * half), r);
             if (lim >= KH) {
@@ -1556,48 +1538,13 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
                 for (int i = 0; i < KH; ++i) x[i] = i < lim ? __uint_as_float(r[i]) : -INFINITY;
             }
         }
-        // int8 caches: the scores are read twice, a scale block's 16 keys at a time (for the max, then for the
-        // weights), in rolled loops: the softmax, converting and issuing warps share the instruction
-        // caches
-        const float4 *prep = m.prep + s * (kTc5Keys / kScaleToks) + half * (KH / kScaleToks);
-        auto scores16 = [&](int g, float (&y)[kScaleToks]) {
-            uint32_t r[kScaleToks];
-            tmem_ld16(sbuf + uint32_t(KH * half + kScaleToks * g), r);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.sfree[j & 1u]);  // the unit's K slot (and meta) may be reused
+        float mx4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-            for (int i = 0; i < kScaleToks; ++i) y[i] = __uint_as_float(r[i]);
-            const int left = lim - kScaleToks * g;
-            if (left < kScaleToks) {
-#pragma unroll
-                for (int i = 0; i < kScaleToks; ++i) y[i] = i < left ? y[i] : -INFINITY;
-            }
-        };
-        float mx;
-        if constexpr (CT == kI8) {
-            if (!wait(&m.dready[s], ph)) break;
-            mx = -INFINITY;
-#pragma unroll 1
-            for (int g = 0; g < KH / kScaleToks; ++g) {
-                float y[kScaleToks];
-                scores16(g, y);
-                const float4 sc = prep[g];
-                float m2[2] = {y[0], y[1]};
-#pragma unroll
-                for (int i = 2; i < kScaleToks; ++i) m2[i & 1] = fmaxf(m2[i & 1], y[i]);
-                mx = fmaxf(mx, fmaf(fmaxf(m2[0], m2[1]), fmaxf(sc.x * crow, 0x1p-126f), sc.y));
-            }
-            mx -= kTc5Head;
-            // fmaxf passes NaN over: a row that has seen a key of a marked block takes some max all the same (a
-            // piece whose max is -inf counts as empty)
-            if (mx == -INFINITY && lim > 0) mx = 0.f;
-        } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&m.sfree[j & 1u]);  // the unit's K slot (and meta) may be reused
-            float mx4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-            for (int i = 4; i < KH; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], x[i]);
-            mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;  // c > 0
-        }
+        for (int i = 4; i < KH; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], x[i]);
+        float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;  // c > 0
         float other;
         if (!exchange(mx, other)) break;
         mx = fmaxf(mx, other);  // the row's tile max: the same in both halves
@@ -1630,41 +1577,16 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
         // weights (2^-inf = 0 for the masked keys; a row without any key so far takes m = 0 and gets zeros)
         {
             const float mneg = mrun == -INFINITY ? 0.f : -mrun;
-            if constexpr (CT == kI8) {
-                // (the weights of group g, 8 columns, go over the scores of group g / 2: this thread's own, read
-                // already; so half h's are columns 64 h .. + 31 of the buffer)
-#pragma unroll 1
-                for (int g = 0; g < KH / kScaleToks; ++g) {
-                    float y[kScaleToks];
-                    scores16(g, y);
-                    const float4 sc = prep[g];
-                    // kc is never zero: a masked key is -inf times it
-                    const float kc = fmaxf(sc.x * crow, 0x1p-126f), bias = sc.y + mneg;
-                    float ps[2] = {0.f, 0.f};
-                    uint32_t w[kScaleToks / 2];
+            float ps[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t w[32];
 #pragma unroll
-                    for (int k = 0; k < kScaleToks / 2; ++k) {
-                        const float p0 = ex2(fmaf(y[2 * k], kc, bias)), p1 = ex2(fmaf(y[2 * k + 1], kc, bias));
-                        ps[k & 1] += p0 + p1;
-                        w[k] = f16x2_of(p0, p1);
-                    }
-                    lrun = fmaf(ps[0] + ps[1], sc.z, lrun);
-                    tmem_st8(sbuf + uint32_t(KH * half + 8 * g), w);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&m.empty[s]);  // the unit's meta and scales are read
-            } else {
-                uint32_t w[32];
-                float ps[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < KH / 2; ++k) {
-                    const float p0 = ex2(fmaf(x[2 * k], c, mneg)), p1 = ex2(fmaf(x[2 * k + 1], c, mneg));
-                    ps[k & 3] += p0 + p1;
-                    w[k] = pack_bf16x2(p0, p1);
-                }
-                lrun += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-                tmem_st32(sbuf + 32u * half, w);
+            for (int k = 0; k < KH / 2; ++k) {
+                const float p0 = ex2(fmaf(x[2 * k], c, mneg)), p1 = ex2(fmaf(x[2 * k + 1], c, mneg));
+                ps[k & 3] += p0 + p1;
+                w[k] = pack_bf16x2(p0, p1);
             }
+            lrun += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+            tmem_st32(sbuf + 32u * half, w);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -1680,7 +1602,7 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
                 if (!wait(&m.mready[sn], s + 1 == p.nst ? ph ^ 1u : ph)) break;
                 const UnitMeta nx = m.metas[sn];
                 if (nx.b >= 0 && (nx.flags & kFirst)) {
-                    if (!write_q(nx)) break;
+                    write_q(nx);
                     q_early = true;
                 }
             }
@@ -1810,8 +1732,9 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
         // TC5: a stage and a Q slot are released by one tcgen05.commit of the MMA warp (int8 caches: by the
-        // softmax warps and the converting warps)
-        const uint32_t releases = TC5 ? (CT == kI8 ? uint32_t(kTc5SoftmaxWarps + kTc5ConvertWarps) : 1u) : uint32_t(p.cons);
+        // softmax warps, the converting warps and the warp that issues the output products)
+        const uint32_t releases =
+            TC5 ? (CT == kI8 ? uint32_t(kTc5SoftmaxWarps + kTc5ConvertWarps + 1) : 1u) : uint32_t(p.cons);
         for (int i = 0; i < p.nst; ++i) {
             mbar_init(&full[i], CT == kI8 ? 33 : 1);  // int8 caches: and the lanes' copies of the scales
             mbar_init(&empty[i], releases);
@@ -1826,10 +1749,11 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
             for (int i = 0; i < 2; ++i) {                   // [i]: of a unit j with j % 2 == i
                 mbar_init(&tc5_bar[i], 1);                  // scores computed
                 mbar_init(&tc5_bar[2 + i], kTc5SoftmaxWarps);  // scores read
-                mbar_init(&tc5_bar[4 + i], kTc5SoftmaxWarps);  // weights written
+                // weights written (int8 caches: a unit is one warp group's)
+                mbar_init(&tc5_bar[4 + i], CT == kI8 ? kTc5SoftmaxWarps / 2 : kTc5SoftmaxWarps);
                 mbar_init(&tc5_bar[6 + i], 1);              // output product done
             }
-            mbar_init(&tc5_bar[8], 1);                      // every product done (before TMEM is freed)
+            mbar_init(&tc5_bar[8], CT == kI8 ? 2 : 1);      // every product done (before TMEM is freed)
             for (int i = 0; i < 4; ++i) mbar_init(&tc5_bar[9 + i], 2);  // the two warps of lane quarter i met
             mbar_init(&tc5_bar[13], kTc5SoftmaxWarps);      // all softmax warps met
             mbar_init(&tc5_bar[14], kTc5SoftmaxWarps);      // a segment's Q tile written
@@ -1927,7 +1851,8 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                 const int l = __ffs(zm) - 1;
                 const long long bz = __shfl_sync(kFull, b, l);
                 const int nz = __shfl_sync(kFull, rows, l) * p.Hq * D / 8;
-                uint4 *o = reinterpret_cast<uint4 *>(p.out + bz * p.qstride * p.Hq * D);
+                const long long r0 = p.row0 ? __ldg(p.row0 + bz) : bz * p.qstride;
+                uint4 *o = reinterpret_cast<uint4 *>(p.out + r0 * p.Hq * D);
                 for (int i = lane; i < nz; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
             }
         }
@@ -1987,6 +1912,7 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
             // because the scoreboard tracks a register for the whole warp.
             Walker iw = nunits > 0 ? walker_locate(scan, p.B, p.nhg, lo + rot) : Walker{0, 0, 0, 1};
             int32_t cur_e = -1, cur_L = 0, cur_c = 1, nxt_e = -1, nxt_L = 0, nxt_c = 1;
+            int32_t cur_r = 0, nxt_r = 0;  // TC5, int8 caches: the entry's first row
             auto prefetch_batch = [&](long long kb) {  // boxes [kb, kb + 32) -> nxt, one per lane
                 const long long x = kb + lane;
                 if (x < nboxes) {
@@ -2000,18 +1926,20 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                     nxt_c = p.row_cnt ? __ldg(p.row_cnt + mine.b) : p.qn;
                     const int32_t trow = p.row_seq ? __ldg(p.row_seq + mine.b) : mine.b;
                     nxt_e = __ldg(p.block_tables + (long long)trow * p.max_blocks + blk);
+                    if constexpr (TC5 && CT == kI8) nxt_r = __ldg(p.row0 + mine.b);
                 }
             };
             // TC5: the query rows of segment w into L2 (the softmax warps load them into tensor memory at
             // the end of the segment before): 8 qn queries x gq heads of kv head g, D values each, as
             // 128-byte lines, lane-strided (plain prefetches: they do not queue behind the copies)
             auto prefetch_q = [&](const Walker &w) {
-                const int nq = min(CT == kI8 ? 128 / p.gq : team_warps(G) * p.qn, p.B - w.b);
+                const long long r0 = CT == kI8 ? __ldg(p.row0 + w.b) : w.b;
+                const int nq = CT == kI8 ? __ldg(p.row_cnt + w.b) : min(team_warps(G) * p.qn, p.B - w.b);
                 const int lines = p.gq * D * 2 / 128;
                 for (int i = lane; i < nq * lines; i += 32) {
                     const int r = i / lines, c = i - r * lines;
                     prefetch_l2(reinterpret_cast<const uint8_t *>(
-                                    p.q + ((long long)(w.b + r) * p.Hq + (long long)w.g * p.gq) * D) +
+                                    p.q + ((r0 + r) * p.Hq + (long long)w.g * p.gq) * D) +
                                 c * 128);
                 }
             };
@@ -2020,6 +1948,7 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                 cur_e = nxt_e;
                 cur_L = nxt_L;
                 cur_c = nxt_c;
+                cur_r = nxt_r;
             }
             for (long long k = 0; k < nunits; ++k) {
                 const long long kb0 = k * p.nbox;  // nbox is a power of two <= 32: batches start on units
@@ -2027,6 +1956,7 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                     cur_e = nxt_e;
                     cur_L = nxt_L;
                     cur_c = nxt_c;
+                    cur_r = nxt_r;
                     if (kb0 + 32 < nboxes) prefetch_batch(kb0 + 32);
                 }
                 const int s = rs;
@@ -2038,6 +1968,8 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                 const int32_t len = __shfl_sync(kFull, cur_L, src);
                 const int32_t cnt = __shfl_sync(kFull, cur_c, src);
                 const int32_t e = __shfl_sync(kFull, cur_e, (src + lane) & 31);  // lane j: box j's entry
+                int32_t row0 = 0;
+                if constexpr (TC5 && CT == kI8) row0 = __shfl_sync(kFull, cur_r, src);
                 const long long x = unit_at(k);
                 const int flags = ((x == lo || iw.u == 0) ? kFirst : 0) |
                                   ((x == hi - 1 || iw.u == iw.n - 1) ? kLast : 0) |
@@ -2111,6 +2043,7 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                     mt.slice = slice;
                     mt.cnt = cnt;
                     mt.newrow = newrow;
+                    if constexpr (TC5 && CT == kI8) mt.row0 = row0;
                     if constexpr (TC5) mbar_arrive(&mready[s]);  // the meta, for a look ahead
                     // TC5: full[s] counts the K half only; the V half has barriers of its own
                     mbar_arrive_expect_tx(&full[s], (TC5 && CT == kBf16 ? 1u : 2u) * nrows * box_bytes);
@@ -2234,15 +2167,20 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
             tm.dready = dready;
             tm.scales = reinterpret_cast<const float2 *>(smem + lay.off_sc);
             tm.prep = reinterpret_cast<float4 *>(smem + lay.off_sc + uint32_t(p.nst) * scale_bytes(p.toks, p.hg));
-            if (warp == kTc5SoftmaxWarps)
-                tc5_mma_warp_i8<D>(p, tm, tmem);
+            if (warp == kTc5SoftmaxWarps || warp == kTc5SoftmaxWarps + 1)
+                tc5_mma_warp_i8<D>(p, tm, tmem, warp != kTc5SoftmaxWarps);
             else if (warp > kTc5SoftmaxWarps)
-                tc5_convert_warps<D>(p, lay, tm, stage0, int(threadIdx.x) - 32 * (kTc5SoftmaxWarps + 1));
+                tc5_convert_warps<D>(p, lay, tm, stage0, int(threadIdx.x) - 32 * (kTc5SoftmaxWarps + 2));
         } else if (warp == kTc5SoftmaxWarps) {
             tc5_mma_warp<D>(p, lay, tm, tmem);
         }
-        if (warp < kTc5SoftmaxWarps)
-            tc5_softmax_warps<D, G, CT>(p, lay, tm, tmem, comb, bound, scan, sh, wts, nslots, gen, wp, adaptive);
+        if (warp < kTc5SoftmaxWarps) {
+            if constexpr (CT == kI8)
+                tc5_softmax_warps_i8<D>(p, lay, tm, tmem, reinterpret_cast<float2 *>(comb), bound, scan, sh, wts,
+                                        nslots, gen, wp, adaptive);
+            else
+                tc5_softmax_warps<D, G>(p, lay, tm, tmem, comb, bound, scan, sh, wts, nslots, gen, wp, adaptive);
+        }
         named_barrier(2, 32 * tc5_consumers(CT));  // every tensor-memory access of the CTA is done
         if (warp == kTc5SoftmaxWarps) {
             tc_fence_after();

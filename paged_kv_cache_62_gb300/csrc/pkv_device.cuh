@@ -110,6 +110,16 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     return __all_sync(kFull, ok);
 }
 
+// mbar_wait_bounded in few instructions, for code that an SM's instruction caches hold only in parts: the limit is
+// a number of tries (each may suspend the thread for a while when the phase is not complete).
+__device__ __forceinline__ bool mbar_wait_lean(uint64_t *bar, uint32_t parity)
+{
+    const uint32_t a = smem_u32(bar);
+    for (uint32_t i = 0; !__all_sync(kFull, mbar_try_wait(a, parity)); ++i)
+        if (i >> 22) return false;
+    return true;
+}
+
 // 8-byte asynchronous copy global -> shared by this thread, and an arrival on `bar` once all of the
 // thread's copies so far have landed (one of the arrivals the barrier was initialised with).
 __device__ __forceinline__ void copy_async8(void *dst, const void *src)

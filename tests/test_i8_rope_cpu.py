@@ -59,7 +59,8 @@ ATT_OK = [FAKE, FAKE, FAKE, FAKE, FAKE, 4, FAKE, FAKE, 2, 5, 16, 8, 128, 16, 10,
 @pytest.mark.parametrize("kw,status", [
     (dict(cu=NULL), pkv.EINVAL), (dict(n=3), pkv.EINVAL), (dict(lens=NULL), pkv.EINVAL), (dict(B=0), pkv.EINVAL),
     (dict(T=pkv.MAX_SEQS + 1), pkv.EBOUNDS), (dict(wsb=64), pkv.EWORKSPACE), (dict(Hq=12), pkv.EINVAL),
-    (dict(T=0, q=NULL), pkv.OK),
+    (dict(Hq=136), pkv.EUNSUPPORTED), (dict(Hq=4096, T=500), pkv.EUNSUPPORTED), (dict(D=96, T=500), pkv.EUNSUPPORTED),
+    (dict(T=500, out=NULL), pkv.EINVAL), (dict(T=500, out=FAKE + 8), pkv.EINVAL), (dict(T=0, q=NULL), pkv.OK),
 ])
 def test_attention_i8(lib, kw, status):
     assert lib.pkv_paged_attention_i8(*swap(ATT, ATT_OK, **kw)) == status
