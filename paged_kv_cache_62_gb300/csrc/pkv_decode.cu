@@ -298,7 +298,7 @@ __global__ void expand_rows_kernel(const int32_t *__restrict__ cu_seqlens_q, int
 // thread checks that the row lies in a consistent sequence and else writes zeros to its output.
 __global__ void expand_entries_kernel(const int32_t *__restrict__ cu_seqlens_q, int32_t new_per_seq,
                                       const int32_t *__restrict__ context_lens, int32_t num_seqs, int32_t num_rows,
-                                      int32_t num_entries, int32_t chunk, int32_t row_values,
+                                      int32_t num_entries, int32_t chunk, int32_t len_limit, int32_t row_values,
                                       int32_t *__restrict__ row_seq, int32_t *__restrict__ row_len,
                                       int32_t *__restrict__ row_cnt, int32_t *__restrict__ row0,
                                       uint16_t *__restrict__ out, int32_t *err)
@@ -320,7 +320,8 @@ __global__ void expand_entries_kernel(const int32_t *__restrict__ cu_seqlens_q, 
         return lo;
     };
     auto consistent = [&](int32_t b, int32_t r0, int32_t r1) {
-        return start(0) == 0 && r0 >= 0 && r0 <= r1 && r1 <= num_rows && r1 - r0 <= __ldg(context_lens + b);
+        const int32_t L = __ldg(context_lens + b);
+        return start(0) == 0 && r0 >= 0 && r0 <= r1 && r1 <= num_rows && r1 - r0 <= L && L <= len_limit;
     };
     if (x < num_entries) {
         const int32_t b = find(x, true), r0 = start(b), r1 = start(b + 1);
@@ -430,11 +431,13 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
         if (entries > num_rows) return PKV_EBOUNDS;  // (not with more than 2 qg rows a sequence)
         if (!out || !q || !aligned16(out)) return PKV_EINVAL;
         int32_t *row0 = reinterpret_cast<int32_t *>(wsb + dec_bytes + 3 * rows_bytes(num_rows));
+        const int32_t len_limit =
+            int32_t(std::min<int64_t>(max_context_len, int64_t(max_blocks_per_seq) * std::max(block_size, 0)));
         const cudaError_t e = launch_pdl(expand_entries_kernel, dim3((num_rows + 255) / 256), dim3(256), 0,
                                          reinterpret_cast<cudaStream_t>(stream),
                                          new_per_seq > 0 ? nullptr : cu_seqlens_q, new_per_seq, context_lens, num_seqs,
-                                         num_rows, entries, chunk, num_q_heads * head_dim, row_seq, row_len, row_cnt,
-                                         row0, out, err_word);
+                                         num_rows, entries, chunk, len_limit, num_q_heads * head_dim, row_seq,
+                                         row_len, row_cnt, row0, out, err_word);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return cuda_fail("expand_entries_kernel launch", e);

@@ -121,7 +121,10 @@ constexpr int kTc5ConvertWarps = 4;
 constexpr int kTc5KConv = 1, kTc5VConv = 1;
 static_assert(kTc5KConv + kTc5VConv <= kTc5VSlots, "their barriers take the places of the V slots'");
 // (and a second warp that issues products: one the scores, one the output products)
-__host__ __device__ constexpr int tc5_consumers(int ct) { return kTc5Consumers + (ct == kI8 ? 1 + kTc5ConvertWarps : 0); }
+__host__ __device__ constexpr int tc5_consumers(int ct)
+{
+    return kTc5Consumers + (ct == kI8 ? 1 + kTc5ConvertWarps : 0);
+}
 
 // Query-split CTAs (qs; long runs of new tokens, see paged_decode_kernel)
 // take 32-token tiles too: one kv head's stage is small, and every warp
@@ -776,6 +779,11 @@ struct I8Scales {
     bool plain, vzero;
 };
 __device__ __forceinline__ I8Scales i8_scales(float2 s);
+// A block whose V scale is zero adds nothing to the output and its weights to the row's sum; the log2 it takes
+// part with in the running max should be that of its neighbours (the weights of the others, or its own, leave the
+// float range otherwise).  Without one: in the middle of what V scales may be, on the small side.
+constexpr float kZeroLog = -64.0f;
+__device__ __forceinline__ void i8_zero_log(I8Scales &s, float lv);
 template <int KS, int HR>
 __device__ __forceinline__ void q_bias(const uint32_t (&qa)[KS][2 * HR], float (&qb)[HR]);
 template <int D, int HR_, bool TAIL>
@@ -2351,6 +2359,13 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                     sct[st] = i8_scales(sc[(jt * TC::NT + st) * p.hg + h]);
                     plain &= sct[st].plain;
                 }
+                if (!plain) {  // V scales of zero take the log2 of the tile's other block (see kZeroLog)
+#pragma unroll
+                    for (int st = 0; st < TC::NT; ++st)
+                        if (sct[st].vzero)
+                            i8_zero_log(sct[st], sct[st ^ 1].plain && kScaleToks * (st ^ 1) < valid ? sct[st ^ 1].lv
+                                                                                                      : kZeroLog);
+                }
                 if (valid == TC::TW && plain)
                     attend_tile_i8<D, TC::HR, false>(kb, kb + lay.kv_bytes, off, qa, rowf, qb, sct, lim, valid, m, l, o,
                                                      lane);
@@ -2593,7 +2608,8 @@ inline bool encode_cache_map(CUtensorMap *map, const void *base, bool fp8, int D
                            // one kv head of 8-bit codes is 64 or 128 bytes of a token's row: a longer fetch would
                            // read another head's
                            fp8 && box_heads == 1 && Hkv > 1 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
-                                                            : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                                                            : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         char msg[64];
         std::snprintf(msg, sizeof msg, "CUresult %d", int(r));

@@ -22,8 +22,8 @@
 //
 // Ordering: codes and scales landed -> full[s]; K operand written -> kready (4 warps), read -> kfree
 // (tcgen05.commit); V likewise vready, vfree; scales prepared -> dready[s]; stage released -> empty[s] (4
-// converting warps, 8 softmax warps, and the warp that issues output products); scores -> sfull[w]; weights -> pfull[w] (4 warps); output product done ->
-// odone[w]; a segment's Q written -> qready (8 warps: after the last scores of the segment before it are in);
+// converting warps, 8 softmax warps, and the warp that issues output products); scores -> sfull[w]; weights ->
+// pfull[w] (4 warps); output product done -> odone[w]; a segment's Q written -> qready (8 warps: after the last scores of the segment before it are in);
 // all softmax warps met -> team.  A group passes the end of a segment only with the other, so no barrier runs
 // two phases ahead of a waiter.
 #pragma once
@@ -79,23 +79,26 @@ __device__ __forceinline__ void tc5_convert_tile(const uint8_t *raw, uint8_t *ds
     }
 }
 
-// What the softmax takes of a scale block (K scale s_k, V scale s_v): (s_k, lv = log2 s_v, 2^-lv).  A block
-// whose scales are not of ordinary size is dealt with in the operands (tc5_mark_block), with scales of 1 here.
+// Whether a scale block's scales (K scale, V scale) are of ordinary size; one whose scales are not is dealt with
+// in the operands (tc5_mark_block), the scales that the softmax takes being 1.
 __device__ __forceinline__ bool tc5_plain(float2 s)
 {
     return s.x > 0.f && s.x < INFINITY && s.y >= kMinVScale && s.y <= kMaxVScale;
 }
 
-// mode 1: zeros, mode 2: NaN, into the 16 rows of scale block g of an operand (all converting warps).
+// mode 1: zeros, mode 2: NaN, into scale block g of an operand: each converting thread over what it wrote there
+// itself (see tc5_convert_tile).
 template <int D>
 __device__ __noinline__ void tc5_mark_block(uint8_t *dst, int g, int mode, int t)
 {
-    constexpr int N = kScaleToks * D / 8;  // 16-byte pieces
+    constexpr int PER = D / 16, ROWS = 32 * kTc5ConvertWarps / PER;
+    const int i = t % PER, r0 = (t / PER) ^ (D == 128 ? i >> 2 : 0);
+    const int row = r0 + g * kScaleToks / ROWS * ROWS, key = r0 & 7, c = 2 * (i & 3);
+    if (row / kScaleToks != g) return;
     const uint32_t v = mode == 2 ? 0x7fff7fffu : 0u;
-    for (int i = t; i < N; i += 32 * kTc5ConvertWarps) {
-        const int slab = i / (kScaleToks * 8), r = i - slab * (kScaleToks * 8);
-        *reinterpret_cast<uint4 *>(dst + slab * kTc5SlabBytes + g * (kScaleToks * 128) + r * 16) = make_uint4(v, v, v, v);
-    }
+    uint8_t *base = dst + (i >> 2) * kTc5SlabBytes + row * 128;
+    *reinterpret_cast<uint4 *>(base + ((c ^ key) << 4)) = make_uint4(v, v, v, v);
+    *reinterpret_cast<uint4 *>(base + (((c + 1) ^ key) << 4)) = make_uint4(v, v, v, v);
 }
 
 // The converting warps: their thread t.  K runs a unit ahead of V: the scores of unit j + 1 can then be computed
@@ -131,7 +134,16 @@ __device__ void tc5_convert_warps(const DecodeParams &p, const CtaLayout &lay, c
                         // a K or V scale of zero: zeros there; a V scale below kMinVScale counts as zero; a NaN, an
                         // infinity or a V scale above kMaxVScale: NaN scores
                         const bool ko = sc.x > 0.f && sc.x < INFINITY, vo = sc.y >= kMinVScale && sc.y <= kMaxVScale;
-                        const float lv = vo ? __log2f(sc.y) : 0.f;
+                        float lv = vo ? __log2f(sc.y) : 0.f;
+                        if (__any_sync((1u << kGroups) - 1u, !vo)) {
+                            // a V scale of zero takes the smallest log2 of the unit's blocks (see kZeroLog)
+                            const bool seen = lane * kScaleToks < m.metas[s].L - m.metas[s].u * kTc5Keys;
+                            float low = vo && seen ? lv : INFINITY;
+#pragma unroll
+                            for (int o = 1; o < kGroups; o <<= 1)
+                                low = fminf(low, __shfl_xor_sync((1u << kGroups) - 1u, low, o));
+                            if (!vo) lv = low < INFINITY ? low : kZeroLog;
+                        }
                         m.prep[s * kGroups + lane] = make_float4(ko ? sc.x : 1.f, lv, ex2(-lv), 0.f);
                     }
                     __syncwarp();
@@ -139,21 +151,18 @@ __device__ void tc5_convert_warps(const DecodeParams &p, const CtaLayout &lay, c
                 }
                 uint8_t *kop = kdst + kb * 2u * lay.kv_bytes;
                 tc5_convert_tile<D>(stage0 + uint32_t(s) * lay.stage_bytes, kop, t);
-                // blocks to mark (the same in every warp): bits 0-7 zeros in K, 8-15 zeros in V, 16-23 NaN in K
+                // blocks to mark (the same in every warp)
                 const bool kz = sc.x == 0.f, vz = sc.y >= 0.f && sc.y < kMinVScale;
-                const bool bad = !plain && !((kz || (sc.x > 0.f && sc.x < INFINITY)) && (vz || (sc.y >= kMinVScale && sc.y <= kMaxVScale)));
-                const unsigned odd = __ballot_sync(kFull, !plain) & ((1u << kGroups) - 1u);
-                if (odd) {
-                    const unsigned mk = __ballot_sync(kFull, kz && !bad), mv = __ballot_sync(kFull, vz && !bad),
-                                   mn = __ballot_sync(kFull, bad);
-                    vzero_next = odd & mv;
-                    named_barrier(3, 32 * kTc5ConvertWarps);  // the rows below were just written by all of them
-                    for (unsigned o = odd; o; o &= o - 1) {
+                vzero_next = 0u;
+                if (const unsigned odd = __ballot_sync(kFull, !plain) & ((1u << kGroups) - 1u)) {
+                    const bool ko = sc.x > 0.f && sc.x < INFINITY, vo = sc.y >= kMinVScale && sc.y <= kMaxVScale;
+                    const unsigned bad = __ballot_sync(kFull, !((ko || kz) && (vo || vz)));
+                    const unsigned zero = __ballot_sync(kFull, kz);
+                    vzero_next = odd & ~bad & __ballot_sync(kFull, vz);
+                    for (unsigned o = odd & (bad | zero); o; o &= o - 1) {
                         const int g = __ffs(o) - 1;
-                        if ((mk | mn) >> g & 1u) tc5_mark_block<D>(kop, g, mn >> g & 1u ? 2 : 1, t);
+                        tc5_mark_block<D>(kop, g, bad >> g & 1u ? 2 : 1, t);
                     }
-                } else {
-                    vzero_next = 0u;
                 }
                 fence_proxy_async_smem();
             }
@@ -168,10 +177,7 @@ __device__ void tc5_convert_warps(const DecodeParams &p, const CtaLayout &lay, c
             if (u >= kTc5VConv && !wait(&m.vfree[vb], ((u / kTc5VConv) - 1) & 1u)) break;
             uint8_t *vop = vdst + vb * 2u * lay.kv_bytes;
             tc5_convert_tile<D>(stage0 + uint32_t(sv) * lay.stage_bytes + lay.kv_bytes, vop, t);
-            if (vzero) {
-                named_barrier(3, 32 * kTc5ConvertWarps);
-                for (unsigned o = vzero; o; o &= o - 1) tc5_mark_block<D>(vop, __ffs(o) - 1, 1, t);
-            }
+            for (unsigned o = vzero; o; o &= o - 1) tc5_mark_block<D>(vop, __ffs(o) - 1, 1, t);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -311,7 +317,8 @@ __device__ __noinline__ void tc5_merge_i8(const DecodeParams &p, const long long
 #pragma unroll
             for (int k = 0; k < C / 8; ++k)
                 *reinterpret_cast<uint4 *>(out + c0 + 8 * k) = make_uint4(
-                    pack_bf16x2(a[8 * k] * inv, a[8 * k + 1] * inv), pack_bf16x2(a[8 * k + 2] * inv, a[8 * k + 3] * inv),
+                    pack_bf16x2(a[8 * k] * inv, a[8 * k + 1] * inv),
+                    pack_bf16x2(a[8 * k + 2] * inv, a[8 * k + 3] * inv),
                     pack_bf16x2(a[8 * k + 4] * inv, a[8 * k + 5] * inv),
                     pack_bf16x2(a[8 * k + 6] * inv, a[8 * k + 7] * inv));
         }
@@ -399,110 +406,110 @@ __device__ void tc5_softmax_warps_i8(const DecodeParams &p, const CtaLayout &lay
     for (bool begun = false;; begun = true) {
         bool own = false;
         if (begun) {
-        if (!wait(&m.dready[s], ph)) break;
-        mt = m.metas[s];
-        if (mt.b < 0) break;
-        if (mt.flags & kFirst) {
-            row_ok = qi < mt.cnt;
-            shift = (mt.cnt - 1) - qi;  // the row's query sees this many fewer of the entry's last keys
-            mrun = -INFINITY;
-            lrun = 0.f;
-            u_first = mt.u;
-            j_first = j;
-            crow = cnext;
-        }
-        own = int(j & 1u) == wg;
-        if (own) {
-            const float4 *prep = m.prep + s * kGroups;
-            const int tok0 = mt.u * kTc5Keys;
-            const int lim = row_ok ? min(kTc5Keys, mt.L - tok0 - shift) : 0;  // visible keys of the tile
-            // the scores of 32 keys, two scale blocks: -inf at or past the row's bound
-            auto scores32 = [&](int g, float (&y)[32]) {
-                uint32_t r[32];
-                tmem_ld32(sbuf + uint32_t(kScaleToks * g), r);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(r[i]);
-                const int left = lim - kScaleToks * g;
-                if (left < 32) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) y[i] = i < left ? y[i] : -INFINITY;
-                }
-            };
-            if (!wait(&m.sfull[wg], (j >> 1) & 1u)) break;
-            tc_fence_after();
-            float mx = -INFINITY;
-#pragma unroll 1
-            for (int g = 0; g < kGroups; g += 2) {
-                float y[32];
-                scores32(g, y);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float4 sc = prep[g + h];
-                    float m2[2] = {y[16 * h], y[16 * h + 1]};
-#pragma unroll
-                    for (int i = 2; i < kScaleToks; ++i) m2[i & 1] = fmaxf(m2[i & 1], y[16 * h + i]);
-                    mx = fmaxf(mx, fmaf(fmaxf(m2[0], m2[1]), fmaxf(sc.x * crow, 0x1p-126f), sc.y));
-                }
+            if (!wait(&m.dready[s], ph)) break;
+            mt = m.metas[s];
+            if (mt.b < 0) break;
+            if (mt.flags & kFirst) {
+                row_ok = qi < mt.cnt;
+                shift = (mt.cnt - 1) - qi;  // the row's query sees this many fewer of the entry's last keys
+                mrun = -INFINITY;
+                lrun = 0.f;
+                u_first = mt.u;
+                j_first = j;
+                crow = cnext;
             }
-            mx -= kI8TcHead;
-            // fmaxf passes NaN over: a row that has seen a key of a marked block takes some max all the same (a
-            // piece whose max is -inf counts as empty)
-            if (mx == -INFINITY && lim > 0) mx = 0.f;
-            float alpha = 1.0f;
-            bool resc = false;
-            if (mx > mrun + kRescaleSlack) {  // also the row's first tile with a key (mrun = -inf)
-                if (mrun != -INFINITY) {
-                    alpha = ex2(mrun - mx);
-                    lrun *= alpha;
-                    resc = true;
-                }
-                mrun = mx;
-            }
-            // the group's output scaled in place once its last product is in (a row that keeps its max: alpha 1)
-            if (__any_sync(kFull, resc)) {
-                if (!wait(&m.odone[wg], ((j >> 1) - 1) & 1u)) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 16) {
-                    uint32_t r[16];
-                    tmem_ld16(obuf + uint32_t(wg * 128 + c0), r);
+            own = int(j & 1u) == wg;
+            if (own) {
+                const float4 *prep = m.prep + s * kGroups;
+                const int tok0 = mt.u * kTc5Keys;
+                const int lim = row_ok ? min(kTc5Keys, mt.L - tok0 - shift) : 0;  // visible keys of the tile
+                // the scores of 32 keys, two scale blocks: -inf at or past the row's bound
+                auto scores32 = [&](int g, float (&y)[32]) {
+                    uint32_t r[32];
+                    tmem_ld32(sbuf + uint32_t(kScaleToks * g), r);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-                    tmem_st16(obuf + uint32_t(wg * 128 + c0), r);
-                }
-            }
-            const float mneg = mrun == -INFINITY ? 0.f : -mrun;
-            // (the weights of blocks g and g + 1, 16 columns, go over scores of the blocks up to g / 2 + 1, read already)
-#pragma unroll 1
-            for (int g = 0; g < kGroups; g += 2) {
-                float y[32];
-                scores32(g, y);
-                uint32_t w[16];
+                    for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(r[i]);
+                    const int left = lim - kScaleToks * g;
+                    if (left < 32) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float4 sc = prep[g + h];
-                    const float kc = fmaxf(sc.x * crow, 0x1p-126f), bias = sc.y + mneg;  // kc: never zero
-                    float ps[2] = {0.f, 0.f};
-#pragma unroll
-                    for (int k = 0; k < kScaleToks / 2; ++k) {
-                        const float p0 = ex2(fmaf(y[16 * h + 2 * k], kc, bias));
-                        const float p1 = ex2(fmaf(y[16 * h + 2 * k + 1], kc, bias));
-                        ps[k & 1] += p0 + p1;
-                        w[8 * h + k] = f16x2_of(p0, p1);
+                        for (int i = 0; i < 32; ++i) y[i] = i < left ? y[i] : -INFINITY;
                     }
-                    lrun = fmaf(ps[0] + ps[1], sc.z, lrun);
+                };
+                if (!wait(&m.sfull[wg], (j >> 1) & 1u)) break;
+                tc_fence_after();
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int g = 0; g < kGroups; g += 2) {
+                    float y[32];
+                    scores32(g, y);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float4 sc = prep[g + h];
+                        float m2[2] = {y[16 * h], y[16 * h + 1]};
+#pragma unroll
+                        for (int i = 2; i < kScaleToks; ++i) m2[i & 1] = fmaxf(m2[i & 1], y[16 * h + i]);
+                        mx = fmaxf(mx, fmaf(fmaxf(m2[0], m2[1]), fmaxf(sc.x * crow, 0x1p-126f), sc.y));
+                    }
                 }
-                tmem_st16(sbuf + uint32_t(8 * g), w);
+                mx -= kI8TcHead;
+                // fmaxf passes NaN over: a row that has seen a key of a marked block takes some max all the same (a
+                // piece whose max is -inf counts as empty)
+                if (mx == -INFINITY && lim > 0) mx = 0.f;
+                float alpha = 1.0f;
+                bool resc = false;
+                if (mx > mrun + kRescaleSlack) {  // also the row's first tile with a key (mrun = -inf)
+                    if (mrun != -INFINITY) {
+                        alpha = ex2(mrun - mx);
+                        lrun *= alpha;
+                        resc = true;
+                    }
+                    mrun = mx;
+                }
+                // the group's output scaled in place once its last product is in (a row that keeps its max: alpha 1)
+                if (__any_sync(kFull, resc)) {
+                    if (!wait(&m.odone[wg], ((j >> 1) - 1) & 1u)) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                        uint32_t r[16];
+                        tmem_ld16(obuf + uint32_t(wg * 128 + c0), r);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+                        tmem_st16(obuf + uint32_t(wg * 128 + c0), r);
+                    }
+                }
+                const float mneg = mrun == -INFINITY ? 0.f : -mrun;
+                // (the weights of blocks g and g + 1, 16 columns, go over scores read already: blocks up to g / 2 + 1)
+#pragma unroll 1
+                for (int g = 0; g < kGroups; g += 2) {
+                    float y[32];
+                    scores32(g, y);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float4 sc = prep[g + h];
+                        const float kc = fmaxf(sc.x * crow, 0x1p-126f), bias = sc.y + mneg;  // kc: never zero
+                        float ps[2] = {0.f, 0.f};
+#pragma unroll
+                        for (int k = 0; k < kScaleToks / 2; ++k) {
+                            const float p0 = ex2(fmaf(y[16 * h + 2 * k], kc, bias));
+                            const float p1 = ex2(fmaf(y[16 * h + 2 * k + 1], kc, bias));
+                            ps[k & 1] += p0 + p1;
+                            w[8 * h + k] = f16x2_of(p0, p1);
+                        }
+                        lrun = fmaf(ps[0] + ps[1], sc.z, lrun);
+                    }
+                    tmem_st16(sbuf + uint32_t(8 * g), w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
             }
-            tmem_wait_st();
-            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (own) mbar_arrive(&m.pfull[wg]);
+                mbar_arrive(&m.empty[s]);  // its meta and scales are read
+            }
         }
-        __syncwarp();
-        if (lane == 0) {
-            if (own) mbar_arrive(&m.pfull[wg]);
-            mbar_arrive(&m.empty[s]);  // its meta and scales are read
-        }
-        }  // begun
         if (mt.flags & kLast) {
             // the segment's part in this slice ends.  First the next one's Q, once the last scores are in (they
             // read this one's), so that its first scores run during what follows
@@ -580,7 +587,8 @@ __device__ void tc5_softmax_warps_i8(const DecodeParams &p, const CtaLayout &lay
         if ((mt.flags & kSliceEnd) && adaptive && t == 0) {
             // balance record for the next call (as the regular consumers leave it)
             const bool mine = mt.slice == home;
-            const float us = float(global_ns() - *reinterpret_cast<const volatile unsigned long long *>(sh + 2)) * 1e-3f;
+            const float us =
+                float(global_ns() - *reinterpret_cast<const volatile unsigned long long *>(sh + 2)) * 1e-3f;
             p.ws_bal->weight[wp][mt.slice] = mine ? wts[mt.slice] : 0.f;
             p.ws_bal->elapsed[wp][mt.slice] = mine ? fmaxf(us, 1e-3f) : 0.f;
             p.ws_bal->tag[wp][mt.slice] = gen ^ kTableMagic;

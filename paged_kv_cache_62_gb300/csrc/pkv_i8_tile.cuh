@@ -56,6 +56,12 @@ __device__ __forceinline__ I8Scales i8_scales(float2 s)
     return r;
 }
 
+__device__ __forceinline__ void i8_zero_log(I8Scales &s, float lv)
+{
+    s.lv = lv;
+    s.iv = ex2(-lv);
+}
+
 // A query row's power of two (see q_pow2): the row's four threads (r4 = 0..3) look at their own dims.
 template <int D>
 __device__ __forceinline__ float q_row_scale(const uint16_t *qr, bool live, int r4, float &mul)

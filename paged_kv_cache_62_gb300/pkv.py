@@ -575,7 +575,7 @@ def rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: tor
                err_word: torch.Tensor | None = None, stream=None) -> None:
     """rope and kv_store in one launch: q turned into q_out, turned k and v stored at slot_mapping of bf16 caches
     (-1: not stored)."""
-    st = _native().rope_store(q, k, v, positions, inv_freq, slot_mapping, q_out, k_cache, v_cache, freq_axis, interleaved,
-                              err_word, stream)
+    st = _native().rope_store(q, k, v, positions, inv_freq, slot_mapping, q_out, k_cache, v_cache, freq_axis,
+                              interleaved, err_word, stream)
     if st != OK:
         raise PkvError(st, "pkv_rope_store")

@@ -369,6 +369,92 @@ def test_marked_blocks_reach_only_queries_that_see_them(heads, D, bs, n):
     assert off[rows].max() <= 0
 
 
+@pytest.mark.parametrize("n", [1, 4, 48])
+@pytest.mark.parametrize("scale", [-0.09, 0.0, 0.5])
+def test_attention_with_any_softmax_scale(n, scale):
+    lens, new = [n + 150, n, n + 7], [n] * 3
+    q, kc, vc, sc, bt, btd, ld = synth(lens, 8, 2, 128, 16, seed=n, new=new, spread=0.2)
+    sc *= 0.3                                                  # scores stay under 2^6
+    out = attend(q, kc, vc, sc, btd, None, ld, scale, n=n)
+    check(out, q, kc, vc, sc, bt, lens, new, scale, f"n{n} scale{scale}")
+
+
+@pytest.mark.parametrize("n", [4, 48])
+def test_attention_scales_of_any_size_and_zero_blocks(n):
+    """V scales of 2^-80, 1 and 2^40 per sequence and 1e-4 apart within one, blocks of zeros in K or V."""
+    lens, new = [n + 200, n + 77, n + 500], [n] * 3
+    q, kc, vc, sc, bt, btd, ld = synth(lens, 8, 4, 128, 32, seed=n, new=new)
+    for b, e in enumerate((2.0 ** -80, 1.0, 2.0 ** 40)):
+        pages = torch.from_numpy(bt[b][bt[b] >= 0].astype(np.int64)).cuda()
+        sc[pages, :, :, 1] *= e
+        sc[pages[::3], :, :, 1] *= 1e-4
+        sc[pages[1], 0, 0, 1] = 0.0
+        sc[pages[1], 1, 1, 0] = 0.0
+    out = attend(q, kc, vc, sc, btd, None, ld, 128 ** -0.5, n=n)
+    check(out, q, kc, vc, sc, bt, lens, new, 128 ** -0.5, f"n{n}")
+
+
+def test_attention_over_many_rows():
+    """The row limit, in chunks and single tokens; entries of 16 query heads a kv head."""
+    rng = np.random.default_rng(1)
+    new = [1] * 200 + rng.integers(1, 260, 112).tolist()
+    new[-1] += pkv.MAX_SEQS - sum(new)
+    assert min(new) > 0
+    lens = [n + int(x) for n, x in zip(new, rng.integers(0, 30, len(new)))]
+    q, kc, vc, sc, bt, btd, ld = synth(lens, 16, 1, 64, 16, seed=2, new=new)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = attend(q, kc, vc, sc, btd, cu, ld, 0.125, err=err)
+    assert err.item() == 0 and torch.isfinite(out).all()
+    # the reference on a part of the sequences
+    for b in [0, 7, 199, 200, 230, 311]:
+        r = sum(new[:b])
+        check(out[r:r + new[b]], q[r:r + new[b]], kc, vc, sc, bt[b:b + 1], [lens[b]], [new[b]], 0.125, f"seq {b}")
+
+
+def test_attention_rows_outside_their_sequences_are_zero_and_flagged():
+    """Chunk path: more rows than cached tokens, lengths beyond the table, rows behind the last offset."""
+    lens, new = [100, 90, 120], [60, 70, 50]
+    q, kc, vc, sc, bt, btd, ld = synth(lens, 4, 2, 64, 32, seed=3, new=new)
+    cu = torch.tensor([0, 60, 130, 170], dtype=torch.int32, device="cuda")     # ten rows behind the last offset
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = attend(q, kc, vc, sc, btd, cu, ld, 0.125, err=err)
+    assert err.item() == pkv.ERR_CONTEXT_RANGE and torch.all(out[170:] == 0)
+    check(out[:130], q[:130], kc, vc, sc, bt[:2], lens[:2], new[:2], 0.125, "rows before")
+    check(out[130:170], q[130:170], kc, vc, sc, bt[2:], lens[2:], [40], 0.125, "the shorter run")
+    err.zero_()
+    cu = torch.tensor([0, 60, 130, 180], dtype=torch.int32, device="cuda")
+    ld[1] = 65                                                                 # 70 new of 65
+    out = attend(q, kc, vc, sc, btd, cu, ld, 0.125, err=err)
+    assert err.item() == pkv.ERR_CONTEXT_RANGE and torch.all(out[60:130] == 0)
+    check(out[:60], q[:60], kc, vc, sc, bt[:1], lens[:1], new[:1], 0.125, "first")
+    err.zero_()
+    ld[1] = 32 * btd.shape[1] + 1                                              # beyond its table row
+    out = attend(q, kc, vc, sc, btd, cu, ld, 0.125, err=err)
+    assert err.item() == pkv.ERR_CONTEXT_RANGE and torch.all(out[60:130] == 0)
+    check(out[130:], q[130:], kc, vc, sc, bt[2:], lens[2:], new[2:], 0.125, "last")
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    """A chunk call and a decode call at the same time on two streams, and the same one after another."""
+    lens, new = [300, 900, 64], [64, 64, 64]
+    a = synth(lens, 16, 8, 128, 64, seed=4, new=new)
+    b = synth([700] * 20, 16, 8, 128, 64, seed=5)
+    one = attend(a[0], *a[1:4], a[5], None, a[6], 128 ** -0.5, n=64, workers=400)
+    two = decode(b[0], *b[1:4], b[5], b[6], 128 ** -0.5, workers=400)
+    wa = pkv.alloc_attention_workspace(a[0].shape[0], 16, 8, 128)
+    wb = pkv.alloc_workspace(20, 16, 8, 128)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    oa, ob = torch.empty_like(one), torch.empty_like(two)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        pkv.paged_attention_i8(a[0], *a[1:4], a[5], None, a[6], 128 ** -0.5, oa, wa, num_workers=400, new_per_seq=64,
+                               stream=s1)
+        pkv.paged_decode_i8(b[0], *b[1:4], b[5], b[6], 128 ** -0.5, ob, wb, num_workers=400, stream=s2)
+    torch.cuda.synchronize()
+    assert torch.equal(oa, one) and torch.equal(ob, two)
+
+
 # ------------------------------------------------------------------------------------------ copies
 @pytest.mark.parametrize("NB,bs,Hkv,D,n", [(64, 16, 8, 128, 20), (24, 256, 8, 128, 9), (40, 16, 1, 64, 13),
                                            (10, 32, 3, 64, 1), (300, 16, 2, 64, 140), (6, 1024, 5, 128, 3)])
