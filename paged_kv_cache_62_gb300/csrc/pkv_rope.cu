@@ -95,7 +95,7 @@ __device__ __forceinline__ void turn16(uint4 &a, uint4 &b, const float2 *cs)
     b = make_uint4(ub[0], ub[1], ub[2], ub[3]);
 }
 
-constexpr int kRopeWarps = 4;  // warps (token parts) a CTA
+constexpr int kRopeWarps = 2;  // warps (token parts) a CTA: small ones, whose last warp holds little back
 
 template <bool ADJ>
 __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams p)

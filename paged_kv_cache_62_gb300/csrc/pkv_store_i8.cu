@@ -107,13 +107,13 @@ __device__ __forceinline__ uint4 lifted(uint4 w)
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// One CTA per slot of the block list; its warps take the (kv head, K or V) pairs of the slot's scale block.
+// One CTA (or, for few slots, a few: blockIdx.y) per slot of the block list; its warps take the (kv head, K or V) pairs of the slot's scale block.
 // Slots: with new_per_seq each sequence has slots_per_seq of them (as many blocks as n rows can reach);
 // with offsets sequence b has those from cu[b] / 16 + 2 b on, which leaves room for the floor((n + 14) / 16)
 // + 1 blocks that n rows can reach, so a slot finds its sequence by a search over the offsets and no prefix
 // over blocks is needed.
 template <int D>
-__global__ void __launch_bounds__(kStoreThreads, 6) kv_store_i8_kernel(const StoreI8Params p)
+__global__ void __launch_bounds__(kStoreThreads, 5) kv_store_i8_kernel(const StoreI8Params p)
 {
     constexpr int LR = D / 8;        // lanes per row (16 bytes of bf16 each)
     constexpr int RPL = 32 / LR;     // rows per load of the warp
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kStoreThreads, 6) kv_store_i8_kernel(const Sto
     }
     const int64_t crow = int64_t(phys) * p.block_size + (base & (p.block_size - 1));  // cache row of the block
 
-    for (int w = warp; w < 2 * p.Hkv; w += nwarps) {
+    for (int w = warp + int(blockIdx.y) * nwarps; w < 2 * p.Hkv; w += nwarps * int(gridDim.y)) {
         const int which = w & 1, h = w >> 1;
         const uint16_t *x = (which ? p.v : p.k) + int64_t(h) * D + col;
         const int64_t stride = which ? p.v_stride : p.k_stride;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kStoreThreads, 6) kv_store_i8_kernel(const Sto
         // the block's largest magnitude; two bf16 a lane-word, compared as such (a NaN wins, infinities are seen)
         __nv_bfloat162 top = __float2bfloat162_rn(0.f);
 #pragma unroll
-        for (int j0 = 0; j0 < NV; j0 += 4) {  // four loads in flight: 42 registers a thread, three CTAs an SM
+        for (int j0 = 0; j0 < NV; j0 += 4) {  // four loads in flight a thread: 40 warps an SM
             uint4 in[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -323,9 +323,18 @@ extern "C" pkv_status pkv_kv_store_i8(const uint16_t *k, const uint16_t *v, int6
     const int64_t grid = new_per_seq > 0 ? int64_t(num_seqs) * p.slots_per_seq
                                          : int64_t(num_tokens) / kSB + 2 * int64_t(num_seqs);
     if (grid > INT32_MAX) return PKV_EBOUNDS;
-    const int threads = std::min(64 * num_kv_heads, kStoreThreads);
+    // Few slots (a decode step): small CTAs with one (kv head, K or V) a warp, several a slot, so that the step takes
+    // one warp's latency (64 rows of 8 kv heads: 4.8 -> 2.8 us).  Many: one CTA a slot, whose warps share the search
+    // for its sequence (22k prompt rows: 30.9 us against 31.5 with the others).
+    DeviceInfo dev;
+    if (!current_device_info(&dev)) return PKV_ECUDA;
+    const bool few = grid < 4 * int64_t(dev.sm_count);
+    const int threads = std::min(64 * num_kv_heads, few ? 128 : kStoreThreads);
+    const int parts = few ? (64 * num_kv_heads + threads - 1) / threads : 1;
+    if (parts > 65535) return PKV_EBOUNDS;
     const cudaError_t e = launch_pdl(head_dim == 64 ? kv_store_i8_kernel<64> : kv_store_i8_kernel<128>,
-                                     dim3(unsigned(grid)), dim3(threads), 0, reinterpret_cast<cudaStream_t>(stream), p);
+                                     dim3(unsigned(grid), unsigned(parts)), dim3(threads), 0,
+                                     reinterpret_cast<cudaStream_t>(stream), p);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return cuda_fail("kv_store_i8_kernel launch", e);
