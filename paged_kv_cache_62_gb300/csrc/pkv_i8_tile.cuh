@@ -229,4 +229,88 @@ __device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const L
     }
 }
 
+template <int D, int G>
+__device__ __noinline__ void merge_pieces_i8(const DecodeParams &p, const long long *bound, int sf, int sl,
+                                             long long x0, int g, int h, int b, int kvh, int nvh, int lane)
+{
+    constexpr int PER = D / 32;                                   // output values per lane
+    constexpr int HB = G < 8 ? G : 8;                             // heads merged together
+    constexpr int BATCH = 64 / (HB * PER) < 8 ? 64 / (HB * PER) : 8;  // pieces whose values are in flight
+    using Vec = typename std::conditional<PER == 4, float4, float2>::type;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
+#pragma unroll 1
+    for (int h0 = 0; h0 < nvh; h0 += HB) {
+        float M[HB], L[HB], a[HB][PER];
+#pragma unroll
+        for (int i = 0; i < HB; ++i) {
+            M[i] = -INFINITY;
+            L[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) a[i][e] = 0.f;
+        }
+#pragma unroll 1
+        for (int s0 = sf; s0 <= sl; s0 += 32) {
+            const int s = s0 + lane;
+            const bool use = s <= sl && bound[s + 1] > bound[s];  // empty slices left nothing
+            const int sk = use ? s : sf;
+            const int slot = int(((slots_by_slice(p.B, p.nhg) ? 2LL * sk + ((sk == sf && x0 != bound[sf]) ? 1 : 0)
+                                                              : sk + (long long)b * p.nhg + g) * p.hg + h));
+            float2 st[HB];
+#pragma unroll
+            for (int i = 0; i < HB; ++i) st[i] = __ldcg(ml + (long long)slot * G + min(h0 + i, G - 1));
+            const int n = min(32, sl - s0 + 1);
+            float w[HB];  // the lane's piece's weight
+#pragma unroll
+            for (int i = 0; i < HB; ++i) {
+                float mx = use ? st[i].x : -INFINITY;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+                mx = fmaxf(mx, M[i]);
+                // a head without a valid token in any piece so far keeps its zero state
+                const float r = mx == -INFINITY ? 1.0f : ex2(M[i] - mx);
+                w[i] = use && st[i].x != -INFINITY ? ex2(st[i].x - mx) : 0.f;
+                L[i] = L[i] * r + warp_sum(use ? w[i] * st[i].y : 0.f);
+#pragma unroll
+                for (int e = 0; e < PER; ++e) a[i][e] *= r;
+                M[i] = mx;
+            }
+#pragma unroll 1
+            for (int k = 0; k < n; k += BATCH) {
+                Vec v[BATCH][HB];
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j) {
+                    const long long sj = __shfl_sync(kFull, slot, min(k + j, n - 1));
+#pragma unroll
+                    for (int i = 0; i < HB; ++i)
+                        v[j][i] = __ldcg(reinterpret_cast<const Vec *>(
+                            p.ws_acc + (sj * G + min(h0 + i, G - 1)) * D + lane * PER));
+                }
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j)
+#pragma unroll
+                    for (int i = 0; i < HB; ++i) {
+                        const float wj = __shfl_sync(kFull, w[i], min(k + j, n - 1));
+                        const float f = k + j < n ? wj : 0.f;
+                        const float *x = reinterpret_cast<const float *>(&v[j][i]);
+#pragma unroll
+                        for (int e = 0; e < PER; ++e) a[i][e] = fmaf(f, x[e], a[i][e]);
+                    }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < HB; ++i) {
+            const int hh = h0 + i;
+            if (hh >= nvh) break;
+            const float inv = 1.0f / L[i];
+            uint16_t *o = p.out + ((int64_t(b) * p.qstride + hh / p.gq) * p.Hq + int64_t(kvh) * p.gq + hh % p.gq) * D +
+                          lane * PER;
+            if constexpr (PER == 4)
+                *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16x2(a[i][0] * inv, a[i][1] * inv),
+                                                           pack_bf16x2(a[i][2] * inv, a[i][3] * inv));
+            else
+                *reinterpret_cast<uint32_t *>(o) = pack_bf16x2(a[i][0] * inv, a[i][1] * inv);
+        }
+    }
+}
+
 }  // namespace pkv
