@@ -88,23 +88,16 @@ __device__ __forceinline__ uint64_t global_ns()
     return t;
 }
 
-// Warp-collective: every lane must call it; the result is the same in all lanes.  The timer is read only once
-// a wait has failed 256 times: a read takes long enough to delay a wait that was about to end.
+// Warp-collective: every lane must call it; the result is the same in all lanes.
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity)
 {
     const uint32_t a = smem_u32(bar);
     bool ok = mbar_try_wait(a, parity);
     if (!ok) {
-        uint64_t t0 = 0;
+        const uint64_t t0 = global_ns();
         for (uint32_t i = 1; !ok; ++i) {
             ok = mbar_try_wait(a, parity);
-            if (!ok && (i & 255u) == 0) {
-                const uint64_t now = global_ns();
-                if (t0 == 0)
-                    t0 = now;
-                else if (now - t0 > kWaitLimitNs)
-                    break;
-            }
+            if (!ok && (i & 255u) == 0 && global_ns() - t0 > kWaitLimitNs) break;
         }
     }
     return __all_sync(kFull, ok);
