@@ -11,6 +11,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <exception>
 
 #include "../../include/pkv.h"
@@ -146,6 +147,13 @@ double real(PyObject *o)
 {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw Refused();
+    return v;
+}
+
+int truth(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Refused();
     return v;
 }
 
@@ -297,7 +305,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n)
         const Rows k_out(r.dev, a[5], "k_out");
         if (!k_out.same(r.k)) refuse(what, "shape mismatch");
         return pkv_rope(r.q.p, r.q.stride, r.k.p, r.k.stride, r.pos, r.axes, r.inv, r.freq_axis, i32(r.q.T, what),
-                        i32(r.q.H, what), i32(r.k.H, what), i32(r.q.D, what), 2 * r.half, PyObject_IsTrue(a[7]),
+                        i32(r.q.H, what), i32(r.k.H, what), i32(r.q.D, what), 2 * r.half, truth(a[7]),
                         r.q_out.p, r.q_out.stride, k_out.p, k_out.stride, r.dev.err(a[8]), r.dev.stream(a[9]));
     });
 }
@@ -316,7 +324,7 @@ PyObject *rope_store(PyObject *, PyObject *const *a, Py_ssize_t n)
             refuse(what, "shape mismatch");
         return pkv_rope_store(r.q.p, r.q.stride, r.k.p, r.k.stride, v.p, v.stride, r.pos, r.axes, r.inv, r.freq_axis,
                               slots, i32(r.q.T, what), i32(r.q.H, what), i32(r.k.H, what), i32(r.q.D, what),
-                              2 * r.half, PyObject_IsTrue(a[10]), r.q_out.p, r.q_out.stride,
+                              2 * r.half, truth(a[10]), r.q_out.p, r.q_out.stride,
                               static_cast<uint16_t *>(kc.data_ptr()), static_cast<uint16_t *>(vc.data_ptr()),
                               i32(kc.size(0), what), i32(kc.size(1), what), r.dev.err(a[11]), r.dev.stream(a[12]));
     });

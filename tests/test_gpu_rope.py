@@ -131,3 +131,46 @@ def test_bad_slots_and_axes_are_flagged():
     axis[3] = 2
     pkv.rope_store(q, k, v, pos, inv, slots.clamp(-1, 5), qo, kc, vc, freq_axis=axis, err_word=err)
     assert err.item() == pkv.ERR_AXIS_RANGE
+
+
+def test_captured_rope_store_replays():
+    T, Hq, Hkv, D, bs, NB = 3, 16, 8, 128, 16, 4
+    q, k, v = inputs(T, Hq, Hkv, D, 5, wide=False)
+    inv = freqs(D)
+    pos, slots = (torch.zeros(T, dtype=torch.int32, device="cuda") for _ in range(2))
+    slots.copy_(torch.tensor([-1, -1, -1], dtype=torch.int32))
+    kc, vc = (torch.zeros(NB, bs, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    qo = torch.empty_like(q)
+    invd = torch.from_numpy(inv).cuda()
+    call = lambda: pkv.rope_store(q, k, v, pos, invd, slots, qo, kc, vc)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for p, s in (([0, 1, 2], [5, 6, 40]), ([9, 77, 3], [-1, 63, 0])):
+        pos.copy_(torch.tensor(p, dtype=torch.int32))
+        slots.copy_(torch.tensor(s, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        close(qo, q, np.array([p]), inv, np.zeros(D // 2, int), False, "q")
+        at = [i for i in range(T) if s[i] >= 0]
+        rows = [s[i] for i in at]
+        close(kc.view(-1, Hkv, D)[rows], k[at], np.array([[p[i] for i in at]]), inv, np.zeros(D // 2, int), False, "k")
+        assert torch.equal(vc.view(-1, Hkv, D)[rows], v[at])
+
+
+def test_an_error_of_the_interleaved_argument_is_passed_on():
+    class Neither:
+        def __bool__(self):
+            raise OverflowError("neither")
+
+    q, k, v = inputs(2, 2, 1, 64, 0)
+    qo, ko = torch.zeros(q.shape, dtype=q.dtype, device="cuda"), torch.zeros(k.shape, dtype=k.dtype, device="cuda")
+    pos, inv = torch.ones(2, dtype=torch.int32, device="cuda"), torch.from_numpy(freqs(64)).cuda()
+    with pytest.raises(OverflowError, match="neither"):
+        pkv.rope(q, k, pos, inv, qo, ko, interleaved=Neither())
+    assert not qo.any() and not ko.any()
