@@ -107,8 +107,8 @@ __device__ __forceinline__ uint4 lifted(uint4 w)
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// One CTA (or, for few slots, a few: blockIdx.y) per slot of the block list; its warps take the (kv head, K or V) pairs of the slot's scale block.
-// Slots: with new_per_seq each sequence has slots_per_seq of them (as many blocks as n rows can reach);
+// One CTA (or, for few slots, a few: blockIdx.y) per slot of the block list; its warps take the (kv head, K or V)
+// pairs of the slot's scale block.  Slots: with new_per_seq each sequence has slots_per_seq of them (as many blocks as n rows can reach);
 // with offsets sequence b has those from cu[b] / 16 + 2 b on, which leaves room for the floor((n + 14) / 16)
 // + 1 blocks that n rows can reach, so a slot finds its sequence by a search over the offsets and no prefix
 // over blocks is needed.
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kStoreThreads, 5) kv_store_i8_kernel(const Sto
         const int32_t r1 = __ldg(p.cu_seqlens + b + 1);
         i = int32_t(blockIdx.x) - ((max(0, r0) >> 4) + 2 * b);
         n = r1 - r0;
-        if (r0 < 0 || n < 0 || r1 > p.num_tokens || (b == 0 && r0 != 0)) {
+        if (r0 < 0 || r1 < r0 || r1 > p.num_tokens || (b == 0 && r0 != 0)) {
             if (threadIdx.x == 0) flag_error(p.err, PKV_ERR_CONTEXT_RANGE);
             return;
         }
@@ -158,8 +158,9 @@ __global__ void __launch_bounds__(kStoreThreads, 5) kv_store_i8_kernel(const Sto
         return;
     }
     const int32_t p0 = L - n;                       // position of the first new row
-    const int32_t base = (p0 & ~(kSB - 1)) + i * kSB;  // position of this block's first row
-    if (base >= L) return;
+    const int64_t base64 = int64_t(p0 & ~(kSB - 1)) + int64_t(i) * kSB;  // position of this block's first row
+    if (base64 >= L) return;
+    const int32_t base = int32_t(base64);
     const int32_t first = max(p0 - base, 0), last = min(L - base, kSB);  // new rows of the block
     const int32_t phys = __ldg(p.block_tables + int64_t(b) * p.max_blocks + (base >> p.log2_bs));
     const int row = lane / LR, col = (lane - row * LR) * 8;

@@ -455,6 +455,72 @@ def test_two_streams_with_workspaces_of_their_own():
     assert torch.equal(oa, one) and torch.equal(ob, two)
 
 
+def test_one_workspace_serves_calls_of_every_kind():
+    """bf16 and int8 calls, decode and several tokens, few and many CTAs, one after another on one workspace:
+    each gives what it gives on a workspace of its own."""
+    Hq, Hkv, D, bs = 16, 8, 128, 64
+    lens, n = [640, 70, 1300, 200], 40
+    qa, kc, vc, sc, bt, btd, ld = synth(lens, Hq, Hkv, D, bs, seed=21, new=[n] * 4)
+    qd = qa[:4].contiguous()
+    kb, vb = (torch.randn(kc.shape, device="cuda").bfloat16() for _ in range(2))
+    scale = D ** -0.5
+
+    def bf16(q, n, ws, workers):
+        out = torch.empty_like(q)
+        if n == 1:
+            pkv.paged_decode(q, kb, vb, btd, ld, scale, out, ws, num_workers=workers)
+        else:
+            pkv.paged_attention(q, kb, vb, btd, None, ld, scale, out, ws, num_workers=workers, new_per_seq=n)
+        return out
+
+    def i8(q, n, ws, workers):
+        if n == 1:
+            return decode(q, kc, vc, sc, btd, ld, scale, workers, ws)
+        return attend(q, kc, vc, sc, btd, None, ld, scale, n, workers, ws)
+
+    q3 = qa[:12].contiguous()
+    calls = [(f, q, m, w) for w in (0, 37, 300) for f, q, m in
+             ((bf16, qd, 1), (i8, qd, 1), (i8, qa, n), (bf16, qa, n), (i8, q3, 3), (bf16, q3, 3))]
+    fresh = [f(q, m, pkv.alloc_attention_workspace(4 * n, Hq, Hkv, D), w) for f, q, m, w in calls]
+    ws = pkv.alloc_attention_workspace(4 * n, Hq, Hkv, D)
+    order = np.random.default_rng(2).permutation(4 * len(calls)) % len(calls)
+    for i in order:
+        f, q, m, w = calls[i]
+        got = f(q, m, ws, w)
+        # (without a number of workers the split may follow earlier calls' times, and with it the last bits)
+        assert torch.equal(got, fresh[i]) if w else torch.isfinite(got).all(), (i, f.__name__, m, w)
+
+
+def test_codes_beyond_32_bits():
+    """A cache of more than 2^31 codes an array (and pages behind its 2^31st): store, copy, decode and a chunk on
+    its last pages."""
+    NB, bs, Hq, Hkv, D = 2100, 1024, 16, 8, 128
+    assert NB * bs * Hkv * D > 2 ** 31 + bs * Hkv * D
+    kc, vc, sc = pkv.alloc_i8_cache(NB, bs, Hkv, D)
+    n, L = 50, 1060
+    bt = np.array([[NB - 1, NB - 4]], np.int32)
+    btd, ld = torch.from_numpy(bt).cuda(), torch.tensor([L], dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn(L, Hkv, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(n, Hq, D, generator=g, device="cuda").bfloat16()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkv.kv_store_i8(k, v, kc, vc, sc, btd, ld, new_per_seq=L, err_word=err)
+    pkv.copy_blocks_i8(kc, vc, sc, torch.tensor([[NB - 4, NB - 2]], dtype=torch.int32, device="cuda"), err)
+    bt[0, 1] = NB - 2
+    btd.copy_(torch.from_numpy(bt))
+    out = attend(q, kc, vc, sc, btd, None, ld, D ** -0.5, n=n, err=err)
+    one = decode(q[-1:].contiguous(), kc, vc, sc, btd, ld, D ** -0.5, err=err)
+    assert err.item() == 0
+    small = [np.zeros((2, bs, Hkv, D), np.int8) for _ in range(2)] + [np.zeros((2, bs // SB, Hkv, 2), np.float32)]
+    table = np.array([[0, 1]], np.int32)
+    store_i8(k.double().cpu().numpy(), v.double().cpu().numpy(), *small, table, [L], [L])
+    for got, want in zip((kc, vc, sc), small):
+        assert np.array_equal(got[[NB - 1, NB - 2]].cpu().numpy(), want)
+    small = [torch.from_numpy(t) for t in small]
+    check(out, q, *small, table, [L], [n], D ** -0.5, "chunk")
+    check(one, q[-1:], *small, table, [L], [1], D ** -0.5, "decode")
+
+
 # ------------------------------------------------------------------------------------------ copies
 @pytest.mark.parametrize("NB,bs,Hkv,D,n", [(64, 16, 8, 128, 20), (24, 256, 8, 128, 9), (40, 16, 1, 64, 13),
                                            (10, 32, 3, 64, 1), (300, 16, 2, 64, 140), (6, 1024, 5, 128, 3)])
@@ -566,3 +632,52 @@ def test_captured_step_replays():
         store_i8(k.double().cpu().numpy(), v.double().cpu().numpy(), *ref, bt, lens, [1] * 4)
         check(out, q, torch.from_numpy(ref[0]), torch.from_numpy(ref[1]), torch.from_numpy(ref[2]), bt, lens, [1] * 4,
               D ** -0.5, f"replay {i}")
+
+
+def test_captured_chunks_of_a_padded_batch_replay():
+    """Store and several-token attention captured once for up to 96 rows of up to 5 sequences, replayed with batches
+    of other lengths and fewer sequences (the offsets past the last one repeat): rows behind the last sequence are
+    not stored, and what they get is zeros and a flag."""
+    Hq, Hkv, D, bs, T = 14, 2, 64, 32, 96
+    top = [200, 64, 333, 90, 128]
+    q, kc, vc, sc, bt, btd, ld = synth(top, Hq, Hkv, D, bs, seed=9, new=[T] + [0] * 4)
+    k, v = (torch.zeros(T, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cu = torch.zeros(6, dtype=torch.int32, device="cuda")
+    out, err = torch.empty_like(q), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = pkv.alloc_attention_workspace(T, Hq, Hkv, D)
+
+    def step():
+        pkv.kv_store_i8(k, v, kc, vc, sc, btd, ld, cu, err_word=err)
+        pkv.paged_attention_i8(q, kc, vc, sc, btd, cu, ld, D ** -0.5, out, ws, err_word=err)
+
+    def batch(lens, new):
+        ld.copy_(torch.tensor(lens, dtype=torch.int32))
+        cu.copy_(torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32))
+
+    batch(top, [0] * 5)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    g = torch.Generator(device="cuda").manual_seed(4)
+    ref = [t.cpu().numpy().copy() for t in (kc, vc, sc)]
+    for lens, new in (([160, 64, 300, 80, 100], [20, 20, 20, 20, 16]), ([200, 0, 333, 0, 0], [40, 0, 33, 0, 0]),
+                      ([161, 1, 301, 81, 101], [1, 1, 1, 1, 1]), ([96, 0, 0, 0, 0], [96, 0, 0, 0, 0])):
+        batch(lens, new)
+        for t in (k, v, q):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+        out.fill_(float("nan"))
+        err.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        n = sum(new)
+        assert err.item() == (pkv.ERR_CONTEXT_RANGE if n < T else 0)
+        store_i8(k.double().cpu().numpy(), v.double().cpu().numpy(), *ref, bt, lens, new)
+        for got, want in zip((kc, vc, sc), ref):
+            assert np.array_equal(got.cpu().numpy(), want, equal_nan=True)
+        check(out[:n], q[:n], *(torch.from_numpy(t) for t in ref), bt, lens, new, D ** -0.5, str(new))
+        assert torch.all(out[n:] == 0)
