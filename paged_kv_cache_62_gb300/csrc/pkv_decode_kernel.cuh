@@ -52,7 +52,7 @@
 // instantiates the bf16-cache kernels for up to 8 virtual heads and defines
 // the C entry points, pkv_decode_wide.cu the bf16 ones for 9 to 16,
 // pkv_decode_qs.cu the query-split ones, pkv_decode_tc5.cu their tensor-memory
-// variant, pkv_decode_fp8.cu the E4M3 ones.
+// variant, pkv_decode_fp8.cu the E4M3 ones, pkv_decode_i8*.cu those of int8 caches.
 #pragma once
 #include <cuda_fp16.h>
 

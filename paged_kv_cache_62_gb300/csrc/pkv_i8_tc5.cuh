@@ -19,12 +19,16 @@
 // on the SM and a line of it is gone from the nearest instruction cache when a warp comes round to it a unit
 // later, so the passes over the keys are loops of 16 keys, waits are as short as they can be
 // (mbar_wait_lean), and the exchange between two threads of a row that the bf16 CTA makes every unit is gone.
+// Measured: 64 new tokens of each of 64 sequences of 512-4096 (16 / 8 heads of 128) 167 us, 480 TFLOP/s, 2.1 TB/s
+// of codes; 3300 cycles a 128-key tile, of which its shared-memory traffic alone needs 1790 (copies in 256,
+// converters 256 read and 512 written, scores 512, outputs 256).  One group of warps over both halves of the keys,
+// as in the bf16 CTA: 179 us; straight-line passes: 283 us; two converting warps: 326 us; warp-level tiles: 535 us.
 //
 // Ordering: codes and scales landed -> full[s]; K operand written -> kready (4 warps), read -> kfree
 // (tcgen05.commit); V likewise vready, vfree; scales prepared -> dready[s]; stage released -> empty[s] (4
 // converting warps, 8 softmax warps, and the warp that issues output products); scores -> sfull[w]; weights ->
-// pfull[w] (4 warps); output product done -> odone[w]; a segment's Q written -> qready (8 warps: after the last scores of the segment before it are in);
-// all softmax warps met -> team.  A group passes the end of a segment only with the other, so no barrier runs
+// pfull[w] (4 warps); output product done -> odone[w]; a segment's Q written -> qready (8 warps: after the last scores of
+// the segment before it are in); all softmax warps met -> team.  A group passes the end of a segment only with the other, so no barrier runs
 // two phases ahead of a waiter.
 #pragma once
 

@@ -16,6 +16,11 @@
 // output of every sub-tile.  Next to a subtraction per pair that saves 128 of about 590 instructions a tile;
 // what the detour costs is fp32 rounding at 1152 times a sub-tile's weights, 2^-13.8 of a code each time.  16-row
 // tiles subtract from V's codes (their two halves would need twice the products).
+//
+// What bounds it: the consumers' latency, two warps a scheduler with few independent chains.  64 sequences of
+// 512-4096 (16 / 8 heads of 128): 58.2 us = 5.15 TB/s (0.76 of the copy rate; 61.6 us with a subtraction per pair of
+// codes); 4 new tokens of each (16-row tiles) 68.8 us; 256 sequences of 1-32768, whose long segments hide it,
+// 217 us = 6.46 TB/s (0.95).
 #pragma once
 
 #include "pkv_decode_kernel.cuh"

@@ -6,7 +6,9 @@ Store and copies must match the 64-bit reference bit for bit.  Attention must st
 of the 64-bit result over the same codes and scales: the bf16 output rounds by at most 2^-8 of itself; each
 weight rounds to f16 by at most 2^-11 of itself, which moves the output by at most 2^-11 A; the fp32 scores,
 exponentials, sums and merges have another 2^-11 A (a score error of 2^-12 at the sizes below: scores stay
-under 2^6, their fp32 sums of at most 128 products err by less than 2^-14 of that).
+under 2^6, their fp32 sums of at most 128 products err by less than 2^-14 of that; where codes enter the sum
+1152 too large, its intermediate values reach 1152 sum|q| times scale and K scale, about 280 at these sizes, and
+eight chained products that each lose up to 2^-23 of that come to about the same 2^-12).
 """
 import numpy as np
 import pytest
