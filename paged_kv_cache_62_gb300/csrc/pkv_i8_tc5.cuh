@@ -372,13 +372,17 @@ __device__ void tc5_softmax_warps_i8(const DecodeParams &p, const CtaLayout &lay
         uint4 v[DH / 8];
 #pragma unroll
         for (int k = 0; k < DH / 8; ++k) v[k] = qi < sg.cnt ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
-        uint32_t mx = 0u;
+        // (two values at a time, as bf16: a NaN wins)
+        __nv_bfloat162 top = __float2bfloat162_rn(0.f);
 #pragma unroll
         for (int k = 0; k < DH / 8; ++k) {
             const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx = max(mx, max(u[e] & 0x7fffu, (u[e] >> 16) & 0x7fffu));
+            for (int e = 0; e < 4; ++e)
+                top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&u[e])));
         }
+        const uint32_t tb = *reinterpret_cast<const uint32_t *>(&top);
+        uint32_t mx = max(tb & 0x7fffu, (tb >> 16) & 0x7fffu);
         qmax[wg * 128 + row] = mx;
         if (!meet()) return false;
         mx = max(mx, qmax[(1 - wg) * 128 + row]);
@@ -539,6 +543,7 @@ __device__ void tc5_softmax_warps_i8(const DecodeParams &p, const CtaLayout &lay
             const int piece = mt.u - u_first + 1;
             const bool whole = piece == mt.n;  // the whole segment ran here: output; else a piece
             const float inv = !whole ? 1.0f : (L > 0.f || L != L ? 1.0f / L : 0.f);
+            const float g0 = has0 ? f0 * inv : 0.f, g1 = has1 ? f1 * inv : 0.f;
             uint16_t *orow =
                 p.out + ((long long)(mt.row0 + qi) * p.Hq + (long long)mt.g * p.gq + qh) * D;
             const long long x0 = (long long)p.nhg * scan[mt.b] + (long long)mt.g * mt.n;
@@ -547,13 +552,11 @@ __device__ void tc5_softmax_warps_i8(const DecodeParams &p, const CtaLayout &lay
 #pragma unroll 1
             for (int c0 = wg * DH; c0 < (wg + 1) * DH; c0 += 16) {
                 uint32_t r0[16], r1[16];
-                if (has0) tmem_ld16(obuf + uint32_t(c0), r0);
-                if (has1) tmem_ld16(obuf + 128u + uint32_t(c0), r1);
+                tmem_ld16(obuf + (has0 ? 0u : 128u) + uint32_t(c0), r0);  // (a group without an output: the other's,
+                tmem_ld16(obuf + (has1 ? 128u : 0u) + uint32_t(c0), r1);  // times zero)
                 float v[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    v[i] = ((has0 ? f0 * __uint_as_float(r0[i]) : 0.f) + (has1 ? f1 * __uint_as_float(r1[i]) : 0.f)) *
-                           inv;
+                for (int i = 0; i < 16; ++i) v[i] = fmaf(g0, __uint_as_float(r0[i]), g1 * __uint_as_float(r1[i]));
                 if (whole) {
                     if (row_ok) {
 #pragma unroll
