@@ -286,35 +286,46 @@ template <int D>
 __device__ __noinline__ void tc5_merge_i8(const DecodeParams &p, const long long *bound, int sf, int sl, long long x0,
                                           int g, int b, int row, int half, uint16_t *out)
 {
-    constexpr int C = 32;  // columns at a time: a piece's eight loads in flight together
+    constexpr int C = 32;  // columns at a time: the eight loads of two pieces each in flight together
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
     auto tile_of = [&](int sk) { return tc5_piece_tile(p, sk, !(sk == sf && x0 != bound[sf]), b, g); };
+    auto next = [&](int sk) {  // the next slice that is not empty (an empty one left nothing)
+        do ++sk;
+        while (sk <= sl && bound[sk + 1] <= bound[sk]);
+        return sk;
+    };
 #pragma unroll 1
     for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += C) {
         float M = -INFINITY, L = 0.f, a[C];
 #pragma unroll
         for (int e = 0; e < C; ++e) a[e] = 0.f;
 #pragma unroll 1
-        for (int sk = sf; sk <= sl; ++sk) {
-            if (bound[sk + 1] <= bound[sk]) continue;  // an empty slice left nothing
-            const long long tile = tile_of(sk);
-            const float2 st = __ldcg(ml + tile * 128 + row);
-            const float4 *src = reinterpret_cast<const float4 *>(p.ws_acc + tile * 128 * D) + (c0 / 4) * 128 + row;
-            float4 v[C / 4];
+        for (int sk = sf; sk <= sl;) {
+            const int s2 = next(sk);
+            const bool two = s2 <= sl;  // else the piece once more, with weight 0
+            const long long t1 = tile_of(sk), t2 = tile_of(two ? s2 : sk);
+            const float2 m1 = __ldcg(ml + t1 * 128 + row);
+            float2 m2 = __ldcg(ml + t2 * 128 + row);
+            const float4 *p1 = reinterpret_cast<const float4 *>(p.ws_acc + t1 * 128 * D) + (c0 / 4) * 128 + row;
+            const float4 *p2 = reinterpret_cast<const float4 *>(p.ws_acc + t2 * 128 * D) + (c0 / 4) * 128 + row;
+            float4 v[C / 4], w[C / 4];
 #pragma unroll
-            for (int k = 0; k < C / 4; ++k) v[k] = __ldcg(src + k * 128);
-            if (st.x == -INFINITY) continue;
-            const float Mn = fmaxf(M, st.x);
-            const float r = M == -INFINITY ? 0.f : ex2(M - Mn), f = ex2(st.x - Mn);
+            for (int k = 0; k < C / 4; ++k) v[k] = __ldcg(p1 + k * 128);
+#pragma unroll
+            for (int k = 0; k < C / 4; ++k) w[k] = __ldcg(p2 + k * 128);
+            if (!two) m2.x = -INFINITY;
+            const float Mn = fmaxf(M, fmaxf(m1.x, m2.x)), at = Mn == -INFINITY ? 0.f : Mn;
+            const float r = ex2(M - at), f1 = ex2(m1.x - at), f2 = ex2(m2.x - at);
             M = Mn;
-            L = fmaf(f, st.y, L * r);
+            L = fmaf(f1, m1.y, fmaf(f2, m2.y, L * r));
 #pragma unroll
             for (int k = 0; k < C / 4; ++k) {
-                a[4 * k] = fmaf(f, v[k].x, a[4 * k] * r);
-                a[4 * k + 1] = fmaf(f, v[k].y, a[4 * k + 1] * r);
-                a[4 * k + 2] = fmaf(f, v[k].z, a[4 * k + 2] * r);
-                a[4 * k + 3] = fmaf(f, v[k].w, a[4 * k + 3] * r);
+                a[4 * k] = fmaf(f1, v[k].x, fmaf(f2, w[k].x, a[4 * k] * r));
+                a[4 * k + 1] = fmaf(f1, v[k].y, fmaf(f2, w[k].y, a[4 * k + 1] * r));
+                a[4 * k + 2] = fmaf(f1, v[k].z, fmaf(f2, w[k].z, a[4 * k + 2] * r));
+                a[4 * k + 3] = fmaf(f1, v[k].w, fmaf(f2, w[k].w, a[4 * k + 3] * r));
             }
+            sk = two ? next(s2) : s2;
         }
         const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
         if (out) {
