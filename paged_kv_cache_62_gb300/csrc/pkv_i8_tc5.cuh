@@ -19,10 +19,12 @@
 // on the SM and a line of it is gone from the nearest instruction cache when a warp comes round to it a unit
 // later, so the passes over the keys are loops of 16 keys, waits are as short as they can be
 // (mbar_wait_lean), and the exchange between two threads of a row that the bf16 CTA makes every unit is gone.
-// Measured: 64 new tokens of each of 64 sequences of 512-4096 (16 / 8 heads of 128) 167 us, 480 TFLOP/s, 2.1 TB/s
-// of codes; 3300 cycles a 128-key tile, of which its shared-memory traffic alone needs 1790 (copies in 256,
+// Measured: 64 new tokens of each of 64 sequences of 512-4096 (16 / 8 heads of 128) 155 us, 517 TFLOP/s, 2.3 TB/s
+// of codes; 3100 cycles a 128-key tile, of which its shared-memory traffic alone needs 1790 (copies in 256,
 // converters 256 read and 512 written, scores 512, outputs 256).  One group of warps over both halves of the keys,
 // as in the bf16 CTA: 179 us; straight-line passes: 283 us; two converting warps: 326 us; warp-level tiles: 535 us.
+// A segment's end takes 9500 cycles (the next Q 3400, outputs 2300, counting 2100) and comes at the pace of its
+// instruction fetch: 180 instructions less there took 8 us off.
 //
 // Ordering: codes and scales landed -> full[s]; K operand written -> kready (4 warps), read -> kfree
 // (tcgen05.commit); V likewise vready, vfree; scales prepared -> dready[s]; stage released -> empty[s] (4
