@@ -136,6 +136,13 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
                 a.requested_workers = int32_t(std::max<int64_t>(1, units_max)) * p.cons;
             }
         }
+        // int8 caches: also with more units than SMs, as long as every segment has an SM (decode batches of 24 to 140
+        // sequences of 130 to 500 tokens, 16 / 8 heads of 128 and 12 / 4 of 64: split 18-27 us, a CTA a segment 10-19;
+        // with 16 units a segment the split is as fast, and faster where lengths differ).
+        if (i8 && !qs && per_seg <= kSegmentUnits && int64_t(num_seqs) * p.nhg <= dev.sm_count) {
+            p.per_segment = 1;
+            a.requested_workers = num_seqs * p.nhg * p.cons;
+        }
         // int8 caches, few segments: a segment's pieces are counted in and folded one after another (about half a
         // microsecond each), its units streamed by as many CTAs as it has pieces, so the sum of both is least at a
         // number of pieces that grows with the root of the units.  Measured on 10 batches of 1 to 16 sequences of
@@ -428,10 +435,22 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     // chunks of a sequence's queries, one entry per row; few new tokens per sequence on average (at
     // most two regular chunks): chunks of qg on regular CTAs, else chunks of 8 * qg on query-split ones.
     // The row arrays sit after the decode workspace.
-    const bool qs = int64_t(num_rows) > 2 * int64_t(qg) * num_seqs;
-    // (query-split int8 entries fill the tensor-memory tile: as many whole queries as 128 rows hold)
-    const int32_t chunk = !qs ? qg : ct == kI8 ? 128 / (num_q_heads / num_kv_heads)
-                                              : entry_queries(num_q_heads, num_kv_heads);
+    // (Query-split int8 entries fill the tensor-memory tile: as many whole queries as 128 rows hold.)
+    const int32_t tile = 128 / std::min(num_q_heads / num_kv_heads, 128);
+    bool qs = int64_t(num_rows) > 2 * int64_t(qg) * num_seqs;
+    if (ct == kI8 && !qs && int64_t(num_rows) > int64_t(qg) * num_seqs) {
+        // Between one and two chunks a sequence: regular CTAs read the keys twice, but take larger calls as fast; in
+        // calls of few tiles their list, one entry a row, most of them empty, costs more (16 new tokens, 16 / 8 heads
+        // of 128: 5 sequences of 200 tokens 48 -> 16 us, of 2000 59 -> 40 us, 32 of 300 43 -> 38 us; 64 of 2000 would
+        // take 111 us against 106).
+        DeviceInfo dev;
+        if (!current_device_info(&dev)) return PKV_ECUDA;
+        const int64_t tiles = int64_t(num_seqs) * num_kv_heads *
+                              ((std::min<int64_t>(max_context_len, int64_t(max_blocks_per_seq) * std::max(block_size, 0)) +
+                                kTc5Keys - 1) / kTc5Keys);
+        qs = tiles < 8 * int64_t(dev.sm_count) && num_rows / tile + num_seqs <= num_rows;
+    }
+    const int32_t chunk = !qs ? qg : ct == kI8 ? tile : entry_queries(num_q_heads, num_kv_heads);
     uint8_t *wsb = static_cast<uint8_t *>(workspace);
     const size_t dec_bytes = need - 4 * rows_bytes(num_rows);
     int32_t *row_seq = reinterpret_cast<int32_t *>(wsb + dec_bytes);

@@ -267,6 +267,23 @@ def test_decode_head_groups_and_repeated_calls(Hkv):
         check(out, q, kc, vc, sc, bt, lens, [1] * 5, 128 ** -0.5, f"Hkv{Hkv} call{call}")
 
 
+@pytest.mark.parametrize("B", [40, 152, 160])
+@pytest.mark.parametrize("heads,D,bs", [((16, 8), 128, 16), ((12, 4), 64, 64)])
+def test_decode_batches_of_short_sequences(B, heads, D, bs):
+    """More units than SMs, at most eight a sequence: with and without an SM for every sequence."""
+    Hq, Hkv = heads
+    lens = [1 + (61 * b) % 250 for b in range(B)]
+    lens[3] = 0
+    q, kc, vc, sc, bt, btd, ld = synth(lens, Hq, Hkv, D, bs, seed=B + D)
+    ws = pkv.alloc_workspace(B, Hq, Hkv, D)
+    for call in range(3):
+        out = decode(q, kc, vc, sc, btd, ld, D ** -0.5, ws=ws, max_context_len=250)
+        assert torch.all(out[3] == 0)
+        keep = [b for b in range(B) if b != 3]
+        check(out[keep], q[keep], kc, vc, sc, bt[keep], [lens[b] for b in keep], [1] * len(keep), D ** -0.5,
+              f"B{B} {heads} call{call}")
+
+
 @pytest.mark.parametrize("workers", [0, 1, 7, 333, 4096])
 def test_decode_splits(workers):
     lens = [1, 15, 17, 40, 300, 0, 3000, 2, 513]
@@ -379,6 +396,20 @@ def test_attention_with_any_softmax_scale(n, scale):
     sc *= 0.3                                                  # scores stay under 2^6
     out = attend(q, kc, vc, sc, btd, None, ld, scale, n=n)
     check(out, q, kc, vc, sc, bt, lens, new, scale, f"n{n} scale{scale}")
+
+
+@pytest.mark.parametrize("heads,D,bs,new", [((16, 1), 128, 16, [1] * 20 + [2]), ((16, 1), 64, 64, [2] * 9 + [1, 3]),
+                                            ((14, 2), 64, 16, [3] * 6 + [0, 2]), ((16, 8), 128, 32, [9, 16, 12, 1, 14]),
+                                            ((11, 1), 128, 32, [1] * 40 + [0, 3])])
+def test_attention_of_between_one_and_two_chunks_a_sequence(heads, D, bs, new):
+    Hq, Hkv = heads
+    lens = [n + 37 * i % 300 if n else 0 for i, n in enumerate(new)]
+    q, kc, vc, sc, bt, btd, ld = synth(lens, Hq, Hkv, D, bs, seed=Hq + D, new=new)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = attend(q, kc, vc, sc, btd, cu, ld, D ** -0.5, err=err)
+    assert err.item() == 0
+    check(out, q, kc, vc, sc, bt, lens, new, D ** -0.5, f"{heads} D{D} bs{bs}")
 
 
 @pytest.mark.parametrize("n", [4, 48])
