@@ -418,7 +418,18 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     if (num_seqs == 0 || !context_lens || (new_per_seq == 0 && !cu_seqlens_q)) return PKV_EINVAL;
     if (new_per_seq > 0 && int64_t(num_seqs) * new_per_seq != num_rows) return PKV_EINVAL;
     if (num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0) return PKV_EINVAL;
-    if (ct == kI8 && ((head_dim != 64 && head_dim != 128) || num_q_heads / num_kv_heads > 16)) return PKV_EUNSUPPORTED;
+    if (ct == kI8) {  // all of decode_call's refusals: a refused call writes nothing
+        if (head_dim <= 0 || block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0 ||
+            num_workers < 0 || !std::isfinite(scale))
+            return PKV_EINVAL;
+        if ((head_dim != 64 && head_dim != 128) || num_q_heads / num_kv_heads > 16 || !is_pow2(block_size) ||
+            block_size < kScaleToks || block_size > 1024)
+            return PKV_EUNSUPPORTED;
+        if (num_workers > PKV_MAX_WORKERS || int64_t(num_blocks) * block_size > INT32_MAX) return PKV_EBOUNDS;
+        if (!q || !k_cache || !v_cache || !scales || !block_tables || !out || !aligned16(q) || !aligned16(k_cache) ||
+            !aligned16(v_cache) || !aligned16(out) || (reinterpret_cast<uintptr_t>(scales) & 7u))
+            return PKV_EINVAL;
+    }
     const size_t need = pkv_paged_attention_workspace_size(num_rows, num_q_heads, num_kv_heads, head_dim);
     if (need == 0) return num_rows > PKV_MAX_SEQS ? PKV_EBOUNDS : PKV_EINVAL;
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return PKV_EWORKSPACE;
@@ -459,7 +470,6 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     if (ct == kI8 && qs) {
         const int32_t entries = num_rows / chunk + num_seqs;
         if (entries > num_rows) return PKV_EBOUNDS;  // (not with more than 2 qg rows a sequence)
-        if (!out || !q || !aligned16(out)) return PKV_EINVAL;
         int32_t *row0 = reinterpret_cast<int32_t *>(wsb + dec_bytes + 3 * rows_bytes(num_rows));
         const int32_t len_limit =
             int32_t(std::min<int64_t>(max_context_len, int64_t(max_blocks_per_seq) * std::max(block_size, 0)));

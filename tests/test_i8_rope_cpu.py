@@ -66,6 +66,18 @@ def test_attention_i8(lib, kw, status):
     assert lib.pkv_paged_attention_i8(*swap(ATT, ATT_OK, **kw)) == status
 
 
+@pytest.mark.parametrize("T", [5, 30, 500])
+@pytest.mark.parametrize("kw,status", [
+    (dict(mx=-1), pkv.EINVAL), (dict(mb=0), pkv.EINVAL), (dict(NB=0), pkv.EINVAL), (dict(bs=0), pkv.EINVAL),
+    (dict(workers=-1), pkv.EINVAL), (dict(scale=float("nan")), pkv.EINVAL), (dict(kc=NULL), pkv.EINVAL),
+    (dict(sc=FAKE + 4), pkv.EINVAL), (dict(vc=FAKE + 8), pkv.EINVAL), (dict(bt=NULL), pkv.EINVAL),
+    (dict(bs=8), pkv.EUNSUPPORTED), (dict(bs=48), pkv.EUNSUPPORTED), (dict(workers=1 << 20), pkv.EBOUNDS),
+    (dict(NB=1 << 28), pkv.EBOUNDS),
+])
+def test_attention_i8_refuses_before_it_launches(lib, T, kw, status):
+    assert lib.pkv_paged_attention_i8(*swap(ATT, ATT_OK, T=T, **kw)) == status
+
+
 COPY = "kc vc sc pairs n NB bs Hkv D err st".split()
 COPY_OK = [FAKE, FAKE, FAKE, FAKE, 3, 10, 16, 8, 128, NULL, NULL]
 
