@@ -355,7 +355,8 @@ PKV_API pkv_status pkv_paged_decode_noalloc(const uint16_t *q, const uint16_t *k
  * key rows, not n * L.  With new_per_seq = n <= q, each sequence is one such
  * pass without the expansion kernel.
  * Rows inconsistent with the offsets (n > L, rows outside every sequence's
- * range) give zeros and PKV_ERR_CONTEXT_RANGE.  num_rows <= PKV_MAX_SEQS;
+ * range; every row, if the offsets decrease anywhere) give zeros and
+ * PKV_ERR_CONTEXT_RANGE.  num_rows <= PKV_MAX_SEQS;
  * other limits, num_workers and errors as pkv_paged_decode.
  */
 PKV_API size_t pkv_paged_attention_workspace_size(int32_t num_rows, int32_t num_q_heads,
@@ -470,13 +471,16 @@ PKV_API pkv_status pkv_paged_decode_store_fp8(const uint16_t *q, const uint16_t 
  *                 v_stride elements apart (multiples of 8, at least
  *                 num_kv_heads * head_dim: parts of a wider projection's rows)
  *   block_tables  [num_seqs, max_blocks_per_seq] int32; context_lens [num_seqs]
- *   cu_seqlens    [num_seqs + 1] int32, non-decreasing from 0, ending at num_tokens
+ *   cu_seqlens    [num_seqs + 1] int32, non-decreasing from 0, ending at num_tokens or before
+ *                 (a padded batch: rows from there on are not read)
  * The scale blocks written must not be shared with another sequence of the
  * call (copy-on-write gives every sequence its own last block).  With
  * new_per_seq, a sequence of context_lens 0 is a padding row: nothing is
  * written.  Sequences with 0 <= context_lens[b] < n, lengths beyond the table
  * and offsets out of order set PKV_ERR_CONTEXT_RANGE, block ids outside the
- * cache PKV_ERR_BLOCK_RANGE; what they name is not written.  head_dim 64 or 128.
+ * cache PKV_ERR_BLOCK_RANGE; what they name is not written.  Where offsets
+ * decrease, the sequences before, at and after that place are not written, and
+ * of the call's others some may not be.  head_dim 64 or 128.
  */
 PKV_API pkv_status pkv_kv_store_i8(const uint16_t *k, const uint16_t *v, int64_t k_stride, int64_t v_stride,
                                    const int32_t *block_tables, int32_t max_blocks_per_seq,

@@ -254,6 +254,15 @@ extern "C" pkv_status pkv_paged_decode_i8(const uint16_t *q, const int8_t *k_cac
 // ------------------------------------------------------------------ several query rows per sequence
 namespace pkv {
 
+// Whether the num_seqs + 1 offsets never decrease.  Every block looks at all of them (every thread of it calls this):
+// a search over offsets that do would miss some of them, and the rows of the others could overlap.
+__device__ __forceinline__ bool offsets_in_order(const int32_t *__restrict__ cu, int32_t num_seqs)
+{
+    bool ok = true;
+    for (int32_t b = threadIdx.x; b < num_seqs; b += blockDim.x) ok &= __ldg(cu + b) <= __ldg(cu + b + 1);
+    return __syncthreads_and(ok) != 0;
+}
+
 // Query row r = cu_seqlens_q[b] + i of sequence b (n = cu_seqlens_q[b+1] -
 // cu_seqlens_q[b] new tokens, L = context_lens[b] in the cache) sits at
 // position L - n + i: it sees the L - n + i + 1 keys before it.  The rows of
@@ -266,8 +275,9 @@ namespace pkv {
 // [0, num_seqs) even when the offsets are inconsistent; such rows (not inside
 // their sequence's range, n > L, offsets not starting at 0) are entries of
 // their own or their chunk's with length 0 (zero output) and set
-// PKV_ERR_CONTEXT_RANGE.  With cu_seqlens_q null, every sequence has
-// new_per_seq rows (row r belongs to sequence r / new_per_seq).
+// PKV_ERR_CONTEXT_RANGE.  Offsets that decrease anywhere make every row one
+// of them: the search sees only some of such offsets.  With cu_seqlens_q null,
+// every sequence has new_per_seq rows (row r belongs to sequence r / new_per_seq).
 __global__ void expand_rows_kernel(const int32_t *__restrict__ cu_seqlens_q, int32_t new_per_seq,
                                    const int32_t *__restrict__ context_lens, int32_t num_seqs, int32_t num_rows,
                                    int32_t chunk, int32_t *__restrict__ row_seq, int32_t *__restrict__ row_len,
@@ -275,6 +285,7 @@ __global__ void expand_rows_kernel(const int32_t *__restrict__ cu_seqlens_q, int
 {
     griddep_launch_dependents();
     griddep_wait();
+    const bool ordered = !cu_seqlens_q || offsets_in_order(cu_seqlens_q, num_seqs);
     const int32_t r = blockIdx.x * blockDim.x + threadIdx.x;
     if (r >= num_rows) return;
     int32_t lo = 0, r0 = 0, r1 = 0;
@@ -296,7 +307,7 @@ __global__ void expand_rows_kernel(const int32_t *__restrict__ cu_seqlens_q, int
     }
     const int32_t L = __ldg(context_lens + lo);
     const int32_t n = r1 - r0, i = r - r0;
-    const bool inside = r0 <= r && r < r1;
+    const bool inside = ordered && r0 <= r && r < r1;
     const bool ok = (!cu_seqlens_q || __ldg(cu_seqlens_q) == 0) && inside && n <= L && r1 <= num_rows;
     if (!ok) flag_error(err, PKV_ERR_CONTEXT_RANGE);
     int32_t cnt = 1, len = 0;  // a row outside its sequence's range: an entry of its own, zero output
@@ -313,7 +324,8 @@ __global__ void expand_rows_kernel(const int32_t *__restrict__ cu_seqlens_q, int
 // are entries cu_seqlens_q[b] / chunk + b on (room for the ceil(n / chunk) chunks of its n rows; entries that are no
 // chunk have row_cnt = 0), num_rows / chunk + num_seqs of them.  One thread per entry and per row: the entry's
 // thread finds its sequence by binary search and writes the entry (row0: the row of its first query), the row's
-// thread checks that the row lies in a consistent sequence and else writes zeros to its output.
+// thread checks that the row lies in a consistent sequence and else writes zeros to its output (every row's, when the
+// offsets decrease anywhere).
 __global__ void expand_entries_kernel(const int32_t *__restrict__ cu_seqlens_q, int32_t new_per_seq,
                                       const int32_t *__restrict__ context_lens, int32_t num_seqs, int32_t num_rows,
                                       int32_t num_entries, int32_t chunk, int32_t len_limit, int32_t row_values,
@@ -323,6 +335,7 @@ __global__ void expand_entries_kernel(const int32_t *__restrict__ cu_seqlens_q, 
 {
     griddep_launch_dependents();
     griddep_wait();
+    const bool ordered = !cu_seqlens_q || offsets_in_order(cu_seqlens_q, num_seqs);
     const int32_t x = blockIdx.x * blockDim.x + threadIdx.x;
     auto start = [&](int32_t b) { return cu_seqlens_q ? __ldg(cu_seqlens_q + b) : b * new_per_seq; };
     // the last b whose key is at most v (keys of consistent offsets are non-decreasing)
@@ -339,7 +352,7 @@ __global__ void expand_entries_kernel(const int32_t *__restrict__ cu_seqlens_q, 
     };
     auto consistent = [&](int32_t b, int32_t r0, int32_t r1) {
         const int32_t L = __ldg(context_lens + b);
-        return start(0) == 0 && r0 >= 0 && r0 <= r1 && r1 <= num_rows && r1 - r0 <= L && L <= len_limit;
+        return ordered && start(0) == 0 && r0 >= 0 && r0 <= r1 && r1 <= num_rows && r1 - r0 <= L && L <= len_limit;
     };
     if (x < num_entries) {
         const int32_t b = find(x, true), r0 = start(b), r1 = start(b + 1);

@@ -126,6 +126,11 @@ __global__ void __launch_bounds__(kStoreThreads, 5) kv_store_i8_kernel(const Sto
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
     int32_t b, i, r0, n, L;
     if (p.cu_seqlens) {
+        // The search below sees only some of the offsets, so CTA x also looks whether offset x decreases (there are
+        // at least two CTAs a sequence).
+        bool down = false;
+        if (threadIdx.x == 0 && int(blockIdx.x) < p.num_seqs)
+            down = __ldg(p.cu_seqlens + blockIdx.x) > __ldg(p.cu_seqlens + blockIdx.x + 1);
         // the last b with cu[b] / 16 + 2 b <= slot, by 32-way steps
         int lo = 0, width = p.num_seqs;
         while (width > 1) {
@@ -142,9 +147,11 @@ __global__ void __launch_bounds__(kStoreThreads, 5) kv_store_i8_kernel(const Sto
         r0 = __ldg(p.cu_seqlens + b);
         L = __ldg(p.context_lens + b);
         const int32_t r1 = __ldg(p.cu_seqlens + b + 1);
+        const int32_t before = __ldg(p.cu_seqlens + max(b - 1, 0)), after = __ldg(p.cu_seqlens + min(b + 2, p.num_seqs));
         i = int32_t(blockIdx.x) - ((max(0, r0) >> 4) + 2 * b);
         n = r1 - r0;
-        if (r0 < 0 || r1 < r0 || r1 > p.num_tokens || (b == 0 && r0 != 0)) {
+        if (down) flag_error(p.err, PKV_ERR_CONTEXT_RANGE);
+        if (r0 < 0 || r1 < r0 || r1 > p.num_tokens || (b == 0 && r0 != 0) || before > r0 || r1 > after) {
             if (threadIdx.x == 0) flag_error(p.err, PKV_ERR_CONTEXT_RANGE);
             return;
         }

@@ -714,3 +714,52 @@ def test_captured_chunks_of_a_padded_batch_replay():
             assert np.array_equal(got.cpu().numpy(), want, equal_nan=True)
         check(out[:n], q[:n], *(torch.from_numpy(t) for t in ref), bt, lens, new, D ** -0.5, str(new))
         assert torch.all(out[n:] == 0)
+
+
+# ------------------------------------------------------------------------------------------ offsets that decrease
+@pytest.mark.parametrize("cu", [[0, 50, 20, 60], [0, 60, 10, 20, 30, 40, 60], [0, 40, 39, 60], [0, 16, 60, 60, 5],
+                                [0, -3, 60], [5, 4, 60]])
+def test_store_flags_offsets_that_decrease(cu):
+    """Flagged wherever they are; the sequences before, at and after the place are not written."""
+    B, T, Hkv, D, bs = len(cu) - 1, 60, 2, 64, 32
+    bt, NB = tables([100] * B, bs, np.random.default_rng(0))
+    kc, vc, sc = garbage_cache(NB, bs, Hkv, D, 1)
+    sc.fill_(0.5)
+    old = [t.clone() for t in (kc, vc, sc)]
+    k, v = (torch.randn(T, Hkv, D, device="cuda").bfloat16() for _ in range(2))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkv.kv_store_i8(k, v, kc, vc, sc, torch.from_numpy(bt).cuda(),
+                    torch.full((B,), 100, dtype=torch.int32, device="cuda"),
+                    torch.tensor(cu, dtype=torch.int32, device="cuda"), err_word=err)
+    torch.cuda.synchronize()
+    assert err.item() == pkv.ERR_CONTEXT_RANGE
+    down = [b for b in range(B) if cu[b] > cu[b + 1]]
+    for b in range(B):
+        if any(abs(b - d) <= 1 for d in down):
+            pages = bt[b][bt[b] >= 0]
+            assert all(torch.equal(t[pages], o[pages]) for t, o in zip((kc, vc, sc), old)), b
+
+
+@pytest.mark.parametrize("pad", [0, 9])
+@pytest.mark.parametrize("kind", ["int8", "bf16"])
+@pytest.mark.parametrize("heads,D", [((16, 8), 128), ((14, 2), 64)])
+@pytest.mark.parametrize("cu", [[0, 50, 20, 60], [0, 50, 60, 20, 30, 60], [0, 60, -1, 60]])
+def test_attention_flags_offsets_that_decrease(cu, heads, D, kind, pad):
+    """Every row zero and the flag, with chunks of 128 (query, head) rows and, with empty sequences behind (pad),
+    with short ones."""
+    Hq, Hkv = heads
+    cu = cu + [60] * pad
+    B = len(cu) - 1
+    q, kc, vc, sc, bt, btd, ld = synth([100] * B, Hq, Hkv, D, 32, seed=8, new=[60] + [0] * (B - 1))
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    if kind == "int8":
+        out = attend(q, kc, vc, sc, btd, cud, ld, D ** -0.5, err=err)
+    else:
+        kb, vb = (torch.randn(kc.shape, device="cuda").bfloat16() for _ in range(2))
+        out = torch.full_like(q, float("nan"))
+        pkv.paged_attention(q, kb, vb, btd, cud, ld, D ** -0.5, out, pkv.alloc_attention_workspace(60, Hq, Hkv, D),
+                            err_word=err)
+    torch.cuda.synchronize()
+    assert err.item() == pkv.ERR_CONTEXT_RANGE
+    assert torch.all(out == 0)
