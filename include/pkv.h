@@ -512,9 +512,16 @@ PKV_API pkv_status pkv_paged_decode_i8(const uint16_t *q, const int8_t *k_cache,
  * pkv_paged_attention_i8 -- pkv_paged_attention over int8 caches (chunks of a
  * prefill over a cached prefix, mixed batches, verify steps); the chunk's K/V
  * already stored by pkv_kv_store_i8.  Workspace:
- * pkv_paged_attention_workspace_size.  Limits as pkv_paged_decode_i8,
- * everything else as pkv_paged_attention.
+ * pkv_paged_attention_i8_workspace_size bytes, which also do for
+ * pkv_paged_attention; with less, down to pkv_paged_attention_workspace_size
+ * (the same in most calls whose num_q_heads / num_kv_heads is a power of two),
+ * long runs of new tokens whose pieces do not fit go without the tensor-memory
+ * CTAs (64 new tokens of 64 sequences of 512-4096, 14 / 2 heads of 64: 484 us
+ * against 148).  Limits as pkv_paged_decode_i8, everything else
+ * as pkv_paged_attention.
  */
+PKV_API size_t pkv_paged_attention_i8_workspace_size(int32_t num_rows, int32_t num_q_heads,
+                                                     int32_t num_kv_heads, int32_t head_dim);
 PKV_API pkv_status pkv_paged_attention_i8(const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache,
                                           const float *scales, const int32_t *block_tables,
                                           int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,

@@ -408,13 +408,27 @@ extern "C" size_t pkv_paged_attention_workspace_size(int32_t num_rows, int32_t n
     if (base == 0) return 0;
     // decode workspace: same-n calls (entries of n <= qg queries, n * G virtual heads), or one
     // chunk entry per row (qg * G virtual heads a warp, on a regular or a query-split CTA); then the
-    // four row arrays
+    // three row arrays
     const int32_t gq = num_q_heads / num_kv_heads, qg = qs_queries(num_q_heads, num_kv_heads);
-    // (int8 calls: 16-row blocks whatever the group)
-    size_t dec = std::max(base, ws_layout(num_rows, gq <= 16 ? 16 : gq * qg, num_kv_heads, head_dim, true).total);
+    size_t dec = std::max(base, ws_layout(num_rows, gq * qg, num_kv_heads, head_dim, true).total);
     for (int32_t qn = 2; qn <= qg; ++qn)
         dec = std::max(dec, ws_layout(num_rows, gq * qn, num_kv_heads, head_dim).total);
-    return align256(dec) + 4 * rows_bytes(num_rows);
+    return align256(dec) + 3 * rows_bytes(num_rows);
+}
+
+// What a query-split int8 call of this many entries takes: pieces of 16-row blocks whatever the group, then four
+// arrays of the entries.
+static size_t i8_entries_bytes(int32_t entries, int32_t num_kv_heads, int32_t head_dim)
+{
+    return align256(ws_layout(entries, 16, num_kv_heads, head_dim, true).total) + align256(size_t(entries) * 16);
+}
+
+extern "C" size_t pkv_paged_attention_i8_workspace_size(int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
+                                                        int32_t head_dim)
+{
+    const size_t base = pkv_paged_attention_workspace_size(num_rows, num_q_heads, num_kv_heads, head_dim);
+    if (base == 0 || num_q_heads / num_kv_heads > 16) return base;
+    return std::max(base, i8_entries_bytes(num_rows, num_kv_heads, head_dim));  // (at most an entry a row)
 }
 
 // Shared by the bf16 and the int8 entry points (scales: the latter's).
@@ -474,22 +488,23 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
                                 kTc5Keys - 1) / kTc5Keys);
         qs = tiles < 8 * int64_t(dev.sm_count) && num_rows / tile + num_seqs <= num_rows;
     }
+    // (entries of a query-split int8 call; without room for their pieces the call takes regular CTAs)
+    const int64_t entries = int64_t(num_rows) / tile + num_seqs;
+    if (ct == kI8 && qs)
+        qs = entries <= num_rows && workspace_bytes >= i8_entries_bytes(int32_t(entries), num_kv_heads, head_dim);
     const int32_t chunk = !qs ? qg : ct == kI8 ? tile : entry_queries(num_q_heads, num_kv_heads);
     uint8_t *wsb = static_cast<uint8_t *>(workspace);
-    const size_t dec_bytes = need - 4 * rows_bytes(num_rows);
-    int32_t *row_seq = reinterpret_cast<int32_t *>(wsb + dec_bytes);
-    int32_t *row_len = reinterpret_cast<int32_t *>(wsb + dec_bytes + rows_bytes(num_rows));
-    int32_t *row_cnt = reinterpret_cast<int32_t *>(wsb + dec_bytes + 2 * rows_bytes(num_rows));
     if (ct == kI8 && qs) {
-        const int32_t entries = num_rows / chunk + num_seqs;
-        if (entries > num_rows) return PKV_EBOUNDS;  // (not with more than 2 qg rows a sequence)
-        int32_t *row0 = reinterpret_cast<int32_t *>(wsb + dec_bytes + 3 * rows_bytes(num_rows));
+        const size_t dec_bytes = i8_entries_bytes(int32_t(entries), num_kv_heads, head_dim) -
+                                 align256(size_t(entries) * 16);
+        int32_t *row_seq = reinterpret_cast<int32_t *>(wsb + dec_bytes), *row_len = row_seq + entries,
+                *row_cnt = row_len + entries, *row0 = row_cnt + entries;
         const int32_t len_limit =
             int32_t(std::min<int64_t>(max_context_len, int64_t(max_blocks_per_seq) * std::max(block_size, 0)));
         const cudaError_t e = launch_pdl(expand_entries_kernel, dim3((num_rows + 255) / 256), dim3(256), 0,
                                          reinterpret_cast<cudaStream_t>(stream),
                                          new_per_seq > 0 ? nullptr : cu_seqlens_q, new_per_seq, context_lens, num_seqs,
-                                         num_rows, entries, chunk, len_limit, num_q_heads * head_dim, row_seq,
+                                         num_rows, int32_t(entries), chunk, len_limit, num_q_heads * head_dim, row_seq,
                                          row_len, row_cnt, row0, out, err_word);
         if (e != cudaSuccess) {
             cudaGetLastError();
@@ -498,10 +513,14 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
         const pkv_status st = launch_status("expand_entries_kernel launch");
         if (st != PKV_OK) return st;
         return decode_call(ct, true, qg, q, k_cache, v_cache, nullptr, nullptr, row_seq, row_cnt, block_tables,
-                           max_blocks_per_seq, row_len, entries, num_q_heads, num_kv_heads, head_dim, block_size,
+                           max_blocks_per_seq, row_len, int32_t(entries), num_q_heads, num_kv_heads, head_dim, block_size,
                            num_blocks, max_context_len, scale, out, workspace, dec_bytes, num_workers, err_word, stream,
                            nullptr, nullptr, nullptr, scales, row0);
     }
+    const size_t dec_bytes = need - 3 * rows_bytes(num_rows);
+    int32_t *row_seq = reinterpret_cast<int32_t *>(wsb + dec_bytes);
+    int32_t *row_len = reinterpret_cast<int32_t *>(wsb + dec_bytes + rows_bytes(num_rows));
+    int32_t *row_cnt = reinterpret_cast<int32_t *>(wsb + dec_bytes + 2 * rows_bytes(num_rows));
     const cudaError_t e = launch_pdl(expand_rows_kernel, dim3((num_rows + 255) / 256), dim3(256), 0,
                                      reinterpret_cast<cudaStream_t>(stream), new_per_seq > 0 ? nullptr : cu_seqlens_q,
                                      new_per_seq, context_lens, num_seqs, num_rows, chunk, row_seq, row_len,

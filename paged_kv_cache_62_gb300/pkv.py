@@ -42,6 +42,7 @@ SIGNATURES = {
     "pkv_diag_wait_timeout": (ctypes.c_int, [_P, _P]),
     "pkv_copy_blocks": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P]),
     "pkv_paged_attention_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
+    "pkv_paged_attention_i8_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
     "pkv_paged_attention": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
                                            _I32, _F32, _P, _I32, _P, _SZ, _I32, _P, _P]),
     "pkv_decode_store": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P]),
@@ -456,8 +457,8 @@ def decode_store(k: torch.Tensor, v: torch.Tensor, block_tables: torch.Tensor, c
 
 
 def alloc_attention_workspace(num_rows: int, num_q_heads: int, num_kv_heads: int, head_dim: int, device=None):
-    """A zero-filled workspace for paged_attention with num_rows query rows."""
-    n = load().pkv_paged_attention_workspace_size(num_rows, num_q_heads, num_kv_heads, head_dim)
+    """A zero-filled workspace for paged_attention and paged_attention_i8 with num_rows query rows."""
+    n = load().pkv_paged_attention_i8_workspace_size(num_rows, num_q_heads, num_kv_heads, head_dim)
     if n == 0:
         raise ValueError("paged_attention: unsupported sizes")
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")

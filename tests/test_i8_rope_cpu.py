@@ -133,3 +133,38 @@ def test_bindings_refuse_cpu_tensors_and_bad_shapes(lib):
         pkv.rope(z(2, 4, 64), z(2, 2, 64), z(2, dt=i32), z(32, dt=torch.float32), z(2, 4, 64), z(2, 2, 64))
     with pytest.raises(ValueError):
         pkv.alloc_i8_cache(4, 8, 2, 64)
+
+
+# ------------------------------------------------------------------------------------------ workspaces
+# bytes that bf16 calls of these sizes took before the library had int8 caches
+BF16_SIZES = {(16384, 36, 4, 128): 42893568, (4096, 9, 1, 64): 19939584, (256, 16, 8, 128): 68324608,
+              (1, 4, 2, 64): 17533952, (3000, 14, 2, 64): 30861824, (100, 15, 5, 128): 63314432,
+              (60, 16, 1, 128): 38237184, (500, 20, 1, 64): 42917120}
+
+
+@pytest.mark.parametrize("sizes", sorted(BF16_SIZES))
+def test_bf16_attention_takes_the_workspace_it_took(lib, sizes):
+    T, Hq, Hkv, D = sizes
+    need = BF16_SIZES[sizes]
+    assert lib.pkv_paged_attention_workspace_size(*sizes) == need
+    assert lib.pkv_paged_attention_i8_workspace_size(*sizes) >= need
+    names = [n for n in ATT if n != "sc"]
+    base = [v for n, v in zip(ATT, ATT_OK) if n != "sc"]
+    if Hq // Hkv <= 16:
+        # a size it takes: the call goes on and ends at the device that is missing here
+        kw = dict(T=T, Hq=Hq, Hkv=Hkv, D=D)
+        assert lib.pkv_paged_attention(*swap(names, base, wsb=need - 1, **kw)) == pkv.EWORKSPACE
+        assert lib.pkv_paged_attention_i8(*swap(ATT, ATT_OK, wsb=need - 1, **kw)) == pkv.EWORKSPACE
+        if not torch.cuda.is_available():
+            assert lib.pkv_paged_attention(*swap(names, base, wsb=need, **kw)) == pkv.ECUDA
+            assert lib.pkv_paged_attention_i8(*swap(ATT, ATT_OK, wsb=need, **kw)) == pkv.ECUDA
+
+
+def test_int8_attention_workspace_sizes(lib):
+    f, g = lib.pkv_paged_attention_i8_workspace_size, lib.pkv_paged_attention_workspace_size
+    assert f(0, 16, 8, 128) == g(0, 16, 8, 128) and f(-1, 16, 8, 128) == 0 and f(4, 16, 6, 128) == 0
+    assert f(pkv.MAX_SEQS + 1, 16, 8, 128) == 0
+    for rows in (1, 60, 500, pkv.MAX_SEQS):
+        for hq, hkv, d in ((16, 8, 128), (14, 2, 64), (9, 1, 64), (16, 1, 128), (15, 5, 128)):
+            assert f(rows, hq, hkv, d) >= g(rows, hq, hkv, d)
+            assert f(rows, hq, hkv, d) <= f(rows + 100, hq, hkv, d) or rows + 100 > pkv.MAX_SEQS
