@@ -680,10 +680,12 @@ PKV_API pkv_status pkv_allocator_tables(const pkv_block_allocator *a, const int3
  * ------------------------------------------------------------------------ */
 
 /*
- * pkv_diag_wait_timeout -- one warp waits on a barrier that nothing completes.
- * Every wait on an asynchronous copy in the library is bounded (about 2 s);
- * this one runs out, sets PKV_ERR_WAIT_TIMEOUT in *err_word (device) and
- * returns, leaving the context usable.  It takes the wait's time limit to
+ * pkv_diag_wait_timeout -- waits on a barrier that nothing completes, a warp
+ * for each form of wait in the library.  Every wait on an asynchronous copy or
+ * a tensor-core product is bounded (about 2 s; int8 several-token kernels 2^32
+ * to 2^33 SM cycles, 2 to 4 s); these run out, set
+ * PKV_ERR_WAIT_TIMEOUT in *err_word (device) when all of them have, and
+ * return, leaving the context usable.  It takes the waits' time limit to
  * complete.  err_word NULL: PKV_EINVAL.
  */
 PKV_API pkv_status pkv_diag_wait_timeout(int32_t *err_word, pkv_stream_t stream);

@@ -18,6 +18,7 @@ constexpr unsigned kFull = 0xffffffffu;
 // Bounded spin on an mbarrier phase: a wait gives up after kWaitLimitNs of
 // wall time (the caller then sets PKV_ERR_WAIT_TIMEOUT); no kernel can hang.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint32_t kWaitLimitTurns = 1;  // of mbar_wait_lean
 
 __device__ __forceinline__ void flag_error(int32_t *err, int32_t bits)
 {
@@ -103,13 +104,28 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     return __all_sync(kFull, ok);
 }
 
-// mbar_wait_bounded in few instructions, for code that an SM's instruction caches hold only in parts: the limit is
-// a number of tries (each may suspend the thread for a while when the phase is not complete).
+// The upper half of the SM's cycle counter: one turn is 2^32 cycles, 2.1 s at 2 GHz.
+__device__ __forceinline__ uint32_t clock_turns()
+{
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%clock_hi;" : "=r"(t));
+    return t;
+}
+
+// mbar_wait_bounded in few instructions, for code that an SM's instruction caches hold only in parts: it gives up when
+// more than kWaitLimitTurns turns have begun since it did, 2^32 to 2^33 cycles.  WARP: every lane calls it and gets the
+// same result, as above; else one thread of a warp does.  (64 new int8 tokens of 64 sequences of 512-4096: 155.3 us,
+// as with a plain count of tries, which has no limit in time; with the nanosecond timer read at every 256th try 164 us,
+// at every 1024th its lower half 159.6; the timed part out of line 167-174.)
+template <bool WARP = true>
 __device__ __forceinline__ bool mbar_wait_lean(uint64_t *bar, uint32_t parity)
 {
     const uint32_t a = smem_u32(bar);
-    for (uint32_t i = 0; !__all_sync(kFull, mbar_try_wait(a, parity)); ++i)
-        if (i >> 22) return false;
+    const uint32_t t0 = clock_turns();
+    while (!(WARP ? __all_sync(kFull, mbar_try_wait(a, parity)) != 0 : mbar_try_wait(a, parity))) {
+        const bool late = clock_turns() - t0 > kWaitLimitTurns;
+        if (WARP ? __any_sync(kFull, late) != 0 : late) return false;
+    }
     return true;
 }
 

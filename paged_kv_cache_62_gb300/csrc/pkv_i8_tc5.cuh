@@ -220,8 +220,7 @@ __device__ void tc5_mma_warp_i8(const DecodeParams &p, const Tc5Smem &m, uint32_
     if (lane == 0) {
         bool dead = false;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            const uint32_t a = smem_u32(bar);
-            for (uint32_t i = 0; !dead && !mbar_try_wait(a, parity); ++i) dead = i >> 22 != 0;
+            dead = !mbar_wait_lean<false>(bar, parity);
             return !dead;
         };
         int s = 0;  // stage of unit k

@@ -253,9 +253,9 @@ extern "C" pkv_status pkv_kv_store(const uint16_t *k, const uint16_t *v, const i
     return launch_status("kv_store_kernel launch");
 }
 
-// A wait on an mbarrier that nothing completes: the bounded wait gives up at
-// its time limit, the kernel flags PKV_ERR_WAIT_TIMEOUT and returns (the
-// timeout path of every wait in the library, exercised without a fault).
+// Waits on an mbarrier that nothing completes, a warp for each form of the library's bounded wait: every one gives up
+// at its time limit, and if all have, the kernel flags PKV_ERR_WAIT_TIMEOUT (the timeout path of every wait in
+// the library, exercised without a fault).
 __global__ void diag_wait_timeout_kernel(int32_t *err)
 {
     __shared__ __align__(8) uint64_t bar;
@@ -263,14 +263,23 @@ __global__ void diag_wait_timeout_kernel(int32_t *err)
         mbar_init(&bar, 1);
         fence_barrier_init();
     }
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    bool done = false;
+    if (warp == 0)
+        done = mbar_wait_bounded(&bar, 0u);
+    else if (warp == 1)
+        done = mbar_wait_lean(&bar, 0u);
+    else if (lane == 0)
+        done = mbar_wait_lean<false>(&bar, 0u);
     __syncwarp();
-    if (!mbar_wait_bounded(&bar, 0u) && threadIdx.x == 0) flag_error(err, PKV_ERR_WAIT_TIMEOUT);
+    if (!__syncthreads_or(done) && threadIdx.x == 0) flag_error(err, PKV_ERR_WAIT_TIMEOUT);
 }
 
 extern "C" pkv_status pkv_diag_wait_timeout(int32_t *err_word, pkv_stream_t stream)
 {
     if (!err_word) return PKV_EINVAL;
-    diag_wait_timeout_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(err_word);
+    diag_wait_timeout_kernel<<<1, 96, 0, reinterpret_cast<cudaStream_t>(stream)>>>(err_word);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail("diag_wait_timeout_kernel launch", e);
     return launch_status("diag_wait_timeout_kernel launch");

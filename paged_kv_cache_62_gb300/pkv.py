@@ -300,7 +300,7 @@ def paged_decode_store_fp8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Te
 
 
 def diag_wait_timeout(err_word: torch.Tensor, stream=None) -> None:
-    """Diagnostic: a bounded wait that runs out on purpose; sets ERR_WAIT_TIMEOUT in err_word after the wait's
+    """Diagnostic: the library's bounded waits run out on purpose; sets ERR_WAIT_TIMEOUT in err_word after their
     limit."""
     _check(load().pkv_diag_wait_timeout(_dev(err_word, torch.int32, "err_word"), _stream(stream)),
            "pkv_diag_wait_timeout")

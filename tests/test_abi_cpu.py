@@ -211,3 +211,23 @@ def test_attention_workspace_holds_the_rows(lib):
             qg = max(1, 8 // (hq // hkv))
             assert f(rows, hq, hkv, d) >= g(rows, hq * qg, hkv, d) + 3 * 4 * rows
     assert f(-1, 16, 8, 128) == 0 and f(4, 16, 6, 128) == 0
+
+
+def test_every_wait_on_a_barrier_has_a_limit_in_time_and_runs_out_in_the_diagnostic():
+    """From the sources: a wait that only counts tries has no bound in time (a try may suspend its thread for as
+    long as the hardware likes), and the diagnostic is what shows that a limit is met."""
+    csrc = os.path.join(ROOT, "paged_kv_cache_62_gb300", "csrc")
+    files = {n: open(os.path.join(csrc, n)).read() for n in os.listdir(csrc) if n.endswith((".cu", ".cuh"))}
+    device = files["pkv_device.cuh"]
+    waits = re.findall(r"^__device__ __forceinline__ bool (mbar_wait_\w+)\(", device, re.M)
+    bodies = re.findall(r"^__device__ __forceinline__ bool mbar_wait_\w+\(.*?^}", device, re.M | re.S)
+    assert set(waits) == {"mbar_wait_bounded", "mbar_wait_lean"}
+    assert all(re.search(r"global_ns\(\) - t0 > kWaitLimitNs|clock_turns\(\) - t0 > kWaitLimitTurns", b) for b in bodies)
+    kernel = re.search(r"diag_wait_timeout_kernel\(.*?^}", files["pkv_store.cu"], re.M | re.S).group(0)
+    for call in ("mbar_wait_bounded(", "mbar_wait_lean(", "mbar_wait_lean<false>("):
+        assert call in kernel
+    # no other function polls a barrier by try_wait
+    for name, text in files.items():
+        text = text if name != "pkv_device.cuh" else re.sub(r"^__device__ __forceinline__ bool mbar_\w+\(.*?^}", "", text,
+                                                            flags=re.M | re.S)
+        assert "mbar_try_wait(" not in text, name

@@ -648,3 +648,17 @@ def test_slot_mapping_range_errors():
     torch.cuda.synchronize()
     assert slots.tolist() == [-1, -1]
     assert err.item() & pkv.ERR_CONTEXT_RANGE and err.item() & pkv.ERR_BLOCK_RANGE
+
+
+def test_every_bounded_wait_runs_out_at_its_limit():
+    """The diagnostic's waits, one of each form, all end: the timed one after two seconds, the one that counts SM cycles
+    after at most 2^33 of them (8 s at 1.07 GHz)."""
+    err = err_word()
+    torch.cuda.synchronize()
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    ev[0].record()
+    pkv.diag_wait_timeout(err)
+    ev[1].record()
+    torch.cuda.synchronize()
+    assert err.item() == pkv.ERR_WAIT_TIMEOUT
+    assert 1900 < ev[0].elapsed_time(ev[1]) < 8000
