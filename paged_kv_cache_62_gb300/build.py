@@ -4,7 +4,9 @@ Every translation unit is compiled for sm_103a only, in parallel, then linked
 into one shared library next to this file.  The CUDA runtime is linked
 statically, so the library needs nothing beyond the NVIDIA driver at run time.
 ``_pkv_torch.so``, the native argument checks of the int8 and rotary bindings,
-is compiled beside it against the installed torch.
+is compiled beside it against the installed torch.  Where that fails (no torch
+or Python headers, say), the library and the other bindings are built all the
+same; the int8 and rotary bindings then raise.
 """
 from __future__ import annotations
 
@@ -21,6 +23,7 @@ ROOT = os.path.dirname(HERE)
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libpkv.so")
 TORCH_PATH = os.path.join(HERE, "_pkv_torch.so")
+TORCH_OBJ, TORCH_KEY = os.path.join(BUILD_DIR, "pkv_torch.o"), os.path.join(BUILD_DIR, "pkv_torch.key")
 SOURCES = ["pkv_api.cu", "pkv_store.cu", "pkv_decode.cu", "pkv_decode_fp8.cu", "pkv_decode_qs.cu", "pkv_decode_wide.cu",
            "pkv_decode_tc5.cu", "pkv_decode_i8.cu", "pkv_decode_i8_wide.cu", "pkv_decode_i8_tc5.cu", "pkv_store_i8.cu",
            "pkv_rope.cu", "pkv_noalloc.cu", "pkv_alloc.cpp"]
@@ -53,16 +56,55 @@ def torch_commands(tmp: str) -> tuple[list[str], list[str]]:
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    obj = os.path.join(BUILD_DIR, "pkv_torch.o")
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-                *(x for i in inc for x in ("-isystem", i)), "-c", os.path.join(CSRC, "pkv_torch.cpp"), "-o", obj]
+                f'-DPKV_TORCH_VERSION="{torch.__version__}"',
+                *(x for i in inc for x in ("-isystem", i)), "-c", os.path.join(CSRC, "pkv_torch.cpp"), "-o", TORCH_OBJ]
     libs = os.path.join(root, "lib")
-    link = ["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-lpkv", "-L", libs, "-ltorch_python", "-ltorch_cpu",
+    link = ["g++", "-shared", "-o", tmp, TORCH_OBJ, "-L", HERE, "-lpkv", "-L", libs, "-ltorch_python", "-ltorch_cpu",
             "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
     return compile_, link
+
+
+def torch_key() -> str:
+    """What _pkv_torch.so is bound to besides its sources: the installed torch and the Python ABI."""
+    import torch
+    return f"{torch.__version__} {sysconfig.get_config_var('SOABI')}"
+
+
+def _torch_part(lib_built: "cf.Future", force: bool) -> str | None:
+    """Build _pkv_torch.so if it is missing, stale or bound to another torch or Python; the library's link is waited
+    for before its own.  Returns why it could not be built (it is then not there, not an old one), or None."""
+    tmp = TORCH_PATH + f".tmp{os.getpid()}"
+    try:
+        key = torch_key()
+        other = not os.path.exists(TORCH_KEY) or open(TORCH_KEY).read() != key
+        deps = [os.path.join(CSRC, "pkv_torch.cpp"), os.path.join(ROOT, "include", "pkv.h")]
+        if force or other or _stale(TORCH_OBJ, deps):
+            _run(torch_commands(tmp)[0])
+        lib_built.result()
+        if force or other or _stale(TORCH_PATH, [TORCH_OBJ, LIB_PATH]):
+            _run(torch_commands(tmp)[1])
+            os.replace(tmp, TORCH_PATH)
+            with open(TORCH_KEY, "w") as f:
+                f.write(key)
+        return None
+    except (RuntimeError, OSError, ImportError) as e:
+        if not lib_built.done() or lib_built.exception() is None:
+            for path in (TORCH_PATH, TORCH_OBJ):
+                if os.path.exists(path):
+                    os.remove(path)
+        return str(e) or type(e).__name__
+
+
+def _run(cmd: list[str], echo: bool = False) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if echo or r.returncode:
+        sys.stderr.write(r.stdout + r.stderr)
+    if r.returncode:
+        raise RuntimeError("failed: " + " ".join(cmd))
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -80,36 +122,22 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append(cmd)
 
-    tsrc, tobj = os.path.join(CSRC, "pkv_torch.cpp"), os.path.join(BUILD_DIR, "pkv_torch.o")
-    ttmp = TORCH_PATH + f".tmp{os.getpid()}"
-    if force or _stale(tobj, [tsrc, os.path.join(include, "pkv.h")]):
-        jobs.insert(0, torch_commands(ttmp)[0])
-
-    def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        return cmd, r
-
+    lib_built = cf.Future()
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        for cmd, r in ex.map(run, jobs):
-            if verbose or ptxas_info or r.returncode:
-                sys.stderr.write(r.stdout + r.stderr)
-            if r.returncode:
-                raise RuntimeError("compilation failed: " + " ".join(cmd))
-    if force or jobs or _stale(LIB_PATH, objs):
-        tmp = LIB_PATH + f".tmp{os.getpid()}"
-        cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode:
-            sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError("link failed: " + " ".join(cmd))
-        os.replace(tmp, LIB_PATH)
-    if force or _stale(TORCH_PATH, [tobj, LIB_PATH]):
-        cmd = torch_commands(ttmp)[1]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode:
-            sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError("link failed: " + " ".join(cmd))
-        os.replace(ttmp, TORCH_PATH)
+        torch_part = ex.submit(_torch_part, lib_built, force)
+        try:
+            for _ in ex.map(lambda cmd: _run(cmd, verbose or ptxas_info), jobs):
+                pass
+            if force or jobs or _stale(LIB_PATH, objs):
+                tmp = LIB_PATH + f".tmp{os.getpid()}"
+                _run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"])
+                os.replace(tmp, LIB_PATH)
+            lib_built.set_result(None)
+        except BaseException as e:
+            lib_built.set_exception(RuntimeError("the library was not built"))
+            raise e
+    if (why := torch_part.result()) is not None:
+        sys.stderr.write(f"_pkv_torch.so was not built, the int8 and rotary bindings are not available: {why}\n")
     return LIB_PATH
 
 

@@ -339,4 +339,10 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pkv_torch", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__pkv_torch(void) { return PyModule_Create(&module); }
+// torch_version: the torch this was compiled against (pkv.py refuses another one).
+PyMODINIT_FUNC PyInit__pkv_torch(void)
+{
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", PKV_TORCH_VERSION) < 0) Py_CLEAR(m);
+    return m;
+}

@@ -502,6 +502,9 @@ def _native():
         except ImportError as e:
             raise RuntimeError("_pkv_torch.so is missing or does not load: build it with "
                                "`python -m paged_kv_cache_62_gb300.build`") from e
+        if _pkv_torch.torch_version != torch.__version__:
+            raise RuntimeError(f"_pkv_torch.so was built for torch {_pkv_torch.torch_version}, this is "
+                               f"{torch.__version__}: build it again with `python -m paged_kv_cache_62_gb300.build`")
         _torch_native = _pkv_torch
     return _torch_native
 
