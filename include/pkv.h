@@ -518,7 +518,9 @@ PKV_API pkv_status pkv_paged_decode_i8(const uint16_t *q, const int8_t *k_cache,
  * long runs of new tokens whose pieces do not fit go without the tensor-memory
  * CTAs (64 new tokens of 64 sequences of 512-4096, 14 / 2 heads of 64: 484 us
  * against 148).  Limits as pkv_paged_decode_i8, everything else
- * as pkv_paged_attention.
+ * as pkv_paged_attention.  The list of rows is kept in shared memory: with
+ * head_dim 128 and few new tokens a sequence, calls of more than about 7000
+ * rows are PKV_EUNSUPPORTED (so they are over bf16 caches).
  */
 PKV_API size_t pkv_paged_attention_i8_workspace_size(int32_t num_rows, int32_t num_q_heads,
                                                      int32_t num_kv_heads, int32_t head_dim);

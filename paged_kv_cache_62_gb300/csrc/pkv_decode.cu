@@ -14,13 +14,23 @@ extern "C" size_t pkv_paged_decode_workspace_size(int32_t num_seqs, int32_t num_
     return ws_layout(num_seqs, num_q_heads / num_kv_heads, num_kv_heads, head_dim).total;
 }
 
+// The units of a call's list at most (`entries` of them hold work): unit counts and positions in the list are kept in
+// 32 bits.  int8 calls count the units of the CTA that runs them, the others 8 tokens of a kv head.
+static int64_t unit_bound(int ct, bool qs, int G, int32_t num_kv_heads, int64_t entries, int64_t len_limit)
+{
+    if (ct != kI8) return int64_t(num_kv_heads) * entries * ((len_limit + 7) / 8);
+    const int hg = qs ? 1 : head_group(num_kv_heads, G);
+    const int toks = warp_tokens(G, true, qs, qs) * (qs ? 1 : warp_slices(G, hg));
+    return num_kv_heads / hg * entries * ((len_limit + toks - 1) / toks);
+}
+
 // Shared by the entry points of all cache types (ct; k_scale / v_scale: the
 // per-kv-head scales of E4M3 caches, scales: those of int8 ones, device arrays).  qn > 1: entry b holds up to qn
 // queries that share its K/V stream as qn * G virtual heads of a kv head --
 // with row_cnt null, every entry is a sequence with qn new tokens (q / out rows
 // b * qn + i; context_lens the sequences' whole lengths); otherwise entry b
 // holds row_cnt[b] queries at rows b + i (row_seq[b]: its sequence,
-// context_lens[b]: the length its last query sees).
+// context_lens[b]: the length its last query sees).  live: the entries that can hold work, where not all do.
 static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, const void *k_cache, const void *v_cache,
                               const float *k_scale, const float *v_scale, const int32_t *row_seq,
                               const int32_t *row_cnt, const int32_t *block_tables,
@@ -30,7 +40,7 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
                               void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word,
                               pkv_stream_t stream, const uint16_t *k_new = nullptr, const uint16_t *v_new = nullptr,
                               int32_t *slot_out = nullptr, const float *scales = nullptr,
-                              const int32_t *row0 = nullptr)
+                              const int32_t *row0 = nullptr, int64_t live = -1)
 {
     const bool fp8 = ct != kBf16, i8 = ct == kI8;  // fp8: one byte per cached element
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
@@ -51,9 +61,7 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
     if (ct == kI8 && (!scales || (reinterpret_cast<uintptr_t>(scales) & 7u))) return PKV_EINVAL;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return PKV_EINVAL;
     const int64_t len_limit = std::min<int64_t>(max_context_len, int64_t(max_blocks_per_seq) * block_size);
-    // unit counts (and positions in the unit list) are kept in 32 bits
-    const int64_t max_units = int64_t(num_kv_heads) * num_seqs * ((len_limit + 7) / 8);
-    if (max_units > INT32_MAX) return PKV_EBOUNDS;
+    if (unit_bound(ct, qs, G, num_kv_heads, live < 0 ? num_seqs : live, len_limit) > INT32_MAX) return PKV_EBOUNDS;
     if (qs && (ct == kE4m3 || !row_cnt || (i8 && !row0))) return PKV_EINVAL;  // query-split entries are chunks of bf16 or int8 calls
     if ((k_new || v_new) && (qs || ct == kI8 || qn != 1 || row_seq || !k_new || !v_new || !aligned16(k_new) ||
                              !aligned16(v_new)))
@@ -445,7 +453,7 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     if (num_seqs == 0 || !context_lens || (new_per_seq == 0 && !cu_seqlens_q)) return PKV_EINVAL;
     if (new_per_seq > 0 && int64_t(num_seqs) * new_per_seq != num_rows) return PKV_EINVAL;
     if (num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0) return PKV_EINVAL;
-    if (ct == kI8) {  // all of decode_call's refusals: a refused call writes nothing
+    if (ct == kI8) {  // decode_call's refusals that need no more than the arguments: a refused call writes nothing
         if (head_dim <= 0 || block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0 ||
             num_workers < 0 || !std::isfinite(scale))
             return PKV_EINVAL;
@@ -494,6 +502,19 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
         qs = entries <= num_rows && workspace_bytes >= i8_entries_bytes(int32_t(entries), num_kv_heads, head_dim);
     const int32_t chunk = !qs ? qg : ct == kI8 ? tile : entry_queries(num_q_heads, num_kv_heads);
     uint8_t *wsb = static_cast<uint8_t *>(workspace);
+    int64_t live = -1;
+    if (ct == kI8) {  // the rest of decode_call's refusals, before the list is laid out
+        const int G = num_q_heads / num_kv_heads * qg, hg = head_group(num_kv_heads, G);
+        live = std::min<int64_t>(num_rows, int64_t(num_rows) / chunk + num_seqs);
+        if (unit_bound(ct, qs, G, num_kv_heads, live,
+                       std::min<int64_t>(max_context_len, int64_t(max_blocks_per_seq) * block_size)) > INT32_MAX)
+            return PKV_EBOUNDS;
+        DeviceInfo dev;
+        if (!current_device_info(&dev)) return PKV_ECUDA;
+        if (!qs && cta_layout(head_dim, G, 1, hg, warp_slices(G, hg), 2, num_rows, false, false, 2, true).total >
+                       uint32_t(dev.max_smem_optin))
+            return PKV_EUNSUPPORTED;
+    }
     if (ct == kI8 && qs) {
         const size_t dec_bytes = i8_entries_bytes(int32_t(entries), num_kv_heads, head_dim) -
                                  align256(size_t(entries) * 16);
@@ -515,7 +536,7 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
         return decode_call(ct, true, qg, q, k_cache, v_cache, nullptr, nullptr, row_seq, row_cnt, block_tables,
                            max_blocks_per_seq, row_len, int32_t(entries), num_q_heads, num_kv_heads, head_dim, block_size,
                            num_blocks, max_context_len, scale, out, workspace, dec_bytes, num_workers, err_word, stream,
-                           nullptr, nullptr, nullptr, scales, row0);
+                           nullptr, nullptr, nullptr, scales, row0, live);
     }
     const size_t dec_bytes = need - 3 * rows_bytes(num_rows);
     int32_t *row_seq = reinterpret_cast<int32_t *>(wsb + dec_bytes);
@@ -534,7 +555,7 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     return decode_call(ct, qs, qg, q, k_cache, v_cache, nullptr, nullptr, row_seq, row_cnt, block_tables,
                        max_blocks_per_seq, row_len, num_rows, num_q_heads, num_kv_heads, head_dim, block_size,
                        num_blocks, max_context_len, scale, out, workspace, dec_bytes, num_workers, err_word, stream,
-                       nullptr, nullptr, nullptr, scales);
+                       nullptr, nullptr, nullptr, scales, nullptr, live);
 }
 
 extern "C" pkv_status pkv_paged_attention(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,

@@ -801,3 +801,41 @@ def test_attention_keeps_to_its_workspace(heads, D, new, kind):
             out = attend(q, kc, vc, sc, btd, cu, ld, D ** -0.5, workers=workers, ws=ws, err=err)
             check(out, q, kc, vc, sc, bt, lens, new, D ** -0.5, f"{heads} {kind} {workers}")
         assert err.item() == 0 and torch.all(block[n:] == 0x5a)
+
+
+@pytest.mark.parametrize("kind", ["decode", "attention"])
+def test_many_rows_of_long_tables(kind):
+    """The row limit with tables of 131072 tokens each, single tokens."""
+    B, Hq, Hkv, D, bs, mb = pkv.MAX_SEQS, 16, 8, 64, 1024, 128
+    lens = [1 + i % 40 for i in range(64)]
+    q, kc, vc, sc, bt, _, ld = synth(lens, Hq, Hkv, D, bs, seed=3)
+    full = np.full((64, mb), -1, np.int32)
+    full[:, :bt.shape[1]] = bt
+    btd = torch.from_numpy(full).cuda().repeat(B // 64, 1)
+    q, ld = q.repeat(B // 64, 1, 1), ld.repeat(B // 64)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    if kind == "decode":
+        out = decode(q, kc, vc, sc, btd, ld, 0.125, err=err)
+    else:
+        out = attend(q, kc, vc, sc, btd, torch.arange(B + 1, dtype=torch.int32, device="cuda"), ld, 0.125, err=err)
+    assert err.item() == 0
+    check(out[:64], q[:64], kc, vc, sc, bt, lens, [1] * 64, 0.125, "first")
+    check(out[-64:], q[-64:], kc, vc, sc, bt, lens, [1] * 64, 0.125, "last")
+
+
+def test_rows_beyond_shared_memory_are_refused_before_anything_is_written():
+    """head_dim 128, 16384 runs of one row: the list does not fit beside the tiles (a decode call takes them)."""
+    B, Hq, Hkv, D = pkv.MAX_SEQS, 16, 8, 128
+    q, kc, vc, sc, bt, btd, ld = synth([5], Hq, Hkv, D, 16, seed=3)
+    q, btd, ld = q.repeat(B, 1, 1), btd.repeat(B, 1), ld.repeat(B)
+    out = torch.full_like(q, 7.0)
+    ws = pkv.alloc_attention_workspace(B, Hq, Hkv, D)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(pkv.PkvError) as e:
+        pkv.paged_attention_i8(q, kc, vc, sc, btd, cu, ld, D ** -0.5, out, ws, err_word=err)
+    torch.cuda.synchronize()
+    assert e.value.status == pkv.EUNSUPPORTED
+    assert torch.all(out == 7.0) and not ws.any() and err.item() == 0
+    one = decode(q, kc, vc, sc, btd, ld, D ** -0.5)
+    check(one[:3], q[:3], kc, vc, sc, np.repeat(bt, 3, 0), [5] * 3, [1] * 3, D ** -0.5, "decode")

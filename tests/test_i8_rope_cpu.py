@@ -168,3 +168,21 @@ def test_int8_attention_workspace_sizes(lib):
         for hq, hkv, d in ((16, 8, 128), (14, 2, 64), (9, 1, 64), (16, 1, 128), (15, 5, 128)):
             assert f(rows, hq, hkv, d) >= g(rows, hq, hkv, d)
             assert f(rows, hq, hkv, d) <= f(rows + 100, hq, hkv, d) or rows + 100 > pkv.MAX_SEQS
+
+
+# ------------------------------------------------------------------------------------------ long unit lists
+def test_unit_lists_beyond_32_bits_are_refused_before_anything_is_launched(lib):
+    """16000 rows of 100 sequences of up to 2^31 - 1 tokens: 350 entries x 8 kv heads x 2^24 tiles; the same in runs
+    of a few rows (a launch would end in ECUDA here)."""
+    kw = dict(mb=1 << 27, mx=(1 << 31) - 1)
+    assert lib.pkv_paged_attention_i8(*swap(ATT, ATT_OK, T=16000, B=100, **kw)) == pkv.EBOUNDS
+    assert lib.pkv_paged_attention_i8(*swap(ATT, ATT_OK, T=7000, B=7000, **kw)) == pkv.EBOUNDS
+    assert lib.pkv_paged_decode_i8(*swap(DEC, DEC_OK, B=7000, **kw)) == pkv.EBOUNDS
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the calls would go on to their launch")
+def test_long_tables_are_not_refused(lib):
+    """A list of at most 16384 x 4096 units (32 tokens of 8 kv heads) fits 32 bits by far."""
+    kw = dict(B=pkv.MAX_SEQS, mb=8192, mx=131072)
+    assert lib.pkv_paged_decode_i8(*swap(DEC, DEC_OK, **kw)) == pkv.ECUDA
+    assert lib.pkv_paged_attention_i8(*swap(ATT, ATT_OK, D=64, T=pkv.MAX_SEQS, **kw)) == pkv.ECUDA
