@@ -839,3 +839,74 @@ def test_rows_beyond_shared_memory_are_refused_before_anything_is_written():
     assert torch.all(out == 7.0) and not ws.any() and err.item() == 0
     one = decode(q, kc, vc, sc, btd, ld, D ** -0.5)
     check(one[:3], q[:3], kc, vc, sc, np.repeat(bt, 3, 0), [5] * 3, [1] * 3, D ** -0.5, "decode")
+
+
+# ------------------------------------------------------------------------------------------ bad pages, default split
+@pytest.mark.parametrize("bad", ["negative", "behind", "far"])
+@pytest.mark.parametrize("heads,D,bs,n", [((16, 8), 128, 16, 3), ((16, 8), 128, 256, 48), ((14, 2), 64, 32, 48),
+                                          ((14, 2), 64, 64, 2)])
+def test_attention_flags_bad_blocks(heads, D, bs, n, bad):
+    """A page outside the cache, first, in the middle or last of a sequence, in the 16-row and the 128-row tiles: the
+    flag, and the other sequences right."""
+    Hq, Hkv = heads
+    lens, new = [n + 300, n + 301, n + 20, n + 340], [n] * 4
+    q, kc, vc, sc, bt, btd, ld = synth(lens, Hq, Hkv, D, bs, seed=17, new=new)
+    ids = {"negative": -1, "behind": kc.shape[0], "far": 2 ** 31 - 1}[bad]
+    last = -(-lens[1] // bs) - 1
+    for at in sorted({0, last // 2, last}):
+        table = btd.clone()
+        table[1, at] = ids
+        for workers in (0, 60):
+            err = torch.zeros(1, dtype=torch.int32, device="cuda")
+            out = attend(q, kc, vc, sc, table, None, ld, D ** -0.5, n=n, workers=workers, err=err)
+            assert err.item() == pkv.ERR_BLOCK_RANGE
+            for b in (0, 2, 3):
+                check(out[b * n:(b + 1) * n], q[b * n:(b + 1) * n], kc, vc, sc, bt[b:b + 1], [lens[b]], [n], D ** -0.5,
+                      f"page {at} {bad} seq {b}")
+
+
+def test_one_workspace_with_the_default_split():
+    """As test_one_workspace_serves_calls_of_every_kind with num_workers = 0, whose split follows earlier calls: every
+    output against the 64-bit reference.  bf16 calls round their weights to bf16, by at most 2^-8 of themselves (2^-8 A,
+    and as much again for the rest)."""
+    Hq, Hkv, D, bs = 16, 8, 128, 64
+    lens, n = [640, 70, 1300, 200], 40
+    qa, kc, vc, sc, bt, btd, ld = synth(lens, Hq, Hkv, D, bs, seed=21, new=[n] * 4)
+    kb, vb = (torch.randn(kc.shape, device="cuda").bfloat16() for _ in range(2))
+    scale = D ** -0.5
+    ones = torch.ones_like(sc)
+    ws = pkv.alloc_attention_workspace(4 * n, Hq, Hkv, D)
+    want = {}
+    for m in (1, 3, n):
+        q = qa[:4 * m].contiguous()
+        want[m] = (q, attend_i8(q.cpu(), kc.cpu(), vc.cpu(), sc.cpu(), bt, lens, [m] * 4, scale),
+                   attend_i8(q.cpu(), kb.cpu(), vb.cpu(), ones.cpu(), bt, lens, [m] * 4, scale))
+    order = np.random.default_rng(3).permutation(48)
+    for i in order:
+        m, int8 = (1, 3, n)[i % 3], (i // 3) % 2 == 0
+        q, w8, wb = want[m]
+        if int8:
+            out = decode(q, kc, vc, sc, btd, ld, scale, 0, ws) if m == 1 else attend(q, kc, vc, sc, btd, None, ld, scale, m, 0, ws)
+        else:
+            out = torch.full_like(q, float("nan"))
+            if m == 1:
+                pkv.paged_decode(q, kb, vb, btd, ld, scale, out, ws)
+            else:
+                pkv.paged_attention(q, kb, vb, btd, None, ld, scale, out, ws, new_per_seq=m)
+        ref, mag = w8 if int8 else wb
+        off = (out.cpu().double() - ref).abs() - (2.0 ** -8 * ref.abs() + 2.0 ** (-10 if int8 else -7) * mag)
+        assert torch.isfinite(out).all() and off.max() <= 0, (i, m, int8, off.max())
+
+
+@pytest.mark.parametrize("n", [1, 4, 64])
+def test_a_fixed_split_repeats_bit_for_bit(n):
+    lens = [900, 64, 2100, 300, 128]
+    q, kc, vc, sc, bt, btd, ld = synth(lens, 16, 8, 128, 64, seed=6, new=[n] * 5)
+    ws = pkv.alloc_attention_workspace(5 * n, 16, 8, 128)
+    run = lambda w: (decode(q, kc, vc, sc, btd, ld, 128 ** -0.5, w, ws) if n == 1 else
+                     attend(q, kc, vc, sc, btd, None, ld, 128 ** -0.5, n, w, ws))
+    first = {w: run(w) for w in (64, 300, 1200)}
+    for _ in range(5):
+        run(0)
+        for w, x in first.items():
+            assert torch.equal(run(w), x)
