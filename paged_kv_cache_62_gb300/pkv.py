@@ -515,7 +515,8 @@ def alloc_i8_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_dim
         raise ValueError(f"int8 caches need a block_size that is a multiple of {I8_BLOCK}")
     shape = (num_blocks, block_size, num_kv_heads, head_dim)
     kc, vc = (torch.zeros(shape, dtype=torch.int8, device=device or "cuda") for _ in range(2))
-    return kc, vc, torch.zeros(num_blocks, block_size // I8_BLOCK, num_kv_heads, 2, device=device or "cuda")
+    return kc, vc, torch.zeros(num_blocks, block_size // I8_BLOCK, num_kv_heads, 2, dtype=torch.float32,
+                               device=device or "cuda")
 
 
 def kv_store_i8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor,

@@ -186,3 +186,16 @@ def test_long_tables_are_not_refused(lib):
     kw = dict(B=pkv.MAX_SEQS, mb=8192, mx=131072)
     assert lib.pkv_paged_decode_i8(*swap(DEC, DEC_OK, **kw)) == pkv.ECUDA
     assert lib.pkv_paged_attention_i8(*swap(ATT, ATT_OK, D=64, T=pkv.MAX_SEQS, **kw)) == pkv.ECUDA
+
+
+# ------------------------------------------------------------------------------------------ allocation
+def test_an_int8_cache_has_fp32_scales_whatever_the_default_type():
+    """Engines set the model's type as torch's default."""
+    old = torch.get_default_dtype()
+    torch.set_default_dtype(torch.bfloat16)
+    try:
+        k, v, sc = pkv.alloc_i8_cache(3, 32, 2, 64, device="cpu")
+    finally:
+        torch.set_default_dtype(old)
+    assert k.dtype == v.dtype == torch.int8 and sc.dtype == torch.float32
+    assert k.shape == v.shape == (3, 32, 2, 64) and sc.shape == (3, 2, 2, 2)
