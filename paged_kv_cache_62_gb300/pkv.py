@@ -166,7 +166,7 @@ def paged_decode_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: i
 def alloc_workspace(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
     """A decode workspace, zero-filled as the library requires before its first use."""
     n = paged_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim)
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(n, dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def paged_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -461,7 +461,7 @@ def alloc_attention_workspace(num_rows: int, num_q_heads: int, num_kv_heads: int
     n = load().pkv_paged_attention_i8_workspace_size(num_rows, num_q_heads, num_kv_heads, head_dim)
     if n == 0:
         raise ValueError("paged_attention: unsupported sizes")
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(n, dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -514,9 +514,9 @@ def alloc_i8_cache(num_blocks: int, block_size: int, num_kv_heads: int, head_dim
     if block_size % I8_BLOCK:
         raise ValueError(f"int8 caches need a block_size that is a multiple of {I8_BLOCK}")
     shape = (num_blocks, block_size, num_kv_heads, head_dim)
-    kc, vc = (torch.zeros(shape, dtype=torch.int8, device=device or "cuda") for _ in range(2))
+    kc, vc = (torch.zeros(shape, dtype=torch.int8, device="cuda" if device is None else device) for _ in range(2))
     return kc, vc, torch.zeros(num_blocks, block_size // I8_BLOCK, num_kv_heads, 2, dtype=torch.float32,
-                               device=device or "cuda")
+                               device="cuda" if device is None else device)
 
 
 def kv_store_i8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor,

@@ -199,3 +199,17 @@ def test_an_int8_cache_has_fp32_scales_whatever_the_default_type():
         torch.set_default_dtype(old)
     assert k.dtype == v.dtype == torch.int8 and sc.dtype == torch.float32
     assert k.shape == v.shape == (3, 32, 2, 64) and sc.shape == (3, 2, 2, 2)
+
+
+@pytest.mark.parametrize("alloc,args", [(pkv.alloc_i8_cache, (3, 32, 2, 64)), (pkv.alloc_workspace, (2, 4, 2, 64)),
+                                        (pkv.alloc_attention_workspace, (5, 4, 2, 64))])
+def test_device_0_is_a_device(lib, monkeypatch, alloc, args):
+    """Device index 0 is not taken as "none given" (the current device)."""
+    asked = []
+    zeros = torch.zeros
+    monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **kw: asked.append(device) or zeros(*a, **kw))
+    alloc(*args, device=0)
+    assert asked and all(d == 0 and d is not None and not isinstance(d, str) for d in asked)
+    asked.clear()
+    alloc(*args)
+    assert asked and all(d == "cuda" for d in asked)
