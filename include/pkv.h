@@ -496,8 +496,13 @@ PKV_API pkv_status pkv_kv_store_i8(const uint16_t *k, const uint16_t *v, int64_t
  * num_workers, errors) as pkv_paged_decode.  Products run in f16 with fp32
  * accumulators: codes are exact, a query row is scaled by a power of two that
  * keeps elements of at least 2^-28 of its largest exact, softmax weights round
- * by at most 2^-11 of themselves; scales enter in fp32.  V scales below 2^-104
- * count as zero, above 2^104 as NaN; within a sequence they may lie 2^90 apart.
+ * by at most 2^-11 of themselves; scales enter in fp32.  Scores of decode calls
+ * and short runs are sums with codes 1152 too large, taken off again: they err
+ * by about 2^-17 of the largest score that the query could have.  V scales
+ * below 2^-104 count as zero (so may, in sequences of more than 1024 tokens,
+ * those below 2^-114 times the length), above 2^104 as NaN; within a sequence
+ * they may lie 2^90 apart.  With num_workers 0 the split follows earlier calls'
+ * times, as pkv_paged_decode's does, and with it the last bits of an output.
  * A NaN scale (see pkv_kv_store_i8) gives NaN to the queries that see its block.
  */
 PKV_API pkv_status pkv_paged_decode_i8(const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache,
@@ -514,8 +519,8 @@ PKV_API pkv_status pkv_paged_decode_i8(const uint16_t *q, const int8_t *k_cache,
  * already stored by pkv_kv_store_i8.  Workspace:
  * pkv_paged_attention_i8_workspace_size bytes, which also do for
  * pkv_paged_attention; with less, down to pkv_paged_attention_workspace_size
- * (the same in most calls whose num_q_heads / num_kv_heads is a power of two),
- * long runs of new tokens whose pieces do not fit go without the tensor-memory
+ * (which does for most calls whose num_q_heads / num_kv_heads is a power of
+ * two), long runs of new tokens whose pieces do not fit go without tensor-memory
  * CTAs (64 new tokens of 64 sequences of 512-4096, 14 / 2 heads of 64: 484 us
  * against 148).  Limits as pkv_paged_decode_i8, everything else
  * as pkv_paged_attention.  The list of rows is kept in shared memory: with

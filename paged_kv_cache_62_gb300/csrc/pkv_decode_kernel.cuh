@@ -2619,7 +2619,8 @@ inline bool encode_cache_map(CUtensorMap *map, const void *base, bool fp8, int D
                            const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                            // one kv head of 8-bit codes is 64 or 128 bytes of a token's row: a longer fetch would
-                           // read another head's
+                           // read another head's (E4M3, 22 / 11 heads, 64 sequences of 2048: 88.2 -> 73.0 us with
+                           // heads of 128, 65.9 -> 57.4 with 64; int8 chunks: DRAM reads 497 -> 344 MB)
                            fp8 && box_heads == 1 && Hkv > 1 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
                                                             : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

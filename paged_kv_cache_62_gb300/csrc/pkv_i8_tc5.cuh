@@ -17,7 +17,7 @@
 //
 // What bounds it: the straight-line instructions between a unit's loops.  Three kinds of warps run different code
 // on the SM and a line of it is gone from the nearest instruction cache when a warp comes round to it a unit
-// later, so the passes over the keys are loops of 16 keys, waits are as short as they can be
+// later, so the passes over the keys are loops of 16 keys, waits are short
 // (mbar_wait_lean), and the exchange between two threads of a row that the bf16 CTA makes every unit is gone.
 // Measured: 64 new tokens of each of 64 sequences of 512-4096 (16 / 8 heads of 128) 155 us, 517 TFLOP/s, 2.3 TB/s
 // of codes; 3100 cycles a 128-key tile, of which its shared-memory traffic alone needs 1790 (copies in 256,

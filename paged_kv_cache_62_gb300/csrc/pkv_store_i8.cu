@@ -12,9 +12,12 @@
 // The store gives one warp a (scale block, kv head, K or V): the block's maximum, its scale and its codes need no
 // atomics and no second launch, and the result does not depend on the order in which warps run.  The rows are read
 // twice, the second time from L1: 16 rows of 128 values held in registers would leave half the warps on an SM.
-// What bounds prompts is issue (widening, rounding, checking and packing each value), then memory: 22k rows of 8
-// heads of 128, 137 MB, in 30.9 us = 4.4 TB/s, 0.65 of the copy rate; with a division a value 73 us, with the rows
-// in registers 52 us.  A decode step's 64 rows take 2.8 us, a launch and its dependent loads.
+// Prompts: 22k rows of 8 heads of 128, 137 MB, in 30.9 us = 4.4 TB/s, 0.65 of the copy rate; with a division a value
+// 73 us, with the rows in registers 52 us.  No one resource holds them: instructions issue in 66 % of the cycles
+// (15 a value and lane, half of them the rounding and its check), and a warp's longest wait is for the rows, its two
+// passes over them one after the other.  A decode step's 64 rows take 2.9 us, a launch and its dependent loads; a
+// step that grows every block's scale 4.5 us with one earlier row to requantise a block and 12 us with fourteen
+// (one code at a time, out of line: rare in a real run, where a block's maximum grows ever more seldom).
 // The copies are memory-bound: 120 pages of 256 tokens, 126 MB, in 20.6 us = 6.1 TB/s, 0.90 of the copy rate.
 #include <algorithm>
 
@@ -111,10 +114,10 @@ __device__ __forceinline__ uint4 lifted(uint4 w)
 }
 
 // One CTA (or, for few slots, a few: blockIdx.y) per slot of the block list; its warps take the (kv head, K or V)
-// pairs of the slot's scale block.  Slots: with new_per_seq each sequence has slots_per_seq of them (as many blocks as n rows can reach);
-// with offsets sequence b has those from cu[b] / 16 + 2 b on, which leaves room for the floor((n + 14) / 16)
-// + 1 blocks that n rows can reach, so a slot finds its sequence by a search over the offsets and no prefix
-// over blocks is needed.
+// pairs of the slot's scale block.  Slots: with new_per_seq each sequence has slots_per_seq of them (as many blocks
+// as n rows can reach); with offsets sequence b has those from cu[b] / 16 + 2 b on, which leaves room for the
+// floor((n + 14) / 16) + 1 blocks that n rows can reach, so a slot finds its sequence by a search over the offsets
+// and no prefix over blocks is needed.
 template <int D>
 __global__ void __launch_bounds__(kStoreThreads, 5) kv_store_i8_kernel(const StoreI8Params p)
 {

@@ -2,9 +2,11 @@
 
 Argument marshalling only: every step runs in the library's CUDA kernels.
 Tensors are torch CUDA tensors (device memory and streams come from torch);
-shapes and dtypes are checked here, then raw device pointers go through the
-C ABI.  There is no fallback: if the library is missing or the tensors are not
-on a CUDA device, the call raises.
+shapes and dtypes are checked here (those of the int8 and rotary calls in
+``_pkv_torch.so``, native code beside the library), then raw device pointers go
+through the C ABI.  There is no fallback: if the library, or for those calls
+``_pkv_torch.so``, is missing, or the tensors are not on a CUDA device, the call
+raises.
 """
 from __future__ import annotations
 
