@@ -540,6 +540,93 @@ PKV_API pkv_status pkv_paged_attention_i8(const uint16_t *q, const int8_t *k_cac
                                           pkv_stream_t stream);
 
 /*
+ * Sliding windows with sinks.  The calls below are pkv_paged_decode,
+ * pkv_paged_decode_fp8, pkv_paged_decode_i8, pkv_paged_attention and
+ * pkv_paged_attention_i8 for models whose layers see a window: the query at
+ * position p (decode: p = context_lens[b] - 1) attends the keys j <= p with
+ *     j > p - window   or   j < sinks.
+ * window >= 1 and sinks >= 0 (else PKV_EINVAL); a window as long as the
+ * sequence sees all of it, window 1 and sinks 0 the query's own key alone.
+ * (The pages have no counterpart; they name no windowed model.)
+ *
+ * Only what some query of a sequence sees is read: the blocks between the
+ * sinks and the window of the sequence's first new token may have been given
+ * back, and their table entries may hold anything (-1, say).  A block that
+ * holds a key that some query sees must be there, its other rows may hold
+ * anything.  block_tables rows still run from the sequence's first block, and
+ * context_lens count every token.  A call streams about
+ * min(L, window + sinks + n) key rows per sequence and kv head and pass over
+ * them (see pkv_paged_attention for n new tokens).
+ * Arguments, workspaces (the same functions size them; a workspace may serve
+ * these calls and the others in turn), num_workers, limits and errors as the
+ * calls without window; max_context_len at most 2^30 (PKV_EBOUNDS).  Where a
+ * call's queries share a pass, K and V of a key that one of them sees should be finite: an
+ * infinity or NaN there may reach the others.
+ */
+PKV_API pkv_status pkv_paged_decode_window(
+    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+    int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+    int32_t num_blocks, int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out,
+    void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream);
+PKV_API pkv_status pkv_paged_decode_window_fp8(
+    const uint16_t *q, const uint8_t *k_cache, const uint8_t *v_cache, const float *k_scale,
+    const float *v_scale, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+    int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+    int32_t num_blocks, int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out,
+    void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream);
+PKV_API pkv_status pkv_paged_decode_window_i8(
+    const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache, const float *scales,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+    int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+    int32_t num_blocks, int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out,
+    void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream);
+PKV_API pkv_status pkv_paged_attention_window(
+    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
+    const int32_t *context_lens, int32_t num_seqs, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, int32_t window,
+    int32_t sinks, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
+    int32_t *err_word, pkv_stream_t stream);
+PKV_API pkv_status pkv_paged_attention_window_i8(
+    const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache, const float *scales,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
+    const int32_t *context_lens, int32_t num_seqs, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, int32_t window,
+    int32_t sinks, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
+    int32_t *err_word, pkv_stream_t stream);
+
+/*
+ * pkv_paged_attention_tree, pkv_paged_attention_tree_i8 -- attention of a
+ * tree of drafted tokens (speculative decoding: several continuations of a
+ * sequence verified in one pass).  As pkv_paged_attention (its i8 form), with
+ * the sequence's n new tokens the nodes of a tree: node i's K and V are stored
+ * at position L - n + i, parents before their children, and query row
+ * cu_seqlens_q[b] + i (b * n + i with new_per_seq = n) attends the keys
+ * j < L - n, and key L - n + t, t <= i, if bit t of its mask is set:
+ *   tree_mask   [num_rows, mask_words] int32, bit t of a row is bit t % 32 of
+ *               word t / 32; bits of later nodes (t > i) are ignored.  A node
+ *               sees itself only if its own bit is set.
+ * A row that sees no key (L = n and an empty mask) gives zeros.  The mask of a
+ * chain is its lower triangle: the results of pkv_paged_attention.
+ * mask_words >= 1; a sequence has at most 32 * mask_words nodes (new_per_seq
+ * beyond: PKV_EINVAL; offsets beyond: zeros and PKV_ERR_CONTEXT_RANGE).  Other
+ * limits, workspaces, sharing of passes and errors as pkv_paged_attention;
+ * max_context_len at most 2^30 (PKV_EBOUNDS).  (The pages have no counterpart.)
+ */
+PKV_API pkv_status pkv_paged_attention_tree(
+    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
+    const int32_t *context_lens, int32_t num_seqs, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, const int32_t *tree_mask,
+    int32_t mask_words, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
+    int32_t *err_word, pkv_stream_t stream);
+PKV_API pkv_status pkv_paged_attention_tree_i8(
+    const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache, const float *scales,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
+    const int32_t *context_lens, int32_t num_seqs, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, const int32_t *tree_mask,
+    int32_t mask_words, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
+    int32_t *err_word, pkv_stream_t stream);
+
+/*
  * pkv_copy_blocks_i8 -- pkv_copy_blocks for int8 caches: block dst of both
  * code arrays and of the scales becomes a copy of block src, for every pair.
  * Pairs, ids and errors as pkv_copy_blocks; block_size a multiple of 16.
@@ -594,6 +681,37 @@ PKV_API pkv_status pkv_rope_store(const uint16_t *q, int64_t q_stride, const uin
                                   int32_t rot_dim, int32_t interleaved, uint16_t *q_out, int64_t q_out_stride,
                                   uint16_t *k_cache, uint16_t *v_cache, int32_t num_blocks, int32_t block_size,
                                   int32_t *err_word, pkv_stream_t stream);
+
+/*
+ * pkv_qk_norm_rope, pkv_qk_norm_rope_store -- pkv_rope and pkv_rope_store with
+ * a root-mean-square norm of each query and key head before the turn, in the
+ * same pass: a head x of q (k) becomes
+ *     y_i = x_i / sqrt(mean_i(x_i^2) + eps) * q_weight[i]  (k_weight[i]),
+ * and y is turned as pkv_rope turns it; dims from rot_dim on are normed too.
+ * fp32 (sums of squares included: a head whose squares pass 2^128 counts as
+ * infinite), rounded to bf16 once; v is stored as it is.
+ *
+ *   q_weight, k_weight  [head_dim] float32, 16-byte aligned (a layer's weights,
+ *                       converted once), or NULL: ones
+ *   eps                 finite, > 0 (a head of zeros stays zeros)
+ * Everything else as pkv_rope / pkv_rope_store.
+ */
+PKV_API pkv_status pkv_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                                    const float *q_weight, const float *k_weight, float eps,
+                                    const int32_t *positions, int32_t num_axes, const float *inv_freq,
+                                    const int32_t *freq_axis, int32_t num_tokens, int32_t num_q_heads,
+                                    int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
+                                    uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
+                                    int32_t *err_word, pkv_stream_t stream);
+PKV_API pkv_status pkv_qk_norm_rope_store(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                                          const uint16_t *v, int64_t v_stride, const float *q_weight,
+                                          const float *k_weight, float eps, const int32_t *positions,
+                                          int32_t num_axes, const float *inv_freq, const int32_t *freq_axis,
+                                          const int32_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                                          int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim,
+                                          int32_t interleaved, uint16_t *q_out, int64_t q_out_stride,
+                                          uint16_t *k_cache, uint16_t *v_cache, int32_t num_blocks,
+                                          int32_t block_size, int32_t *err_word, pkv_stream_t stream);
 
 /*
  * pkv_copy_blocks -- batched copy-on-write block copies.

@@ -24,6 +24,31 @@ static int64_t unit_bound(int ct, bool qs, int G, int32_t num_kv_heads, int64_t 
     return num_kv_heads / hg * entries * ((len_limit + toks - 1) / toks);
 }
 
+// What a masked call adds (see DecodeParams): a window and sinks, or a tree over the sequences' new tokens.
+struct MaskArgs {
+    int32_t window = INT32_MAX, sinks = 0;
+    const uint32_t *tree = nullptr;
+    int32_t tree_words = 0, tree_n = 0;
+    const int32_t *tree_lens = nullptr, *tree_cu = nullptr;
+};
+
+// Longest sequences of masked calls: a position less a window length or a tile's start stays in 32 bits.
+constexpr int64_t kMaskMaxLen = 1 << 30;
+
+static pkv_status check_mask(const MaskArgs &m, bool tree)
+{
+    if (!tree) return m.window < 1 || m.sinks < 0 ? PKV_EINVAL : PKV_OK;
+    if (m.tree_words < 1 || m.tree_n > 32LL * m.tree_words || (reinterpret_cast<uintptr_t>(m.tree) & 3u))
+        return PKV_EINVAL;
+    return PKV_OK;
+}
+
+// Tokens of a sequence that its last n queries see, at most.
+static int64_t seen_bound(const MaskArgs *m, int64_t len_limit, int64_t n)
+{
+    return m ? std::min<int64_t>(len_limit, int64_t(m->window) + m->sinks + n - 1) : len_limit;
+}
+
 // Shared by the entry points of all cache types (ct; k_scale / v_scale: the
 // per-kv-head scales of E4M3 caches, scales: those of int8 ones, device arrays).  qn > 1: entry b holds up to qn
 // queries that share its K/V stream as qn * G virtual heads of a kv head --
@@ -40,7 +65,7 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
                               void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word,
                               pkv_stream_t stream, const uint16_t *k_new = nullptr, const uint16_t *v_new = nullptr,
                               int32_t *slot_out = nullptr, const float *scales = nullptr,
-                              const int32_t *row0 = nullptr, int64_t live = -1)
+                              const int32_t *row0 = nullptr, int64_t live = -1, const MaskArgs *mask = nullptr)
 {
     const bool fp8 = ct != kBf16, i8 = ct == kI8;  // fp8: one byte per cached element
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
@@ -62,6 +87,7 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return PKV_EINVAL;
     const int64_t len_limit = std::min<int64_t>(max_context_len, int64_t(max_blocks_per_seq) * block_size);
     if (unit_bound(ct, qs, G, num_kv_heads, live < 0 ? num_seqs : live, len_limit) > INT32_MAX) return PKV_EBOUNDS;
+    if (mask && len_limit > kMaskMaxLen) return PKV_EBOUNDS;
     if (qs && (ct == kE4m3 || !row_cnt || (i8 && !row0))) return PKV_EINVAL;  // query-split entries are chunks of bf16 or int8 calls
     if ((k_new || v_new) && (qs || ct == kI8 || qn != 1 || row_seq || !k_new || !v_new || !aligned16(k_new) ||
                              !aligned16(v_new)))
@@ -121,6 +147,15 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
     p.v_cache_w = static_cast<uint8_t *>(const_cast<void *>(v_cache));
     p.slot_out = k_new ? slot_out : nullptr;
     p.qstride = row_cnt ? 1 : qn;
+    if (mask) {
+        p.window = std::min(mask->window, std::max(p.len_limit, 1));  // (one as long as the sequences sees all)
+        p.sinks = std::min(mask->sinks, p.len_limit);
+        p.tree = mask->tree;
+        p.tree_words = mask->tree_words;
+        p.tree_n = mask->tree_n;
+        p.tree_lens = mask->tree_lens;
+        p.tree_cu = mask->tree_cu;
+    }
     a.k_cache = k_cache;
     a.v_cache = v_cache;
     a.device = dev.device;
@@ -134,7 +169,11 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
     // instead: a few units in one CTA's pipeline cost less than the split-K pieces and merge of a
     // split (per back-to-back call: tiny workload 8.3 -> 7.0 us, Qwen2.5-shaped 14.2 -> 9.0 us).
     if (num_workers == 0) {
-        const int64_t per_seg = (len_limit + p.toks - 1) / p.toks;
+        // (a window that begins inside a unit, or sinks that end inside one: a unit more each)
+        int64_t per_seg = (len_limit + p.toks - 1) / p.toks;
+        if (mask)
+            per_seg = std::min(per_seg, (seen_bound(mask, len_limit, int64_t(qn) * (qs ? team_warps(G) : 1)) +
+                                         p.toks - 1) / p.toks + 2);
         const int64_t units_max = int64_t(num_seqs) * p.nhg * per_seg;
         if (units_max < dev.sm_count) {
             if ((!qs || i8) && per_seg <= kSegmentUnits && int64_t(num_seqs) * p.nhg <= kMaxSlots) {
@@ -165,7 +204,13 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
     }
     a.stream = reinterpret_cast<cudaStream_t>(stream);
 
-    LaunchFn fn = ct == kE4m3 ? pick_decode_fp8(head_dim, G)
+    LaunchFn fn = mask && ct == kE4m3 ? pick_mask_fp8(head_dim, G)
+                  : mask && ct == kI8 ? (qs ? pick_mask_i8_tc5(head_dim)
+                                            : G > 8 ? pick_mask_i8_wide(head_dim, G) : pick_mask_i8(head_dim, G))
+                  : mask ? (tc5 ? pick_mask_tc5(head_dim)
+                            : qs  ? pick_mask_qs(head_dim, G)
+                            : G > 8 ? pick_mask_wide(head_dim, G) : pick_mask(head_dim, G))
+                  : ct == kE4m3 ? pick_decode_fp8(head_dim, G)
                   : ct == kI8 ? (qs ? pick_decode_i8_tc5(head_dim)
                                     : G > 8 ? pick_decode_i8_wide(head_dim, G) : pick_decode_i8(head_dim, G))
                   : tc5  ? pick_decode_tc5(head_dim)
@@ -285,11 +330,12 @@ __device__ __forceinline__ bool offsets_in_order(const int32_t *__restrict__ cu,
 // their own or their chunk's with length 0 (zero output) and set
 // PKV_ERR_CONTEXT_RANGE.  Offsets that decrease anywhere make every row one
 // of them: the search sees only some of such offsets.  With cu_seqlens_q null,
-// every sequence has new_per_seq rows (row r belongs to sequence r / new_per_seq).
+// every sequence has new_per_seq rows (row r belongs to sequence r / new_per_seq).  More than max_new rows of a
+// sequence (what a tree's masks hold) are inconsistent too.
 __global__ void expand_rows_kernel(const int32_t *__restrict__ cu_seqlens_q, int32_t new_per_seq,
                                    const int32_t *__restrict__ context_lens, int32_t num_seqs, int32_t num_rows,
-                                   int32_t chunk, int32_t *__restrict__ row_seq, int32_t *__restrict__ row_len,
-                                   int32_t *__restrict__ row_cnt, int32_t *err)
+                                   int32_t chunk, int32_t max_new, int32_t *__restrict__ row_seq,
+                                   int32_t *__restrict__ row_len, int32_t *__restrict__ row_cnt, int32_t *err)
 {
     griddep_launch_dependents();
     griddep_wait();
@@ -316,7 +362,7 @@ __global__ void expand_rows_kernel(const int32_t *__restrict__ cu_seqlens_q, int
     const int32_t L = __ldg(context_lens + lo);
     const int32_t n = r1 - r0, i = r - r0;
     const bool inside = ordered && r0 <= r && r < r1;
-    const bool ok = (!cu_seqlens_q || __ldg(cu_seqlens_q) == 0) && inside && n <= L && r1 <= num_rows;
+    const bool ok = (!cu_seqlens_q || __ldg(cu_seqlens_q) == 0) && inside && n <= L && n <= max_new && r1 <= num_rows;
     if (!ok) flag_error(err, PKV_ERR_CONTEXT_RANGE);
     int32_t cnt = 1, len = 0;  // a row outside its sequence's range: an entry of its own, zero output
     if (inside) {
@@ -336,8 +382,8 @@ __global__ void expand_rows_kernel(const int32_t *__restrict__ cu_seqlens_q, int
 // offsets decrease anywhere).
 __global__ void expand_entries_kernel(const int32_t *__restrict__ cu_seqlens_q, int32_t new_per_seq,
                                       const int32_t *__restrict__ context_lens, int32_t num_seqs, int32_t num_rows,
-                                      int32_t num_entries, int32_t chunk, int32_t len_limit, int32_t row_values,
-                                      int32_t *__restrict__ row_seq, int32_t *__restrict__ row_len,
+                                      int32_t num_entries, int32_t chunk, int32_t max_new, int32_t len_limit,
+                                      int32_t row_values, int32_t *__restrict__ row_seq, int32_t *__restrict__ row_len,
                                       int32_t *__restrict__ row_cnt, int32_t *__restrict__ row0,
                                       uint16_t *__restrict__ out, int32_t *err)
 {
@@ -360,7 +406,8 @@ __global__ void expand_entries_kernel(const int32_t *__restrict__ cu_seqlens_q, 
     };
     auto consistent = [&](int32_t b, int32_t r0, int32_t r1) {
         const int32_t L = __ldg(context_lens + b);
-        return ordered && start(0) == 0 && r0 >= 0 && r0 <= r1 && r1 <= num_rows && r1 - r0 <= L && L <= len_limit;
+        return ordered && start(0) == 0 && r0 >= 0 && r0 <= r1 && r1 <= num_rows && r1 - r0 <= L &&
+               r1 - r0 <= max_new && L <= len_limit;
     };
     if (x < num_entries) {
         const int32_t b = find(x, true), r0 = start(b), r1 = start(b + 1);
@@ -446,25 +493,30 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
                                  int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                  int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale,
                                  uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes,
-                                 int32_t num_workers, int32_t *err_word, pkv_stream_t stream)
+                                 int32_t num_workers, int32_t *err_word, pkv_stream_t stream,
+                                 const MaskArgs *mask = nullptr)
 {
     if (num_seqs < 0 || num_rows < 0 || new_per_seq < 0) return PKV_EINVAL;
     if (num_rows == 0) return PKV_OK;
     if (num_seqs == 0 || !context_lens || (new_per_seq == 0 && !cu_seqlens_q)) return PKV_EINVAL;
     if (new_per_seq > 0 && int64_t(num_seqs) * new_per_seq != num_rows) return PKV_EINVAL;
     if (num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0) return PKV_EINVAL;
-    if (ct == kI8) {  // decode_call's refusals that need no more than the arguments: a refused call writes nothing
+    if (ct == kI8 || mask) {  // decode_call's refusals that need no more than the arguments: a refused call writes nothing
         if (head_dim <= 0 || block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0 ||
             num_workers < 0 || !std::isfinite(scale))
             return PKV_EINVAL;
         if ((head_dim != 64 && head_dim != 128) || num_q_heads / num_kv_heads > 16 || !is_pow2(block_size) ||
-            block_size < kScaleToks || block_size > 1024)
+            block_size < (ct == kI8 ? kScaleToks : 8) || block_size > 1024)
             return PKV_EUNSUPPORTED;
         if (num_workers > PKV_MAX_WORKERS || int64_t(num_blocks) * block_size > INT32_MAX) return PKV_EBOUNDS;
-        if (!q || !k_cache || !v_cache || !scales || !block_tables || !out || !aligned16(q) || !aligned16(k_cache) ||
-            !aligned16(v_cache) || !aligned16(out) || (reinterpret_cast<uintptr_t>(scales) & 7u))
+        if (!q || !k_cache || !v_cache || (ct == kI8 && !scales) || !block_tables || !out || !aligned16(q) ||
+            !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+            (reinterpret_cast<uintptr_t>(scales) & 7u))
             return PKV_EINVAL;
     }
+    const int64_t len_max = std::min<int64_t>(max_context_len, int64_t(max_blocks_per_seq) * std::max(block_size, 0));
+    if (mask && len_max > kMaskMaxLen) return PKV_EBOUNDS;
+    const int32_t max_new = mask && mask->tree ? int32_t(std::min<int64_t>(32LL * mask->tree_words, INT32_MAX)) : INT32_MAX;
     const size_t need = pkv_paged_attention_workspace_size(num_rows, num_q_heads, num_kv_heads, head_dim);
     if (need == 0) return num_rows > PKV_MAX_SEQS ? PKV_EBOUNDS : PKV_EINVAL;
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return PKV_EWORKSPACE;
@@ -477,7 +529,8 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
         return decode_call(ct, false, new_per_seq, q, k_cache, v_cache, nullptr, nullptr, nullptr, nullptr,
                            block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads, num_kv_heads,
                            head_dim, block_size, num_blocks, max_context_len, scale, out, workspace,
-                           workspace_bytes, num_workers, err_word, stream, nullptr, nullptr, nullptr, scales);
+                           workspace_bytes, num_workers, err_word, stream, nullptr, nullptr, nullptr, scales,
+                           nullptr, -1, mask);
     // chunks of a sequence's queries, one entry per row; few new tokens per sequence on average (at
     // most two regular chunks): chunks of qg on regular CTAs, else chunks of 8 * qg on query-split ones.
     // The row arrays sit after the decode workspace.
@@ -492,8 +545,7 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
         DeviceInfo dev;
         if (!current_device_info(&dev)) return PKV_ECUDA;
         const int64_t tiles = int64_t(num_seqs) * num_kv_heads *
-                              ((std::min<int64_t>(max_context_len, int64_t(max_blocks_per_seq) * std::max(block_size, 0)) +
-                                kTc5Keys - 1) / kTc5Keys);
+                              ((seen_bound(mask, len_max, 2 * qg) + kTc5Keys - 1) / kTc5Keys);
         qs = tiles < 8 * int64_t(dev.sm_count) && num_rows / tile + num_seqs <= num_rows;
     }
     // (entries of a query-split int8 call; without room for their pieces the call takes regular CTAs)
@@ -503,7 +555,7 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     const int32_t chunk = !qs ? qg : ct == kI8 ? tile : entry_queries(num_q_heads, num_kv_heads);
     uint8_t *wsb = static_cast<uint8_t *>(workspace);
     int64_t live = -1;
-    if (ct == kI8) {  // the rest of decode_call's refusals, before the list is laid out
+    if (ct == kI8 || mask) {  // the rest of decode_call's refusals, before the list is laid out
         const int G = num_q_heads / num_kv_heads * qg, hg = head_group(num_kv_heads, G);
         live = std::min<int64_t>(num_rows, int64_t(num_rows) / chunk + num_seqs);
         if (unit_bound(ct, qs, G, num_kv_heads, live,
@@ -511,8 +563,10 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
             return PKV_EBOUNDS;
         DeviceInfo dev;
         if (!current_device_info(&dev)) return PKV_ECUDA;
-        if (!qs && cta_layout(head_dim, G, 1, hg, warp_slices(G, hg), 2, num_rows, false, false, 2, true).total >
-                       uint32_t(dev.max_smem_optin))
+        const bool i8 = ct == kI8;
+        if (!(qs && i8) && cta_layout(head_dim, G, i8 ? 1 : 2, qs ? 1 : hg, qs ? team_warps(G) : warp_slices(G, hg), 2,
+                                      num_rows, qs, false, one_q_buffer_ok(G, i8, qs, false) ? 1 : 2, i8).total >
+                               uint32_t(dev.max_smem_optin))
             return PKV_EUNSUPPORTED;
     }
     if (ct == kI8 && qs) {
@@ -520,13 +574,12 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
                                  align256(size_t(entries) * 16);
         int32_t *row_seq = reinterpret_cast<int32_t *>(wsb + dec_bytes), *row_len = row_seq + entries,
                 *row_cnt = row_len + entries, *row0 = row_cnt + entries;
-        const int32_t len_limit =
-            int32_t(std::min<int64_t>(max_context_len, int64_t(max_blocks_per_seq) * std::max(block_size, 0)));
+        const int32_t len_limit = int32_t(len_max);
         const cudaError_t e = launch_pdl(expand_entries_kernel, dim3((num_rows + 255) / 256), dim3(256), 0,
                                          reinterpret_cast<cudaStream_t>(stream),
                                          new_per_seq > 0 ? nullptr : cu_seqlens_q, new_per_seq, context_lens, num_seqs,
-                                         num_rows, int32_t(entries), chunk, len_limit, num_q_heads * head_dim, row_seq,
-                                         row_len, row_cnt, row0, out, err_word);
+                                         num_rows, int32_t(entries), chunk, max_new, len_limit,
+                                         num_q_heads * head_dim, row_seq, row_len, row_cnt, row0, out, err_word);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return cuda_fail("expand_entries_kernel launch", e);
@@ -536,7 +589,7 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
         return decode_call(ct, true, qg, q, k_cache, v_cache, nullptr, nullptr, row_seq, row_cnt, block_tables,
                            max_blocks_per_seq, row_len, int32_t(entries), num_q_heads, num_kv_heads, head_dim, block_size,
                            num_blocks, max_context_len, scale, out, workspace, dec_bytes, num_workers, err_word, stream,
-                           nullptr, nullptr, nullptr, scales, row0, live);
+                           nullptr, nullptr, nullptr, scales, row0, live, mask);
     }
     const size_t dec_bytes = need - 3 * rows_bytes(num_rows);
     int32_t *row_seq = reinterpret_cast<int32_t *>(wsb + dec_bytes);
@@ -544,8 +597,8 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     int32_t *row_cnt = reinterpret_cast<int32_t *>(wsb + dec_bytes + 2 * rows_bytes(num_rows));
     const cudaError_t e = launch_pdl(expand_rows_kernel, dim3((num_rows + 255) / 256), dim3(256), 0,
                                      reinterpret_cast<cudaStream_t>(stream), new_per_seq > 0 ? nullptr : cu_seqlens_q,
-                                     new_per_seq, context_lens, num_seqs, num_rows, chunk, row_seq, row_len,
-                                     row_cnt, err_word);
+                                     new_per_seq, context_lens, num_seqs, num_rows, chunk, max_new, row_seq,
+                                     row_len, row_cnt, err_word);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return cuda_fail("expand_rows_kernel launch", e);
@@ -555,7 +608,7 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     return decode_call(ct, qs, qg, q, k_cache, v_cache, nullptr, nullptr, row_seq, row_cnt, block_tables,
                        max_blocks_per_seq, row_len, num_rows, num_q_heads, num_kv_heads, head_dim, block_size,
                        num_blocks, max_context_len, scale, out, workspace, dec_bytes, num_workers, err_word, stream,
-                       nullptr, nullptr, nullptr, scales, nullptr, live);
+                       nullptr, nullptr, nullptr, scales, nullptr, live, mask);
 }
 
 extern "C" pkv_status pkv_paged_attention(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
@@ -587,4 +640,133 @@ extern "C" pkv_status pkv_paged_attention_i8(const uint16_t *q, const int8_t *k_
                           context_lens, num_seqs, num_rows, num_q_heads, num_kv_heads, head_dim, block_size,
                           num_blocks, max_context_len, scale, out, new_per_seq, workspace, workspace_bytes,
                           num_workers, err_word, stream);
+}
+
+// ------------------------------------------------------------------ sliding windows with sinks, trees
+extern "C" pkv_status pkv_paged_decode_window(
+    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+    int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+    int32_t num_blocks, int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out,
+    void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream)
+{
+    MaskArgs m;
+    m.window = window;
+    m.sinks = sinks;
+    if (const pkv_status st = check_mask(m, false); st != PKV_OK) return st;
+    return decode_call(kBf16, false, 1, q, k_cache, v_cache, nullptr, nullptr, nullptr, nullptr, block_tables,
+                       max_blocks_per_seq, context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                       num_blocks, max_context_len, scale, out, workspace, workspace_bytes, num_workers, err_word,
+                       stream, nullptr, nullptr, nullptr, nullptr, nullptr, -1, &m);
+}
+
+extern "C" pkv_status pkv_paged_decode_window_fp8(
+    const uint16_t *q, const uint8_t *k_cache, const uint8_t *v_cache, const float *k_scale,
+    const float *v_scale, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+    int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+    int32_t num_blocks, int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out,
+    void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream)
+{
+    MaskArgs m;
+    m.window = window;
+    m.sinks = sinks;
+    if (const pkv_status st = check_mask(m, false); st != PKV_OK) return st;
+    return decode_call(kE4m3, false, 1, q, k_cache, v_cache, k_scale, v_scale, nullptr, nullptr, block_tables,
+                       max_blocks_per_seq, context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                       num_blocks, max_context_len, scale, out, workspace, workspace_bytes, num_workers, err_word,
+                       stream, nullptr, nullptr, nullptr, nullptr, nullptr, -1, &m);
+}
+
+extern "C" pkv_status pkv_paged_decode_window_i8(
+    const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache, const float *scales,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+    int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+    int32_t num_blocks, int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out,
+    void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream)
+{
+    MaskArgs m;
+    m.window = window;
+    m.sinks = sinks;
+    if (const pkv_status st = check_mask(m, false); st != PKV_OK) return st;
+    return decode_call(kI8, false, 1, q, k_cache, v_cache, nullptr, nullptr, nullptr, nullptr, block_tables,
+                       max_blocks_per_seq, context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                       num_blocks, max_context_len, scale, out, workspace, workspace_bytes, num_workers, err_word,
+                       stream, nullptr, nullptr, nullptr, scales, nullptr, -1, &m);
+}
+
+extern "C" pkv_status pkv_paged_attention_window(
+    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
+    const int32_t *context_lens, int32_t num_seqs, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, int32_t window,
+    int32_t sinks, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
+    int32_t *err_word, pkv_stream_t stream)
+{
+    MaskArgs m;
+    m.window = window;
+    m.sinks = sinks;
+    if (const pkv_status st = check_mask(m, false); st != PKV_OK) return st;
+    return attention_call(kBf16, q, k_cache, v_cache, nullptr, block_tables, max_blocks_per_seq, cu_seqlens_q,
+                          context_lens, num_seqs, num_rows, num_q_heads, num_kv_heads, head_dim, block_size,
+                          num_blocks, max_context_len, scale, out, new_per_seq, workspace, workspace_bytes,
+                          num_workers, err_word, stream, &m);
+}
+
+extern "C" pkv_status pkv_paged_attention_window_i8(
+    const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache, const float *scales,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
+    const int32_t *context_lens, int32_t num_seqs, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, int32_t window,
+    int32_t sinks, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
+    int32_t *err_word, pkv_stream_t stream)
+{
+    MaskArgs m;
+    m.window = window;
+    m.sinks = sinks;
+    if (const pkv_status st = check_mask(m, false); st != PKV_OK) return st;
+    return attention_call(kI8, q, k_cache, v_cache, scales, block_tables, max_blocks_per_seq, cu_seqlens_q,
+                          context_lens, num_seqs, num_rows, num_q_heads, num_kv_heads, head_dim, block_size,
+                          num_blocks, max_context_len, scale, out, new_per_seq, workspace, workspace_bytes,
+                          num_workers, err_word, stream, &m);
+}
+
+extern "C" pkv_status pkv_paged_attention_tree(
+    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
+    const int32_t *context_lens, int32_t num_seqs, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, const int32_t *tree_mask,
+    int32_t mask_words, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
+    int32_t *err_word, pkv_stream_t stream)
+{
+    if (num_rows > 0 && !tree_mask) return PKV_EINVAL;
+    MaskArgs m;
+    m.tree = reinterpret_cast<const uint32_t *>(tree_mask);
+    m.tree_words = mask_words;
+    m.tree_n = new_per_seq;
+    m.tree_lens = context_lens;
+    m.tree_cu = cu_seqlens_q;
+    if (const pkv_status st = check_mask(m, true); st != PKV_OK) return st;
+    return attention_call(kBf16, q, k_cache, v_cache, nullptr, block_tables, max_blocks_per_seq, cu_seqlens_q,
+                          context_lens, num_seqs, num_rows, num_q_heads, num_kv_heads, head_dim, block_size,
+                          num_blocks, max_context_len, scale, out, new_per_seq, workspace, workspace_bytes,
+                          num_workers, err_word, stream, &m);
+}
+
+extern "C" pkv_status pkv_paged_attention_tree_i8(
+    const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache, const float *scales,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
+    const int32_t *context_lens, int32_t num_seqs, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, const int32_t *tree_mask,
+    int32_t mask_words, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
+    int32_t *err_word, pkv_stream_t stream)
+{
+    if (num_rows > 0 && !tree_mask) return PKV_EINVAL;
+    MaskArgs m;
+    m.tree = reinterpret_cast<const uint32_t *>(tree_mask);
+    m.tree_words = mask_words;
+    m.tree_n = new_per_seq;
+    m.tree_lens = context_lens;
+    m.tree_cu = cu_seqlens_q;
+    if (const pkv_status st = check_mask(m, true); st != PKV_OK) return st;
+    return attention_call(kI8, q, k_cache, v_cache, scales, block_tables, max_blocks_per_seq, cu_seqlens_q,
+                          context_lens, num_seqs, num_rows, num_q_heads, num_kv_heads, head_dim, block_size,
+                          num_blocks, max_context_len, scale, out, new_per_seq, workspace, workspace_bytes,
+                          num_workers, err_word, stream, &m);
 }

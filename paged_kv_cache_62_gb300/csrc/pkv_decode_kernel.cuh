@@ -198,6 +198,14 @@ struct DecodeParams {
     const uint16_t *k_new, *v_new;
     uint8_t *k_cache_w, *v_cache_w;
     int32_t *slot_out;
+    // Masked calls (MASK kernels; see seen_units and row_sees): a query at position p sees the keys j <= p
+    // with j > p - window or j < sinks, and of the drafted nodes (tree not null: the tokens from a
+    // sequence's position L - n on, n its new tokens) those whose bit is set in its row of tree,
+    // [query rows][tree_words].  A call has a window or a tree; without a window it is INT32_MAX.
+    int32_t window, sinks;
+    const uint32_t *tree;
+    int32_t tree_words, tree_n;              // tree_n: new tokens of every sequence (0: as tree_cu says)
+    const int32_t *tree_lens, *tree_cu;      // by sequence: context lengths, offsets of the query rows
 };
 
 // What the producer tells the consumers about the unit in a stage.
@@ -205,8 +213,9 @@ struct alignas(16) UnitMeta {
     int32_t b, g, u, n;            // unit u of the n units of (b, group g); b < 0: no more work
     int32_t L, flags, slice, cnt;  // context length of b, kFirst | kLast | kSliceEnd, slice of the unit,
                                    // queries of entry b
-    int32_t newrow, row0, pad[2];  // fused store: cache row of token L - 1 if the unit holds it, else -1;
+    int32_t newrow, row0;          // fused store: cache row of token L - 1 if the unit holds it, else -1;
                                    // query-split int8 calls: first q / out row of the entry
+    int32_t tu, base;              // masked calls: the unit's tokens are tu * toks on; first drafted position
 };
 constexpr int kFirst = 1;     // first unit of (b, g) in this slice
 constexpr int kLast = 2;      // last unit of (b, g) in this slice
@@ -362,6 +371,69 @@ inline WsLayout ws_layout(int32_t B, int32_t G, int32_t Hkv, int32_t D, bool qs 
     return w;
 }
 
+// ------------------------------------------------------------------ masked calls
+// The units of an entry that some query of it sees: its L tokens' units from 0 to head - 1 (they hold the
+// sinks) and from head + skip on (they hold the window of the entry's first query and all that follows).  The
+// entry's unit list is numbered without the gap: unit u of it is the tokens from token_unit(u) * toks on.
+struct SeenUnits {
+    int32_t n, head, skip;
+    __device__ __forceinline__ int32_t token_unit(int32_t u) const { return u < head ? u : u + skip; }
+};
+
+// First position of the window of the entry's first query (its cnt queries are the last of its L tokens).
+__device__ __forceinline__ int32_t window_start(const DecodeParams &p, int32_t L, int32_t cnt)
+{
+    return max(0, L - cnt + 1 - p.window);
+}
+
+__device__ __forceinline__ SeenUnits seen_units(const DecodeParams &p, int32_t L, int32_t cnt)
+{
+    const int32_t total = (L + p.toks - 1) / p.toks;
+    SeenUnits s;
+    s.head = (min(p.sinks, L) + p.toks - 1) / p.toks;
+    s.skip = max(window_start(p, L, cnt) / p.toks - s.head, 0);
+    s.n = total - s.skip;
+    return s;
+}
+
+// 32 bits of a tree mask row from bit `off` on (off > -32; bits before the row's first or past its last: 0).
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t *row, int32_t words, int32_t off)
+{
+    if (off < 0) return __ldg(row) << -off;
+    const int32_t w = off >> 5;
+    const uint32_t lo = w < words ? __ldg(row + w) : 0u, hi = w + 1 < words ? __ldg(row + w + 1) : 0u;
+    return __funnelshift_r(lo, hi, off & 31);
+}
+
+// Bits [0, n) of a word, n clamped to 0 .. 32.
+__device__ __forceinline__ uint32_t low_bits(int32_t n)
+{
+    return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u;
+}
+
+// Which of the 32 tokens from tok0 on the query of position pos sees (bit t: token tok0 + t), base: the first drafted
+// position, mask: its row of the tree (null: no tree).
+__device__ __forceinline__ uint32_t row_sees(const DecodeParams &p, int32_t tok0, int32_t pos, int32_t base,
+                                             const uint32_t *mask)
+{
+    uint32_t v = low_bits(pos + 1 - tok0) & (~low_bits(pos + 1 - p.window - tok0) | low_bits(p.sinks - tok0));
+    if (mask && base - tok0 < 32) v &= low_bits(base - tok0) | tree_bits(mask, p.tree_words, tok0 - base);
+    return v;
+}
+
+// Which of the 32 tokens from tok0 on some query of the entry sees (or, a drafted one, may see).
+__device__ __forceinline__ uint32_t entry_sees(const DecodeParams &p, int32_t tok0, int32_t L, int32_t cnt)
+{
+    return low_bits(L - tok0) & (~low_bits(window_start(p, L, cnt) - tok0) | low_bits(p.sinks - tok0));
+}
+
+// Whether every query of the entry sees all n tokens from tok0 on.
+__device__ __forceinline__ bool all_see(const DecodeParams &p, int32_t tok0, int32_t n, int32_t L, int32_t cnt,
+                                        int32_t base)
+{
+    return tok0 + n <= L - cnt + 1 && (tok0 >= L - p.window || tok0 + n <= p.sinks) && (!p.tree || tok0 + n <= base);
+}
+
 // ------------------------------------------------------------------ unit list walking
 // Units in (b, group, u) order; scan[b] = sum over earlier sequences of their
 // units per group, so the list holds nhg * scan[B] units.
@@ -410,6 +482,7 @@ __device__ __forceinline__ void setup_sync(int nt)
 
 // Units per sequence -> exclusive prefix in scan[0..B].
 // `tmp` needs 32 ints of shared memory that is free during the call.
+template <bool MASK>
 static __device__ void unit_prefix_scan(const DecodeParams &p, int32_t *scan, int32_t *tmp, int nt)
 {
     const int tid = threadIdx.x;
@@ -420,9 +493,13 @@ static __device__ void unit_prefix_scan(const DecodeParams &p, int32_t *scan, in
     const int lo = min(p.B, tid * per), hi = min(p.B, lo + per);
     int32_t sum = 0;
     for (int i0 = lo; i0 < hi; i0 += kScanBatch) {
-        int32_t len[kScanBatch];
+        int32_t len[kScanBatch], cnt[MASK ? kScanBatch : 1];
 #pragma unroll
         for (int k = 0; k < kScanBatch; ++k) len[k] = i0 + k < hi ? __ldg(p.context_lens + i0 + k) : 0;
+        if constexpr (MASK) {
+#pragma unroll
+            for (int k = 0; k < kScanBatch; ++k) cnt[k] = p.row_cnt && i0 + k < hi ? __ldg(p.row_cnt + i0 + k) : p.qn;
+        }
 #pragma unroll
         for (int k = 0; k < kScanBatch; ++k) {
             if (i0 + k >= hi) break;
@@ -432,7 +509,10 @@ static __device__ void unit_prefix_scan(const DecodeParams &p, int32_t *scan, in
             if (len[k] < 0 || len[k] > p.len_limit || (!p.row_cnt && p.qn > 1 && len[k] < p.qn)) {
                 if (blockIdx.x == 0) flag_error(p.err, PKV_ERR_CONTEXT_RANGE);
             } else {
-                n = (len[k] + p.toks - 1) / p.toks;
+                if constexpr (MASK)
+                    n = seen_units(p, len[k], cnt[k]).n;
+                else
+                    n = (len[k] + p.toks - 1) / p.toks;
             }
             scan[i0 + k] = n;
             sum += n;
@@ -587,12 +667,13 @@ __device__ __forceinline__ uint32_t f16x2_sat(float lo, float hi)
 // tile's first) below it count for the thread's row of half hr (the causal
 // bound of its query); TAIL: tokens from `valid` on are not the sequence's
 // (their rows may hold anything, even NaN), so their V values are zeroed
-// before the product.  E4M3 caches run the products in f16 (every E4M3 value
+// before the product.  MASK: lim[hr] has a bit for each token that the row sees, valid one for each that
+// some row of the entry sees.  E4M3 caches run the products in f16 (every E4M3 value
 // is exact in f16, and so is every bf16 query element of magnitude
 // 2^-14 .. 65504; smaller ones keep f16's subnormal steps of 2^-24, larger
 // ones saturate at 65504); the kv head's K scale is in ksc, its V scale is
 // applied by the caller.
-template <int D, int CT, bool QS, int HR_, bool TAIL>
+template <int D, int CT, bool QS, int HR_, bool TAIL, bool MASK>
 __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb,
                                             const LaneOffsets<D, CT, QS> &off,
                                             const uint32_t (&qa)[Tc<D, CT, QS, HR_>::KS][2 * Tc<D, CT, QS, HR_>::HR],
@@ -659,7 +740,8 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb,
                     const int k = 4 * st + 2 * nt + e;
                     float sum = sa[st][0][nt][2 * hr + e];
                     if constexpr (CH == 2) sum += sa[st][1][nt][2 * hr + e];
-                    x[hr][k] = 16 * st + 8 * nt + 2 * r4 + e < lim[hr] ? sum * ksc : -INFINITY;
+                    const int t = 16 * st + 8 * nt + 2 * r4 + e;
+                    x[hr][k] = (MASK ? (lim[hr] >> t) & 1 : t < lim[hr]) ? sum * ksc : -INFINITY;
                 }
     float mx[HR];
     bool grow = false;
@@ -730,7 +812,11 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb,
         // transposed V tiles: the low half of a register is token 2 r4 (8 + 2 r4) of the sub-tile, the
         // high half the next one
         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-        if constexpr (TAIL) {
+        if constexpr (TAIL && MASK) {
+            const uint32_t v0 = uint32_t(valid) >> (16 * st + 2 * r4);
+            keep0 = (v0 & 1u ? 0x0000ffffu : 0u) | (v0 & 2u ? 0xffff0000u : 0u);
+            keep1 = (v0 & 0x100u ? 0x0000ffffu : 0u) | (v0 & 0x200u ? 0xffff0000u : 0u);
+        } else if constexpr (TAIL) {
             const int v0 = valid - 16 * st;
             keep0 = (2 * r4 < v0 ? 0x0000ffffu : 0u) | (2 * r4 + 1 < v0 ? 0xffff0000u : 0u);
             keep1 = (2 * r4 + 8 < v0 ? 0x0000ffffu : 0u) | (2 * r4 + 9 < v0 ? 0xffff0000u : 0u);
@@ -786,7 +872,7 @@ constexpr float kZeroLog = -64.0f;
 __device__ __forceinline__ void i8_zero_log(I8Scales &s, float lv);
 template <int KS, int HR>
 __device__ __forceinline__ void q_bias(const uint32_t (&qa)[KS][2 * HR], float (&qb)[HR]);
-template <int D, int HR_, bool TAIL>
+template <int D, int HR_, bool TAIL, bool MASK>
 __device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const LaneOffsets<D, kI8, false> &off,
                                                const uint32_t (&qa)[Tc<D, kI8, false, HR_>::KS][2 * HR_],
                                                const float (&rowf)[HR_], const float (&qb)[HR_],
@@ -1082,7 +1168,7 @@ __device__ __forceinline__ int slice_of(const long long *bound, int nslots, long
 // (the online-softmax algebra; m in log2 units).  The pieces were written by
 // other SMs, so they are read through L2 (ld.global.cg), BATCH pieces at a
 // time with independent loads, folded into a running (M, l, acc).
-template <int D, int G, int CT, bool QS>
+template <int D, int G, int CT, bool QS, bool MASK>
 __device__ __forceinline__ void merge_pieces(const DecodeParams &p, const long long *bound, int sf, int sl,
                                              long long x0, int g, int h, int jq, int b, int kvh, int nvh, int lane)
 {
@@ -1146,7 +1232,7 @@ __device__ __forceinline__ void merge_pieces(const DecodeParams &p, const long l
         for (int i = 0; i < HB; ++i) {
             const int hh = h0 + i;
             if (hh >= nvh) break;
-            const float inv = (CT == kE4m3 ? __ldg(p.v_scale + kvh) : 1.0f) / lsum[i];
+            const float inv = MASK && lsum[i] == 0.f ? 0.f : (CT == kE4m3 ? __ldg(p.v_scale + kvh) : 1.0f) / lsum[i];
             uint16_t *o = p.out + ((int64_t(b) * p.qstride + jq * p.qn + hh / p.gq) * p.Hq + int64_t(kvh) * p.gq +
                                    hh % p.gq) * D + lane * PER;
             if constexpr (PER == 4)
@@ -1163,7 +1249,7 @@ __device__ __forceinline__ void merge_pieces(const DecodeParams &p, const long l
 // 69 -> 59 us a call).  With few pieces its two round trips cost more than they save (a batch of 64 sequences, 4
 // new tokens each: 70.2 us against 68.3).
 constexpr int kManyPieces = 8;
-template <int D, int G>
+template <int D, int G, bool MASK>
 __device__ void merge_pieces_i8(const DecodeParams &p, const long long *bound, int sf, int sl, long long x0, int g,
                                 int h, int b, int kvh, int nvh, int lane);
 
@@ -1406,13 +1492,13 @@ static_assert(team_warps(16) * 16 == 128, "a tensor-memory piece tile is 8 slots
 
 // int8 caches: their softmax warps, the warp that issues the products and the warps that turn codes into f16
 // operands (defined in pkv_i8_tc5.cuh, which the translation unit of these kernels includes).
-template <int D>
+template <int D, bool MASK>
 __device__ void tc5_softmax_warps_i8(const DecodeParams &p, const CtaLayout &lay, const Tc5Smem &m, uint32_t tmem,
                                      float2 *xch, const long long *bound, const int32_t *scan, int *sh,
                                      const float *wts, int nslots, uint32_t gen, int wp, bool adaptive);
 template <int D>
 __device__ void tc5_mma_warp_i8(const DecodeParams &p, const Tc5Smem &m, uint32_t tmem, bool output);
-template <int D>
+template <int D, bool MASK>
 __device__ void tc5_convert_warps(const DecodeParams &p, const CtaLayout &lay, const Tc5Smem &m, uint8_t *stage0,
                                   int t);
 
@@ -1420,7 +1506,7 @@ __device__ void tc5_convert_warps(const DecodeParams &p, const CtaLayout &lay, c
 // keys 64 h .. 64 h + 63 of every tile, h = w / 4.  The two threads of a row (warps w and w + 4) hold the
 // same running max: they exchange their tile max each tile; each keeps the sum of its own keys' weights.
 // When a segment starts they write its Q tile (dims 64 h .. 64 h + 63 of row r) into tensor memory.
-template <int D, int G>
+template <int D, int G, bool MASK>
 __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, const Tc5Smem &m, uint32_t tmem,
                                   float *xch, const long long *bound, const int32_t *scan, int *sh,
                                   const float *wts, int nslots, uint32_t gen, int wp, bool adaptive)
@@ -1523,10 +1609,25 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
             if (!q_early) write_q(mt);
             q_early = false;
         }
-        const int tok0 = mt.u * kTc5Keys;
+        const int tok0 = (MASK ? mt.tu : mt.u) * kTc5Keys;
         const int valid = min(kTc5Keys, mt.L - tok0);
         const int lim = row_ok ? min(valid, mt.L - tok0 - shift) - KH * half : 0;  // keys of this half
-        if (valid < kTc5Keys) {
+        if constexpr (MASK) {
+            // V rows that no query sees are zeroed too: those from the sinks' end to the window's start
+            const int z0 = max(p.sinks - tok0, 0), z1 = min(window_start(p, mt.L, mt.cnt) - tok0, valid);
+            if (valid < kTc5Keys || z0 < z1) {
+                if (!wait(&m.vfull[j % kTc5VSlots], (j / kTc5VSlots) & 1u)) break;
+                uint8_t *vrows = m.vbase + size_t(j % kTc5VSlots) * tc5_vslot_bytes(lay);
+                const int gap = max(z1 - z0, 0), per_part = (gap + kTc5Keys - valid) * 8, n = per_part * (D / 64);
+                for (int i = t; i < n; i += 32 * kTc5SoftmaxWarps) {
+                    const int part = i / per_part, r = i - part * per_part, k = r >> 3;
+                    *reinterpret_cast<uint4 *>(vrows + part * kTc5SlabBytes +
+                                               (k < gap ? z0 + k : valid + k - gap) * 128 + (r & 7) * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();  // for the tensor core
+            }
+        } else if (valid < kTc5Keys) {
             // V rows past the sequence's end hold anything (NaN included) and 0 * NaN is NaN: zero them,
             // once the V copy has landed
             if (!wait(&m.vfull[j % kTc5VSlots], (j / kTc5VSlots) & 1u)) break;
@@ -1547,7 +1648,22 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
         {
             uint32_t r[KH];
             tmem_ld64(sbuf + uint32_t(KH * half), r);
-            if (lim >= KH) {
+            if constexpr (MASK) {
+                uint32_t v0 = 0u, v1 = 0u;  // the half's keys that the row sees
+                if (row_ok) {
+                    const uint32_t *mask = p.tree ? p.tree + (long long)(mt.b + qi) * p.tree_words : nullptr;
+                    v0 = row_sees(p, tok0 + KH * half, mt.L - 1 - shift, mt.base, mask);
+                    v1 = row_sees(p, tok0 + KH * half + 32, mt.L - 1 - shift, mt.base, mask);
+                }
+                if ((v0 & v1) == 0xffffffffu) {
+#pragma unroll
+                    for (int i = 0; i < KH; ++i) x[i] = __uint_as_float(r[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < KH; ++i)
+                        x[i] = ((i < 32 ? v0 : v1) >> (i & 31)) & 1u ? __uint_as_float(r[i]) : -INFINITY;
+                }
+            } else if (lim >= KH) {
 #pragma unroll
                 for (int i = 0; i < KH; ++i) x[i] = __uint_as_float(r[i]);
             } else {
@@ -1709,7 +1825,7 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
 // CTA for long runs of new tokens, where the entry's up to sub * qn queries
 // share every K/V tile).  TC5 (with QS): the same entries on the tensor-memory
 // consumers (see tc5_softmax_warps).
-template <int D, int G, int CT, bool QS, bool TC5 = false>
+template <int D, int G, int CT, bool QS, bool TC5 = false, bool MASK = false>
 __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_warps(G) + 1) * 32, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                         const DecodeParams p)
@@ -1852,7 +1968,7 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
         // the query count of this thread's first entry to check for zeros below, loaded with the rest
         const long long b_first = blockIdx.x + (long long)threadIdx.x * gridDim.x;
         const int rows_first = p.row_cnt && b_first < p.B ? __ldg(p.row_cnt + b_first) : p.qn;
-        unit_prefix_scan(p, scan, reinterpret_cast<int32_t *>(smem), nset);
+        unit_prefix_scan<MASK>(p, scan, reinterpret_cast<int32_t *>(smem), nset);
         const long long T = (long long)p.nhg * scan[p.B];
         // Entries without units (L == 0, or a rejected length) get zeros in their query rows; CTAs
         // share the job (CTA c takes entries c, c + grid, ...), a set-up thread checks one of them at a
@@ -1930,11 +2046,16 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
             Walker iw = nunits > 0 ? walker_locate(scan, p.B, p.nhg, lo + rot) : Walker{0, 0, 0, 1};
             int32_t cur_e = -1, cur_L = 0, cur_c = 1, nxt_e = -1, nxt_L = 0, nxt_c = 1;
             int32_t cur_r = 0, nxt_r = 0;  // TC5, int8 caches: the entry's first row
+            int32_t cur_t = 0, nxt_t = 0;  // masked calls: the entry's first drafted position
             auto prefetch_batch = [&](long long kb) {  // boxes [kb, kb + 32) -> nxt, one per lane
                 const long long x = kb + lane;
                 if (x < nboxes) {
                     const Walker mine = walker_locate(scan, p.B, p.nhg, unit_at(x >> p.lg_nbox));
-                    const int32_t pos = mine.u * p.toks + int32_t(x & (p.nbox - 1)) * p.boxtok;
+                    int32_t tu = mine.u;
+                    if constexpr (MASK)  // (the length, which the set-up of this CTA read, comes first)
+                        tu = seen_units(p, __ldg(p.context_lens + mine.b),
+                                        p.row_cnt ? __ldg(p.row_cnt + mine.b) : p.qn).token_unit(tu);
+                    const int32_t pos = tu * p.toks + int32_t(x & (p.nbox - 1)) * p.boxtok;
                     // The entry is only used for pos < L, where pos / bs < max_blocks (lengths
                     // beyond the table were rejected by the scan); clamping keeps the load in
                     // the row and lets it go out together with the length's.
@@ -1944,6 +2065,13 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                     const int32_t trow = p.row_seq ? __ldg(p.row_seq + mine.b) : mine.b;
                     nxt_e = __ldg(p.block_tables + (long long)trow * p.max_blocks + blk);
                     if constexpr (TC5 && CT == kI8) nxt_r = __ldg(p.row0 + mine.b);
+                    if constexpr (MASK) {
+                        if (p.tree)
+                            nxt_t = p.row_cnt ? __ldg(p.tree_lens + trow) -
+                                                    (p.tree_n > 0 ? p.tree_n
+                                                                  : __ldg(p.tree_cu + trow + 1) - __ldg(p.tree_cu + trow))
+                                              : nxt_L - p.qn;
+                    }
                 }
             };
             // TC5: the query rows of segment w into L2 (the softmax warps load them into tensor memory at
@@ -1966,6 +2094,7 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                 cur_L = nxt_L;
                 cur_c = nxt_c;
                 cur_r = nxt_r;
+                cur_t = nxt_t;
             }
             for (long long k = 0; k < nunits; ++k) {
                 const long long kb0 = k * p.nbox;  // nbox is a power of two <= 32: batches start on units
@@ -1974,6 +2103,7 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                     cur_L = nxt_L;
                     cur_c = nxt_c;
                     cur_r = nxt_r;
+                    cur_t = nxt_t;
                     if (kb0 + 32 < nboxes) prefetch_batch(kb0 + 32);
                 }
                 const int s = rs;
@@ -1987,6 +2117,8 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                 const int32_t e = __shfl_sync(kFull, cur_e, (src + lane) & 31);  // lane j: box j's entry
                 int32_t row0 = 0;
                 if constexpr (TC5 && CT == kI8) row0 = __shfl_sync(kFull, cur_r, src);
+                int32_t base = 0;
+                if constexpr (MASK) base = __shfl_sync(kFull, cur_t, src);
                 const long long x = unit_at(k);
                 const int flags = ((x == lo || iw.u == 0) ? kFirst : 0) |
                                   ((x == hi - 1 || iw.u == iw.n - 1) ? kLast : 0) |
@@ -2028,10 +2160,14 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                     }
                     ++segs;
                 }
-                // box j of the unit: tokens [pos, pos + boxtok) of one physical block
-                const int32_t pos = iw.u * p.toks + lane * p.boxtok;
+                // box j of the unit: tokens [pos, pos + boxtok) of one physical block (masked calls: a box that no
+                // query sees is not loaded, and its table entry not looked at)
+                int32_t tu = iw.u;
+                if constexpr (MASK) tu = seen_units(p, len, cnt).token_unit(iw.u);
+                const int32_t pos = tu * p.toks + lane * p.boxtok;
                 int32_t row = -1;
-                if (lane < p.nbox && pos < len) {
+                if (lane < p.nbox && pos < len &&
+                    (!MASK || pos < p.sinks || pos + p.boxtok > window_start(p, len, cnt))) {
                     if (e >= 0 && e < p.NB)
                         row = e * p.bs + (pos & (p.bs - 1));
                     else
@@ -2060,6 +2196,8 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                     mt.slice = slice;
                     mt.cnt = cnt;
                     mt.newrow = newrow;
+                    if constexpr (MASK) mt.tu = tu;
+                    if constexpr (MASK) mt.base = base;
                     if constexpr (TC5 && CT == kI8) mt.row0 = row0;
                     if constexpr (TC5) mbar_arrive(&mready[s]);  // the meta, for a look ahead
                     // TC5: full[s] counts the K half only; the V half has barriers of its own
@@ -2069,7 +2207,7 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                 if (k == 0 && lane == 0 && adaptive && !p.row_seq && slice == sh[0] && row >= 0 &&
                     my_sm < unsigned(kMaxSlots)) {
                     p.ws_bal->hint[my_sm][0] = make_int4(row, iw.g * p.hg, int32_t(gen) ^ kHintMagic, iw.b);
-                    p.ws_bal->hint[my_sm][1] = make_int4((iw.u * p.toks) >> p.log2_bs, len, 0, 0);
+                    p.ws_bal->hint[my_sm][1] = make_int4((tu * p.toks) >> p.log2_bs, len, 0, 0);
                 }
                 if constexpr (TC5 && CT == kBf16) {
                     // K now (its half of the stage is free once the previous scores of the slot are done);
@@ -2187,16 +2325,16 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
             if (warp == kTc5SoftmaxWarps || warp == kTc5SoftmaxWarps + 1)
                 tc5_mma_warp_i8<D>(p, tm, tmem, warp != kTc5SoftmaxWarps);
             else if (warp > kTc5SoftmaxWarps)
-                tc5_convert_warps<D>(p, lay, tm, stage0, int(threadIdx.x) - 32 * (kTc5SoftmaxWarps + 2));
+                tc5_convert_warps<D, MASK>(p, lay, tm, stage0, int(threadIdx.x) - 32 * (kTc5SoftmaxWarps + 2));
         } else if (warp == kTc5SoftmaxWarps) {
             tc5_mma_warp<D>(p, lay, tm, tmem);
         }
         if (warp < kTc5SoftmaxWarps) {
             if constexpr (CT == kI8)
-                tc5_softmax_warps_i8<D>(p, lay, tm, tmem, reinterpret_cast<float2 *>(comb), bound, scan, sh, wts,
+                tc5_softmax_warps_i8<D, MASK>(p, lay, tm, tmem, reinterpret_cast<float2 *>(comb), bound, scan, sh, wts,
                                         nslots, gen, wp, adaptive);
             else
-                tc5_softmax_warps<D, G>(p, lay, tm, tmem, comb, bound, scan, sh, wts, nslots, gen, wp, adaptive);
+                tc5_softmax_warps<D, G, MASK>(p, lay, tm, tmem, comb, bound, scan, sh, wts, nslots, gen, wp, adaptive);
         }
         named_barrier(2, 32 * tc5_consumers(CT));  // every tensor-memory access of the CTA is done
         if (warp == kTc5SoftmaxWarps) {
@@ -2326,9 +2464,11 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
             ++segs;
             u_first = mt.u;
         }
-        const int tok0 = mt.u * p.toks + jt * TC::TW;
-        const int valid = min(TC::TW, mt.L - tok0);
-        if (valid > 0 && nvh > 0) {
+        const int tok0 = (MASK ? mt.tu : mt.u) * p.toks + jt * TC::TW;
+        // tokens of the tile (masked calls: a bit for each that some query of the entry sees)
+        constexpr int kAll = MASK ? int(0xffffffffu >> (32 - TC::TW)) : TC::TW;
+        const int valid = MASK ? int(entry_sees(p, tok0, mt.L, mt.cnt)) & kAll : min(TC::TW, mt.L - tok0);
+        if ((MASK ? valid != 0 : valid > 0) && nvh > 0) {
             const uint32_t kb = stage_addr + uint32_t(s) * lay.stage_bytes;
             if constexpr (!QS && CT != kI8) {
                 // fused store: the tile holding the new token takes its K/V row from k_new / v_new (the
@@ -2356,8 +2496,27 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                 }
             }
             int lim[HR];
+            if constexpr (MASK) {
+                const bool all = all_see(p, tok0, TC::TW, mt.L, mt.cnt, mt.base);
 #pragma unroll
-            for (int hr = 0; hr < HR; ++hr) lim[hr] = min(valid, mt.L - tok0 - shift[hr]);
+                for (int hr = 0; hr < HR; ++hr) {
+                    lim[hr] = kAll;
+                    if (!all) {
+                        const int row = g8 + 8 * hr;
+                        // rows that are no query's see nothing
+                        lim[hr] = row < nvh ? int(row_sees(p, tok0, mt.L - 1 - shift[hr], mt.base,
+                                                           p.tree ? p.tree + ((long long)mt.b * p.qstride + jq * p.qn +
+                                                                              row / p.gq) * p.tree_words
+                                                                  : nullptr))
+                                            : 0;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int hr = 0; hr < HR; ++hr) lim[hr] = min(valid, mt.L - tok0 - shift[hr]);
+            }
+            // whether the tile has a token of its 16-token sub-tile st
+            auto has = [&](int st) { return MASK ? ((valid >> (16 * st)) & 0xffff) != 0 : kScaleToks * st < valid; };
             if constexpr (CT == kI8) {
                 const float2 *sc = reinterpret_cast<const float2 *>(smem + lay.off_sc +
                                                                     uint32_t(s) * scale_bytes(p.toks, p.hg));
@@ -2372,19 +2531,19 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
 #pragma unroll
                     for (int st = 0; st < TC::NT; ++st)
                         if (sct[st].vzero)
-                            i8_zero_log(sct[st], sct[st ^ 1].plain && kScaleToks * (st ^ 1) < valid ? sct[st ^ 1].lv
+                            i8_zero_log(sct[st], sct[st ^ 1].plain && has(st ^ 1) ? sct[st ^ 1].lv
                                                                                                       : kZeroLog);
                 }
-                if (valid == TC::TW && plain)
-                    attend_tile_i8<D, TC::HR, false>(kb, kb + lay.kv_bytes, off, qa, rowf, qb, sct, lim, valid, m, l, o,
+                if (valid == kAll && plain)
+                    attend_tile_i8<D, TC::HR, false, MASK>(kb, kb + lay.kv_bytes, off, qa, rowf, qb, sct, lim, valid, m, l, o,
                                                      lane);
                 else
-                    attend_tile_i8<D, TC::HR, true>(kb, kb + lay.kv_bytes, off, qa, rowf, qb, sct, lim, valid, m, l, o,
+                    attend_tile_i8<D, TC::HR, true, MASK>(kb, kb + lay.kv_bytes, off, qa, rowf, qb, sct, lim, valid, m, l, o,
                                                     lane);
-            } else if (valid == TC::TW)
-                attend_tile<D, CT, QS, TC::HR, false>(kb, kb + lay.kv_bytes, off, qa, ksc, lim, valid, m, l, o, lane);
+            } else if (valid == kAll)
+                attend_tile<D, CT, QS, TC::HR, false, MASK>(kb, kb + lay.kv_bytes, off, qa, ksc, lim, valid, m, l, o, lane);
             else
-                attend_tile<D, CT, QS, TC::HR, true>(kb, kb + lay.kv_bytes, off, qa, ksc, lim, valid, m, l, o, lane);
+                attend_tile<D, CT, QS, TC::HR, true, MASK>(kb, kb + lay.kv_bytes, off, qa, ksc, lim, valid, m, l, o, lane);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[s]);
@@ -2493,7 +2652,7 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                         for (int e = 0; e < 2; ++e) {
                             const int hh = 8 * hr + 2 * r4 + e;
                             if (hh < nvh) {
-                                const float inv = vsc / lc[hr][e];
+                                const float inv = MASK && lc[hr][e] == 0.f ? 0.f : vsc / lc[hr][e];
                                 uint16_t *orow = p.out + (((long long)mt.b * p.qstride + jq * p.qn + hh / p.gq) * p.Hq +
                                                           (long long)kvh * p.gq + hh % p.gq) * D;
 #pragma unroll
@@ -2553,9 +2712,9 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                         bool many = false;
                         if constexpr (CT == kI8) {
                             many = sl - sf >= kManyPieces;
-                            if (many) merge_pieces_i8<D, G>(p, bound, sf, sl, x0, mt.g, h, mt.b, kvh, nvh, lane);
+                            if (many) merge_pieces_i8<D, G, MASK>(p, bound, sf, sl, x0, mt.g, h, mt.b, kvh, nvh, lane);
                         }
-                        if (!many) merge_pieces<D, G, CT, QS>(p, bound, sf, sl, x0, mt.g, h, jq, mt.b, kvh, nvh, lane);
+                        if (!many) merge_pieces<D, G, CT, QS, MASK>(p, bound, sf, sl, x0, mt.g, h, jq, mt.b, kvh, nvh, lane);
                     }
                 }
             }
@@ -2669,9 +2828,9 @@ inline bool cached_cache_map(CUtensorMap *map, int dev, const void *base, bool f
 
 // cudaFuncSetAttribute once per device and kernel variant (it is a host-side
 // driver call; repeating it on every launch costs microseconds).  Keyed on
-// <D, G, CT, QS, TC5>: every variant has the same function-pointer type, so
+// <D, G, CT, QS, TC5, MASK>: every variant has the same function-pointer type, so
 // the memo must be per instantiation.
-template <int D, int G, int CT, bool QS, bool TC5, typename Kernel>
+template <int D, int G, int CT, bool QS, bool TC5, bool MASK, typename Kernel>
 inline bool ensure_smem_attribute(Kernel kern, int dev, size_t smem)
 {
     static std::mutex mu;
@@ -2689,7 +2848,7 @@ inline bool ensure_smem_attribute(Kernel kern, int dev, size_t smem)
     return true;
 }
 
-template <int D, int G, int CT, bool QS, bool TC5 = false>
+template <int D, int G, int CT, bool QS, bool TC5 = false, bool MASK = false>
 pkv_status launch_decode(LaunchArgs &a)
 {
     DecodeParams &p = a.p;
@@ -2731,8 +2890,8 @@ pkv_status launch_decode(LaunchArgs &a)
         !cached_cache_map(&vmap, a.device, a.v_cache, CT != kBf16, D, p.Hkv, rows, p.hg, p.boxtok))
         return PKV_ECUDA;
 
-    auto kern = paged_decode_kernel<D, G, CT, QS, TC5>;
-    if (!ensure_smem_attribute<D, G, CT, QS, TC5>(kern, a.device, lay.total)) return PKV_ECUDA;
+    auto kern = paged_decode_kernel<D, G, CT, QS, TC5, MASK>;
+    if (!ensure_smem_attribute<D, G, CT, QS, TC5, MASK>(kern, a.device, lay.total)) return PKV_ECUDA;
     const cudaError_t e =
         launch_pdl(kern, dim3(grid), dim3((p.cons + 1) * 32), lay.total, a.stream, kmap, vmap, p);
     if (e != cudaSuccess) {
@@ -2744,18 +2903,35 @@ pkv_status launch_decode(LaunchArgs &a)
 
 using LaunchFn = pkv_status (*)(LaunchArgs &);
 
-template <int D, int CT, bool QS>
+template <int D, int CT, bool QS, bool MASK = false>
 LaunchFn pick_group(int G)
 {
     switch (G) {
-    case 1: return launch_decode<D, 1, CT, QS>;
-    case 2: return launch_decode<D, 2, CT, QS>;
-    case 3: return launch_decode<D, 3, CT, QS>;
-    case 4: return launch_decode<D, 4, CT, QS>;
-    case 5: return launch_decode<D, 5, CT, QS>;
-    case 6: return launch_decode<D, 6, CT, QS>;
-    case 7: return launch_decode<D, 7, CT, QS>;
-    case 8: return launch_decode<D, 8, CT, QS>;
+    case 1: return launch_decode<D, 1, CT, QS, false, MASK>;
+    case 2: return launch_decode<D, 2, CT, QS, false, MASK>;
+    case 3: return launch_decode<D, 3, CT, QS, false, MASK>;
+    case 4: return launch_decode<D, 4, CT, QS, false, MASK>;
+    case 5: return launch_decode<D, 5, CT, QS, false, MASK>;
+    case 6: return launch_decode<D, 6, CT, QS, false, MASK>;
+    case 7: return launch_decode<D, 7, CT, QS, false, MASK>;
+    case 8: return launch_decode<D, 8, CT, QS, false, MASK>;
+    default: return nullptr;
+    }
+}
+
+// 9 to 16 virtual heads.
+template <int D, int CT, bool MASK = false>
+LaunchFn pick_wide_group(int G)
+{
+    switch (G) {
+    case 9: return launch_decode<D, 9, CT, false, false, MASK>;
+    case 10: return launch_decode<D, 10, CT, false, false, MASK>;
+    case 11: return launch_decode<D, 11, CT, false, false, MASK>;
+    case 12: return launch_decode<D, 12, CT, false, false, MASK>;
+    case 13: return launch_decode<D, 13, CT, false, false, MASK>;
+    case 14: return launch_decode<D, 14, CT, false, false, MASK>;
+    case 15: return launch_decode<D, 15, CT, false, false, MASK>;
+    case 16: return launch_decode<D, 16, CT, false, false, MASK>;
     default: return nullptr;
     }
 }
@@ -2771,6 +2947,15 @@ LaunchFn pick_decode_i8(int D, int G);        // int8 caches, 1 to 8 virtual hea
 LaunchFn pick_decode_i8_wide(int D, int G);   // int8 caches, 9 to 16 virtual heads (pkv_decode_i8_wide.cu)
 LaunchFn pick_decode_i8_tc5(int D);           // int8 caches, tensor-memory query-split CTAs (pkv_decode_i8_tc5.cu)
 LaunchFn pick_decode_tc5(int D);          // tensor-memory query-split CTAs, 16 virtual heads (pkv_decode_tc5.cu)
+// The same families with masks (windows with sinks, trees), in pkv_mask*.cu.
+LaunchFn pick_mask(int D, int G);
+LaunchFn pick_mask_wide(int D, int G);
+LaunchFn pick_mask_qs(int D, int G);
+LaunchFn pick_mask_tc5(int D);
+LaunchFn pick_mask_fp8(int D, int G);
+LaunchFn pick_mask_i8(int D, int G);
+LaunchFn pick_mask_i8_wide(int D, int G);
+LaunchFn pick_mask_i8_tc5(int D);
 
 // Whether a query-split call can run on the tensor-memory CTAs: bf16 caches, entries of 128 rows
 // (16 virtual heads per block: the query heads of a kv head a power of two), 128-key tiles within one

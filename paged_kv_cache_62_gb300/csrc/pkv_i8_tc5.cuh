@@ -110,7 +110,7 @@ __device__ __noinline__ void tc5_mark_block(uint8_t *dst, int g, int mode, int t
 // The converting warps: their thread t.  K runs a unit ahead of V: the scores of unit j + 1 can then be computed
 // while the softmax warps work on unit j, and V's buffer, free only when the output product of unit j - 1 is
 // done, holds nothing else back.
-template <int D>
+template <int D, bool MASK>
 __device__ void tc5_convert_warps(const DecodeParams &p, const CtaLayout &lay, const Tc5Smem &m, uint8_t *stage0, int t)
 {
     const int lane = t & 31;
@@ -143,7 +143,12 @@ __device__ void tc5_convert_warps(const DecodeParams &p, const CtaLayout &lay, c
                         float lv = vo ? __log2f(sc.y) : 0.f;
                         if (__any_sync((1u << kGroups) - 1u, !vo)) {
                             // a V scale of zero takes the smallest log2 of the unit's blocks (see kZeroLog)
-                            const bool seen = lane * kScaleToks < m.metas[s].L - m.metas[s].u * kTc5Keys;
+                            bool seen;
+                            if constexpr (MASK)
+                                seen = (entry_sees(p, m.metas[s].tu * kTc5Keys + lane * kScaleToks, m.metas[s].L,
+                                                   m.metas[s].cnt) & 0xffffu) != 0u;
+                            else
+                                seen = lane * kScaleToks < m.metas[s].L - m.metas[s].u * kTc5Keys;
                             float low = vo && seen ? lv : INFINITY;
 #pragma unroll
                             for (int o = 1; o < kGroups; o <<= 1)
@@ -345,7 +350,7 @@ __device__ __noinline__ void tc5_merge_i8(const DecodeParams &p, const long long
 // query r / gq, head r % gq.  x_j = kc s_j + lv with s_j the score of key j's codes, kc the row's factor times the
 // K scale of its block and lv = log2 of the V scale; weights 2^(x_j - m); the row's sum takes them over the V
 // scale (2^-lv).
-template <int D>
+template <int D, bool MASK>
 __device__ void tc5_softmax_warps_i8(const DecodeParams &p, const CtaLayout &lay, const Tc5Smem &m, uint32_t tmem,
                                      float2 *xch, const long long *bound, const int32_t *scan, int *sh,
                                      const float *wts, int nslots, uint32_t gen, int wp, bool adaptive)
@@ -441,14 +446,35 @@ __device__ void tc5_softmax_warps_i8(const DecodeParams &p, const CtaLayout &lay
             own = int(j & 1u) == wg;
             if (own) {
                 const float4 *prep = m.prep + s * kGroups;
-                const int tok0 = mt.u * kTc5Keys;
+                const int tok0 = (MASK ? mt.tu : mt.u) * kTc5Keys;
                 const int lim = row_ok ? min(kTc5Keys, mt.L - tok0 - shift) : 0;  // visible keys of the tile
+                // masked calls: the keys that the row sees, 32 a word
+                uint32_t vis[MASK ? kTc5Keys / 32 : 1] = {};
+                if constexpr (MASK) {
+                    const uint32_t *mask = p.tree ? p.tree + (long long)(mt.row0 + qi) * p.tree_words : nullptr;
+                    if (row_ok) {
+#pragma unroll 1
+                        for (int w = 0; w < kTc5Keys / 32; ++w) {
+                            const uint32_t v = row_sees(p, tok0 + 32 * w, mt.L - 1 - shift, mt.base, mask);
+#pragma unroll
+                            for (int i = 0; i < kTc5Keys / 32; ++i) vis[i] = i == w ? v : vis[i];
+                        }
+                    }
+                }
                 // the scores of 32 keys, two scale blocks: -inf at or past the row's bound
                 auto scores32 = [&](int g, float (&y)[32]) {
                     uint32_t r[32];
                     tmem_ld32(sbuf + uint32_t(kScaleToks * g), r);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(r[i]);
+                    if constexpr (MASK) {
+                        const uint32_t v = g & 4 ? (g & 2 ? vis[3] : vis[2]) : (g & 2 ? vis[1] : vis[0]);
+                        if (v != 0xffffffffu) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) y[i] = (v >> i) & 1u ? y[i] : -INFINITY;
+                        }
+                        return;
+                    }
                     const int left = lim - kScaleToks * g;
                     if (left < 32) {
 #pragma unroll
@@ -474,7 +500,9 @@ __device__ void tc5_softmax_warps_i8(const DecodeParams &p, const CtaLayout &lay
                 mx -= kI8TcHead;
                 // fmaxf passes NaN over: a row that has seen a key of a marked block takes some max all the same (a
                 // piece whose max is -inf counts as empty)
-                if (mx == -INFINITY && lim > 0) mx = 0.f;
+                bool sees = lim > 0;
+                if constexpr (MASK) sees = (vis[0] | vis[1] | vis[2] | vis[3]) != 0u;
+                if (mx == -INFINITY && sees) mx = 0.f;
                 float alpha = 1.0f;
                 bool resc = false;
                 if (mx > mrun + kRescaleSlack) {  // also the row's first tile with a key (mrun = -inf)

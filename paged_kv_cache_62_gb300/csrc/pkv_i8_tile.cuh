@@ -84,7 +84,7 @@ __device__ __forceinline__ float q_row_scale(const uint16_t *qr, bool live, int 
     return q_pow2(mx, mul);
 }
 
-template <int D, int HR_, bool TAIL>
+template <int D, int HR_, bool TAIL, bool MASK>
 __device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const LaneOffsets<D, kI8, false> &off,
                                                const uint32_t (&qa)[Tc<D, kI8, false, HR_>::KS][2 * HR_],
                                                const float (&rowf)[HR_], const float (&qb)[HR_],
@@ -138,10 +138,12 @@ __device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const L
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    x[hr][4 * st + 2 * nt + e] = 16 * st + 8 * nt + 2 * r4 + e < lim[hr]
+                for (int e = 0; e < 2; ++e) {
+                    const int t = 16 * st + 8 * nt + 2 * r4 + e;
+                    x[hr][4 * st + 2 * nt + e] = (MASK ? (lim[hr] >> t) & 1 : t < lim[hr])
                                                      ? fmaf(sa[st][nt][2 * hr + e], f, sc[st].lv)
                                                      : -INFINITY;
+                }
         }
     float mx[HR];
     bool grow = false;
@@ -171,6 +173,8 @@ __device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const L
             }
         }
     }
+    // whether sub-tile st has a token (else it has no scales either)
+    auto has = [&](int st) { return !TAIL || (MASK ? ((valid >> (16 * st)) & 0xffff) != 0 : 16 * st < valid); };
     uint32_t pb[HR][NT][2];
 #pragma unroll
     for (int hr = 0; hr < HR; ++hr) {
@@ -180,17 +184,23 @@ __device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const L
             float pr[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) pr[k] = ex2(x[hr][4 * st + k] - mr);
-            // (a sub-tile without a token has no scales either)
-            if (!TAIL || 16 * st < valid) l[hr] = fmaf((pr[0] + pr[1]) + (pr[2] + pr[3]), sc[st].iv, l[hr]);
+            if (has(st)) l[hr] = fmaf((pr[0] + pr[1]) + (pr[2] + pr[3]), sc[st].iv, l[hr]);
 #pragma unroll
             for (int c = 0; c < 2; ++c) pb[hr][st][c] = f16x2_of(pr[2 * c], pr[2 * c + 1]);
         }
     }
 #pragma unroll
     for (int st = 0; st < NT; ++st) {
-        if (TAIL && 16 * st >= valid) break;  // no token
+        if (MASK ? !has(st) : TAIL && 16 * st >= valid) {  // no token
+            if constexpr (MASK) continue;
+            break;
+        }
         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-        if constexpr (TAIL) {
+        if constexpr (TAIL && MASK) {
+            const uint32_t v0 = sc[st].vzero ? 0u : uint32_t(valid) >> (16 * st + 2 * r4);
+            keep0 = (v0 & 1u ? 0x0000ffffu : 0u) | (v0 & 2u ? 0xffff0000u : 0u);
+            keep1 = (v0 & 0x100u ? 0x0000ffffu : 0u) | (v0 & 0x200u ? 0xffff0000u : 0u);
+        } else if constexpr (TAIL) {
             const int v0 = sc[st].vzero ? 0 : valid - 16 * st;
             keep0 = (2 * r4 < v0 ? 0x0000ffffu : 0u) | (2 * r4 + 1 < v0 ? 0xffff0000u : 0u);
             keep1 = (2 * r4 + 8 < v0 ? 0x0000ffffu : 0u) | (2 * r4 + 9 < v0 ? 0xffff0000u : 0u);
@@ -234,7 +244,7 @@ __device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const L
     }
 }
 
-template <int D, int G>
+template <int D, int G, bool MASK>
 __device__ __noinline__ void merge_pieces_i8(const DecodeParams &p, const long long *bound, int sf, int sl,
                                              long long x0, int g, int h, int b, int kvh, int nvh, int lane)
 {
@@ -306,7 +316,7 @@ __device__ __noinline__ void merge_pieces_i8(const DecodeParams &p, const long l
         for (int i = 0; i < HB; ++i) {
             const int hh = h0 + i;
             if (hh >= nvh) break;
-            const float inv = 1.0f / L[i];
+            const float inv = MASK && L[i] == 0.f ? 0.f : 1.0f / L[i];
             uint16_t *o = p.out + ((int64_t(b) * p.qstride + hh / p.gq) * p.Hq + int64_t(kvh) * p.gq + hh % p.gq) * D +
                           lane * PER;
             if constexpr (PER == 4)

@@ -17,7 +17,12 @@
 // its eight cosines and sines stay in registers for all heads.  16384 rows of 16 + 2 x 8 heads of 128 on three axes,
 // 269 MB: 47.1 us = 5.7 TB/s, 0.84 of the copy rate (a CTA a token group with a barrier after the cosines: 61 us);
 // 64 rows: 3.1 us, a launch and two dependent loads.
+//
+// With a norm (NORM), a q or k head x becomes x / sqrt(mean x^2 + eps) * w before the turn: the D / 16 lanes that
+// hold a head add up their squares with shuffles, and the row's factor and the weights join the turn's products, so
+// the head makes no second trip through registers.
 #include <algorithm>
+#include <cmath>
 
 #include "pkv_device.cuh"
 #include "pkv_host.h"
@@ -34,6 +39,8 @@ struct RopeParams {
     const float *inv_freq;
     int32_t axes, T, Hq, Hkv, D, rot, parts;
     long long num_slots;
+    const float *qw, *kw;  // NORM: weights of a q and a k head (null: ones)
+    float eps;
     int32_t *err;
 };
 
@@ -97,9 +104,71 @@ __device__ __forceinline__ void turn16(uint4 &a, uint4 &b, const float2 *cs)
     b = make_uint4(ub[0], ub[1], ub[2], ub[3]);
 }
 
+// The same for a head that is normed first: a and b times r and the weights at wa and wb (null: ones); turned or not.
+template <bool ADJ>
+__device__ __forceinline__ void norm_turn16(uint4 &a, uint4 &b, const float2 *cs, bool turn, float r, const float *wa,
+                                            const float *wb)
+{
+    const uint32_t ua[4] = {a.x, a.y, a.z, a.w}, ub[4] = {b.x, b.y, b.z, b.w};
+    float x[8], y[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[2 * j] = __uint_as_float(ua[j] << 16) * r;
+        x[2 * j + 1] = __uint_as_float(ua[j] & 0xffff0000u) * r;
+        y[2 * j] = __uint_as_float(ub[j] << 16) * r;
+        y[2 * j + 1] = __uint_as_float(ub[j] & 0xffff0000u) * r;
+    }
+    if (wa) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float4 u = __ldg(reinterpret_cast<const float4 *>(wa) + j);
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(wb) + j);
+            x[4 * j] *= u.x;
+            x[4 * j + 1] *= u.y;
+            x[4 * j + 2] *= u.z;
+            x[4 * j + 3] *= u.w;
+            y[4 * j] *= v.x;
+            y[4 * j + 1] *= v.y;
+            y[4 * j + 2] *= v.z;
+            y[4 * j + 3] *= v.w;
+        }
+    }
+    if (turn) {
+#pragma unroll
+        for (int e = 0; e < (ADJ ? 4 : 8); ++e) {
+            if constexpr (ADJ) {
+                const float p = x[2 * e], q = y[2 * e];
+                x[2 * e] = p * cs[e].x - x[2 * e + 1] * cs[e].y;
+                x[2 * e + 1] = x[2 * e + 1] * cs[e].x + p * cs[e].y;
+                y[2 * e] = q * cs[4 + e].x - y[2 * e + 1] * cs[4 + e].y;
+                y[2 * e + 1] = y[2 * e + 1] * cs[4 + e].x + q * cs[4 + e].y;
+            } else {
+                const float p = x[e];
+                x[e] = p * cs[e].x - y[e] * cs[e].y;
+                y[e] = y[e] * cs[e].x + p * cs[e].y;
+            }
+        }
+    }
+    a = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    b = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+}
+
+__device__ __forceinline__ float squares(uint4 a)
+{
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float lo = __uint_as_float(u[j] << 16), hi = __uint_as_float(u[j] & 0xffff0000u);
+        s0 = fmaf(lo, lo, s0);
+        s1 = fmaf(hi, hi, s1);
+    }
+    return s0 + s1;
+}
+
 constexpr int kRopeWarps = 2;  // warps (token parts) a CTA: small ones, whose last warp holds little back
 
-template <bool ADJ>
+template <bool ADJ, bool NORM>
 __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams p)
 {
     __shared__ __align__(16) float2 cs_all[kRopeWarps][kRopeMaxHalf];
@@ -140,7 +209,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams 
     // a turning piece of pairs of halves lies in two places of the head
     auto d0 = [&](int h) { return c < turned && !ADJ && h < turning ? 8 * c : 16 * c; };
     auto d1 = [&](int h) { return c < turned && !ADJ && h < turning ? half + 8 * c : 16 * c + 8; };
-    uint4 a[B], b[B];
+    uint4 a[B] = {}, b[B] = {};
     auto load = [&](int h0) {
 #pragma unroll
         for (int k = 0; k < B; ++k) {
@@ -169,14 +238,41 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams 
 #pragma unroll
         for (int e = 0; e < 8; ++e) mycs[e] = cs[8 * c + e];
     }
-    for (int h1 = h0; h1 < heads; h1 += step) {
+    const bool pow2 = (per & (per - 1)) == 0;
+    for (int h1 = h0; NORM ? h1 - hl < heads : h1 < heads; h1 += step) {  // (NORM: the lanes stay together)
+        float rs[B];
+        if constexpr (NORM) {
+            float ss[B];
+#pragma unroll
+            for (int k = 0; k < B; ++k) ss[k] = squares(a[k]) + squares(b[k]);
+            if (pow2) {
+                for (int o = 1; o < per; o <<= 1)
+#pragma unroll
+                    for (int k = 0; k < B; ++k) ss[k] += __shfl_xor_sync(kFull, ss[k], o);
+            } else {
+                float all[B] = {};
+                for (int i = 0; i < per; ++i)
+#pragma unroll
+                    for (int k = 0; k < B; ++k) all[k] += __shfl_sync(kFull, ss[k], hl * per + i);
+#pragma unroll
+                for (int k = 0; k < B; ++k) ss[k] = all[k];
+            }
+#pragma unroll
+            for (int k = 0; k < B; ++k) rs[k] = rsqrtf(fmaf(ss[k], 1.0f / float(p.D), p.eps));
+        }
 #pragma unroll
         for (int k = 0; k < B; ++k) {
             const int h = h1 + k * hpw * p.parts;
             const uint16_t *src;
             uint16_t *dst;
             if (place(h, src, dst)) {
-                if (c < turned && h < turning) turn16<ADJ>(a[k], b[k], mycs);
+                if constexpr (NORM) {
+                    if (h < turning) {
+                        const float *w = h < p.Hq ? p.qw : p.kw;
+                        norm_turn16<ADJ>(a[k], b[k], mycs, c < turned, rs[k], w ? w + d0(h) : nullptr, w + d1(h));
+                    }
+                } else if (c < turned && h < turning)
+                    turn16<ADJ>(a[k], b[k], mycs);
                 *reinterpret_cast<uint4 *>(dst + d0(h)) = a[k];
                 *reinterpret_cast<uint4 *>(dst + d1(h)) = b[k];
             }
@@ -185,7 +281,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams 
     }
 }
 
-static pkv_status rope_call(RopeParams &p, int interleaved, pkv_stream_t stream)
+static pkv_status rope_call(RopeParams &p, int interleaved, pkv_stream_t stream, bool norm = false)
 {
     DeviceInfo dev;
     if (!current_device_info(&dev)) return PKV_ECUDA;
@@ -195,8 +291,10 @@ static pkv_status rope_call(RopeParams &p, int interleaved, pkv_stream_t stream)
     const int most = (heads + hpw - 1) / hpw;
     p.parts = int(std::min<int64_t>(most, std::max<int64_t>(1, int64_t(dev.sm_count) * 8 / p.T)));
     const int64_t grid = (int64_t(p.T) * p.parts + kRopeWarps - 1) / kRopeWarps;
-    const cudaError_t e = launch_pdl(interleaved ? rope_kernel<true> : rope_kernel<false>, dim3(unsigned(grid)),
-                                     dim3(32 * kRopeWarps), 0, reinterpret_cast<cudaStream_t>(stream), p);
+    auto kern = norm ? (interleaved ? rope_kernel<true, true> : rope_kernel<false, true>)
+                     : (interleaved ? rope_kernel<true, false> : rope_kernel<false, false>);
+    const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(32 * kRopeWarps), 0,
+                                     reinterpret_cast<cudaStream_t>(stream), p);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return cuda_fail("rope_kernel launch", e);
@@ -229,12 +327,23 @@ static pkv_status rope_check(const uint16_t *q, int64_t q_stride, const uint16_t
 
 using namespace pkv;
 
-extern "C" pkv_status pkv_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
-                               const int32_t *positions, int32_t num_axes, const float *inv_freq,
-                               const int32_t *freq_axis, int32_t num_tokens, int32_t num_q_heads,
-                               int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
-                               uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
-                               int32_t *err_word, pkv_stream_t stream)
+// The norm of a call that has one.
+struct Norm {
+    const float *qw, *kw;
+    float eps;
+};
+
+static bool norm_ok(const Norm &n)
+{
+    return std::isfinite(n.eps) && n.eps > 0.f && aligned16(n.qw) && aligned16(n.kw);  // (null is aligned)
+}
+
+static pkv_status rope_impl(const Norm *norm, const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                            const int32_t *positions, int32_t num_axes, const float *inv_freq,
+                            const int32_t *freq_axis, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
+                            uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
+                            int32_t *err_word, pkv_stream_t stream)
 {
     const pkv_status st = rope_check(q, q_stride, k, k_stride, q_out, q_out_stride, num_tokens, num_q_heads,
                                      num_kv_heads, head_dim, rot_dim, positions, num_axes, inv_freq);
@@ -260,16 +369,21 @@ extern "C" pkv_status pkv_rope(const uint16_t *q, int64_t q_stride, const uint16
     p.D = head_dim;
     p.rot = rot_dim;
     p.err = err_word;
-    return rope_call(p, interleaved, stream);
+    if (norm) {
+        p.qw = norm->qw;
+        p.kw = norm->kw;
+        p.eps = norm->eps;
+    }
+    return rope_call(p, interleaved, stream, norm != nullptr);
 }
 
-extern "C" pkv_status pkv_rope_store(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
-                                     const uint16_t *v, int64_t v_stride, const int32_t *positions, int32_t num_axes,
-                                     const float *inv_freq, const int32_t *freq_axis, const int32_t *slot_mapping,
-                                     int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
-                                     int32_t rot_dim, int32_t interleaved, uint16_t *q_out, int64_t q_out_stride,
-                                     uint16_t *k_cache, uint16_t *v_cache, int32_t num_blocks, int32_t block_size,
-                                     int32_t *err_word, pkv_stream_t stream)
+static pkv_status rope_store_impl(const Norm *norm, const uint16_t *q, int64_t q_stride, const uint16_t *k,
+                                  int64_t k_stride, const uint16_t *v, int64_t v_stride, const int32_t *positions,
+                                  int32_t num_axes, const float *inv_freq, const int32_t *freq_axis,
+                                  const int32_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                                  int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
+                                  uint16_t *q_out, int64_t q_out_stride, uint16_t *k_cache, uint16_t *v_cache,
+                                  int32_t num_blocks, int32_t block_size, int32_t *err_word, pkv_stream_t stream)
 {
     if (num_blocks <= 0 || block_size <= 0) return PKV_EINVAL;
     const pkv_status st = rope_check(q, q_stride, k, k_stride, q_out, q_out_stride, num_tokens, num_q_heads,
@@ -304,5 +418,67 @@ extern "C" pkv_status pkv_rope_store(const uint16_t *q, int64_t q_stride, const 
     p.rot = rot_dim;
     p.num_slots = int64_t(num_blocks) * block_size;
     p.err = err_word;
-    return rope_call(p, interleaved, stream);
+    if (norm) {
+        p.qw = norm->qw;
+        p.kw = norm->kw;
+        p.eps = norm->eps;
+    }
+    return rope_call(p, interleaved, stream, norm != nullptr);
+}
+
+extern "C" pkv_status pkv_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                               const int32_t *positions, int32_t num_axes, const float *inv_freq,
+                               const int32_t *freq_axis, int32_t num_tokens, int32_t num_q_heads,
+                               int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
+                               uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
+                               int32_t *err_word, pkv_stream_t stream)
+{
+    return rope_impl(nullptr, q, q_stride, k, k_stride, positions, num_axes, inv_freq, freq_axis, num_tokens,
+                     num_q_heads, num_kv_heads, head_dim, rot_dim, interleaved, q_out, q_out_stride, k_out,
+                     k_out_stride, err_word, stream);
+}
+
+extern "C" pkv_status pkv_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                                       const float *q_weight, const float *k_weight, float eps,
+                                       const int32_t *positions, int32_t num_axes, const float *inv_freq,
+                                       const int32_t *freq_axis, int32_t num_tokens, int32_t num_q_heads,
+                                       int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
+                                       uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
+                                       int32_t *err_word, pkv_stream_t stream)
+{
+    const Norm n{q_weight, k_weight, eps};
+    if (!norm_ok(n)) return PKV_EINVAL;
+    return rope_impl(&n, q, q_stride, k, k_stride, positions, num_axes, inv_freq, freq_axis, num_tokens,
+                     num_q_heads, num_kv_heads, head_dim, rot_dim, interleaved, q_out, q_out_stride, k_out,
+                     k_out_stride, err_word, stream);
+}
+
+extern "C" pkv_status pkv_rope_store(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                                     const uint16_t *v, int64_t v_stride, const int32_t *positions, int32_t num_axes,
+                                     const float *inv_freq, const int32_t *freq_axis, const int32_t *slot_mapping,
+                                     int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                     int32_t rot_dim, int32_t interleaved, uint16_t *q_out, int64_t q_out_stride,
+                                     uint16_t *k_cache, uint16_t *v_cache, int32_t num_blocks, int32_t block_size,
+                                     int32_t *err_word, pkv_stream_t stream)
+{
+    return rope_store_impl(nullptr, q, q_stride, k, k_stride, v, v_stride, positions, num_axes, inv_freq, freq_axis,
+                           slot_mapping, num_tokens, num_q_heads, num_kv_heads, head_dim, rot_dim, interleaved, q_out,
+                           q_out_stride, k_cache, v_cache, num_blocks, block_size, err_word, stream);
+}
+
+extern "C" pkv_status pkv_qk_norm_rope_store(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                                             const uint16_t *v, int64_t v_stride, const float *q_weight,
+                                             const float *k_weight, float eps, const int32_t *positions,
+                                             int32_t num_axes, const float *inv_freq, const int32_t *freq_axis,
+                                             const int32_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+                                             int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim,
+                                             int32_t interleaved, uint16_t *q_out, int64_t q_out_stride,
+                                             uint16_t *k_cache, uint16_t *v_cache, int32_t num_blocks,
+                                             int32_t block_size, int32_t *err_word, pkv_stream_t stream)
+{
+    const Norm n{q_weight, k_weight, eps};
+    if (!norm_ok(n)) return PKV_EINVAL;
+    return rope_store_impl(&n, q, q_stride, k, k_stride, v, v_stride, positions, num_axes, inv_freq, freq_axis,
+                           slot_mapping, num_tokens, num_q_heads, num_kv_heads, head_dim, rot_dim, interleaved, q_out,
+                           q_out_stride, k_cache, v_cache, num_blocks, block_size, err_word, stream);
 }

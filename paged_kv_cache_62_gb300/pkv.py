@@ -2,7 +2,7 @@
 
 Argument marshalling only: every step runs in the library's CUDA kernels.
 Tensors are torch CUDA tensors (device memory and streams come from torch);
-shapes and dtypes are checked here (those of the int8 and rotary calls in
+shapes and dtypes are checked here (those of the int8, rotary, windowed and tree calls in
 ``_pkv_torch.so``, native code beside the library), then raw device pointers go
 through the C ABI.  There is no fallback: if the library, or for those calls
 ``_pkv_torch.so``, is missing, or the tensors are not on a CUDA device, the call
@@ -62,6 +62,24 @@ SIGNATURES = {
                                 _P, _I64, _P, _P]),
     "pkv_rope_store": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _I32, _P, _P, _P, _I32, _I32, _I32, _I32,
                                       _I32, _I32, _P, _I64, _P, _P, _I32, _I32, _P, _P]),
+    "pkv_paged_decode_window": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32, _I32, _I32,
+        _P, _P, _SZ, _I32, _P, _P]),
+    "pkv_paged_decode_window_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32, _I32, _I32,
+        _P, _P, _SZ, _I32, _P, _P]),
+    "pkv_paged_decode_window_i8": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32, _I32, _I32,
+        _P, _P, _SZ, _I32, _P, _P]),
+    "pkv_paged_attention_window": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32,
+        _I32, _I32, _P, _I32, _P, _SZ, _I32, _P, _P]),
+    "pkv_paged_attention_window_i8": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32,
+        _I32, _I32, _P, _I32, _P, _SZ, _I32, _P, _P]),
+    "pkv_paged_attention_tree": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32,
+        _P, _I32, _P, _I32, _P, _SZ, _I32, _P, _P]),
+    "pkv_paged_attention_tree_i8": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32,
+        _P, _I32, _P, _I32, _P, _SZ, _I32, _P, _P]),
+    "pkv_qk_norm_rope": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _F32, _P, _I32, _P, _P, _I32, _I32, _I32, _I32,
+                                        _I32, _I32, _P, _I64, _P, _I64, _P, _P]),
+    "pkv_qk_norm_rope_store": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _F32, _P, _I32, _P, _P, _P, _I32,
+                                              _I32, _I32, _I32, _I32, _I32, _P, _I64, _P, _P, _I32, _I32, _P, _P]),
     "pkv_allocator_create": (_P, [_I32, _I32]),
     "pkv_allocator_destroy": (None, [_P]),
     "pkv_allocator_add": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32]),
@@ -586,3 +604,126 @@ def rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: tor
                               interleaved, err_word, stream)
     if st != OK:
         raise PkvError(st, "pkv_rope_store")
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | None, k_weight: torch.Tensor | None,
+                 eps: float, positions: torch.Tensor, inv_freq: torch.Tensor, q_out: torch.Tensor,
+                 k_out: torch.Tensor, freq_axis: torch.Tensor | None = None, interleaved: bool = False,
+                 err_word: torch.Tensor | None = None, stream=None) -> None:
+    """rope with a root-mean-square norm of every q and k head before the turn: x / sqrt(mean(x^2) + eps) * weight,
+    weights float32 [D] (None: ones), eps > 0.  Other arguments as rope's."""
+    st = _native().qk_norm_rope(q, k, q_weight, k_weight, eps, positions, inv_freq, q_out, k_out, freq_axis,
+                                interleaved, err_word, stream)
+    if st != OK:
+        raise PkvError(st, "pkv_qk_norm_rope")
+
+
+def qk_norm_rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: torch.Tensor | None,
+                       k_weight: torch.Tensor | None, eps: float, positions: torch.Tensor, inv_freq: torch.Tensor,
+                       slot_mapping: torch.Tensor, q_out: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       freq_axis: torch.Tensor | None = None, interleaved: bool = False,
+                       err_word: torch.Tensor | None = None, stream=None) -> None:
+    """qk_norm_rope and kv_store in one launch: rope_store with the norm of qk_norm_rope before the turn."""
+    st = _native().qk_norm_rope_store(q, k, v, q_weight, k_weight, eps, positions, inv_freq, slot_mapping, q_out,
+                                      k_cache, v_cache, freq_axis, interleaved, err_word, stream)
+    if st != OK:
+        raise PkvError(st, "pkv_qk_norm_rope_store")
+
+
+def paged_decode_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                        context_lens: torch.Tensor, scale: float, window: int, sinks: int, out: torch.Tensor,
+                        workspace: torch.Tensor, max_context_len: int | None = None, num_workers: int = 0,
+                        err_word: torch.Tensor | None = None, stream=None) -> None:
+    """paged_decode over the last `window` keys of each sequence and its first `sinks`; table entries of blocks
+    between them are not read."""
+    st = _native().paged_decode_window(q, k_cache, v_cache, None, None, block_tables, context_lens, scale, window, sinks,
+                                       out, workspace, max_context_len, num_workers, err_word, stream)
+    if st != OK:
+        raise PkvError(st, "pkv_paged_decode_window")
+
+
+def paged_decode_window_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                            v_scale: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                            scale: float, window: int, sinks: int, out: torch.Tensor, workspace: torch.Tensor,
+                            max_context_len: int | None = None, num_workers: int = 0,
+                            err_word: torch.Tensor | None = None, stream=None) -> None:
+    """paged_decode_window over E4M3 caches (uint8 [NB, bs, Hkv, D]) with per-kv-head float32 scales."""
+    if k_scale is None or v_scale is None:
+        raise ValueError("paged_decode_window_fp8: k_scale and v_scale are needed")
+    st = _native().paged_decode_window(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, window,
+                                       sinks, out, workspace, max_context_len, num_workers, err_word, stream)
+    if st != OK:
+        raise PkvError(st, "pkv_paged_decode_window_fp8")
+
+
+def paged_decode_window_i8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor,
+                           block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, window: int,
+                           sinks: int, out: torch.Tensor, workspace: torch.Tensor, max_context_len: int | None = None,
+                           num_workers: int = 0, err_word: torch.Tensor | None = None, stream=None) -> None:
+    """paged_decode_window over an int8 cache (int8 [NB, bs, Hkv, D]) with scales [NB, bs / 16, Hkv, 2]."""
+    if scales is None:
+        raise ValueError("paged_decode_window_i8: scales are needed")
+    st = _native().paged_decode_window(q, k_cache, v_cache, scales, None, block_tables, context_lens, scale, window,
+                                       sinks, out, workspace, max_context_len, num_workers, err_word, stream)
+    if st != OK:
+        raise PkvError(st, "pkv_paged_decode_window_i8")
+
+
+def paged_attention_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                           cu_seqlens_q: torch.Tensor | None, context_lens: torch.Tensor, scale: float, window: int,
+                           sinks: int, out: torch.Tensor, workspace: torch.Tensor, max_context_len: int | None = None,
+                           num_workers: int = 0, err_word: torch.Tensor | None = None, stream=None,
+                           new_per_seq: int = 0) -> None:
+    """paged_attention in which each new token sees the last `window` keys up to its own and the sequence's first
+    `sinks`; table entries of blocks that no new token sees are not read."""
+    st = _native().paged_attention_mask(q, k_cache, v_cache, None, block_tables, cu_seqlens_q, context_lens, None, window,
+                                        sinks, scale, out, workspace, max_context_len, num_workers, err_word, stream,
+                                        new_per_seq)
+    if st != OK:
+        raise PkvError(st, "pkv_paged_attention_window")
+
+
+def paged_attention_window_i8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor,
+                              block_tables: torch.Tensor, cu_seqlens_q: torch.Tensor | None,
+                              context_lens: torch.Tensor, scale: float, window: int, sinks: int, out: torch.Tensor,
+                              workspace: torch.Tensor, max_context_len: int | None = None, num_workers: int = 0,
+                              err_word: torch.Tensor | None = None, stream=None, new_per_seq: int = 0) -> None:
+    """paged_attention_window over an int8 cache (int8 [NB, bs, Hkv, D]) with scales [NB, bs / 16, Hkv, 2]."""
+    if scales is None:
+        raise ValueError("paged_attention_window_i8: scales are needed")
+    st = _native().paged_attention_mask(q, k_cache, v_cache, scales, block_tables, cu_seqlens_q, context_lens, None,
+                                        window, sinks, scale, out, workspace, max_context_len, num_workers, err_word,
+                                        stream, new_per_seq)
+    if st != OK:
+        raise PkvError(st, "pkv_paged_attention_window_i8")
+
+
+def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                         cu_seqlens_q: torch.Tensor | None, context_lens: torch.Tensor, tree_mask: torch.Tensor,
+                         scale: float, out: torch.Tensor, workspace: torch.Tensor, max_context_len: int | None = None,
+                         num_workers: int = 0, err_word: torch.Tensor | None = None, stream=None,
+                         new_per_seq: int = 0) -> None:
+    """paged_attention of drafted trees: a sequence's n new tokens are nodes, parents first, and node i sees the keys
+    before the draft and the nodes t <= i whose bit is set in its row of tree_mask (int32 [rows, words])."""
+    if tree_mask is None:
+        raise ValueError("paged_attention_tree: tree_mask is needed")
+    st = _native().paged_attention_mask(q, k_cache, v_cache, None, block_tables, cu_seqlens_q, context_lens, tree_mask, 0,
+                                        0, scale, out, workspace, max_context_len, num_workers, err_word, stream,
+                                        new_per_seq)
+    if st != OK:
+        raise PkvError(st, "pkv_paged_attention_tree")
+
+
+def paged_attention_tree_i8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, scales: torch.Tensor,
+                            block_tables: torch.Tensor, cu_seqlens_q: torch.Tensor | None, context_lens: torch.Tensor,
+                            tree_mask: torch.Tensor, scale: float, out: torch.Tensor, workspace: torch.Tensor,
+                            max_context_len: int | None = None, num_workers: int = 0,
+                            err_word: torch.Tensor | None = None, stream=None, new_per_seq: int = 0) -> None:
+    """paged_attention_tree over an int8 cache (int8 [NB, bs, Hkv, D]) with scales [NB, bs / 16, Hkv, 2]."""
+    if scales is None or tree_mask is None:
+        raise ValueError("paged_attention_tree_i8: scales and tree_mask are needed")
+    st = _native().paged_attention_mask(q, k_cache, v_cache, scales, block_tables, cu_seqlens_q, context_lens, tree_mask,
+                                        0, 0, scale, out, workspace, max_context_len, num_workers, err_word, stream,
+                                        new_per_seq)
+    if st != OK:
+        raise PkvError(st, "pkv_paged_attention_tree_i8")
