@@ -557,9 +557,10 @@ PKV_API pkv_status pkv_paged_attention_i8(const uint16_t *q, const int8_t *k_cac
  * context_lens count every token.  A call streams about
  * min(L, window + sinks + n) key rows per sequence and kv head and pass over
  * them (see pkv_paged_attention for n new tokens).
- * Arguments, workspaces (the same functions size them; a workspace may serve
- * these calls and the others in turn), num_workers, limits and errors as the
- * calls without window; max_context_len at most 2^30 (PKV_EBOUNDS).  Where a
+ * Arguments, workspaces (pkv_paged_decode_workspace_size for one new token,
+ * pkv_paged_attention_i8_workspace_size for several, whatever the cache; a
+ * workspace may serve these calls and the others in turn), num_workers, limits
+ * and errors as the calls without window; max_context_len at most 2^30 (PKV_EBOUNDS).  Where a
  * call's queries share a pass, K and V of a key that one of them sees should be finite: an
  * infinity or NaN there may reach the others.
  */
@@ -608,8 +609,9 @@ PKV_API pkv_status pkv_paged_attention_window_i8(
  * A row that sees no key (L = n and an empty mask) gives zeros.  The mask of a
  * chain is its lower triangle: the results of pkv_paged_attention.
  * mask_words >= 1; a sequence has at most 32 * mask_words nodes (new_per_seq
- * beyond: PKV_EINVAL; offsets beyond: zeros and PKV_ERR_CONTEXT_RANGE).  Other
- * limits, workspaces, sharing of passes and errors as pkv_paged_attention;
+ * beyond: PKV_EINVAL; offsets beyond: zeros and PKV_ERR_CONTEXT_RANGE).
+ * Workspace: pkv_paged_attention_i8_workspace_size bytes, whatever the cache.
+ * Other limits, sharing of passes and errors as pkv_paged_attention;
  * max_context_len at most 2^30 (PKV_EBOUNDS).  (The pages have no counterpart.)
  */
 PKV_API pkv_status pkv_paged_attention_tree(

@@ -26,7 +26,7 @@ TORCH_PATH = os.path.join(HERE, "_pkv_torch.so")
 TORCH_OBJ, TORCH_KEY = os.path.join(BUILD_DIR, "pkv_torch.o"), os.path.join(BUILD_DIR, "pkv_torch.key")
 SOURCES = ["pkv_api.cu", "pkv_store.cu", "pkv_decode.cu", "pkv_decode_fp8.cu", "pkv_decode_qs.cu", "pkv_decode_wide.cu",
            "pkv_decode_tc5.cu", "pkv_decode_i8.cu", "pkv_decode_i8_wide.cu", "pkv_decode_i8_tc5.cu", "pkv_store_i8.cu",
-           "pkv_mask.cu", "pkv_mask_wide.cu", "pkv_mask_qs.cu", "pkv_mask_fp8.cu", "pkv_mask_i8.cu", "pkv_mask_i8_wide.cu",
+           "pkv_mask.cu", "pkv_mask_wide.cu", "pkv_mask_tile.cu", "pkv_mask_fp8.cu", "pkv_mask_i8.cu", "pkv_mask_i8_wide.cu",
            "pkv_mask_i8_tc5.cu",
            "pkv_rope.cu", "pkv_noalloc.cu", "pkv_alloc.cpp"]
 HEADERS = ["pkv_device.cuh", "pkv_host.h", "pkv_decode_kernel.cuh", "pkv_i8_tile.cuh", "pkv_i8_codes.cuh",

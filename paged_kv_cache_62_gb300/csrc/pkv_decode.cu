@@ -43,6 +43,18 @@ static pkv_status check_mask(const MaskArgs &m, bool tree)
     return PKV_OK;
 }
 
+// (p.len_limit is set)
+static void set_mask(DecodeParams &p, const MaskArgs &m)
+{
+    p.window = std::min(m.window, std::max(p.len_limit, 1));  // (one as long as the sequences sees all)
+    p.sinks = std::min(m.sinks, p.len_limit);
+    p.tree = m.tree;
+    p.tree_words = m.tree_words;
+    p.tree_n = m.tree_n;
+    p.tree_lens = m.tree_lens;
+    p.tree_cu = m.tree_cu;
+}
+
 // Tokens of a sequence that its last n queries see, at most.
 static int64_t seen_bound(const MaskArgs *m, int64_t len_limit, int64_t n)
 {
@@ -147,15 +159,7 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
     p.v_cache_w = static_cast<uint8_t *>(const_cast<void *>(v_cache));
     p.slot_out = k_new ? slot_out : nullptr;
     p.qstride = row_cnt ? 1 : qn;
-    if (mask) {
-        p.window = std::min(mask->window, std::max(p.len_limit, 1));  // (one as long as the sequences sees all)
-        p.sinks = std::min(mask->sinks, p.len_limit);
-        p.tree = mask->tree;
-        p.tree_words = mask->tree_words;
-        p.tree_n = mask->tree_n;
-        p.tree_lens = mask->tree_lens;
-        p.tree_cu = mask->tree_cu;
-    }
+    if (mask) set_mask(p, *mask);
     a.k_cache = k_cache;
     a.v_cache = v_cache;
     a.device = dev.device;
@@ -207,9 +211,7 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
     LaunchFn fn = mask && ct == kE4m3 ? pick_mask_fp8(head_dim, G)
                   : mask && ct == kI8 ? (qs ? pick_mask_i8_tc5(head_dim)
                                             : G > 8 ? pick_mask_i8_wide(head_dim, G) : pick_mask_i8(head_dim, G))
-                  : mask ? (tc5 ? pick_mask_tc5(head_dim)
-                            : qs  ? pick_mask_qs(head_dim, G)
-                            : G > 8 ? pick_mask_wide(head_dim, G) : pick_mask(head_dim, G))
+                  : mask ? (G > 8 ? pick_mask_wide(head_dim, G) : pick_mask(head_dim, G))
                   : ct == kE4m3 ? pick_decode_fp8(head_dim, G)
                   : ct == kI8 ? (qs ? pick_decode_i8_tc5(head_dim)
                                     : G > 8 ? pick_decode_i8_wide(head_dim, G) : pick_decode_i8(head_dim, G))
@@ -518,6 +520,8 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     if (mask && len_max > kMaskMaxLen) return PKV_EBOUNDS;
     const int32_t max_new = mask && mask->tree ? int32_t(std::min<int64_t>(32LL * mask->tree_words, INT32_MAX)) : INT32_MAX;
     const size_t need = pkv_paged_attention_workspace_size(num_rows, num_q_heads, num_kv_heads, head_dim);
+    if (mask && workspace_bytes < pkv_paged_attention_i8_workspace_size(num_rows, num_q_heads, num_kv_heads, head_dim))
+        return PKV_EWORKSPACE;
     if (need == 0) return num_rows > PKV_MAX_SEQS ? PKV_EBOUNDS : PKV_EINVAL;
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return PKV_EWORKSPACE;
     // Up to qg queries of a sequence fit one regular CTA warp's MMA tile (qg * G <= 16 virtual heads):
@@ -534,7 +538,8 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     // chunks of a sequence's queries, one entry per row; few new tokens per sequence on average (at
     // most two regular chunks): chunks of qg on regular CTAs, else chunks of 8 * qg on query-split ones.
     // The row arrays sit after the decode workspace.
-    // (Query-split int8 entries fill the tensor-memory tile: as many whole queries as 128 rows hold.)
+    // (Query-split int8 entries, and those of masked calls, fill the tensor-memory tile: as many whole queries as 128
+    // rows hold.)
     const int32_t tile = 128 / std::min(num_q_heads / num_kv_heads, 128);
     bool qs = int64_t(num_rows) > 2 * int64_t(qg) * num_seqs;
     if (ct == kI8 && !qs && int64_t(num_rows) > int64_t(qg) * num_seqs) {
@@ -552,22 +557,46 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     const int64_t entries = int64_t(num_rows) / tile + num_seqs;
     if (ct == kI8 && qs)
         qs = entries <= num_rows && workspace_bytes >= i8_entries_bytes(int32_t(entries), num_kv_heads, head_dim);
-    const int32_t chunk = !qs ? qg : ct == kI8 ? tile : entry_queries(num_q_heads, num_kv_heads);
+    const int32_t chunk = !qs ? qg : ct == kI8 || mask ? tile : entry_queries(num_q_heads, num_kv_heads);
     uint8_t *wsb = static_cast<uint8_t *>(workspace);
     int64_t live = -1;
     if (ct == kI8 || mask) {  // the rest of decode_call's refusals, before the list is laid out
         const int G = num_q_heads / num_kv_heads * qg, hg = head_group(num_kv_heads, G);
         live = std::min<int64_t>(num_rows, int64_t(num_rows) / chunk + num_seqs);
-        if (unit_bound(ct, qs, G, num_kv_heads, live,
-                       std::min<int64_t>(max_context_len, int64_t(max_blocks_per_seq) * block_size)) > INT32_MAX)
+        if (mask && qs && ct == kBf16) {  // (a segment's list counts a few units more there)
+            if (live * num_kv_heads * ((seen_bound(mask, len_max, tile) + kMtKeys - 1) / kMtKeys + 8) > INT32_MAX)
+                return PKV_EBOUNDS;
+        } else if (unit_bound(ct, qs, G, num_kv_heads, live, len_max) > INT32_MAX) {
             return PKV_EBOUNDS;
+        }
         DeviceInfo dev;
         if (!current_device_info(&dev)) return PKV_ECUDA;
         const bool i8 = ct == kI8;
-        if (!(qs && i8) && cta_layout(head_dim, G, i8 ? 1 : 2, qs ? 1 : hg, qs ? team_warps(G) : warp_slices(G, hg), 2,
-                                      num_rows, qs, false, one_q_buffer_ok(G, i8, qs, false) ? 1 : 2, i8).total >
-                               uint32_t(dev.max_smem_optin))
+        if (!qs && cta_layout(head_dim, G, i8 ? 1 : 2, hg, warp_slices(G, hg), 2, num_rows, false, false,
+                              one_q_buffer_ok(G, i8, false, false) ? 1 : 2, i8).total > uint32_t(dev.max_smem_optin))
             return PKV_EUNSUPPORTED;
+        if (qs && !i8) {
+            const int32_t n = mask_tile_entries(num_seqs, num_rows, new_per_seq, tile);
+            if (!mask_tile_fits(head_dim, n, new_per_seq == 0, dev.max_smem_optin)) return PKV_EUNSUPPORTED;
+            DecodeParams p{};
+            p.q = q;
+            p.block_tables = block_tables;
+            p.context_lens = context_lens;
+            p.out = out;
+            p.err = err_word;
+            p.Hq = num_q_heads;
+            p.Hkv = num_kv_heads;
+            p.gq = num_q_heads / num_kv_heads;
+            p.bs = block_size;
+            p.log2_bs = ilog2(block_size);
+            p.NB = num_blocks;
+            p.max_blocks = max_blocks_per_seq;
+            p.len_limit = int32_t(len_max);
+            p.scale_log2 = float(double(scale) * 1.4426950408889634);
+            set_mask(p, *mask);
+            return mask_tile_call(p, k_cache, v_cache, cu_seqlens_q, num_seqs, num_rows, new_per_seq, max_new, head_dim,
+                                  wsb, num_workers, reinterpret_cast<cudaStream_t>(stream));
+        }
     }
     if (ct == kI8 && qs) {
         const size_t dec_bytes = i8_entries_bytes(int32_t(entries), num_kv_heads, head_dim) -

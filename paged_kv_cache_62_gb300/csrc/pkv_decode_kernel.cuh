@@ -203,6 +203,7 @@ struct DecodeParams {
     // sequence's position L - n on, n its new tokens) those whose bit is set in its row of tree,
     // [query rows][tree_words].  A call has a window or a tree; without a window it is INT32_MAX.
     int32_t window, sinks;
+    int32_t seg_cost;                        // mask_tile_kernel: what a segment's list counts beside its units
     const uint32_t *tree;
     int32_t tree_words, tree_n;              // tree_n: new tokens of every sequence (0: as tree_cu says)
     const int32_t *tree_lens, *tree_cu;      // by sequence: context lengths, offsets of the query rows
@@ -1506,7 +1507,7 @@ __device__ void tc5_convert_warps(const DecodeParams &p, const CtaLayout &lay, c
 // keys 64 h .. 64 h + 63 of every tile, h = w / 4.  The two threads of a row (warps w and w + 4) hold the
 // same running max: they exchange their tile max each tile; each keeps the sum of its own keys' weights.
 // When a segment starts they write its Q tile (dims 64 h .. 64 h + 63 of row r) into tensor memory.
-template <int D, int G, bool MASK>
+template <int D, int G>
 __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, const Tc5Smem &m, uint32_t tmem,
                                   float *xch, const long long *bound, const int32_t *scan, int *sh,
                                   const float *wts, int nslots, uint32_t gen, int wp, bool adaptive)
@@ -1609,25 +1610,10 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
             if (!q_early) write_q(mt);
             q_early = false;
         }
-        const int tok0 = (MASK ? mt.tu : mt.u) * kTc5Keys;
+        const int tok0 = mt.u * kTc5Keys;
         const int valid = min(kTc5Keys, mt.L - tok0);
         const int lim = row_ok ? min(valid, mt.L - tok0 - shift) - KH * half : 0;  // keys of this half
-        if constexpr (MASK) {
-            // V rows that no query sees are zeroed too: those from the sinks' end to the window's start
-            const int z0 = max(p.sinks - tok0, 0), z1 = min(window_start(p, mt.L, mt.cnt) - tok0, valid);
-            if (valid < kTc5Keys || z0 < z1) {
-                if (!wait(&m.vfull[j % kTc5VSlots], (j / kTc5VSlots) & 1u)) break;
-                uint8_t *vrows = m.vbase + size_t(j % kTc5VSlots) * tc5_vslot_bytes(lay);
-                const int gap = max(z1 - z0, 0), per_part = (gap + kTc5Keys - valid) * 8, n = per_part * (D / 64);
-                for (int i = t; i < n; i += 32 * kTc5SoftmaxWarps) {
-                    const int part = i / per_part, r = i - part * per_part, k = r >> 3;
-                    *reinterpret_cast<uint4 *>(vrows + part * kTc5SlabBytes +
-                                               (k < gap ? z0 + k : valid + k - gap) * 128 + (r & 7) * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();  // for the tensor core
-            }
-        } else if (valid < kTc5Keys) {
+        if (valid < kTc5Keys) {
             // V rows past the sequence's end hold anything (NaN included) and 0 * NaN is NaN: zero them,
             // once the V copy has landed
             if (!wait(&m.vfull[j % kTc5VSlots], (j / kTc5VSlots) & 1u)) break;
@@ -1648,22 +1634,7 @@ __device__ void tc5_softmax_warps(const DecodeParams &p, const CtaLayout &lay, c
         {
             uint32_t r[KH];
             tmem_ld64(sbuf + uint32_t(KH * half), r);
-            if constexpr (MASK) {
-                uint32_t v0 = 0u, v1 = 0u;  // the half's keys that the row sees
-                if (row_ok) {
-                    const uint32_t *mask = p.tree ? p.tree + (long long)(mt.b + qi) * p.tree_words : nullptr;
-                    v0 = row_sees(p, tok0 + KH * half, mt.L - 1 - shift, mt.base, mask);
-                    v1 = row_sees(p, tok0 + KH * half + 32, mt.L - 1 - shift, mt.base, mask);
-                }
-                if ((v0 & v1) == 0xffffffffu) {
-#pragma unroll
-                    for (int i = 0; i < KH; ++i) x[i] = __uint_as_float(r[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < KH; ++i)
-                        x[i] = ((i < 32 ? v0 : v1) >> (i & 31)) & 1u ? __uint_as_float(r[i]) : -INFINITY;
-                }
-            } else if (lim >= KH) {
+            if (lim >= KH) {
 #pragma unroll
                 for (int i = 0; i < KH; ++i) x[i] = __uint_as_float(r[i]);
             } else {
@@ -1832,6 +1803,7 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
 {
     static_assert(!TC5 || (QS && CT != kE4m3 && G == 16 && (D == 64 || D == 128)),
                   "tensor-memory CTAs: query-split, bf16 or int8 caches");
+    static_assert(!MASK || !QS || CT == kI8, "masked query-split calls over bf16 caches: mask_tile_kernel");
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr int ES = CT != kBf16 ? 1 : 2;  // bytes per cached element
     const int qslots = one_q_buffer_ok(G, CT != kBf16, QS, TC5) ? p.qslots : 2;
@@ -2334,7 +2306,7 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                 tc5_softmax_warps_i8<D, MASK>(p, lay, tm, tmem, reinterpret_cast<float2 *>(comb), bound, scan, sh, wts,
                                         nslots, gen, wp, adaptive);
             else
-                tc5_softmax_warps<D, G, MASK>(p, lay, tm, tmem, comb, bound, scan, sh, wts, nslots, gen, wp, adaptive);
+                tc5_softmax_warps<D, G>(p, lay, tm, tmem, comb, bound, scan, sh, wts, nslots, gen, wp, adaptive);
         }
         named_barrier(2, 32 * tc5_consumers(CT));  // every tensor-memory access of the CTA is done
         if (warp == kTc5SoftmaxWarps) {
@@ -2760,8 +2732,9 @@ struct LaunchArgs {
 // driver takes.  A box is box_rows tokens x all parts x box_heads kv heads and
 // lands in shared memory as [kv head][part][token][RB bytes], the copy
 // swizzling the RB-byte rows (see the stage layout at Tc).
+// box_parts: the parts a box takes (0: all).
 inline bool encode_cache_map(CUtensorMap *map, const void *base, bool fp8, int D, int Hkv, int64_t rows,
-                             int box_heads, int box_rows)
+                             int box_heads, int box_rows, int box_parts)
 {
     EncodeTiledFn enc = encode_tiled_fn();
     if (!enc) {
@@ -2772,7 +2745,8 @@ inline bool encode_cache_map(CUtensorMap *map, const void *base, bool fp8, int D
     const int rb = row_bytes_smem(D, es), parts = D * es / rb;
     const cuuint64_t dims[4] = {cuuint64_t(rb / es), cuuint64_t(rows), cuuint64_t(parts), cuuint64_t(Hkv)};
     const cuuint64_t strides[3] = {cuuint64_t(Hkv) * D * es, cuuint64_t(rb), cuuint64_t(D) * es};
-    const cuuint32_t box[4] = {cuuint32_t(rb / es), cuuint32_t(box_rows), cuuint32_t(parts), cuuint32_t(box_heads)};
+    const cuuint32_t box[4] = {cuuint32_t(rb / es), cuuint32_t(box_rows), cuuint32_t(box_parts ? box_parts : parts),
+                               cuuint32_t(box_heads)};
     const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
     const CUresult r = enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                            const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -2780,7 +2754,7 @@ inline bool encode_cache_map(CUtensorMap *map, const void *base, bool fp8, int D
                            // one kv head of 8-bit codes is 64 or 128 bytes of a token's row: a longer fetch would
                            // read another head's (E4M3, 22 / 11 heads, 64 sequences of 2048: 88.2 -> 73.0 us with
                            // heads of 128, 65.9 -> 57.4 with 64; int8 chunks: DRAM reads 497 -> 344 MB)
-                           fp8 && box_heads == 1 && Hkv > 1 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                           (fp8 || (box_parts && parts == 1)) && box_heads == 1 && Hkv > 1 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
                                                             : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
@@ -2797,7 +2771,7 @@ inline bool encode_cache_map(CUtensorMap *map, const void *base, bool fp8, int D
 // most recent ones (an engine binds one k_cache / v_cache view per layer, as in
 // the nano-vllm KV-cache post, §3.2).
 inline bool cached_cache_map(CUtensorMap *map, int dev, const void *base, bool fp8, int D, int Hkv, int64_t rows,
-                             int box_heads, int box_rows)
+                             int box_heads, int box_rows, int box_parts = 0)
 {
     struct Entry {
         int dev;
@@ -2805,7 +2779,7 @@ inline bool cached_cache_map(CUtensorMap *map, int dev, const void *base, bool f
         bool fp8;
         int D, Hkv;
         int64_t rows;
-        int box_heads, box;
+        int box_heads, box, box_parts;
         CUtensorMap map;
     };
     constexpr size_t kMaxEntries = 256;
@@ -2815,14 +2789,14 @@ inline bool cached_cache_map(CUtensorMap *map, int dev, const void *base, bool f
     for (size_t i = 0; i < cache.size(); ++i) {
         const Entry &e = cache[i];
         if (e.dev == dev && e.base == base && e.fp8 == fp8 && e.D == D && e.Hkv == Hkv && e.rows == rows &&
-            e.box_heads == box_heads && e.box == box_rows) {
+            e.box_heads == box_heads && e.box == box_rows && e.box_parts == box_parts) {
             *map = e.map;
             return true;
         }
     }
-    if (!encode_cache_map(map, base, fp8, D, Hkv, rows, box_heads, box_rows)) return false;
+    if (!encode_cache_map(map, base, fp8, D, Hkv, rows, box_heads, box_rows, box_parts)) return false;
     if (cache.size() >= kMaxEntries) cache.erase(cache.begin());
-    cache.push_back(Entry{dev, base, fp8, D, Hkv, rows, box_heads, box_rows, *map});
+    cache.push_back(Entry{dev, base, fp8, D, Hkv, rows, box_heads, box_rows, box_parts, *map});
     return true;
 }
 
@@ -2950,12 +2924,18 @@ LaunchFn pick_decode_tc5(int D);          // tensor-memory query-split CTAs, 16 
 // The same families with masks (windows with sinks, trees), in pkv_mask*.cu.
 LaunchFn pick_mask(int D, int G);
 LaunchFn pick_mask_wide(int D, int G);
-LaunchFn pick_mask_qs(int D, int G);
-LaunchFn pick_mask_tc5(int D);
 LaunchFn pick_mask_fp8(int D, int G);
 LaunchFn pick_mask_i8(int D, int G);
 LaunchFn pick_mask_i8_wide(int D, int G);
 LaunchFn pick_mask_i8_tc5(int D);
+// Long runs of queries in masked calls over bf16 caches (pkv_mask_tile.cu): units of kMtKeys keys; the entries of such a
+// call, whether its lists fit a CTA, and the call (p: everything but what the entries' layout decides).
+constexpr int kMtKeys = 64;
+int32_t mask_tile_entries(int32_t num_seqs, int32_t num_rows, int32_t per_seq, int32_t tile);
+bool mask_tile_fits(int D, int32_t entries, bool ragged, int max_smem);
+pkv_status mask_tile_call(DecodeParams &p, const void *k_cache, const void *v_cache, const int32_t *cu, int32_t num_seqs,
+                          int32_t num_rows, int32_t per_seq, int32_t max_new, int32_t head_dim, uint8_t *workspace,
+                          int32_t num_workers, cudaStream_t stream);
 
 // Whether a query-split call can run on the tensor-memory CTAs: bf16 caches, entries of 128 rows
 // (16 virtual heads per block: the query heads of a kv head a power of two), 128-key tiles within one

@@ -129,6 +129,7 @@ __device__ __forceinline__ bool mbar_wait_lean(uint64_t *bar, uint32_t parity)
     return true;
 }
 
+
 // 8-byte asynchronous copy global -> shared by this thread, and an arrival on `bar` once all of the
 // thread's copies so far have landed (one of the arrivals the barrier was initialised with).
 __device__ __forceinline__ void copy_async8(void *dst, const void *src)
@@ -165,6 +166,17 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, i
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
         " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+// The same in three dimensions, without a cache policy.
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2,
+                                            uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+            "r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -325,11 +337,11 @@ __device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem,
 }
 
 // Arrive on `bar` once every tcgen05 operation this thread issued so far has completed.
-__device__ __forceinline__ void tc_commit(uint64_t *bar)
+__device__ __forceinline__ void tc_commit_at(uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void tc_commit(uint64_t *bar) { tc_commit_at(smem_u32(bar)); }
 
 // 32 consecutive columns of this thread's TMEM lane (warp w reaches lanes 32 (w % 4) .. + 31).  The wait
 // is in the same statement, so no use of r can be scheduled before the values have arrived.
