@@ -43,9 +43,10 @@ static pkv_status check_mask(const MaskArgs &m, bool tree)
     return PKV_OK;
 }
 
-// (p.len_limit is set)
+// (p.len_limit and p.toks are set)
 static void set_mask(DecodeParams &p, const MaskArgs &m)
 {
+    p.lg_toks = ilog2(p.toks);
     p.window = std::min(m.window, std::max(p.len_limit, 1));  // (one as long as the sequences sees all)
     p.sinks = std::min(m.sinks, p.len_limit);
     p.tree = m.tree;
@@ -593,6 +594,7 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
             p.max_blocks = max_blocks_per_seq;
             p.len_limit = int32_t(len_max);
             p.scale_log2 = float(double(scale) * 1.4426950408889634);
+            p.toks = kMtKeys;
             set_mask(p, *mask);
             return mask_tile_call(p, k_cache, v_cache, cu_seqlens_q, num_seqs, num_rows, new_per_seq, max_new, head_dim,
                                   wsb, num_workers, reinterpret_cast<cudaStream_t>(stream));

@@ -202,7 +202,7 @@ struct DecodeParams {
     // with j > p - window or j < sinks, and of the drafted nodes (tree not null: the tokens from a
     // sequence's position L - n on, n its new tokens) those whose bit is set in its row of tree,
     // [query rows][tree_words].  A call has a window or a tree; without a window it is INT32_MAX.
-    int32_t window, sinks;
+    int32_t window, sinks, lg_toks;          // lg_toks: log2(toks)
     int32_t seg_cost;                        // mask_tile_kernel: what a segment's list counts beside its units
     const uint32_t *tree;
     int32_t tree_words, tree_n;              // tree_n: new tokens of every sequence (0: as tree_cu says)
@@ -221,6 +221,7 @@ struct alignas(16) UnitMeta {
 constexpr int kFirst = 1;     // first unit of (b, g) in this slice
 constexpr int kLast = 2;      // last unit of (b, g) in this slice
 constexpr int kSliceEnd = 4;  // last unit of the slice
+constexpr int kWhole = 8;     // masked calls: every query of the entry sees every token of the unit
 
 // Shared-memory layout, computed the same way on the host (size) and device (offsets).
 struct CtaLayout {
@@ -389,10 +390,10 @@ __device__ __forceinline__ int32_t window_start(const DecodeParams &p, int32_t L
 
 __device__ __forceinline__ SeenUnits seen_units(const DecodeParams &p, int32_t L, int32_t cnt)
 {
-    const int32_t total = (L + p.toks - 1) / p.toks;
+    const int32_t total = (L + p.toks - 1) >> p.lg_toks;
     SeenUnits s;
-    s.head = (min(p.sinks, L) + p.toks - 1) / p.toks;
-    s.skip = max(window_start(p, L, cnt) / p.toks - s.head, 0);
+    s.head = (min(p.sinks, L) + p.toks - 1) >> p.lg_toks;
+    s.skip = max((window_start(p, L, cnt) >> p.lg_toks) - s.head, 0);
     s.n = total - s.skip;
     return s;
 }
@@ -668,8 +669,8 @@ __device__ __forceinline__ uint32_t f16x2_sat(float lo, float hi)
 // tile's first) below it count for the thread's row of half hr (the causal
 // bound of its query); TAIL: tokens from `valid` on are not the sequence's
 // (their rows may hold anything, even NaN), so their V values are zeroed
-// before the product.  MASK: lim[hr] has a bit for each token that the row sees, valid one for each that
-// some row of the entry sees.  E4M3 caches run the products in f16 (every E4M3 value
+// before the product.  MASK: every row sees the whole tile, or (TAIL) lim[hr] has a bit for each token that
+// the row sees, valid one for each that some row of the entry sees.  E4M3 caches run the products in f16 (every E4M3 value
 // is exact in f16, and so is every bf16 query element of magnitude
 // 2^-14 .. 65504; smaller ones keep f16's subnormal steps of 2^-24, larger
 // ones saturate at 65504); the kv head's K scale is in ksc, its V scale is
@@ -742,7 +743,7 @@ __device__ __forceinline__ void attend_tile(uint32_t kb, uint32_t vb,
                     float sum = sa[st][0][nt][2 * hr + e];
                     if constexpr (CH == 2) sum += sa[st][1][nt][2 * hr + e];
                     const int t = 16 * st + 8 * nt + 2 * r4 + e;
-                    x[hr][k] = (MASK ? (lim[hr] >> t) & 1 : t < lim[hr]) ? sum * ksc : -INFINITY;
+                    x[hr][k] = (MASK ? !TAIL || ((lim[hr] >> t) & 1) : t < lim[hr]) ? sum * ksc : -INFINITY;
                 }
     float mx[HR];
     bool grow = false;
@@ -2149,7 +2150,7 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                 // fused store: the cache row of the sequence's new token (position L - 1), if this unit
                 // holds it (-1 where its block id was rejected)
                 int32_t newrow = -1;
-                const int32_t u0 = iw.u * p.toks;
+                const int32_t u0 = tu * p.toks;
                 if (p.k_new && len - 1 >= u0 && len - 1 < u0 + p.toks) {
                     const int32_t off = len - 1 - u0;
                     const int32_t rb = __shfl_sync(kFull, row, off >> (__ffs(p.boxtok) - 1));
@@ -2170,6 +2171,7 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                     mt.newrow = newrow;
                     if constexpr (MASK) mt.tu = tu;
                     if constexpr (MASK) mt.base = base;
+                    if constexpr (MASK) mt.flags |= all_see(p, u0, p.toks, len, cnt, base) ? kWhole : 0;
                     if constexpr (TC5 && CT == kI8) mt.row0 = row0;
                     if constexpr (TC5) mbar_arrive(&mready[s]);  // the meta, for a look ahead
                     // TC5: full[s] counts the K half only; the V half has barriers of its own
@@ -2439,7 +2441,8 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
         const int tok0 = (MASK ? mt.tu : mt.u) * p.toks + jt * TC::TW;
         // tokens of the tile (masked calls: a bit for each that some query of the entry sees)
         constexpr int kAll = MASK ? int(0xffffffffu >> (32 - TC::TW)) : TC::TW;
-        const int valid = MASK ? int(entry_sees(p, tok0, mt.L, mt.cnt)) & kAll : min(TC::TW, mt.L - tok0);
+        const bool whole = MASK && (mt.flags & kWhole) != 0;
+        const int valid = !MASK ? min(TC::TW, mt.L - tok0) : whole ? kAll : int(entry_sees(p, tok0, mt.L, mt.cnt)) & kAll;
         if ((MASK ? valid != 0 : valid > 0) && nvh > 0) {
             const uint32_t kb = stage_addr + uint32_t(s) * lay.stage_bytes;
             if constexpr (!QS && CT != kI8) {
@@ -2468,8 +2471,9 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                 }
             }
             int lim[HR];
+            bool all = !MASK && valid == kAll;  // no tail to the tile
             if constexpr (MASK) {
-                const bool all = all_see(p, tok0, TC::TW, mt.L, mt.cnt, mt.base);
+                all = whole || all_see(p, tok0, TC::TW, mt.L, mt.cnt, mt.base);
 #pragma unroll
                 for (int hr = 0; hr < HR; ++hr) {
                     lim[hr] = kAll;
@@ -2506,13 +2510,13 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                             i8_zero_log(sct[st], sct[st ^ 1].plain && has(st ^ 1) ? sct[st ^ 1].lv
                                                                                                       : kZeroLog);
                 }
-                if (valid == kAll && plain)
+                if (all && plain)
                     attend_tile_i8<D, TC::HR, false, MASK>(kb, kb + lay.kv_bytes, off, qa, rowf, qb, sct, lim, valid, m, l, o,
                                                      lane);
                 else
                     attend_tile_i8<D, TC::HR, true, MASK>(kb, kb + lay.kv_bytes, off, qa, rowf, qb, sct, lim, valid, m, l, o,
                                                     lane);
-            } else if (valid == kAll)
+            } else if (all)
                 attend_tile<D, CT, QS, TC::HR, false, MASK>(kb, kb + lay.kv_bytes, off, qa, ksc, lim, valid, m, l, o, lane);
             else
                 attend_tile<D, CT, QS, TC::HR, true, MASK>(kb, kb + lay.kv_bytes, off, qa, ksc, lim, valid, m, l, o, lane);

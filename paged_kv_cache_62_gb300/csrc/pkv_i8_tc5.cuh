@@ -452,7 +452,10 @@ __device__ void tc5_softmax_warps_i8(const DecodeParams &p, const CtaLayout &lay
                 uint32_t vis[MASK ? kTc5Keys / 32 : 1] = {};
                 if constexpr (MASK) {
                     const uint32_t *mask = p.tree ? p.tree + (long long)(mt.row0 + qi) * p.tree_words : nullptr;
-                    if (row_ok) {
+                    if (row_ok && (mt.flags & kWhole)) {
+#pragma unroll
+                        for (int i = 0; i < kTc5Keys / 32; ++i) vis[i] = 0xffffffffu;
+                    } else if (row_ok) {
 #pragma unroll 1
                         for (int w = 0; w < kTc5Keys / 32; ++w) {
                             const uint32_t v = row_sees(p, tok0 + 32 * w, mt.L - 1 - shift, mt.base, mask);

@@ -140,7 +140,7 @@ __device__ __forceinline__ void attend_tile_i8(uint32_t kb, uint32_t vb, const L
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int t = 16 * st + 8 * nt + 2 * r4 + e;
-                    x[hr][4 * st + 2 * nt + e] = (MASK ? (lim[hr] >> t) & 1 : t < lim[hr])
+                    x[hr][4 * st + 2 * nt + e] = (MASK ? !TAIL || ((lim[hr] >> t) & 1) : t < lim[hr])
                                                      ? fmaf(sa[st][nt][2 * hr + e], f, sc[st].lv)
                                                      : -INFINITY;
                 }

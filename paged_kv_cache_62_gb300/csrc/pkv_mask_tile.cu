@@ -1077,7 +1077,6 @@ pkv_status mask_tile_call(DecodeParams &p, const void *k_cache, const void *v_ca
     p.hg = 1;
     p.nhg = p.Hkv;
     p.sub = team_warps(16);
-    p.toks = kMtKeys;
     p.boxtok = std::min(kMtKeys, p.bs);
     p.nbox = kMtKeys / p.boxtok;
     p.lg_nbox = ilog2(p.nbox);

@@ -17,12 +17,9 @@
 // its eight cosines and sines stay in registers for all heads.  16384 rows of 16 + 2 x 8 heads of 128 on three axes,
 // 269 MB: 47.1 us = 5.7 TB/s, 0.84 of the copy rate (a CTA a token group with a barrier after the cosines: 61 us);
 // 64 rows: 3.1 us, a launch and two dependent loads.
-//
-// With a norm (NORM), a q or k head x becomes x / sqrt(mean x^2 + eps) * w before the turn: the D / 16 lanes that
-// hold a head add up their squares with shuffles, and the row's factor and the weights join the turn's products, so
-// the head makes no second trip through registers.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "pkv_device.cuh"
 #include "pkv_host.h"
@@ -39,8 +36,6 @@ struct RopeParams {
     const float *inv_freq;
     int32_t axes, T, Hq, Hkv, D, rot, parts;
     long long num_slots;
-    const float *qw, *kw;  // NORM: weights of a q and a k head (null: ones)
-    float eps;
     int32_t *err;
 };
 
@@ -104,71 +99,9 @@ __device__ __forceinline__ void turn16(uint4 &a, uint4 &b, const float2 *cs)
     b = make_uint4(ub[0], ub[1], ub[2], ub[3]);
 }
 
-// The same for a head that is normed first: a and b times r and the weights at wa and wb (null: ones); turned or not.
-template <bool ADJ>
-__device__ __forceinline__ void norm_turn16(uint4 &a, uint4 &b, const float2 *cs, bool turn, float r, const float *wa,
-                                            const float *wb)
-{
-    const uint32_t ua[4] = {a.x, a.y, a.z, a.w}, ub[4] = {b.x, b.y, b.z, b.w};
-    float x[8], y[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[2 * j] = __uint_as_float(ua[j] << 16) * r;
-        x[2 * j + 1] = __uint_as_float(ua[j] & 0xffff0000u) * r;
-        y[2 * j] = __uint_as_float(ub[j] << 16) * r;
-        y[2 * j + 1] = __uint_as_float(ub[j] & 0xffff0000u) * r;
-    }
-    if (wa) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float4 u = __ldg(reinterpret_cast<const float4 *>(wa) + j);
-            const float4 v = __ldg(reinterpret_cast<const float4 *>(wb) + j);
-            x[4 * j] *= u.x;
-            x[4 * j + 1] *= u.y;
-            x[4 * j + 2] *= u.z;
-            x[4 * j + 3] *= u.w;
-            y[4 * j] *= v.x;
-            y[4 * j + 1] *= v.y;
-            y[4 * j + 2] *= v.z;
-            y[4 * j + 3] *= v.w;
-        }
-    }
-    if (turn) {
-#pragma unroll
-        for (int e = 0; e < (ADJ ? 4 : 8); ++e) {
-            if constexpr (ADJ) {
-                const float p = x[2 * e], q = y[2 * e];
-                x[2 * e] = p * cs[e].x - x[2 * e + 1] * cs[e].y;
-                x[2 * e + 1] = x[2 * e + 1] * cs[e].x + p * cs[e].y;
-                y[2 * e] = q * cs[4 + e].x - y[2 * e + 1] * cs[4 + e].y;
-                y[2 * e + 1] = y[2 * e + 1] * cs[4 + e].x + q * cs[4 + e].y;
-            } else {
-                const float p = x[e];
-                x[e] = p * cs[e].x - y[e] * cs[e].y;
-                y[e] = y[e] * cs[e].x + p * cs[e].y;
-            }
-        }
-    }
-    a = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-    b = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-}
-
-__device__ __forceinline__ float squares(uint4 a)
-{
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float lo = __uint_as_float(u[j] << 16), hi = __uint_as_float(u[j] & 0xffff0000u);
-        s0 = fmaf(lo, lo, s0);
-        s1 = fmaf(hi, hi, s1);
-    }
-    return s0 + s1;
-}
-
 constexpr int kRopeWarps = 2;  // warps (token parts) a CTA: small ones, whose last warp holds little back
 
-template <bool ADJ, bool NORM>
+template <bool ADJ>
 __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams p)
 {
     __shared__ __align__(16) float2 cs_all[kRopeWarps][kRopeMaxHalf];
@@ -209,7 +142,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams 
     // a turning piece of pairs of halves lies in two places of the head
     auto d0 = [&](int h) { return c < turned && !ADJ && h < turning ? 8 * c : 16 * c; };
     auto d1 = [&](int h) { return c < turned && !ADJ && h < turning ? half + 8 * c : 16 * c + 8; };
-    uint4 a[B] = {}, b[B] = {};
+    uint4 a[B], b[B];
     auto load = [&](int h0) {
 #pragma unroll
         for (int k = 0; k < B; ++k) {
@@ -238,41 +171,14 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams 
 #pragma unroll
         for (int e = 0; e < 8; ++e) mycs[e] = cs[8 * c + e];
     }
-    const bool pow2 = (per & (per - 1)) == 0;
-    for (int h1 = h0; NORM ? h1 - hl < heads : h1 < heads; h1 += step) {  // (NORM: the lanes stay together)
-        float rs[B];
-        if constexpr (NORM) {
-            float ss[B];
-#pragma unroll
-            for (int k = 0; k < B; ++k) ss[k] = squares(a[k]) + squares(b[k]);
-            if (pow2) {
-                for (int o = 1; o < per; o <<= 1)
-#pragma unroll
-                    for (int k = 0; k < B; ++k) ss[k] += __shfl_xor_sync(kFull, ss[k], o);
-            } else {
-                float all[B] = {};
-                for (int i = 0; i < per; ++i)
-#pragma unroll
-                    for (int k = 0; k < B; ++k) all[k] += __shfl_sync(kFull, ss[k], hl * per + i);
-#pragma unroll
-                for (int k = 0; k < B; ++k) ss[k] = all[k];
-            }
-#pragma unroll
-            for (int k = 0; k < B; ++k) rs[k] = rsqrtf(fmaf(ss[k], 1.0f / float(p.D), p.eps));
-        }
+    for (int h1 = h0; h1 < heads; h1 += step) {
 #pragma unroll
         for (int k = 0; k < B; ++k) {
             const int h = h1 + k * hpw * p.parts;
             const uint16_t *src;
             uint16_t *dst;
             if (place(h, src, dst)) {
-                if constexpr (NORM) {
-                    if (h < turning) {
-                        const float *w = h < p.Hq ? p.qw : p.kw;
-                        norm_turn16<ADJ>(a[k], b[k], mycs, c < turned, rs[k], w ? w + d0(h) : nullptr, w + d1(h));
-                    }
-                } else if (c < turned && h < turning)
-                    turn16<ADJ>(a[k], b[k], mycs);
+                if (c < turned && h < turning) turn16<ADJ>(a[k], b[k], mycs);
                 *reinterpret_cast<uint4 *>(dst + d0(h)) = a[k];
                 *reinterpret_cast<uint4 *>(dst + d1(h)) = b[k];
             }
@@ -281,25 +187,265 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams 
     }
 }
 
-static pkv_status rope_call(RopeParams &p, int interleaved, pkv_stream_t stream, bool norm = false)
+// ------------------------------------------------------------------ with a norm
+// A q or k head x becomes x / sqrt(mean x^2 + eps) * w before the turn; the layout is the one above, the D / 16 lanes of
+// a head add up their squares with shuffles.  Memory-bound in principle; what stands between is the warps that registers
+// leave room for and the instructions a piece takes.  So cosines and sines stay in shared memory and weights in the
+// nearest cache, a lane has two pieces in flight, products are two to an instruction (f32x2), offsets have 32 bits, and
+// the common head sizes have instances of their own (PER).  16384 rows of 16 + 2 x 8 heads of 128, 269 MB: 48.7 us = 5.5 TB/s,
+// 0.81 of the copy rate; on the way there: the kernel above with factors in registers and three pieces in flight 73 us
+// (168 registers a thread), with weights from memory 62.6 us, rows through shared memory by bulk copies 58 us (16 warps
+// an SM), two products an instruction 52.3 us.  64 rows: 3.3 us.
+constexpr int kNormPieces = 2;  // pieces of a lane in flight (1: 48.8-50.4 us, 3: 49.6-57 us)
+// CTAs an SM that registers have to leave room for: 12 for pairs of halves (8: 49.5 us, 14: 51.5 us); pairs of
+// neighbours and unusual head sizes take more registers (1531 rows of 14 + 2 heads of 80: 5.9 us, with 12 7.7 us).
+__host__ __device__ constexpr int norm_ctas(bool adj, int per) { return adj || per == 0 ? 8 : 12; }
+
+// Two floats in one register pair.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 f32x2_parts(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack8(uint4 v, uint64_t (&x)[4])
+{
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = f32x2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
+}
+__device__ __forceinline__ uint4 pack8(const uint64_t (&x)[4])
+{
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = f32x2_parts(x[j]);
+        u[j] = pack_bf16x2(f.x, f.y);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+struct NormParams {
+    RopeParams r;
+    const float *qw, *kw;  // [D] or null: ones
+    float eps;
+};
+
+// PER: 16-dim pieces of a head (0: p.D / 16, any number).
+template <bool ADJ, int PER>
+__global__ void __launch_bounds__(32 * kRopeWarps, norm_ctas(ADJ, PER)) norm_rope_kernel(const __grid_constant__ NormParams np)
+{
+    // pairs of halves: cosines, then sines; of neighbours: (cos, cos) and (-sin, sin) of each
+    __shared__ __align__(16) float cs_all[kRopeWarps][(ADJ ? 4 : 2) * kRopeMaxHalf];
+    const RopeParams &p = np.r;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t wi = int64_t(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5);
+    const int t = int(wi / p.parts), part = int(wi - int64_t(t) * p.parts);
+    if (t >= p.T) return;  // warps do not meet after this
+    float *cs = cs_all[threadIdx.x >> 5];
+    const int D = PER ? 16 * PER : p.D;
+    const int half = p.rot >> 1, per = PER ? PER : p.D >> 4, turned = p.rot >> 4;  // 16-dim pieces of a head, those that turn
+    const int hpw = 32 / per;                                           // heads a step takes
+    const int hl = lane / per, c = lane - hl * per;                     // the lane's head of a step, its piece
+    const int heads = p.Hq + p.Hkv + (p.v ? p.Hkv : 0), turning = p.Hq + p.Hkv;
+    const bool mine = PER != 0 || hl < hpw, turn = c < turned, pow2 = (per & (per - 1)) == 0;
+    const int64_t slot = p.slots ? int64_t(__ldg(p.slots + t)) : int64_t(t);
+    const bool drop = p.slots && (slot < 0 || slot >= p.num_slots);
+    if (p.slots && (slot < -1 || slot >= p.num_slots) && lane == 0) flag_error(p.err, PKV_ERR_SLOT_RANGE);
+    // the lane's dims of a head: a turning piece of pairs of halves lies in two places (v heads do not turn, but move the
+    // same way)
+    const int e0 = turn && !ADJ ? 8 * c : 16 * c, e1 = turn && !ADJ ? half + 8 * c : 16 * c + 8;
+    // (from every row's place as if it were the first of the token's heads: head h is h D on from there; a token's heads
+    // have less than 2^30 elements)
+    const uint16_t *qs = p.q + t * p.q_stride, *ks = p.k + t * p.k_stride - p.Hq * D, *vs = p.v + t * p.v_stride - turning * D;
+    uint16_t *qd = p.q_out + t * p.qo_stride, *kd = p.k_out + slot * p.ko_stride - p.Hq * D,
+             *vd = p.v_out + slot * p.vo_stride - turning * D;
+    const int last = mine ? (drop ? p.Hq : heads) : 0;  // the lane's heads with something to write end here
+    auto load = [&](int h, uint4 &a, uint4 &b) {
+        if (h >= last) return;
+        const uint16_t *src = (h < p.Hq ? qs : h < turning ? ks : vs) + h * D;
+        a = *reinterpret_cast<const uint4 *>(src + e0);
+        b = *reinterpret_cast<const uint4 *>(src + e1);
+    };
+    const int step = hpw * p.parts;
+    int h = part * hpw + hl;
+    uint4 a[kNormPieces] = {}, b[kNormPieces] = {};
+#pragma unroll
+    for (int k = 0; k < kNormPieces; ++k) load(h + k * step, a[k], b[k]);
+    for (int i = lane; i < half; i += 32) {
+        int ax = p.freq_axis ? __ldg(p.freq_axis + i) : 0;
+        if (ax < 0 || ax >= p.axes) {
+            flag_error(p.err, PKV_ERR_AXIS_RANGE);
+            ax = 0;
+        }
+        const float2 v = turn_cos_sin(turn_fraction(__ldg(p.inv_freq + i)), __ldg(p.positions + int64_t(ax) * p.T + t));
+        if constexpr (ADJ) {
+            *reinterpret_cast<float2 *>(cs + 2 * i) = make_float2(v.x, v.x);
+            *reinterpret_cast<float2 *>(cs + 2 * kRopeMaxHalf + 2 * i) = make_float2(-v.y, v.y);
+        } else {
+            cs[i] = v.x;
+            cs[kRopeMaxHalf + i] = v.y;
+        }
+    }
+    __syncwarp();
+    const float invd = 1.0f / float(D);
+    // a piece at head g: normed, turned, stored; its registers take the piece kNormPieces steps on meanwhile
+    auto piece = [&](int g, uint4 &ra, uint4 &rb) {
+        uint64_t x[4], y[4];
+        const uint4 va = ra, vb = rb;
+        unpack8(va, x);
+        unpack8(vb, y);
+        load(g + kNormPieces * step, ra, rb);
+        uint64_t s2 = mul2(x[0], x[0]), t2 = mul2(y[0], y[0]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j) {
+            s2 = fma2(x[j], x[j], s2);
+            t2 = fma2(y[j], y[j], t2);
+        }
+        const float2 sp = f32x2_parts(s2), tp = f32x2_parts(t2);
+        float ss = (sp.x + sp.y) + (tp.x + tp.y);
+        if (PER != 0 || pow2) {
+#pragma unroll
+            for (int o = 1; o < per; o <<= 1) ss += __shfl_xor_sync(kFull, ss, o);
+        } else {
+            float all = 0.f;
+            for (int i = 0; i < per; ++i) all += __shfl_sync(kFull, ss, hl * per + i);
+            ss = all;
+        }
+        if (g >= last) return;
+        uint16_t *dst = (g < p.Hq ? qd : g < turning ? kd : vd) + g * D;
+        if (g >= turning) {
+            *reinterpret_cast<uint4 *>(dst + e0) = va;
+            *reinterpret_cast<uint4 *>(dst + e1) = vb;
+            return;
+        }
+        const float r = rsqrtf(fmaf(ss, invd, np.eps));
+        const uint64_t r2 = f32x2(r, r);
+        const float *w = g < p.Hq ? np.qw : np.kw;
+        auto scale = [&](uint64_t (&z)[4], int e) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint64_t w0 = r2, w1 = r2;
+                if (w) {
+                    const ulonglong2 u = __ldg(reinterpret_cast<const ulonglong2 *>(w + e) + j);
+                    w0 = mul2(u.x, r2);
+                    w1 = mul2(u.y, r2);
+                }
+                z[2 * j] = mul2(z[2 * j], w0);
+                z[2 * j + 1] = mul2(z[2 * j + 1], w1);
+            }
+        };
+        scale(x, e0);
+        scale(y, e1);
+        if (turn) {
+            if constexpr (ADJ) {
+                auto turn4 = [&](uint64_t (&z)[4], int f) {  // frequencies f .. f + 3
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const ulonglong2 cc = *(reinterpret_cast<const ulonglong2 *>(cs + 2 * f) + j);
+                        const ulonglong2 sn = *(reinterpret_cast<const ulonglong2 *>(cs + 2 * kRopeMaxHalf + 2 * f) + j);
+                        const float2 z0 = f32x2_parts(z[2 * j]), z1 = f32x2_parts(z[2 * j + 1]);
+                        z[2 * j] = fma2(z[2 * j], cc.x, mul2(f32x2(z0.y, z0.x), sn.x));
+                        z[2 * j + 1] = fma2(z[2 * j + 1], cc.y, mul2(f32x2(z1.y, z1.x), sn.y));
+                    }
+                };
+                turn4(x, 8 * c);
+                turn4(y, 8 * c + 4);
+            } else {
+                constexpr uint64_t kMinus = 0x8000000080000000ull;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const ulonglong2 cc = *(reinterpret_cast<const ulonglong2 *>(cs + 8 * c) + j);
+                    const ulonglong2 sn = *(reinterpret_cast<const ulonglong2 *>(cs + kRopeMaxHalf + 8 * c) + j);
+                    uint64_t u = x[2 * j];
+                    x[2 * j] = fma2(u, cc.x, mul2(y[2 * j], sn.x) ^ kMinus);
+                    y[2 * j] = fma2(y[2 * j], cc.x, mul2(u, sn.x));
+                    u = x[2 * j + 1];
+                    x[2 * j + 1] = fma2(u, cc.y, mul2(y[2 * j + 1], sn.y) ^ kMinus);
+                    y[2 * j + 1] = fma2(y[2 * j + 1], cc.y, mul2(u, sn.y));
+                }
+            }
+        }
+        *reinterpret_cast<uint4 *>(dst + e0) = pack8(x);
+        *reinterpret_cast<uint4 *>(dst + e1) = pack8(y);
+    };
+    // (the lanes stay together: they add up across a head)
+    for (; h - hl < heads; h += kNormPieces * step)
+#pragma unroll
+        for (int k = 0; k < kNormPieces; ++k)
+            if (h + k * step - hl < heads) piece(h + k * step, a[k], b[k]);
+}
+
+// Warps a token.  Few tokens: several, each with a part of the heads (as many as leave every lane a piece), until the SMs
+// have eight warps each.
+static int rope_parts(const RopeParams &p, int sm_count)
+{
+    const int heads = p.Hq + p.Hkv + (p.v ? p.Hkv : 0), hpw = 32 / (p.D / 16);
+    const int most = (heads + hpw - 1) / hpw;
+    return int(std::min<int64_t>(most, std::max<int64_t>(1, int64_t(sm_count) * 8 / p.T)));
+}
+
+static pkv_status rope_call(RopeParams &p, int interleaved, pkv_stream_t stream)
 {
     DeviceInfo dev;
     if (!current_device_info(&dev)) return PKV_ECUDA;
-    // few tokens: several warps a token, each with a part of the heads (as many as leave every lane a piece), until
-    // the SMs have eight warps each
-    const int heads = p.Hq + p.Hkv + (p.v ? p.Hkv : 0), hpw = 32 / (p.D / 16);
-    const int most = (heads + hpw - 1) / hpw;
-    p.parts = int(std::min<int64_t>(most, std::max<int64_t>(1, int64_t(dev.sm_count) * 8 / p.T)));
+    p.parts = rope_parts(p, dev.sm_count);
     const int64_t grid = (int64_t(p.T) * p.parts + kRopeWarps - 1) / kRopeWarps;
-    auto kern = norm ? (interleaved ? rope_kernel<true, true> : rope_kernel<false, true>)
-                     : (interleaved ? rope_kernel<true, false> : rope_kernel<false, false>);
-    const cudaError_t e = launch_pdl(kern, dim3(unsigned(grid)), dim3(32 * kRopeWarps), 0,
-                                     reinterpret_cast<cudaStream_t>(stream), p);
+    const cudaError_t e = launch_pdl(interleaved ? rope_kernel<true> : rope_kernel<false>, dim3(unsigned(grid)),
+                                     dim3(32 * kRopeWarps), 0, reinterpret_cast<cudaStream_t>(stream), p);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return cuda_fail("rope_kernel launch", e);
     }
     return launch_status("rope_kernel launch");
+}
+
+// The norm of a call that has one.
+struct Norm {
+    const float *qw, *kw;
+    float eps;
+};
+
+static pkv_status norm_call(const RopeParams &r, const Norm &n, int interleaved, pkv_stream_t stream)
+{
+    DeviceInfo dev;
+    if (!current_device_info(&dev)) return PKV_ECUDA;
+    NormParams np{r, n.qw, n.kw, n.eps};
+    RopeParams &p = np.r;
+    p.parts = rope_parts(p, dev.sm_count);
+    const int64_t grid = (int64_t(p.T) * p.parts + kRopeWarps - 1) / kRopeWarps;
+    auto pick = [&](auto adj) {
+        constexpr bool ADJ = decltype(adj)::value;
+        return p.D == 128  ? norm_rope_kernel<ADJ, 8>
+               : p.D == 64 ? norm_rope_kernel<ADJ, 4> : p.D == 256 ? norm_rope_kernel<ADJ, 16> : norm_rope_kernel<ADJ, 0>;
+    };
+    const cudaError_t e = launch_pdl(interleaved ? pick(std::true_type{}) : pick(std::false_type{}), dim3(unsigned(grid)),
+                                     dim3(32 * kRopeWarps), 0, reinterpret_cast<cudaStream_t>(stream), np);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return cuda_fail("norm_rope_kernel launch", e);
+    }
+    return launch_status("norm_rope_kernel launch");
 }
 
 // Checks shared by the two entry points; the sizes are nonnegative afterwards.
@@ -326,12 +472,6 @@ static pkv_status rope_check(const uint16_t *q, int64_t q_stride, const uint16_t
 }  // namespace pkv
 
 using namespace pkv;
-
-// The norm of a call that has one.
-struct Norm {
-    const float *qw, *kw;
-    float eps;
-};
 
 static bool norm_ok(const Norm &n)
 {
@@ -369,12 +509,8 @@ static pkv_status rope_impl(const Norm *norm, const uint16_t *q, int64_t q_strid
     p.D = head_dim;
     p.rot = rot_dim;
     p.err = err_word;
-    if (norm) {
-        p.qw = norm->qw;
-        p.kw = norm->kw;
-        p.eps = norm->eps;
-    }
-    return rope_call(p, interleaved, stream, norm != nullptr);
+    if (norm) return norm_call(p, *norm, interleaved, stream);
+    return rope_call(p, interleaved, stream);
 }
 
 static pkv_status rope_store_impl(const Norm *norm, const uint16_t *q, int64_t q_stride, const uint16_t *k,
@@ -418,12 +554,8 @@ static pkv_status rope_store_impl(const Norm *norm, const uint16_t *q, int64_t q
     p.rot = rot_dim;
     p.num_slots = int64_t(num_blocks) * block_size;
     p.err = err_word;
-    if (norm) {
-        p.qw = norm->qw;
-        p.kw = norm->kw;
-        p.eps = norm->eps;
-    }
-    return rope_call(p, interleaved, stream, norm != nullptr);
+    if (norm) return norm_call(p, *norm, interleaved, stream);
+    return rope_call(p, interleaved, stream);
 }
 
 extern "C" pkv_status pkv_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
