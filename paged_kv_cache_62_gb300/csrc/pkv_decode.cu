@@ -529,7 +529,7 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     // the CTA's warps split the K/V tokens, as in decode.  Longer runs of new tokens go to query-split
     // CTAs, whose warps split an entry of up to 8 * qg queries and share every K/V tile.
     const int32_t qg = qs_queries(num_q_heads, num_kv_heads);
-    if (new_per_seq > 1 && new_per_seq <= qg)
+    if (new_per_seq > (mask ? 0 : 1) && new_per_seq <= qg)
         // every sequence's n new tokens share its K/V stream: read once, n * G virtual heads
         return decode_call(ct, false, new_per_seq, q, k_cache, v_cache, nullptr, nullptr, nullptr, nullptr,
                            block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads, num_kv_heads,
@@ -542,7 +542,10 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     // (Query-split int8 entries, and those of masked calls, fill the tensor-memory tile: as many whole queries as 128
     // rows hold.)
     const int32_t tile = 128 / std::min(num_q_heads / num_kv_heads, 128);
-    bool qs = int64_t(num_rows) > 2 * int64_t(qg) * num_seqs;
+    // (Masked calls over bf16 caches: mask_tile_kernel reads the keys once, at any number of new tokens.  64 sequences of
+    // 512-4096, 16 / 8 heads of 128: 12 nodes each 115 us against 224 on regular CTAs, 1 to 4 nodes 105 against 112; two
+    // sequences of 9 nodes 38 against 159; 256 sequences of 50-300 with 1 to 4 nodes 63 against 54.)
+    bool qs = (mask && ct == kBf16) || int64_t(num_rows) > 2 * int64_t(qg) * num_seqs;
     if (ct == kI8 && !qs && int64_t(num_rows) > int64_t(qg) * num_seqs) {
         // Between one and two chunks a sequence: regular CTAs read the keys twice, but take larger calls as fast; in
         // calls of few tiles their list, one entry a row, most of them empty, costs more (16 new tokens, 16 / 8 heads

@@ -26,6 +26,8 @@
 // a segment that lies in several slices are merged by the CTA that completes it.  The slices, and with them the sums'
 // order, depend on the list and the grid alone: the results repeat bit for bit.  The copying warp walks the list and
 // hands each segment to the others in shared memory (MtDesc), the next one before it copies the last unit of this one.
+// Calls of few segments, whose pieces are many, leave them to a second kernel (mask_merge_kernel): one CTA's merge goes
+// through a segment's pieces one after another.
 #include "pkv_decode_kernel.cuh"
 
 namespace pkv {
@@ -43,6 +45,8 @@ constexpr int kMtMinSlice = 4;
 constexpr int kMtSegCost = 4;
 // A slice's bound this near to a segment's start or end, in units, moves there: no piece to merge.
 constexpr int kMtSnap = 8;
+// Pieces a segment (CTAs over segments) from which on a second kernel merges them.
+constexpr int kMtSplit = 4;
 
 struct TileParams {
     DecodeParams p;       // B: entries, context_lens: by sequence, nst: ring slots, seg_cost, num_workers unused
@@ -51,12 +55,14 @@ struct TileParams {
     int32_t tile;         // queries of an entry
     int32_t per_entry;    // null cu: entries of a sequence
     int32_t max_new;
+    int32_t split;        // pieces are left to mask_merge_kernel
 };
 
 // A segment's part in the CTA's slice, as the softmax warps and the issuing one see it: units u .. u + len - 1 of the n
-// of entry b and kv head g (len 0: no more), the segment's start in the list, and what its entry says.
+// of entry b and kv head g (len 0: no more), the segment's start in the list, whether it is the
+// slice's first (see tc5_piece_tile), and what its entry says.
 struct alignas(16) MtDesc {
-    int32_t b, g, u, n, len, x0, L, cnt, row0, base;
+    int32_t b, g, u, n, len, x0, first, L, cnt, row0, base;
 };
 
 struct MtLayout {
@@ -216,6 +222,16 @@ struct MtSlices {
     float inv;
 };
 
+// One slice a CTA, none much shorter than kMtMinSlice.
+__device__ __forceinline__ MtSlices mt_slices(const DecodeParams &p, int32_t T, int ctas)
+{
+    MtSlices q{T, min(ctas, max(1, T / (kMtMinSlice + p.seg_cost))), 0, 0, 0.f};
+    q.each = T / q.nsl;
+    q.rest = T - q.each * q.nsl;
+    q.inv = 1.0f / float(q.nsl);
+    return q;
+}
+
 // Where slice i begins (i = nsl: the list's end).
 __device__ __forceinline__ int32_t mt_bound(const DecodeParams &p, const int32_t *scan, const MtSlices &q, int i)
 {
@@ -297,8 +313,8 @@ __device__ __forceinline__ void mt_output(float l, uint32_t o, uint16_t *out)
 // left join the row's own state (m, l):
 //     M = max m_i,  l = sum 2^(m_i - M) l_i,  out = sum 2^(m_i - M) acc_i / l,
 // summed in slice order, products rounded before they are added: the result does not depend on which piece came last.
-// (With one other piece, the usual case, a sum of two: the other's loads go out a step of 32 columns ahead, the first
-// before its (m, l) are looked at.)
+// Every load is a trip to the other pieces' SMs' side of L2 and nothing else hides it, so (m, l) come four pieces at a
+// time and sums, 32 columns a step, a piece ahead.
 template <int D>
 __device__ __forceinline__ void mt_merge(const DecodeParams &p, const int32_t *bound, int sf, int sl, int own, int32_t x0,
                                          int g, int b, int row, float m, float l, uint32_t o, uint16_t *out)
@@ -310,70 +326,71 @@ __device__ __forceinline__ void mt_merge(const DecodeParams &p, const int32_t *b
         return sk;
     };
     auto tile_of = [&](int sk) { return tc5_piece_tile(p, sk, x0 <= bound[sk], b, g); };
-    auto state = [&](int sk) { return sk == own ? make_float2(m, l) : __ldcg(ml + tile_of(sk) * 128 + row); };
+    auto state = [&](int sk) { return sk == own || sk > sl ? make_float2(m, l) : __ldcg(ml + tile_of(sk) * 128 + row); };
     const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
-    const int s0 = next(sf - 1), s1 = next(s0);
-    const bool two = next(s1) > sl;
-    const float4 *src = nullptr;  // of the piece at hand
-    auto seek = [&](int sk) { src = reinterpret_cast<const float4 *>(p.ws_acc + tile_of(sk) * 128 * D) + row; };
-    auto load = [&](float4 (&v)[8], int c0) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __ldcg(src + (c0 / 4 + j) * 128);
+    const int s0 = next(sf - 1);
+    struct Piece {
+        float4 v[8];
+        float2 st;
     };
-    float4 v[8], ahead[8];
-    if (two) {
-        seek(s0 == own ? s1 : s0);
-        load(v, 0);
-    }
+    // piece sk's columns c0 .. c0 + 31 (the own one's stay in tensor memory until they are due)
+    auto load = [&](Piece &q, int sk, int c0) {
+        q.st = state(sk);
+        if (sk == own) return;
+        const float4 *src = reinterpret_cast<const float4 *>(p.ws_acc + tile_of(sk) * 128 * D) + row;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q.v[j] = __ldcg(src + (c0 / 4 + j) * 128);
+    };
+    Piece q, ahead;
+    load(q, s0, 0);
     float M = -INFINITY, L = 0.f;
 #pragma unroll 1
-    for (int sk = s0; sk <= sl; sk = next(sk)) M = fmaxf(M, state(sk).x);
-    const float at = M == -INFINITY ? 0.f : M;
-#pragma unroll 1
-    for (int sk = s0; sk <= sl; sk = next(sk)) {
-        const float2 st = state(sk);
-        L = __fadd_rn(L, __fmul_rn(ex2(st.x - at), st.y));
+    for (int sk = s0; sk <= sl;) {
+        float2 st[4];
+        bool in[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            st[j] = state(sk);
+            in[j] = sk <= sl;
+            if (in[j]) sk = next(sk);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float mn = fmaxf(M, st[j].x), at = mn == -INFINITY ? 0.f : mn;
+            if (in[j]) {
+                L = __fadd_rn(__fmul_rn(L, ex2(M - at)), __fmul_rn(ex2(st[j].x - at), st[j].y));
+                M = mn;
+            }
+        }
     }
-    const float inv = L == 0.f ? 0.f : 1.0f / L;
-    auto weight = [&](int sk) { return ex2(state(sk).x - at) * inv; };
-    const float fo = ex2(m - at) * inv, f2 = weight(s0 == own ? s1 : s0);
+    const float at = M == -INFINITY ? 0.f : M, inv = L == 0.f ? 0.f : 1.0f / L;
 #pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += 32) {
         float a[32];
-        auto join = [&](float f) {  // a += f v
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                a[4 * j] = __fadd_rn(a[4 * j], __fmul_rn(f, v[j].x));
-                a[4 * j + 1] = __fadd_rn(a[4 * j + 1], __fmul_rn(f, v[j].y));
-                a[4 * j + 2] = __fadd_rn(a[4 * j + 2], __fmul_rn(f, v[j].z));
-                a[4 * j + 3] = __fadd_rn(a[4 * j + 3], __fmul_rn(f, v[j].w));
-            }
-        };
-        auto join_own = [&]() {
-            uint32_t r[32];
-            tmem_ld32(o + uint32_t(c0), r);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) a[j] = __fadd_rn(a[j], __fmul_rn(fo, __uint_as_float(r[j])));
-        };
 #pragma unroll
         for (int j = 0; j < 32; ++j) a[j] = 0.f;
-        if (two) {
-            if (c0 + 32 < D) load(ahead, c0 + 32);
-            join_own();
-            join(f2);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = ahead[j];
-        } else {
 #pragma unroll 1
-            for (int sk = s0; sk <= sl; sk = next(sk)) {
-                if (sk == own) {
-                    join_own();
-                } else {
-                    seek(sk);
-                    load(v, c0);
-                    join(weight(sk));
+        for (int sk = s0; sk <= sl;) {
+            const int nk = next(sk);
+            const bool step = nk > sl;  // the columns' last piece
+            if (!step || c0 + 32 < D) load(ahead, step ? s0 : nk, step ? c0 + 32 : c0);
+            const float f = ex2(q.st.x - at) * inv;
+            if (sk == own) {
+                uint32_t r[32];
+                tmem_ld32(o + uint32_t(c0), r);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) a[j] = __fadd_rn(a[j], __fmul_rn(f, __uint_as_float(r[j])));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    a[4 * j] = __fadd_rn(a[4 * j], __fmul_rn(f, q.v[j].x));
+                    a[4 * j + 1] = __fadd_rn(a[4 * j + 1], __fmul_rn(f, q.v[j].y));
+                    a[4 * j + 2] = __fadd_rn(a[4 * j + 2], __fmul_rn(f, q.v[j].z));
+                    a[4 * j + 3] = __fadd_rn(a[4 * j + 3], __fmul_rn(f, q.v[j].w));
                 }
             }
+            q = ahead;
+            sk = nk;
         }
         if (out) {
 #pragma unroll
@@ -525,7 +542,7 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
         // The segment's part here ends, with the last output product.
         uint16_t *orow = row_ok ? p.out + ((long long)(row0 + qi) * p.Hq + (long long)sg.g * p.gq + qh) * D : nullptr;
         bool done = len == sg.n;
-        if (!done) {
+        if (!done && !tp.split) {
             if (!bounded) {  // all slices' bounds, where a CTA's first piece asks for them
                 for (int i = t; i <= sl.nsl; i += 32 * kMtSoftmaxWarps) bound[i] = mt_bound(p, m.scan, sl, i);
                 bounded = true;
@@ -543,7 +560,7 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
         tc_fence_after();
         if (!done) {
             // the piece: (m, l, O) of every row into the slice's piece tile, then counted in
-            const long long tile = tc5_piece_tile(p, slice, sg.x0 <= bound[slice], sg.b, sg.g);
+            const long long tile = tc5_piece_tile(p, slice, sg.first != 0, sg.b, sg.g);
             float4 *dst = reinterpret_cast<float4 *>(p.ws_acc + tile * 128 * D) + t;
 #pragma unroll 1
             for (int cc = 0; cc < D; cc += 32) {
@@ -555,14 +572,16 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
                                                           __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
             }
             reinterpret_cast<float2 *>(p.ws_ml)[tile * 128 + t] = make_float2(mrun, lrun);
-            // the whole piece is written before it is counted in (the counting thread's fence carries all of them)
-            if (!meet()) return;
-            if (t == 0) {
-                __threadfence();
-                sh[1] = arrive_last(ctr(), gen, uint32_t(len), uint32_t(sg.n), p.err);
+            if (!tp.split) {
+                // the whole piece is written before it is counted in (the counting thread's fence carries all of them)
+                if (!meet()) return;
+                if (t == 0) {
+                    __threadfence();
+                    sh[1] = arrive_last(ctr(), gen, uint32_t(len), uint32_t(sg.n), p.err);
+                }
+                if (!meet()) return;
+                done = sh[1] != 0;
             }
-            if (!meet()) return;
-            done = sh[1] != 0;
         }
         if (done && len == sg.n) {
             mt_output<D>(lrun, tlane + kMtOCol, orow);
@@ -572,7 +591,7 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
                         mt_slice_of(bound, sl.nsl, slice, sg.x0 + p.seg_cost + sg.n - 1), slice, sg.x0, sg.g, sg.b, t, mrun,
                         lrun, tlane + kMtOCol, orow);
         }
-        if (len < sg.n && !meet()) return;  // sh[1] is read before it is written again
+        if (len < sg.n && !tp.split && !meet()) return;  // sh[1] is read before it is written again
         tc_fence_before();  // the reads of O come before the next segment's first product overwrites it
         __syncwarp();
         if (lane == 0) mbar_arrive(&m.dempty[j % kMtDescs]);
@@ -672,6 +691,11 @@ __device__ void mt_copies(const TileParams &tp, const MtSmem &m, uint8_t *ring, 
     const uint64_t policy = policy_evict_first();
     const uint32_t ns = uint32_t(p.nst), slot_bytes = uint32_t(kMtKeys * D * 2);
     const uint32_t box_bytes = uint32_t(p.boxtok) * 128u;
+    // the slice's bounds, and its last segment's start or its own
+    int32_t x = 0;
+    if (lane < 2) x = mt_bound(p, m.scan, sl, int(blockIdx.x) + lane);
+    MtRange rg{__shfl_sync(kFull, x, 0), __shfl_sync(kFull, x, 1), 0};
+    rg.rot = rg.lo < rg.hi ? max(rg.lo, rg.hi - 1 - mt_locate(p, m.scan, rg.hi - 1).u) : rg.lo;
     struct Seg {
         MtSeg s;
         MtEntry e;
@@ -686,7 +710,7 @@ __device__ void mt_copies(const TileParams &tp, const MtSmem &m, uint8_t *ring, 
             return;
         }
         if (lane == 0) {
-            m.desc[d] = MtDesc{x.s.b, x.s.g, x.s.u, x.s.n, end ? 0 : x.s.len, x.s.x0, x.e.L, x.e.cnt, x.e.row0, x.e.base};
+            m.desc[d] = MtDesc{x.s.b, x.s.g, x.s.u, x.s.n, end ? 0 : x.s.len, x.s.x0, x.s.x0 <= rg.lo, x.e.L, x.e.cnt, x.e.row0, x.e.base};
             mbar_arrive(&m.dfull[d]);
         }
         ++told;
@@ -749,11 +773,6 @@ __device__ void mt_copies(const TileParams &tp, const MtSmem &m, uint8_t *ring, 
             vph ^= 1u;
         }
     };
-    // the slice's bounds, and its last segment's start or its own
-    int32_t x = 0;
-    if (lane < 2) x = mt_bound(p, m.scan, sl, int(blockIdx.x) + lane);
-    MtRange rg{__shfl_sync(kFull, x, 0), __shfl_sync(kFull, x, 1), 0};
-    rg.rot = rg.lo < rg.hi ? max(rg.lo, rg.hi - 1 - mt_locate(p, m.scan, rg.hi - 1).u) : rg.lo;
     uint32_t k = 0;
     int32_t vrow = -1, vg = 0;
     Seg cur{}, nxt{};
@@ -816,17 +835,19 @@ __device__ __noinline__ void mt_zero_rows(const TileParams &tp, int32_t values)
     }
 }
 
-// The entries' sequences and the prefix of their list lengths, by all threads, each a run of entries.
+// The entries' sequences and the prefix of their list lengths, by all NT threads, each a run of entries; zeros for rows
+// that get no other output (values > 0: of a row).
+template <int NT>
 __device__ __forceinline__ void mt_setup(const TileParams &tp, int32_t *scan, uint16_t *seq, int32_t *tmp, int32_t values)
 {
     const DecodeParams &p = tp.p;
     const int t = threadIdx.x, lane = t & 31, wid = t >> 5;
-    const int per = (p.B + kMtThreads - 1) / kMtThreads;
+    const int per = (p.B + NT - 1) / NT;
     const int lo = min(p.B, t * per), hi = min(p.B, lo + per);
     bool trouble = false;  // offsets out of order, rows of no sequence, or a sequence whose rows and length do not fit
     int32_t s = 0;
     if (tp.cu) {
-        for (int32_t b = t; b < tp.num_seqs; b += kMtThreads) trouble |= __ldg(tp.cu + b) > __ldg(tp.cu + b + 1);
+        for (int32_t b = t; b < tp.num_seqs; b += NT) trouble |= __ldg(tp.cu + b) > __ldg(tp.cu + b + 1);
         if (t == 0) trouble |= __ldg(tp.cu) != 0 || __ldg(tp.cu + tp.num_seqs) != tp.num_rows;
         if (lo < hi) {  // the last sequence whose entries start at lo or before
             int32_t a = 0, b = tp.num_seqs;
@@ -855,14 +876,14 @@ __device__ __forceinline__ void mt_setup(const TileParams &tp, int32_t *scan, ui
         sum += n;
     }
     if (__syncthreads_or(trouble)) {
-        mt_zero_rows(tp, values);
+        if (values > 0) mt_zero_rows(tp, values);
         bool ok = true;
         if (tp.cu) {
-            for (int32_t b = t; b < tp.num_seqs; b += kMtThreads) ok &= __ldg(tp.cu + b) <= __ldg(tp.cu + b + 1);
+            for (int32_t b = t; b < tp.num_seqs; b += NT) ok &= __ldg(tp.cu + b) <= __ldg(tp.cu + b + 1);
             ok &= __ldg(tp.cu) == 0;
         }
         if (!__syncthreads_and(ok)) {
-            for (int i = t; i <= p.B; i += kMtThreads) scan[i] = 0;
+            for (int i = t; i <= p.B; i += NT) scan[i] = 0;
             __syncthreads();
             return;
         }
@@ -942,13 +963,9 @@ __global__ void __launch_bounds__(kMtThreads, 2)
     const uint32_t gen = epoch + 1u;  // this call's tag of the arrival counters (see BalanceState)
     if (threadIdx.x == 0 && blockIdx.x == 0 && stamp != (epoch ^ kEpochMagic) && !(epoch == 0u && stamp == 0u))
         flag_error(p.err, PKV_ERR_WORKSPACE);
-    mt_setup(tp, scan, const_cast<uint16_t *>(m.seq), sh + 8, p.Hq * D);
-    // slices: one a CTA, none much shorter than kMtMinSlice
+    mt_setup<kMtThreads>(tp, scan, const_cast<uint16_t *>(m.seq), sh + 8, p.Hq * D);
     const int32_t T = p.nhg * scan[p.B];
-    MtSlices sl{T, min(int(gridDim.x), max(1, T / (kMtMinSlice + p.seg_cost))), 0, 0, 0.f};
-    sl.each = T / sl.nsl;
-    sl.rest = T - sl.each * sl.nsl;
-    sl.inv = 1.0f / float(sl.nsl);
+    const MtSlices sl = mt_slices(p, T, int(gridDim.x));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -980,6 +997,77 @@ __global__ void __launch_bounds__(kMtThreads, 2)
             p.ws_bal->stamp = (epoch + 1u) ^ kEpochMagic;
         }
     }
+}
+
+// The pieces that a split call's slices of `ctas` CTAs left, merged: CTA (x, y) four columns, from 4 x on, of the 128 rows
+// of segment y (entry y / nhg), a thread a row, eight pieces' loads in flight.  (One draft of 25 nodes over 30000 tokens,
+// 16 / 8 heads of 128: 8 segments of 38 pieces; merged by the CTA that completes a segment 125 us.)
+constexpr int kMtMergeThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kMtMergeThreads) mask_merge_kernel(const __grid_constant__ TileParams tp, int ctas)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const DecodeParams &p = tp.p;
+    int32_t *tmp = reinterpret_cast<int32_t *>(smem), *bound = tmp + 8, *scan = bound + kMaxSlots + 1;
+    uint16_t *seq = tp.cu ? reinterpret_cast<uint16_t *>(scan + p.B + 1) : nullptr;
+    griddep_launch_dependents();
+    griddep_wait();
+    mt_setup<kMtMergeThreads>(tp, scan, seq, tmp, 0);
+    const int b = int(blockIdx.y) / p.nhg, g = int(blockIdx.y) - b * p.nhg, row = threadIdx.x;
+    const int32_t n = scan[b + 1] - scan[b];
+    if (n == 0) return;
+    const MtSlices sl = mt_slices(p, p.nhg * scan[p.B], ctas);
+    const int32_t x0 = p.nhg * scan[b] + g * n, first = x0 + p.seg_cost, last = x0 + n - 1;
+    // the slices that hold its units: from about where they would be without moved bounds
+    int sf = min(max(first / max(sl.each, 1) - 2, 0), sl.nsl - 1);
+    while (sf > 0 && mt_bound(p, scan, sl, sf) > first) --sf;
+    while (mt_bound(p, scan, sl, sf + 1) <= first) ++sf;
+    for (int i = sf + row; i <= sl.nsl; i += kMtMergeThreads) {
+        bound[i] = mt_bound(p, scan, sl, i);
+        if (bound[i] > last) break;
+    }
+    __syncthreads();
+    int end = sf;
+    while (bound[end + 1] <= last) ++end;
+    if (end == sf) return;  // one piece: its output is written
+    const MtEntry e = mt_entry(tp, b, seq ? int32_t(seq[b]) : b / tp.per_entry);
+    const int qi = row / p.gq, c4 = int(blockIdx.x);
+    float M = -INFINITY, L = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s0 = sf; s0 <= end; s0 += 8) {
+        float2 st[8];
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int s = min(s0 + k, end);
+            const long long tile = tc5_piece_tile(p, s, x0 <= bound[s], b, g);
+            st[k] = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml) + tile * 128 + row);
+            v[k] = __ldcg(reinterpret_cast<const float4 *>(p.ws_acc + tile * 128 * D) + c4 * 128 + row);
+        }
+        float mn = M;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (s0 + k <= end && bound[s0 + k + 1] > bound[s0 + k]) mn = fmaxf(mn, st[k].x);
+        const float at = mn == -INFINITY ? 0.f : mn, r = ex2(M - at);
+        L *= r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] *= r;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (s0 + k <= end && bound[s0 + k + 1] > bound[s0 + k]) {
+                const float f = ex2(st[k].x - at);
+                L = fmaf(f, st[k].y, L);
+                a[0] = fmaf(f, v[k].x, a[0]);
+                a[1] = fmaf(f, v[k].y, a[1]);
+                a[2] = fmaf(f, v[k].z, a[2]);
+                a[3] = fmaf(f, v[k].w, a[3]);
+            }
+        M = mn;
+    }
+    if (qi >= e.cnt) return;
+    const float inv = L == 0.f ? 0.f : 1.0f / L;
+    uint16_t *out = p.out + ((long long)(e.row0 + qi) * p.Hq + (long long)g * p.gq + (row - qi * p.gq)) * D + 4 * c4;
+    *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv));
 }
 
 // Q as [num_rows][Hq][D], a box of `tile` queries x gq heads x 64 dims landing as 128-byte-swizzled rows.
@@ -1026,6 +1114,9 @@ static pkv_status launch_tile(TileParams &tp, const void *k_cache, const void *v
     p.seg_cost = kMtSegCost;
     const uint32_t total = mt_layout(D, n, p.B, tp.cu != nullptr).total;
     int grid = std::min(dev.sm_count * ctas, kMaxSlots);
+    // Few segments for the CTAs: their pieces are merged by a second kernel.
+    const int64_t seen = std::min<int64_t>(p.len_limit, int64_t(p.window) + p.sinks + tp.tile);
+    tp.split = int64_t(p.B) * p.nhg * kMtSplit <= grid && seen > kMtSplit * (kMtMinSlice + kMtSegCost) * kMtKeys;
     if (num_workers > 0) grid = std::min((num_workers + team_warps(16) - 1) / team_warps(16), kMaxSlots);
     CUtensorMap qmap, kmap, vmap;
     const int64_t rows = int64_t(p.NB) * p.bs;
@@ -1040,7 +1131,16 @@ static pkv_status launch_tile(TileParams &tp, const void *k_cache, const void *v
         cudaGetLastError();
         return cuda_fail("mask_tile_kernel launch", e);
     }
-    return launch_status("mask_tile_kernel launch");
+    const pkv_status st = launch_status("mask_tile_kernel launch");
+    if (st != PKV_OK || !tp.split) return st;
+    const size_t bytes = size_t(8 + kMaxSlots + 1 + p.B + 1) * 4 + size_t(p.B) * 2;
+    const cudaError_t em = launch_pdl(mask_merge_kernel<D>, dim3(D / 4, unsigned(p.B * p.nhg)), dim3(kMtMergeThreads), bytes,
+                                      stream, tp, grid);
+    if (em != cudaSuccess) {
+        cudaGetLastError();
+        return cuda_fail("mask_merge_kernel launch", em);
+    }
+    return launch_status("mask_merge_kernel launch");
 }
 
 int32_t mask_tile_entries(int32_t num_seqs, int32_t num_rows, int32_t per_seq, int32_t tile)

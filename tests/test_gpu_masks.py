@@ -4,8 +4,9 @@ caches.
 Attention must stay within  2^-8 |out| + w A  of the 64-bit result, A = the softmax-weighted mean of |v|: the bf16
 output rounds by at most 2^-8 of itself, and the weights' errors move it by at most their relative size times A.
 bf16 caches: a weight is two bf16 parts (2^-16), its fp32 score errs by less than 2^-12 (scores stay below 2^6, a sum
-of at most 128 products errs by less than 2^-14 of that), sums and merges have the rest of w = 2^-11.  Calls whose
-sequences have more than two chunks of queries round a weight to one bf16 part, 2^-8: w = 2^-8 + 2^-11.  E4M3 and int8
+of at most 128 products errs by less than 2^-14 of that), sums and merges have the rest of w = 2^-11.  Calls with
+offsets, or with more new tokens a sequence than 16 / (query heads a kv head), run on the tensor-memory tile, which
+rounds a weight to one bf16 part, 2^-8: w = 2^-8 + 2^-11 (long_runs).  E4M3 and int8
 caches round it to f16, 2^-11, and their scores err by up to twice 2^-12: w = 2^-10.
 """
 import numpy as np
@@ -137,7 +138,7 @@ def test_attention_windows(cache, n, window, sinks, bs):
     prob = Problem(cache, [window_sees(L, n, window, sinks) for L in lens], 16, 8, 128, bs, seed=n + window)
     for workers, uniform in ((0, n), (24, 0)):
         out = attend(prob, (window, sinks), uniform=uniform, workers=workers)
-        check(out, prob, f"workers {workers}", long_runs=n > 16)
+        check(out, prob, f"workers {workers}", long_runs=n > 8 or not uniform)
 
 
 @pytest.mark.parametrize("cache", ["bf16", "int8"])
@@ -154,7 +155,7 @@ def test_attention_ragged(cache, Hq, Hkv, D, bs):
 def test_attention_with_sequences_without_new_tokens():
     lens, new = [40, 0, 300, 20, 0], [3, 0, 0, 20, 0]
     prob = Problem("bf16", [window_sees(L, n, 16, 2) for L, n in zip(lens, new)], 8, 4, 64, 16, seed=2)
-    check(attend(prob, (16, 2)), prob, "some without")
+    check(attend(prob, (16, 2)), prob, "some without", long_runs=True)
 
 
 # ------------------------------------------------------------------------------------------ trees
@@ -171,7 +172,7 @@ def test_trees(cache, n, words):
         md = torch.from_numpy(masks).cuda()
         for workers, uniform in ((0, n), (24, 0)):
             out = attend(prob, (md,), "tree", uniform=uniform, workers=workers)
-            check(out, prob, f"heads {Hq} workers {workers}", long_runs=n * Hq > 32 * Hkv)
+            check(out, prob, f"heads {Hq} workers {workers}", long_runs=n * Hq > 16 * Hkv or not uniform)
 
 
 @pytest.mark.parametrize("cache", ["bf16", "int8"])
@@ -206,25 +207,42 @@ def test_rows_that_see_nothing_give_zeros(cache, n):
     for uniform in (n, 0):
         out = attend(prob, (torch.from_numpy(masks).cuda(),), "tree", uniform=uniform)
         assert not out[:n].any() and not out[n:2 * n:2].any()
-        check(out, prob, "some empty", long_runs=n > 16)
+        check(out, prob, "some empty", long_runs=n > 8 or not uniform)
 
 
-@pytest.mark.parametrize("n", [5, 16, 40])
+@pytest.mark.parametrize("n", [1, 5, 8, 16, 40])
 def test_a_chain_is_the_plain_attention(n):
     lens = [max(L, n) for L in LENS]
     chain = np.tril(np.ones((n, 64), np.uint8))
     mask = np.packbits(chain, axis=1, bitorder="little").view(np.int32)
     masks = torch.from_numpy(np.tile(mask, (len(lens), 1))).cuda()
     prob = Problem("bf16", [window_sees(L, n, 1 << 20, 0) for L in lens], 16, 8, 128, 128, seed=n)
-    q, c, bt, ld, cu = dev = prob.cuda()
-    ws = pkv.alloc_attention_workspace(q.shape[0], 16, 8, 128)
-    out = torch.empty_like(q)
-    pkv.paged_attention(q, *c, bt, cu, ld, prob.scale, out, ws, num_workers=20)
-    tree, window = (attend(prob, *a, workers=20, dev=dev) for a in (((masks,), "tree"), ((1 << 20, 0),)))
-    assert torch.equal(tree, window)
-    check(tree, prob, "chain", long_runs=n > 16)
-    if n <= 16:  # (longer runs of masked calls have a kernel of their own, whose sums have another order)
-        assert torch.equal(out, tree)
+    dev = prob.cuda()
+    for uniform in (n, 0):
+        tree, window = (attend(prob, *a, workers=20, dev=dev, uniform=uniform) for a in (((masks,), "tree"), ((1 << 20, 0),)))
+        assert torch.equal(tree, window)
+        check(tree, prob, "chain", long_runs=n > 8 or not uniform)
+        if 1 < n <= 8 and uniform:  # (the others run on another kernel than the plain call, whose sums have another order)
+            q, c, bt, ld, cu = dev
+            ws = pkv.alloc_attention_workspace(q.shape[0], 16, 8, 128)
+            out = torch.empty_like(q)
+            pkv.paged_attention(q, *c, bt, cu, ld, prob.scale, out, ws, num_workers=20, new_per_seq=n)
+            assert torch.equal(out, tree)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,bs", [(16, 8, 128, 256), (4, 1, 64, 16), (15, 5, 128, 32)])
+@pytest.mark.parametrize("lens,new", [([30000], [25]), ([9000, 700, 20000], [33, 1, 150]), ([12345, 4000], [64, 64])])
+def test_few_long_sequences(Hq, Hkv, D, bs, lens, new):
+    """Segments of many pieces, merged by a kernel of their own."""
+    masks = random_trees(new, 5, np.random.default_rng(3))
+    cu = np.concatenate([[0], np.cumsum(new)])
+    prob = Problem("bf16", [tree_sees(L, n, masks[a:a + n]) for L, n, a in zip(lens, new, cu)], Hq, Hkv, D, bs, seed=Hq)
+    md, dev = torch.from_numpy(masks).cuda(), prob.cuda()
+    ws = pkv.alloc_attention_workspace(sum(new), Hq, Hkv, D)
+    for workers in (0, 100):
+        out = attend(prob, (md,), "tree", workers=workers, dev=dev, ws=ws)
+        check(out, prob, f"workers {workers}", long_runs=True)
+        assert torch.equal(out, attend(prob, (md,), "tree", workers=workers, dev=dev, ws=ws))
 
 
 # ------------------------------------------------------------------------------------------ what the device refuses
