@@ -22,12 +22,17 @@
 // the one before are in).  S(k) is issued when P(k - 2) V is done, P(k - 1) V after S(k), or before it where unit k
 // opens a segment.  Every barrier's next phase needs its waiter's own next step, so none runs two phases ahead.
 //
-// The list is cut into equal slices, one a CTA, whose bounds move to a segment's start or end that is near; the pieces of
-// a segment that lies in several slices are merged by the CTA that completes it.  The slices, and with them the sums'
-// order, depend on the list and the grid alone: the results repeat bit for bit.  The copying warp walks the list and
-// hands each segment to the others in shared memory (MtDesc), the next one before it copies the last unit of this one.
-// Calls of few segments, whose pieces are many, leave them to a second kernel (mask_merge_kernel): one CTA's merge goes
-// through a segment's pieces one after another.
+// The list is cut into equal slices, one a CTA.  Slices, and with them the sums' order, depend on the list and the grid
+// alone: the results repeat bit for bit.  The pieces of a segment that lies in several slices are merged
+//   - by the CTA that completes it (MERGE).  A piece costs its CTA two meetings of its warps, a fence and a counter,
+//     and the last one a trip through L2 for every other piece, so bounds move to a segment's start or end that is near;
+//   - or, where segments are few and their pieces many, by a second kernel (mask_merge_kernel): the merges of one CTA
+//     would come one after another (25 nodes over one sequence of 30000 tokens, 38 pieces a segment: 125 us, so
+//     43 us; of four sequences of 512-4096 34 us, so 26).  With many segments the second kernel's start would cost more
+//     than the merges do (64 sequences: 64-token chunks 66 us, so 78; 32-node trees 110 and 120).
+// Where segments are short, slices end at their starts and there is nothing to merge.  The copying warp walks the list
+// and hands each segment to the others in shared memory (MtDesc), the next one before it copies the last unit of this
+// one.
 #include "pkv_decode_kernel.cuh"
 
 namespace pkv {
@@ -38,15 +43,18 @@ constexpr uint32_t kMtSlab = kMtKeys * 128;   // one 64-dim half of a K or V til
 constexpr uint32_t kMtQSlab = 128 * 128;      // one 64-dim half of Q
 constexpr uint32_t kMtCols = 256, kMtOCol = 128;
 constexpr int kMtMaxSlots = 8, kMtDescs = 4;
-// A slice of the unit list is at least this long: a piece costs its CTA and the one that merges it about as much as a
-// few units.
+// A slice of the unit list is at least this long: a piece costs its CTA and its merge about as much as a few units.
 constexpr int kMtMinSlice = 4;
 // What a segment's start and end cost, in units (see MtSeg).
 constexpr int kMtSegCost = 4;
-// A slice's bound this near to a segment's start or end, in units, moves there: no piece to merge.
-constexpr int kMtSnap = 8;
-// Pieces a segment (CTAs over segments) from which on a second kernel merges them.
-constexpr int kMtSplit = 4;
+// A slice's bound this near to a segment's start or end, in units, moves there: MERGE (none: 73 us the 64-token chunks
+// under a 1024 window, 6 or 8: 66), and where a second kernel merges.
+constexpr int kMtSnap = 8, kMtSnapFew = 1;
+// Segments of at most this many units are not cut: bounds move to their starts.  More where there is a segment for
+// every CTA (the 64-token chunks, 17 units a segment: 65.5 us, so 63.3).
+constexpr int kMtWhole = 12, kMtWholeMany = 20;
+// CTAs over segments from which on a second kernel merges.
+constexpr int kMtFew = 4;
 
 struct TileParams {
     DecodeParams p;       // B: entries, context_lens: by sequence, nst: ring slots, seg_cost, num_workers unused
@@ -55,7 +63,8 @@ struct TileParams {
     int32_t tile;         // queries of an entry
     int32_t per_entry;    // null cu: entries of a sequence
     int32_t max_new;
-    int32_t split;        // pieces are left to mask_merge_kernel
+    int32_t snap;         // see kMtSnap, kMtWhole
+    int32_t merge;        // 1: the CTA that completes a segment merges it; 2: a second kernel does; 0: nothing to merge
 };
 
 // A segment's part in the CTA's slice, as the softmax warps and the issuing one see it: units u .. u + len - 1 of the n
@@ -69,7 +78,7 @@ struct MtLayout {
     uint32_t off_q, off_bar, off_desc, off_bound, off_tmp, off_scan, off_seq, total;
 };
 
-__host__ __device__ inline MtLayout mt_layout(int D, int nslots, int B, bool seqs)
+__host__ __device__ inline MtLayout mt_layout(int D, int nslots, int B, bool seqs, bool merge)
 {
     MtLayout l;
     uint32_t o = uint32_t(nslots) * uint32_t(kMtKeys * D * 2);
@@ -80,7 +89,7 @@ __host__ __device__ inline MtLayout mt_layout(int D, int nslots, int B, bool seq
     l.off_desc = o;
     o += uint32_t(kMtDescs * sizeof(MtDesc));
     l.off_bound = o;
-    o += (kMaxSlots + 1) * 4u;
+    o += merge ? (kMaxSlots + 1) * 4u : 0u;
     l.off_tmp = o;
     o += 40u * 4u;
     l.off_scan = o;
@@ -218,14 +227,14 @@ __device__ __forceinline__ bool mt_next(const DecodeParams &p, const int32_t *sc
 
 // The slices: nsl of T list positions.
 struct MtSlices {
-    int32_t T, nsl, each, rest;
+    int32_t T, nsl, each, rest, snap;
     float inv;
 };
 
 // One slice a CTA, none much shorter than kMtMinSlice.
-__device__ __forceinline__ MtSlices mt_slices(const DecodeParams &p, int32_t T, int ctas)
+__device__ __forceinline__ MtSlices mt_slices(const TileParams &tp, int32_t T, int ctas)
 {
-    MtSlices q{T, min(ctas, max(1, T / (kMtMinSlice + p.seg_cost))), 0, 0, 0.f};
+    MtSlices q{T, min(ctas, max(1, T / (kMtMinSlice + tp.p.seg_cost))), 0, 0, tp.snap, 0.f};
     q.each = T / q.nsl;
     q.rest = T - q.each * q.nsl;
     q.inv = 1.0f / float(q.nsl);
@@ -239,9 +248,9 @@ __device__ __forceinline__ int32_t mt_bound(const DecodeParams &p, const int32_t
     int32_t x = q.each * i + min(int32_t(float(q.rest * i) * q.inv), q.rest);  // (grows with i, as it should)
     if (i > 0) {
         const Walker w = mt_locate(p, scan, x);
-        if (w.u <= p.seg_cost + kMtSnap)
+        if (w.u - p.seg_cost <= q.snap)
             x -= w.u;
-        else if (w.n - w.u <= kMtSnap)
+        else if (w.n - w.u <= q.snap)
             x += w.n - w.u;
     }
     return x;
@@ -405,7 +414,7 @@ __device__ __forceinline__ void mt_merge(const DecodeParams &p, const int32_t *b
 }
 
 // The softmax warps (see the head of the file).
-template <int D>
+template <int D, bool MERGE>
 __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const MtSmem &m, uint8_t *ring, uint8_t *qop,
                            uint32_t tmem, int32_t *bound, int *sh, const MtSlices &sl, uint32_t gen)
 {
@@ -421,8 +430,9 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
         if (lane == 0) flag_error(p.err, PKV_ERR_WAIT_TIMEOUT);
         return false;
     };
-    uint32_t meets = 0;
-    auto meet = [&]() {  // of the four warps
+    [[maybe_unused]] uint32_t meets = 0;
+    [[maybe_unused]] bool bounded = false;
+    [[maybe_unused]] auto meet = [&]() {  // of the four warps
         __syncwarp();
         if (lane == 0) mbar_arrive(m.team);
         return wait(m.team, meets++ & 1u);
@@ -436,8 +446,6 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
     uint32_t k = 0;  // unit of the CTA
     if (!wait(&m.dfull[0], 0u)) return;
     if (t == 0 && m.desc[0].len > 0) copy_q(m.desc[0]);
-    const int slice = int(blockIdx.x);
-    bool bounded = false;
     for (uint32_t j = 0;; ++j) {
         const MtDesc &sg = m.desc[j % kMtDescs], &nsg = m.desc[(j + 1) % kMtDescs];
         const int32_t len = sg.len;
@@ -450,37 +458,40 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
         // token units that every query sees whole
         const int32_t all0 = (max(L - p.window, 0) + kMtKeys - 1) / kMtKeys;
         const int32_t all1 = (p.tree ? min(L - cnt + 1, base) : L - cnt + 1) / kMtKeys;
-        auto ctr = [&]() { return p.ws_count + ((long long)sg.b * p.Hkv + sg.g) * p.sub; };
-        unsigned long long arrived = 0;
+        [[maybe_unused]] auto ctr = [&]() { return p.ws_count + ((long long)sg.b * p.Hkv + sg.g) * p.sub; };
+        [[maybe_unused]] unsigned long long arrived = 0;
         float mrun = -INFINITY, lrun = 0.f;
         for (int i = 0; i < len; ++i, ++k) {
             const int32_t tu = su.token_unit(u0 + i), tok0 = tu * kMtKeys;
             const bool all = tu >= all0 && tu < all1;
-            uint32_t v0 = 0xffffffffu, v1 = 0xffffffffu;  // the keys that the row sees
+            uint32_t v0 = 0xffffffffu, v1 = 0xffffffffu, e0 = v0, e1 = v0;  // the keys that the row sees, that any row does
             if (!all) {
                 v0 = row_ok ? row_sees(p, tok0, pos, base, mask) : 0u;
                 v1 = row_ok ? row_sees(p, tok0 + 32, pos, base, mask) : 0u;
-                // V rows that no query sees may hold anything, and 0 * NaN is NaN: zeros there, once they have landed
-                const uint32_t e0 = entry_sees(p, tok0, L, cnt), e1 = entry_sees(p, tok0 + 32, L, cnt);
-                if ((e0 & e1) != 0xffffffffu) {
-                    const uint32_t item = mt_vitem(k);
-                    if (!wait(&m.full[item % ns], (item / ns) & 1u)) return;
-                    uint8_t *v = ring + (item % ns) * uint32_t(kMtKeys * D * 2);
-                    for (int j = t; j < kMtKeys * (D / 8); j += 32 * kMtSoftmaxWarps) {
-                        const int r = (j >> 3) & (kMtKeys - 1);
-                        if (!(((r < 32 ? e0 : e1) >> (r & 31)) & 1u))
-                            *reinterpret_cast<uint4 *>(v + j * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();  // for the tensor core
-                }
+                e0 = entry_sees(p, tok0, L, cnt);
+                e1 = entry_sees(p, tok0 + 32, L, cnt);
             }
             if (!wait(&m.sfull[k & 1u], (k >> 1) & 1u)) return;
             tc_fence_after();
+            if ((e0 & e1) != 0xffffffffu) {
+                // V rows that no query sees may hold anything, and 0 * NaN is NaN: zeros there, once they have landed.
+                // (Not before the scores are in: only those tell that the slot's item before this one has landed, and a
+                // barrier two phases behind would pass for one that is done.)
+                const uint32_t item = mt_vitem(k);
+                if (!wait(&m.full[item % ns], (item / ns) & 1u)) return;
+                uint8_t *v = ring + (item % ns) * uint32_t(kMtKeys * D * 2);
+                for (int j = t; j < kMtKeys * (D / 8); j += 32 * kMtSoftmaxWarps) {
+                    const int r = (j >> 3) & (kMtKeys - 1);
+                    if (!(((r < 32 ? e0 : e1) >> (r & 31)) & 1u))
+                        *reinterpret_cast<uint4 *>(v + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();  // for the tensor core
+            }
             if (i == len - 1) {  // the segment's last scores are in
                 if (!wait(&m.dfull[(j + 1) % kMtDescs], ((j + 1) / kMtDescs) & 1u)) return;
                 if (t == 0 && nsg.len > 0) copy_q(nsg);
-                // (looked at once the output is in: whether this piece completes the segment)
-                if (t == 0 && len < sg.n) arrived = *reinterpret_cast<volatile unsigned long long *>(ctr());
+                if constexpr (MERGE)  // looked at once the weights are out: whether this piece completes the segment
+                    if (t == 0 && len < sg.n) arrived = *reinterpret_cast<volatile unsigned long long *>(ctr());
             }
             const uint32_t sbuf = tlane + (k & 1u) * kMtKeys;
             uint32_t r[kMtKeys];
@@ -541,25 +552,27 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
         }
         // The segment's part here ends, with the last output product.
         uint16_t *orow = row_ok ? p.out + ((long long)(row0 + qi) * p.Hq + (long long)sg.g * p.gq + qh) * D : nullptr;
+        [[maybe_unused]] const int slice = int(blockIdx.x);
         bool done = len == sg.n;
-        if (!done && !tp.split) {
-            if (!bounded) {  // all slices' bounds, where a CTA's first piece asks for them
-                for (int i = t; i <= sl.nsl; i += 32 * kMtSoftmaxWarps) bound[i] = mt_bound(p, m.scan, sl, i);
-                bounded = true;
+        if constexpr (MERGE)
+            if (!done) {
+                if (!bounded) {  // all slices' bounds, where a CTA's first piece asks for them
+                    for (int i = t; i <= sl.nsl; i += 32 * kMtSoftmaxWarps) bound[i] = mt_bound(p, m.scan, sl, i);
+                    bounded = true;
+                }
+                // Every other piece counted in: this one stays where it is and the others join it.
+                if (t == 0) {
+                    sh[1] = uint32_t(arrived >> 32) == gen && uint32_t(arrived) + uint32_t(len) == uint32_t(sg.n);
+                    __threadfence();
+                }
+                if (!meet()) return;
+                done = sh[1] != 0;
+                if (done && t == 0) atomicExch(ctr(), 0ull);  // the counter at rest again
             }
-            // Every other piece counted in: this one stays where it is and the others join it.
-            if (t == 0) {
-                sh[1] = uint32_t(arrived >> 32) == gen && uint32_t(arrived) + uint32_t(len) == uint32_t(sg.n);
-                __threadfence();
-            }
-            if (!meet()) return;
-            done = sh[1] != 0;
-            if (done && t == 0) atomicExch(ctr(), 0ull);  // the counter at rest again
-        }
         if (!wait(&m.odone[(k - 1) & 1u], ((k - 1) >> 1) & 1u)) return;
         tc_fence_after();
         if (!done) {
-            // the piece: (m, l, O) of every row into the slice's piece tile, then counted in
+            // a piece: (m, l, O) of every row into the slice's piece tile
             const long long tile = tc5_piece_tile(p, slice, sg.first != 0, sg.b, sg.g);
             float4 *dst = reinterpret_cast<float4 *>(p.ws_acc + tile * 128 * D) + t;
 #pragma unroll 1
@@ -572,7 +585,7 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
                                                           __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
             }
             reinterpret_cast<float2 *>(p.ws_ml)[tile * 128 + t] = make_float2(mrun, lrun);
-            if (!tp.split) {
+            if constexpr (MERGE) {
                 // the whole piece is written before it is counted in (the counting thread's fence carries all of them)
                 if (!meet()) return;
                 if (t == 0) {
@@ -583,15 +596,17 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
                 done = sh[1] != 0;
             }
         }
-        if (done && len == sg.n) {
+        if (len == sg.n) {
             mt_output<D>(lrun, tlane + kMtOCol, orow);
-        } else if (done) {
-            __threadfence();
-            mt_merge<D>(p, bound, mt_slice_of(bound, sl.nsl, slice, sg.x0 + p.seg_cost),
-                        mt_slice_of(bound, sl.nsl, slice, sg.x0 + p.seg_cost + sg.n - 1), slice, sg.x0, sg.g, sg.b, t, mrun,
-                        lrun, tlane + kMtOCol, orow);
+        } else if constexpr (MERGE) {
+            if (done) {
+                __threadfence();
+                mt_merge<D>(p, bound, mt_slice_of(bound, sl.nsl, slice, sg.x0 + p.seg_cost),
+                            mt_slice_of(bound, sl.nsl, slice, sg.x0 + p.seg_cost + sg.n - 1), slice, sg.x0, sg.g, sg.b, t,
+                            mrun, lrun, tlane + kMtOCol, orow);
+            }
+            if (!meet()) return;  // sh[1] is read before it is written again
         }
-        if (len < sg.n && !tp.split && !meet()) return;  // sh[1] is read before it is written again
         tc_fence_before();  // the reads of O come before the next segment's first product overwrites it
         __syncwarp();
         if (lane == 0) mbar_arrive(&m.dempty[j % kMtDescs]);
@@ -907,14 +922,14 @@ __device__ __forceinline__ void mt_setup(const TileParams &tp, int32_t *scan, ui
     __syncthreads();
 }
 
-template <int D>
+template <int D, bool MERGE>
 __global__ void __launch_bounds__(kMtThreads, 2)
     mask_tile_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TileParams tp)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     const DecodeParams &p = tp.p;
-    const MtLayout lay = mt_layout(D, p.nst, p.B, tp.cu != nullptr);
+    const MtLayout lay = mt_layout(D, p.nst, p.B, tp.cu != nullptr, tp.merge == 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t *scan = reinterpret_cast<int32_t *>(smem + lay.off_scan);
     MtSmem m;
@@ -931,7 +946,7 @@ __global__ void __launch_bounds__(kMtThreads, 2)
     m.desc = reinterpret_cast<MtDesc *>(smem + lay.off_desc);
     m.scan = scan;
     m.seq = tp.cu ? reinterpret_cast<uint16_t *>(smem + lay.off_seq) : nullptr;
-    int32_t *bound = reinterpret_cast<int32_t *>(smem + lay.off_bound);
+    int32_t *bound = reinterpret_cast<int32_t *>(smem + lay.off_bound);  // MERGE
     int *sh = reinterpret_cast<int *>(smem + lay.off_tmp);  // [0] tensor-memory address, [1] a segment is complete, [8..] scan
     if (threadIdx.x == 0) {
         prefetch_tensormap(&qmap);
@@ -959,13 +974,17 @@ __global__ void __launch_bounds__(kMtThreads, 2)
     __syncthreads();  // a next kernel's CTA on this SM takes its tensor memory after this one
     griddep_launch_dependents();
     griddep_wait();
-    const uint32_t epoch = __ldcg(&p.ws_bal->epoch), stamp = __ldcg(&p.ws_bal->stamp);
+    uint32_t epoch = 0;
+    if constexpr (MERGE) {
+        epoch = __ldcg(&p.ws_bal->epoch);
+        const uint32_t stamp = __ldcg(&p.ws_bal->stamp);
+        if (threadIdx.x == 0 && blockIdx.x == 0 && stamp != (epoch ^ kEpochMagic) && !(epoch == 0u && stamp == 0u))
+            flag_error(p.err, PKV_ERR_WORKSPACE);
+    }
     const uint32_t gen = epoch + 1u;  // this call's tag of the arrival counters (see BalanceState)
-    if (threadIdx.x == 0 && blockIdx.x == 0 && stamp != (epoch ^ kEpochMagic) && !(epoch == 0u && stamp == 0u))
-        flag_error(p.err, PKV_ERR_WORKSPACE);
     mt_setup<kMtThreads>(tp, scan, const_cast<uint16_t *>(m.seq), sh + 8, p.Hq * D);
     const int32_t T = p.nhg * scan[p.B];
-    const MtSlices sl = mt_slices(p, T, int(gridDim.x));
+    const MtSlices sl = mt_slices(tp, T, int(gridDim.x));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -973,7 +992,7 @@ __global__ void __launch_bounds__(kMtThreads, 2)
     uint8_t *qop = smem + lay.off_q;
     if (int(blockIdx.x) < sl.nsl) {
         if (warp < kMtSoftmaxWarps) {
-            mt_softmax<D>(tp, &qmap, m, smem, qop, tmem, bound, sh, sl, gen);
+            mt_softmax<D, MERGE>(tp, &qmap, m, smem, qop, tmem, bound, sh, sl, gen);
         } else if (warp == kMtSoftmaxWarps) {
             if (lane == 0) mt_products<D>(p, m, smem_u32(smem), smem_u32(qop), tmem);
             __syncwarp();
@@ -989,7 +1008,7 @@ __global__ void __launch_bounds__(kMtThreads, 2)
         tmem_dealloc(tmem, kMtCols);
     }
     // count this CTA in (it read the control block long ago); the last one leaves the block ready for the next call
-    if (threadIdx.x == 0) {
+    if (MERGE && threadIdx.x == 0) {
         __threadfence();
         if (atomicAdd(&p.ws_bal->done, 1u) == gridDim.x - 1) {
             p.ws_bal->done = 0u;
@@ -999,9 +1018,10 @@ __global__ void __launch_bounds__(kMtThreads, 2)
     }
 }
 
-// The pieces that a split call's slices of `ctas` CTAs left, merged: CTA (x, y) four columns, from 4 x on, of the 128 rows
-// of segment y (entry y / nhg), a thread a row, eight pieces' loads in flight.  (One draft of 25 nodes over 30000 tokens,
-// 16 / 8 heads of 128: 8 segments of 38 pieces; merged by the CTA that completes a segment 125 us.)
+// Merges the pieces of the segments that lie in several of the `ctas` slices, in slice order:
+//     M = max m_i,  l = sum 2^(m_i - M) l_i,  out = sum 2^(m_i - M) acc_i / l.
+// CTA (x, y): four columns, from 4 x on, of the 128 rows of segment y (entry y / nhg), a thread a row, eight pieces'
+// loads in flight.
 constexpr int kMtMergeThreads = 128;
 
 template <int D>
@@ -1017,7 +1037,7 @@ __global__ void __launch_bounds__(kMtMergeThreads) mask_merge_kernel(const __gri
     const int b = int(blockIdx.y) / p.nhg, g = int(blockIdx.y) - b * p.nhg, row = threadIdx.x;
     const int32_t n = scan[b + 1] - scan[b];
     if (n == 0) return;
-    const MtSlices sl = mt_slices(p, p.nhg * scan[p.B], ctas);
+    const MtSlices sl = mt_slices(tp, p.nhg * scan[p.B], ctas);
     const int32_t x0 = p.nhg * scan[b] + g * n, first = x0 + p.seg_cost, last = x0 + n - 1;
     // the slices that hold its units: from about where they would be without moved bounds
     int sf = min(max(first / max(sl.each, 1) - 2, 0), sl.nsl - 1);
@@ -1037,9 +1057,11 @@ __global__ void __launch_bounds__(kMtMergeThreads) mask_merge_kernel(const __gri
     for (int s0 = sf; s0 <= end; s0 += 8) {
         float2 st[8];
         float4 v[8];
+        bool in[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int s = min(s0 + k, end);
+            in[k] = s0 + k <= end && bound[s + 1] > bound[s];  // (an empty slice left nothing)
             const long long tile = tc5_piece_tile(p, s, x0 <= bound[s], b, g);
             st[k] = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml) + tile * 128 + row);
             v[k] = __ldcg(reinterpret_cast<const float4 *>(p.ws_acc + tile * 128 * D) + c4 * 128 + row);
@@ -1047,14 +1069,14 @@ __global__ void __launch_bounds__(kMtMergeThreads) mask_merge_kernel(const __gri
         float mn = M;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if (s0 + k <= end && bound[s0 + k + 1] > bound[s0 + k]) mn = fmaxf(mn, st[k].x);
+            if (in[k]) mn = fmaxf(mn, st[k].x);
         const float at = mn == -INFINITY ? 0.f : mn, r = ex2(M - at);
         L *= r;
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] *= r;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if (s0 + k <= end && bound[s0 + k + 1] > bound[s0 + k]) {
+            if (in[k]) {
                 const float f = ex2(st[k].x - at);
                 L = fmaf(f, st[k].y, L);
                 a[0] = fmaf(f, v[k].x, a[0]);
@@ -1101,7 +1123,7 @@ static pkv_status launch_tile(TileParams &tp, const void *k_cache, const void *v
     const uint32_t half = uint32_t((dev.max_smem_optin + 1024) / 2 - 1024), all = uint32_t(dev.max_smem_optin);
     auto depth = [&](uint32_t room) {
         int n = kMtMaxSlots;
-        while (n > 0 && mt_layout(D, n, p.B, tp.cu != nullptr).total > room) --n;
+        while (n > 0 && mt_layout(D, n, p.B, tp.cu != nullptr, tp.merge == 1).total > room) --n;
         return n;
     };
     int ctas = 2, n = depth(half);
@@ -1112,11 +1134,8 @@ static pkv_status launch_tile(TileParams &tp, const void *k_cache, const void *v
     if (n < 3) return PKV_EUNSUPPORTED;
     p.nst = n;
     p.seg_cost = kMtSegCost;
-    const uint32_t total = mt_layout(D, n, p.B, tp.cu != nullptr).total;
+    const uint32_t total = mt_layout(D, n, p.B, tp.cu != nullptr, tp.merge == 1).total;
     int grid = std::min(dev.sm_count * ctas, kMaxSlots);
-    // Few segments for the CTAs: their pieces are merged by a second kernel.
-    const int64_t seen = std::min<int64_t>(p.len_limit, int64_t(p.window) + p.sinks + tp.tile);
-    tp.split = int64_t(p.B) * p.nhg * kMtSplit <= grid && seen > kMtSplit * (kMtMinSlice + kMtSegCost) * kMtKeys;
     if (num_workers > 0) grid = std::min((num_workers + team_warps(16) - 1) / team_warps(16), kMaxSlots);
     CUtensorMap qmap, kmap, vmap;
     const int64_t rows = int64_t(p.NB) * p.bs;
@@ -1124,16 +1143,18 @@ static pkv_status launch_tile(TileParams &tp, const void *k_cache, const void *v
         !cached_cache_map(&kmap, dev.device, k_cache, false, D, p.Hkv, rows, 1, p.boxtok, 1) ||
         !cached_cache_map(&vmap, dev.device, v_cache, false, D, p.Hkv, rows, 1, p.boxtok, 1))
         return PKV_ECUDA;
-    auto kern = mask_tile_kernel<D>;
-    if (!ensure_smem_attribute<D, 16, kBf16, true, true, true>(kern, dev.device, total)) return PKV_ECUDA;
+    auto kern = tp.merge == 1 ? mask_tile_kernel<D, true> : mask_tile_kernel<D, false>;
+    if (!(tp.merge == 1 ? ensure_smem_attribute<D, 16, kBf16, true, true, true>(kern, dev.device, total)
+                        : ensure_smem_attribute<D, 15, kBf16, true, true, true>(kern, dev.device, total)))
+        return PKV_ECUDA;
     const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kMtThreads), total, stream, qmap, kmap, vmap, tp);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return cuda_fail("mask_tile_kernel launch", e);
     }
     const pkv_status st = launch_status("mask_tile_kernel launch");
-    if (st != PKV_OK || !tp.split) return st;
-    const size_t bytes = size_t(8 + kMaxSlots + 1 + p.B + 1) * 4 + size_t(p.B) * 2;
+    if (st != PKV_OK || tp.merge != 2) return st;
+    const size_t bytes = size_t(8 + kMaxSlots + 1 + p.B + 1) * 4 + size_t(p.B) * 2;  // (few segments: a few KiB)
     const cudaError_t em = launch_pdl(mask_merge_kernel<D>, dim3(D / 4, unsigned(p.B * p.nhg)), dim3(kMtMergeThreads), bytes,
                                       stream, tp, grid);
     if (em != cudaSuccess) {
@@ -1151,7 +1172,7 @@ int32_t mask_tile_entries(int32_t num_seqs, int32_t num_rows, int32_t per_seq, i
 
 bool mask_tile_fits(int D, int32_t entries, bool ragged, int max_smem)
 {
-    return mt_layout(D, 3, entries, ragged).total <= uint32_t(max_smem);
+    return mt_layout(D, 3, entries, ragged, true).total <= uint32_t(max_smem);
 }
 
 pkv_status mask_tile_call(DecodeParams &p, const void *k_cache, const void *v_cache, const int32_t *cu, int32_t num_seqs,
@@ -1170,8 +1191,6 @@ pkv_status mask_tile_call(DecodeParams &p, const void *k_cache, const void *v_ca
     tp.max_new = max_new;
     p.B = mask_tile_entries(num_seqs, num_rows, per_seq, tp.tile);
     const WsLayout ws = ws_layout(p.B, 16, p.Hkv, head_dim, true);
-    p.ws_count = reinterpret_cast<unsigned long long *>(workspace + ws.count_off);
-    p.ws_bal = reinterpret_cast<BalanceState *>(workspace + ws.bal_off);
     p.ws_ml = reinterpret_cast<float *>(workspace + ws.ml_off);
     p.ws_acc = reinterpret_cast<float *>(workspace + ws.acc_off);
     p.hg = 1;
@@ -1180,14 +1199,29 @@ pkv_status mask_tile_call(DecodeParams &p, const void *k_cache, const void *v_ca
     p.boxtok = std::min(kMtKeys, p.bs);
     p.nbox = kMtKeys / p.boxtok;
     p.lg_nbox = ilog2(p.nbox);
-    tp.p = p;
-    if (ws.count_clear) {  // counters outside the fixed region start at zero (see WsLayout)
-        const cudaError_t e = cudaMemsetAsync(p.ws_count, 0, ws.count_bytes, stream);
-        if (e != cudaSuccess) {
-            cudaGetLastError();
-            return cuda_fail("cudaMemsetAsync (arrival counters)", e);
+    const int64_t seen = std::min<int64_t>(p.len_limit, int64_t(p.window) + p.sinks + tp.tile);
+    const int64_t segments = int64_t(p.B) * p.nhg;
+    const int ctas = 2 * dev.sm_count;
+    if ((seen + kMtKeys - 1) / kMtKeys + 2 <= (segments >= ctas ? kMtWholeMany : kMtWhole)) {
+        tp.merge = 0;
+        tp.snap = INT32_MAX / 2;
+    } else if (segments * kMtFew <= ctas) {
+        tp.merge = 2;
+        tp.snap = kMtSnapFew;
+    } else {
+        tp.merge = 1;
+        tp.snap = kMtSnap;
+        p.ws_count = reinterpret_cast<unsigned long long *>(workspace + ws.count_off);
+        p.ws_bal = reinterpret_cast<BalanceState *>(workspace + ws.bal_off);
+        if (ws.count_clear) {  // counters outside the fixed region start at zero (see WsLayout)
+            const cudaError_t e = cudaMemsetAsync(p.ws_count, 0, ws.count_bytes, stream);
+            if (e != cudaSuccess) {
+                cudaGetLastError();
+                return cuda_fail("cudaMemsetAsync (arrival counters)", e);
+            }
         }
     }
+    tp.p = p;
     return head_dim == 64 ? launch_tile<64>(tp, k_cache, v_cache, dev, num_workers, stream)
                           : launch_tile<128>(tp, k_cache, v_cache, dev, num_workers, stream);
 }

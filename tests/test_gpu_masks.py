@@ -245,6 +245,104 @@ def test_few_long_sequences(Hq, Hkv, D, bs, lens, new):
         assert torch.equal(out, attend(prob, (md,), "tree", workers=workers, dev=dev, ws=ws))
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,B,top", [(16, 8, 128, 40, 4000), (14, 2, 64, 48, 3000), (32, 8, 128, 16, 4000)])
+def test_many_long_sequences(Hq, Hkv, D, B, top):
+    """Segments of several pieces, more of them than CTAs: the CTAs that complete them merge.  Pages end in the middle of
+    a unit, and what lies behind a sequence's last token is not a number: every copy has to have landed before those
+    rows are overwritten, time after time."""
+    rng = np.random.default_rng(B)
+    lens = [int(L) for L in rng.integers(500, top, B)]
+    new = [20] * B
+    masks = random_trees(new, 1, rng)
+    prob = Problem("bf16", [tree_sees(L, 20, masks[20 * b:20 * b + 20]) for b, L in enumerate(lens)], Hq, Hkv, D, 256, seed=B)
+    md, dev = torch.from_numpy(masks).cuda(), prob.cuda()
+    ws = pkv.alloc_attention_workspace(20 * B, Hq, Hkv, D)
+    big = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for uniform in (20, 0):
+        first = attend(prob, (md,), "tree", uniform=uniform, dev=dev, ws=ws)
+        check(first, prob, "many", long_runs=True)
+        for i in range(20):
+            if i % 2:
+                big.fill_(i)  # (the caches have to come from memory again)
+            assert torch.equal(first, attend(prob, (md,), "tree", uniform=uniform, dev=dev, ws=ws))
+    prob.sees = [window_sees(L, 20, 2000, 70) for L in lens]
+    check(attend(prob, (2000, 70), dev=dev, ws=ws), prob, "windows", long_runs=True)
+
+
+# ------------------------------------------------------------------------------------------ arguments of every kind
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("scale", [-0.07, 0.0])
+def test_scales_of_either_sign(cache, scale):
+    lens = [3, 64, 130, 700]
+    prob = Problem(cache, [window_sees(L, 1, 90, 4) for L in lens], 16, 8, 64, 32, seed=1)
+    prob.scale = scale
+    check(decode(prob, 90, 4), prob, "decode")
+    for n in (3, 40) if cache != "fp8" else ():
+        prob = Problem(cache, [window_sees(L, min(L, n), 90, 4) for L in lens], 16, 8, 64, 32, seed=n)
+        prob.scale = scale
+        check(attend(prob, (90, 4)), prob, f"window {n}", long_runs=True)
+        masks = random_trees([min(L, n) for L in lens], 2, np.random.default_rng(n))
+        cu = np.concatenate([[0], np.cumsum(prob.new)])
+        prob.sees = [tree_sees(L, m, masks[a:a + m]) for L, m, a in zip(lens, prob.new, cu)]
+        prob = Problem(cache, prob.sees, 16, 8, 64, 32, seed=n)
+        prob.scale = scale
+        check(attend(prob, (torch.from_numpy(masks).cuda(),), "tree"), prob, f"tree {n}", long_runs=True)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "int8"])
+@pytest.mark.parametrize("n", [4, 33])
+def test_outputs_queries_and_masks_at_their_least_alignment(cache, n):
+    """q and out begin 16 bytes after a boundary of 32, the mask 4 after one of 8; what surrounds out stays."""
+    lens = [40, 300, 77]
+    masks = random_trees([n] * 3, 2, np.random.default_rng(n))
+    prob = Problem(cache, [tree_sees(L, n, masks[b * n:b * n + n]) for b, L in enumerate(lens)], 14, 2, 64, 16, seed=n)
+    q, c, bt, ld, cu = prob.cuda()
+    T = q.shape[0]
+    place = lambda t, pad: torch.full((t.numel() + 2 * pad,), -7, dtype=t.dtype, device="cuda")
+    qb, ob, mb = place(q, 8), place(q, 8), place(torch.from_numpy(masks), 1)
+    qb[8:-8], mb[1:-1] = q.flatten(), torch.from_numpy(masks).cuda().flatten()
+    view = lambda b: b[8:-8].view(T, 14, 64)
+    ws = pkv.alloc_attention_workspace(T, 14, 2, 64)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    fn = pkv.paged_attention_tree if cache == "bf16" else pkv.paged_attention_tree_i8
+    for uniform in (0, n):
+        ob.fill_(-7)
+        fn(view(qb), *c, bt, None if uniform else cu, ld, mb[1:-1].view(T, 2), prob.scale, view(ob), ws, err_word=err,
+           new_per_seq=uniform)
+        assert err.item() == 0 and (ob[:8] == -7).all() and (ob[-8:] == -7).all()
+        check(view(ob), prob, f"uniform {uniform}", long_runs=True)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "int8"])
+@pytest.mark.parametrize("cu", [[0, 40, 20, 90], [0, 90, 90, 10, 90], [3, 30, 90], [0, -3, 90], [0, 30, 60], [0, 0, 0],
+                                [0, 30, 95], [0, 10, 90]])
+def test_offsets_that_do_not_fit(cache, cu):
+    """Flagged; rows of no sequence, of sequences that do not fit, or of offsets out of order give zeros, and the
+    others what they give alone."""
+    T, Hq, Hkv, D = 90, 8, 2, 64
+    lens = [70] * (len(cu) - 1)
+    prob = Problem(cache, [window_sees(70, 1, 4000, 0)] * len(lens), Hq, Hkv, D, 16, seed=5)
+    _, c, bt, ld, _ = prob.cuda()
+    prob.q = torch.randn(T, Hq, D, generator=torch.Generator().manual_seed(1)).bfloat16()
+    order = cu[0] == 0 and all(a <= b for a, b in zip(cu, cu[1:]))
+    prob.sees, want_zero = [], []
+    for a, b, L in zip(cu, cu[1:], lens):
+        if order:
+            good = b - a <= L and b <= T
+            prob.sees.append(window_sees(L, b - a, 33, 2) if good else np.zeros((min(b, T) - a, L), bool))
+            want_zero += range(a, min(b, T)) if not good else ()
+    if not order:
+        prob.sees, prob.bt, want_zero = [np.zeros((T, 70), bool)], prob.bt[:1], range(T)
+    elif cu[-1] < T:
+        prob.sees.append(np.zeros((T - cu[-1], 70), bool))
+        prob.bt = np.concatenate([prob.bt, prob.bt[:1]])
+        want_zero += range(cu[-1], T)
+    off = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    out = attend(prob, (33, 2), err_is=pkv.ERR_CONTEXT_RANGE, dev=(prob.q.cuda(), c, bt, ld, off))
+    assert not out[list(want_zero)].any()
+    check(out, prob, str(cu), long_runs=True)
+
+
 # ------------------------------------------------------------------------------------------ what the device refuses
 def test_bad_pages_lengths_and_offsets_are_flagged():
     prob = Problem("bf16", [window_sees(L, 1, 30, 2) for L in (100, 200)], 4, 2, 64, 16, seed=0)
