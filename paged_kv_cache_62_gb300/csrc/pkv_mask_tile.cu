@@ -85,7 +85,7 @@ __host__ __device__ inline MtLayout mt_layout(int D, int nslots, int B, bool seq
     l.off_q = o;
     o += 128u * uint32_t(D) * 2u;
     l.off_bar = o;
-    o += uint32_t(2 * kMtMaxSlots + 10 + 2 * kMtDescs) * 8u;
+    o += uint32_t(2 * kMtMaxSlots + 12 + 2 * kMtDescs) * 8u;
     l.off_desc = o;
     o += uint32_t(kMtDescs * sizeof(MtDesc));
     l.off_bound = o;
@@ -276,6 +276,42 @@ __device__ __forceinline__ int mt_slice_of(const int32_t *bound, int nsl, int s,
             hi = mid;
     }
     return lo;
+}
+
+// Two fp32 values an instruction, and the largest of three.
+__device__ __forceinline__ uint64_t mt_two(float lo, float hi)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+
+__device__ __forceinline__ float2 mt_parts(uint64_t v)
+{
+    float2 p;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(p.x), "=f"(p.y) : "l"(v));
+    return p;
+}
+
+__device__ __forceinline__ uint64_t mt_fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t mt_add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float mt_max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // 32 bytes to a 16-byte aligned place (one store where it is 32-byte aligned).
@@ -509,8 +545,13 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
 #pragma unroll
             for (int j = 0; j < 4; ++j) mx4[j] = __uint_as_float(r[j]);
 #pragma unroll
-            for (int j = 4; j < kMtKeys; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(r[j]));
-            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c;
+            for (int j = 4; j < kMtKeys - 4; j += 8)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mx4[i] = mt_max3(mx4[i], __uint_as_float(r[j + i]), __uint_as_float(r[j + 4 + i]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx4[i] = fmaxf(mx4[i], __uint_as_float(r[kMtKeys - 4 + i]));
+            const float mx = fmaxf(mt_max3(mx4[0], mx4[1], mx4[2]), mx4[3]) * c;
             float alpha = 1.0f;
             bool resc = false;
             if (mx > mrun + kRescaleSlack) {  // also the row's first unit with a key (mrun = -inf)
@@ -534,21 +575,28 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
                 }
             }
             const float mneg = mrun == -INFINITY ? 0.f : -mrun;
-            float ps[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t w[kMtKeys / 2];
+            const uint64_t c2 = mt_two(c, c), m2 = mt_two(mneg, mneg);
+            uint64_t ps[2] = {0ull, 0ull};
 #pragma unroll
-            for (int j = 0; j < kMtKeys / 2; ++j) {
-                const float p0 = ex2(fmaf(__uint_as_float(r[2 * j]), c, mneg));
-                const float p1 = ex2(fmaf(__uint_as_float(r[2 * j + 1]), c, mneg));
-                ps[j & 3] += p0 + p1;
-                w[j] = pack_bf16x2(p0, p1);
+            for (int h = 0; h < 2; ++h) {  // 32 keys at a time: the first half's output product runs beside the second
+                uint32_t w[kMtKeys / 4];
+#pragma unroll
+                for (int j = 0; j < kMtKeys / 4; ++j) {
+                    const int e = 32 * h + 2 * j;
+                    const float2 x =
+                        mt_parts(mt_fma2(mt_two(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2, m2));
+                    const float p0 = ex2(x.x), p1 = ex2(x.y);
+                    ps[j & 1] = mt_add2(ps[j & 1], mt_two(p0, p1));
+                    w[j] = pack_bf16x2(p0, p1);
+                }
+                tmem_st16(sbuf + uint32_t(16 * h), w);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m.pfull[2 * (k & 1u) + h]);
             }
-            lrun += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-            tmem_st32(sbuf, w);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&m.pfull[k & 1u]);
+            const float2 pa = mt_parts(ps[0]), pb = mt_parts(ps[1]);
+            lrun += (pa.x + pa.y) + (pb.x + pb.y);
         }
         // The segment's part here ends, with the last output product.
         uint16_t *orow = row_ok ? p.out + ((long long)(row0 + qi) * p.Hq + (long long)sg.g * p.gq + qh) * D : nullptr;
@@ -654,13 +702,18 @@ __device__ void mt_products(const DecodeParams &p, const MtSmem &m, uint32_t rin
         return true;
     };
     auto output = [&](uint32_t b, uint32_t ph, bool first) {
-        if (!wait(m.pfull + b, ph) || !wait(m.full + vs, vph)) return false;
+        if (!wait(m.pfull + 2 * b, ph) || !wait(m.full + vs, vph)) return false;
         tc_fence_after();
         const uint64_t vd = vdesc + vs * kSlot16;
         const uint32_t pa = tmem + b * kMtKeys, d = tmem + kMtOCol;
 #pragma unroll
-        for (int i = 0; i < kMtKeys / 16; ++i)
+        for (int i = 0; i < kMtKeys / 16; ++i) {
+            if (i == kMtKeys / 32) {
+                if (!wait(m.pfull + 2 * b + 1, ph)) return false;
+                tc_fence_after();
+            }
             tc_mma_bf16_ta(d, pa + uint32_t(8 * i), vd + uint32_t(i) * (2048 / 16), IP, i > 0 || !first);
+        }
         tc_commit_at(odone + 8 * b);
         tc_commit_at(empty + 8 * vs);
         vs += 2;
@@ -937,7 +990,7 @@ __global__ void __launch_bounds__(kMtThreads, 2)
     m.empty = m.full + kMtMaxSlots;
     m.sfull = m.empty + kMtMaxSlots;
     m.pfull = m.sfull + 2;
-    m.odone = m.pfull + 2;
+    m.odone = m.pfull + 4;
     m.qready = m.odone + 2;
     m.drain = m.qready + 1;
     m.team = m.drain + 1;
@@ -958,7 +1011,8 @@ __global__ void __launch_bounds__(kMtThreads, 2)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&m.sfull[i], 1);
-            mbar_init(&m.pfull[i], kMtSoftmaxWarps);
+            mbar_init(&m.pfull[2 * i], kMtSoftmaxWarps);
+            mbar_init(&m.pfull[2 * i + 1], kMtSoftmaxWarps);
             mbar_init(&m.odone[i], 1);
         }
         for (int i = 0; i < kMtDescs; ++i) {
