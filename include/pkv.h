@@ -563,6 +563,11 @@ PKV_API pkv_status pkv_paged_attention_i8(const uint16_t *q, const int8_t *k_cac
  * and errors as the calls without window; max_context_len at most 2^30 (PKV_EBOUNDS).  Where a
  * call's queries share a pass, K and V of a key that one of them sees should be finite: an
  * infinity or NaN there may reach the others.
+ * Several new tokens over bf16 caches: with new_per_seq n, n * num_q_heads / num_kv_heads
+ * <= 16, as pkv_paged_attention's single pass.  Else in tiles of 128 / (num_q_heads /
+ * num_kv_heads) queries on the tensor cores, the softmax's weights rounded to bf16 (2^-8 of a
+ * weight at most); num_workers then counts eighths of a CTA of the tile kernel, and 0 takes
+ * two CTAs an SM.
  */
 PKV_API pkv_status pkv_paged_decode_window(
     const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
@@ -607,9 +612,11 @@ PKV_API pkv_status pkv_paged_attention_window_i8(
  *               word t / 32; bits of later nodes (t > i) are ignored.  A node
  *               sees itself only if its own bit is set.
  * A row that sees no key (L = n and an empty mask) gives zeros.  The mask of a
- * chain is its lower triangle: the results of pkv_paged_attention.
+ * chain is its lower triangle: the results of pkv_paged_attention (to rounding,
+ * where another kernel runs).
  * mask_words >= 1; a sequence has at most 32 * mask_words nodes (new_per_seq
  * beyond: PKV_EINVAL; offsets beyond: zeros and PKV_ERR_CONTEXT_RANGE).
+ * Tiles and roundings over bf16 caches as pkv_paged_attention_window.
  * Workspace: pkv_paged_attention_i8_workspace_size bytes, whatever the cache.
  * Other limits, sharing of passes and errors as pkv_paged_attention;
  * max_context_len at most 2^30 (PKV_EBOUNDS).  (The pages have no counterpart.)

@@ -543,8 +543,8 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     // rows hold.)
     const int32_t tile = 128 / std::min(num_q_heads / num_kv_heads, 128);
     // (Masked calls over bf16 caches: mask_tile_kernel reads the keys once, at any number of new tokens.  64 sequences of
-    // 512-4096, 16 / 8 heads of 128: 12 nodes each 115 us against 224 on regular CTAs, 1 to 4 nodes 105 against 112; two
-    // sequences of 9 nodes 38 against 159; 256 sequences of 50-300 with 1 to 4 nodes 63 against 54.)
+    // 512-4096, 16 / 8 heads of 128: 12 nodes each 114 us against 224 on regular CTAs, 1 to 4 nodes 105 against 112; two
+    // sequences of 9 nodes 24 against 159; 256 sequences of 50-300 with 1 to 4 nodes 53 against 54.)
     bool qs = (mask && ct == kBf16) || int64_t(num_rows) > 2 * int64_t(qg) * num_seqs;
     if (ct == kI8 && !qs && int64_t(num_rows) > int64_t(qg) * num_seqs) {
         // Between one and two chunks a sequence: regular CTAs read the keys twice, but take larger calls as fast; in

@@ -1,5 +1,6 @@
 // Masked attention for several new tokens per sequence on the 5th-generation tensor cores: sliding windows with sinks
-// and trees of drafted tokens over bf16 caches, sequences of more than two chunks of queries (see attention_call).
+// and trees of drafted tokens over bf16 caches, but for calls whose sequences' new tokens all fit one pass of the decode
+// kernel (see attention_call).
 //
 // An entry is up to 128 / gq consecutive queries of a sequence; with the gq query heads of a kv head they are the up to
 // 128 rows of a tile (row r: query r / gq, head r % gq).  A unit is 64 keys of an (entry, kv head) segment; the unit
@@ -17,13 +18,16 @@
 //
 // Warps: 0-3 softmax (thread t is row t of the tile and TMEM lane t), 4 issues the products (one thread), 5 the copies
 // of K and V.  Ordering (unit k of the CTA's list, buffer k % 2): copy landed -> full[slot]; scores -> sfull[k % 2] and
-// the K slot free (commits); weights written, over their scores -> pfull[k % 2] (4 warps); output product ->
+// the K slot free (commits); weights written, over their scores -> pfull[k % 2][half] (4 warps); output product ->
 // odone[k % 2] and the V slot free; a segment's Q landed -> qready (its copy is issued once the last scores that read
 // the one before are in).  S(k) is issued when P(k - 2) V is done, P(k - 1) V after S(k), or before it where unit k
-// opens a segment.  Every barrier's next phase needs its waiter's own next step, so none runs two phases ahead.
+// opens a segment.  The weights go out 32 keys at a time, so that the first half's product runs beside the second
+// half's exponentials (32-node trees of 64 sequences 106.4 us, so 104.7).  Every barrier's next phase needs its waiter's
+// own next step, so none runs two phases ahead; the softmax warps, which see only some V tiles, look at their barrier
+// after the unit's scores, which come behind the slot's item before.
 //
 // The list is cut into equal slices, one a CTA.  Slices, and with them the sums' order, depend on the list and the grid
-// alone: the results repeat bit for bit.  The pieces of a segment that lies in several slices are merged
+// alone: the results repeat bit for bit.  Pieces of a segment that lies in several slices are merged
 //   - by the CTA that completes it (MERGE).  A piece costs its CTA two meetings of its warps, a fence and a counter,
 //     and the last one a trip through L2 for every other piece, so bounds move to a segment's start or end that is near;
 //   - or, where segments are few and their pieces many, by a second kernel (mask_merge_kernel): the merges of one CTA
@@ -33,6 +37,13 @@
 // Where segments are short, slices end at their starts and there is nothing to merge.  The copying warp walks the list
 // and hands each segment to the others in shared memory (MtDesc), the next one before it copies the last unit of this
 // one.
+//
+// What bounds it (64 sequences of 512-4096, 16 / 8 heads of 128, 1.95 GHz): 32-node trees, 604 MB, 109 us of 88.8 at the
+// copy rate; 64-token chunks under a window of 1024, 63 us of 45; whole prompts of 1-2048 tokens under a window of 512,
+// 57 us of 15 at the products' rate.  A unit takes a CTA 2000-2200 cycles: softmax 1000, a wait of 500-900 for the next
+// scores, which share one tensor pipe with the other CTA's products and wait for the output product that reads the
+// same columns, masks and instruction fetch 400.  Tensor memory holds no third score buffer at head_dim 128.  A
+// segment's end costs 5000 to 7000 cycles: its last product, 128 rows of 256 bytes, the first unit's masks.
 #include "pkv_decode_kernel.cuh"
 
 namespace pkv {
@@ -68,10 +79,10 @@ struct TileParams {
 };
 
 // A segment's part in the CTA's slice, as the softmax warps and the issuing one see it: units u .. u + len - 1 of the n
-// of entry b and kv head g (len 0: no more), the segment's start in the list, whether it is the
-// slice's first (see tc5_piece_tile), and what its entry says.
+// of an entry and kv head g (len 0: no more), the segment's start in the list, whether it is the slice's first (see
+// mt_piece), and what its entry says.
 struct alignas(16) MtDesc {
-    int32_t b, g, u, n, len, x0, first, L, cnt, row0, base;
+    int32_t g, u, n, len, x0, first, L, cnt, row0, base;
 };
 
 struct MtLayout {
@@ -314,6 +325,15 @@ __device__ __forceinline__ float mt_max3(float a, float b, float c)
     return r;
 }
 
+// A segment's piece of a slice, as tc5_piece_tile, with the entry's first row in the entry's place: entries that have
+// rows have different first rows, in the list's order, so a workspace for num_rows entries does, however many sequences
+// have no rows.  The arrival counters are numbered alike.
+__device__ __forceinline__ long long mt_piece(const TileParams &tp, int slice, bool slice_first, int32_t row0, int g)
+{
+    return slots_by_slice(tp.num_rows, tp.p.nhg) ? 2LL * slice + (slice_first ? 0 : 1)
+                                                 : slice + (long long)row0 * tp.p.nhg + g;
+}
+
 // 32 bytes to a 16-byte aligned place (one store where it is 32-byte aligned).
 __device__ __forceinline__ void store32(uint16_t *dst, const uint32_t (&v)[8], bool wide)
 {
@@ -361,16 +381,17 @@ __device__ __forceinline__ void mt_output(float l, uint32_t o, uint16_t *out)
 // Every load is a trip to the other pieces' SMs' side of L2 and nothing else hides it, so (m, l) come four pieces at a
 // time and sums, 32 columns a step, a piece ahead.
 template <int D>
-__device__ __forceinline__ void mt_merge(const DecodeParams &p, const int32_t *bound, int sf, int sl, int own, int32_t x0,
-                                         int g, int b, int row, float m, float l, uint32_t o, uint16_t *out)
+__device__ __forceinline__ void mt_merge(const TileParams &tp, const int32_t *bound, int sf, int sl, int own, int32_t x0,
+                                         int g, int32_t row0, int row, float m, float l, uint32_t o, uint16_t *out)
 {
+    const DecodeParams &p = tp.p;
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
     auto next = [&](int sk) {  // the next slice that is not empty (an empty one left nothing)
         do ++sk;
         while (sk <= sl && bound[sk + 1] <= bound[sk]);
         return sk;
     };
-    auto tile_of = [&](int sk) { return tc5_piece_tile(p, sk, x0 <= bound[sk], b, g); };
+    auto tile_of = [&](int sk) { return mt_piece(tp, sk, x0 <= bound[sk], row0, g); };
     auto state = [&](int sk) { return sk == own || sk > sl ? make_float2(m, l) : __ldcg(ml + tile_of(sk) * 128 + row); };
     const bool wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
     const int s0 = next(sf - 1);
@@ -494,7 +515,7 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
         // token units that every query sees whole
         const int32_t all0 = (max(L - p.window, 0) + kMtKeys - 1) / kMtKeys;
         const int32_t all1 = (p.tree ? min(L - cnt + 1, base) : L - cnt + 1) / kMtKeys;
-        [[maybe_unused]] auto ctr = [&]() { return p.ws_count + ((long long)sg.b * p.Hkv + sg.g) * p.sub; };
+        [[maybe_unused]] auto ctr = [&]() { return p.ws_count + ((long long)row0 * p.Hkv + sg.g) * p.sub; };
         [[maybe_unused]] unsigned long long arrived = 0;
         float mrun = -INFINITY, lrun = 0.f;
         for (int i = 0; i < len; ++i, ++k) {
@@ -621,7 +642,7 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
         tc_fence_after();
         if (!done) {
             // a piece: (m, l, O) of every row into the slice's piece tile
-            const long long tile = tc5_piece_tile(p, slice, sg.first != 0, sg.b, sg.g);
+            const long long tile = mt_piece(tp, slice, sg.first != 0, row0, sg.g);
             float4 *dst = reinterpret_cast<float4 *>(p.ws_acc + tile * 128 * D) + t;
 #pragma unroll 1
             for (int cc = 0; cc < D; cc += 32) {
@@ -649,8 +670,8 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
         } else if constexpr (MERGE) {
             if (done) {
                 __threadfence();
-                mt_merge<D>(p, bound, mt_slice_of(bound, sl.nsl, slice, sg.x0 + p.seg_cost),
-                            mt_slice_of(bound, sl.nsl, slice, sg.x0 + p.seg_cost + sg.n - 1), slice, sg.x0, sg.g, sg.b, t,
+                mt_merge<D>(tp, bound, mt_slice_of(bound, sl.nsl, slice, sg.x0 + p.seg_cost),
+                            mt_slice_of(bound, sl.nsl, slice, sg.x0 + p.seg_cost + sg.n - 1), slice, sg.x0, sg.g, row0, t,
                             mrun, lrun, tlane + kMtOCol, orow);
             }
             if (!meet()) return;  // sh[1] is read before it is written again
@@ -778,7 +799,8 @@ __device__ void mt_copies(const TileParams &tp, const MtSmem &m, uint8_t *ring, 
             return;
         }
         if (lane == 0) {
-            m.desc[d] = MtDesc{x.s.b, x.s.g, x.s.u, x.s.n, end ? 0 : x.s.len, x.s.x0, x.s.x0 <= rg.lo, x.e.L, x.e.cnt, x.e.row0, x.e.base};
+            m.desc[d] = MtDesc{x.s.g, x.s.u,   x.s.n,   end ? 0 : x.s.len, x.s.x0, x.s.x0 <= rg.lo,
+                               x.e.L, x.e.cnt, x.e.row0, x.e.base};
             mbar_arrive(&m.dfull[d]);
         }
         ++told;
@@ -1116,7 +1138,7 @@ __global__ void __launch_bounds__(kMtMergeThreads) mask_merge_kernel(const __gri
         for (int k = 0; k < 8; ++k) {
             const int s = min(s0 + k, end);
             in[k] = s0 + k <= end && bound[s + 1] > bound[s];  // (an empty slice left nothing)
-            const long long tile = tc5_piece_tile(p, s, x0 <= bound[s], b, g);
+            const long long tile = mt_piece(tp, s, x0 <= bound[s], e.row0, g);
             st[k] = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml) + tile * 128 + row);
             v[k] = __ldcg(reinterpret_cast<const float4 *>(p.ws_acc + tile * 128 * D) + c4 * 128 + row);
         }
@@ -1244,7 +1266,7 @@ pkv_status mask_tile_call(DecodeParams &p, const void *k_cache, const void *v_ca
     tp.per_entry = per_seq > 0 ? (per_seq + tp.tile - 1) / tp.tile : 0;
     tp.max_new = max_new;
     p.B = mask_tile_entries(num_seqs, num_rows, per_seq, tp.tile);
-    const WsLayout ws = ws_layout(p.B, 16, p.Hkv, head_dim, true);
+    const WsLayout ws = ws_layout(num_rows, 16, p.Hkv, head_dim, true);  // (see mt_piece)
     p.ws_ml = reinterpret_cast<float *>(workspace + ws.ml_off);
     p.ws_acc = reinterpret_cast<float *>(workspace + ws.acc_off);
     p.hg = 1;

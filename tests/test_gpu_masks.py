@@ -269,6 +269,26 @@ def test_many_long_sequences(Hq, Hkv, D, B, top):
     check(attend(prob, (2000, 70), dev=dev, ws=ws), prob, "windows", long_runs=True)
 
 
+@pytest.mark.parametrize("cache", ["bf16", "int8"])
+@pytest.mark.parametrize("B,Hkv", [(400, 8), (300, 2), (70, 1)])
+def test_most_sequences_without_new_tokens(cache, B, Hkv):
+    """A workspace for the rows does, whatever the number of sequences: what lies behind it stays."""
+    lens = [5000 + 13 * b if b % (B // 10) == 3 else 40 for b in range(B)]
+    new = [1 + b % 3 if L > 40 else 0 for b, L in enumerate(lens)]
+    masks = random_trees(new, 1, np.random.default_rng(B))
+    cu = np.concatenate([[0], np.cumsum(new)])
+    prob = Problem(cache, [tree_sees(L, n, masks[a:a + n]) for L, n, a in zip(lens, new, cu)], 2 * Hkv, Hkv, 64, 64, seed=B)
+    n = pkv.alloc_attention_workspace(sum(new), 2 * Hkv, Hkv, 64).numel()
+    whole = torch.zeros(n + (1 << 22), dtype=torch.uint8, device="cuda")
+    whole[n:] = 0xA5
+    dev, md = prob.cuda(), torch.from_numpy(masks).cuda()
+    first = attend(prob, (md,), "tree", dev=dev, ws=whole[:n])
+    check(first, prob, "few rows", long_runs=True)
+    for workers in (0, 4096):
+        check(attend(prob, (md,), "tree", dev=dev, ws=whole[:n], workers=workers), prob, f"workers {workers}", long_runs=True)
+    assert (whole[n:] == 0xA5).all()
+
+
 # ------------------------------------------------------------------------------------------ arguments of every kind
 @pytest.mark.parametrize("cache", ["bf16", "fp8", "int8"])
 @pytest.mark.parametrize("scale", [-0.07, 0.0])
