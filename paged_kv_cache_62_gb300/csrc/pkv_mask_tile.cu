@@ -75,14 +75,15 @@ struct TileParams {
     int32_t per_entry;    // null cu: entries of a sequence
     int32_t max_new;
     int32_t snap;         // see kMtSnap, kMtWhole
+    bool ctr_by_row;      // arrival counters by the entry's first row, not by entry
     int32_t merge;        // 1: the CTA that completes a segment merges it; 2: a second kernel does; 0: nothing to merge
 };
 
 // A segment's part in the CTA's slice, as the softmax warps and the issuing one see it: units u .. u + len - 1 of the n
-// of an entry and kv head g (len 0: no more), the segment's start in the list, whether it is the slice's first (see
+// of entry b and kv head g (len 0: no more), the segment's start in the list, whether it is the slice's first (see
 // mt_piece), and what its entry says.
 struct alignas(16) MtDesc {
-    int32_t g, u, n, len, x0, first, L, cnt, row0, base;
+    int32_t b, g, u, n, len, x0, first, L, cnt, row0, base;
 };
 
 struct MtLayout {
@@ -327,7 +328,7 @@ __device__ __forceinline__ float mt_max3(float a, float b, float c)
 
 // A segment's piece of a slice, as tc5_piece_tile, with the entry's first row in the entry's place: entries that have
 // rows have different first rows, in the list's order, so a workspace for num_rows entries does, however many sequences
-// have no rows.  The arrival counters are numbered alike.
+// have no rows.
 __device__ __forceinline__ long long mt_piece(const TileParams &tp, int slice, bool slice_first, int32_t row0, int g)
 {
     return slots_by_slice(tp.num_rows, tp.p.nhg) ? 2LL * slice + (slice_first ? 0 : 1)
@@ -515,7 +516,7 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
         // token units that every query sees whole
         const int32_t all0 = (max(L - p.window, 0) + kMtKeys - 1) / kMtKeys;
         const int32_t all1 = (p.tree ? min(L - cnt + 1, base) : L - cnt + 1) / kMtKeys;
-        [[maybe_unused]] auto ctr = [&]() { return p.ws_count + ((long long)row0 * p.Hkv + sg.g) * p.sub; };
+        [[maybe_unused]] auto ctr = [&]() { return p.ws_count + (long long)(tp.ctr_by_row ? row0 : sg.b) * p.Hkv + sg.g; };
         [[maybe_unused]] unsigned long long arrived = 0;
         float mrun = -INFINITY, lrun = 0.f;
         for (int i = 0; i < len; ++i, ++k) {
@@ -799,7 +800,7 @@ __device__ void mt_copies(const TileParams &tp, const MtSmem &m, uint8_t *ring, 
             return;
         }
         if (lane == 0) {
-            m.desc[d] = MtDesc{x.s.g, x.s.u,   x.s.n,   end ? 0 : x.s.len, x.s.x0, x.s.x0 <= rg.lo,
+            m.desc[d] = MtDesc{x.s.b, x.s.g, x.s.u, x.s.n, end ? 0 : x.s.len, x.s.x0, x.s.x0 <= rg.lo,
                                x.e.L, x.e.cnt, x.e.row0, x.e.base};
             mbar_arrive(&m.dfull[d]);
         }
@@ -1271,7 +1272,6 @@ pkv_status mask_tile_call(DecodeParams &p, const void *k_cache, const void *v_ca
     p.ws_acc = reinterpret_cast<float *>(workspace + ws.acc_off);
     p.hg = 1;
     p.nhg = p.Hkv;
-    p.sub = team_warps(16);
     p.boxtok = std::min(kMtKeys, p.bs);
     p.nbox = kMtKeys / p.boxtok;
     p.lg_nbox = ilog2(p.nbox);
@@ -1287,10 +1287,16 @@ pkv_status mask_tile_call(DecodeParams &p, const void *k_cache, const void *v_ca
     } else {
         tp.merge = 1;
         tp.snap = kMtSnap;
-        p.ws_count = reinterpret_cast<unsigned long long *>(workspace + ws.count_off);
         p.ws_bal = reinterpret_cast<BalanceState *>(workspace + ws.bal_off);
-        if (ws.count_clear) {  // counters outside the fixed region start at zero (see WsLayout)
-            const cudaError_t e = cudaMemsetAsync(p.ws_count, 0, ws.count_bytes, stream);
+        // Counters in the fixed region where it has one for every segment (by entry, or, with many sequences that have no
+        // rows, by row), else in the one behind it, which starts at zero (see WsLayout; the clearing costs 2 us).
+        tp.ctr_by_row = segments > int64_t(kFixedCounters);
+        const bool clear = tp.ctr_by_row && size_t(num_rows) * size_t(p.Hkv) > kFixedCounters;
+        p.ws_count = reinterpret_cast<unsigned long long *>(
+            workspace + (clear ? ws.count_off : align256(sizeof(BalanceState))));
+        if (clear) {
+            const cudaError_t e =
+                cudaMemsetAsync(p.ws_count, 0, size_t(num_rows) * size_t(p.Hkv) * sizeof(unsigned long long), stream);
             if (e != cudaSuccess) {
                 cudaGetLastError();
                 return cuda_fail("cudaMemsetAsync (arrival counters)", e);

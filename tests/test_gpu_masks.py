@@ -270,7 +270,7 @@ def test_many_long_sequences(Hq, Hkv, D, B, top):
 
 
 @pytest.mark.parametrize("cache", ["bf16", "int8"])
-@pytest.mark.parametrize("B,Hkv", [(400, 8), (300, 2), (70, 1)])
+@pytest.mark.parametrize("B,Hkv", [(400, 8), (300, 2), (70, 1), (2200, 8)])
 def test_most_sequences_without_new_tokens(cache, B, Hkv):
     """A workspace for the rows does, whatever the number of sequences: what lies behind it stays."""
     lens = [5000 + 13 * b if b % (B // 10) == 3 else 40 for b in range(B)]
@@ -287,6 +287,22 @@ def test_most_sequences_without_new_tokens(cache, B, Hkv):
     for workers in (0, 4096):
         check(attend(prob, (md,), "tree", dev=dev, ws=whole[:n], workers=workers), prob, f"workers {workers}", long_runs=True)
     assert (whole[n:] == 0xA5).all()
+
+
+def test_more_segments_than_the_fixed_counters():
+    """2100 sequences of one node each and more on 8 kv heads: counters by row, cleared by the call."""
+    B = 2100
+    lens, new = [1400 + b % 5 if b % 50 == 0 else 30 for b in range(B)], [1 + b % 3 for b in range(B)]
+    masks = random_trees(new, 1, np.random.default_rng(1))
+    cu = np.concatenate([[0], np.cumsum(new)])
+    prob = Problem("bf16", [tree_sees(L, n, masks[a:a + n]) for L, n, a in zip(lens, new, cu)], 8, 8, 64, 32, seed=1)
+    dev, md = prob.cuda(), torch.from_numpy(masks).cuda()
+    ws = pkv.alloc_attention_workspace(sum(new), 8, 8, 64)
+    ws.random_(generator=torch.Generator(device="cuda").manual_seed(0))
+    ws[:1 << 18] = 0  # (the part that has to be zero before the first use)
+    first = attend(prob, (md,), "tree", dev=dev, ws=ws)
+    check(first, prob, "many", long_runs=True)
+    assert torch.equal(first, attend(prob, (md,), "tree", dev=dev, ws=ws))
 
 
 # ------------------------------------------------------------------------------------------ arguments of every kind
