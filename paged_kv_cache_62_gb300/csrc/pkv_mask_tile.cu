@@ -38,9 +38,9 @@
 // and hands each segment to the others in shared memory (MtDesc), the next one before it copies the last unit of this
 // one.
 //
-// What bounds it (64 sequences of 512-4096, 16 / 8 heads of 128, 1.95 GHz): 32-node trees, 604 MB, 109 us of 88.8 at the
+// What bounds it (64 sequences of 512-4096, 16 / 8 heads of 128, 1.95 GHz): 32-node trees, 596 MB, 110 us of 87.7 at the
 // copy rate; 64-token chunks under a window of 1024, 63 us of 45; whole prompts of 1-2048 tokens under a window of 512,
-// 57 us of 15 at the products' rate.  A unit takes a CTA 2000-2200 cycles: softmax 1000, a wait of 500-900 for the next
+// 55 us of 15 at the products' rate.  A unit takes a CTA 2000-2200 cycles: softmax 1000, a wait of 500-900 for the next
 // scores, which share one tensor pipe with the other CTA's products and wait for the output product that reads the
 // same columns, masks and instruction fetch 400.  Tensor memory holds no third score buffer at head_dim 128.  A
 // segment's end costs 5000 to 7000 cycles: its last product, 128 rows of 256 bytes, the first unit's masks.
@@ -531,20 +531,6 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
             }
             if (!wait(&m.sfull[k & 1u], (k >> 1) & 1u)) return;
             tc_fence_after();
-            if ((e0 & e1) != 0xffffffffu) {
-                // V rows that no query sees may hold anything, and 0 * NaN is NaN: zeros there, once they have landed.
-                // (Not before the scores are in: only those tell that the slot's item before this one has landed, and a
-                // barrier two phases behind would pass for one that is done.)
-                const uint32_t item = mt_vitem(k);
-                if (!wait(&m.full[item % ns], (item / ns) & 1u)) return;
-                uint8_t *v = ring + (item % ns) * uint32_t(kMtKeys * D * 2);
-                for (int j = t; j < kMtKeys * (D / 8); j += 32 * kMtSoftmaxWarps) {
-                    const int r = (j >> 3) & (kMtKeys - 1);
-                    if (!(((r < 32 ? e0 : e1) >> (r & 31)) & 1u))
-                        *reinterpret_cast<uint4 *>(v + j * 16) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();  // for the tensor core
-            }
             if (i == len - 1) {  // the segment's last scores are in
                 if (!wait(&m.dfull[(j + 1) % kMtDescs], ((j + 1) / kMtDescs) & 1u)) return;
                 if (t == 0 && nsg.len > 0) copy_q(nsg);
@@ -610,6 +596,21 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
                     const float p0 = ex2(x.x), p1 = ex2(x.y);
                     ps[j & 1] = mt_add2(ps[j & 1], mt_two(p0, p1));
                     w[j] = pack_bf16x2(p0, p1);
+                }
+                if (h == 0 && (e0 & e1) != 0xffffffffu) {
+                    // V rows that no query sees may hold anything, and 0 * NaN is NaN: zeros there, once they have landed.
+                    // (Not before the scores are in: only those tell that the slot's item before this one has landed, and a
+                    // barrier two phases behind would pass for one that is done.  Here rather than right after them the
+                    // tile has had more time to land: 64-token chunks 60.6 us, so 59.5.)
+                    const uint32_t item = mt_vitem(k);
+                    if (!wait(&m.full[item % ns], (item / ns) & 1u)) return;
+                    uint8_t *v = ring + (item % ns) * uint32_t(kMtKeys * D * 2);
+                    for (int j = t; j < kMtKeys * (D / 8); j += 32 * kMtSoftmaxWarps) {
+                        const int r = (j >> 3) & (kMtKeys - 1);
+                        if (!(((r < 32 ? e0 : e1) >> (r & 31)) & 1u))
+                            *reinterpret_cast<uint4 *>(v + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();  // for the tensor core
                 }
                 tmem_st16(sbuf + uint32_t(16 * h), w);
                 tmem_wait_st();
