@@ -223,3 +223,55 @@ def test_a_layer_of_a_windowed_model_over_an_int8_cache():
             off = (out[r:r + n].double() - want).abs() - (2.0 ** -8 * want.abs() + 2.0 ** -10 * mag)
             assert off.max() <= 0, (step, kind, off.max().item())
             r += n
+
+
+def test_a_layer_over_a_bf16_cache():
+    """qk_norm_rope_store, then windowed prompts, decode steps and a drafted tree over one bf16 cache and workspace."""
+    from mask_reference import random_trees, tree_sees, window_sees
+    Hq, Hkv, D, bs, window, sinks = 8, 2, 128, 32, 100, 3
+    prompts = [700, 1, 140, 64]
+    B, mb = len(prompts), 24
+    bt = torch.randperm(B * mb, generator=torch.Generator().manual_seed(1)).int().cuda().view(B, mb)
+    kc, vc = (torch.full((B * mb, bs, Hkv, D), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    inv = torch.from_numpy(freqs(D)).cuda()
+    lens = [0] * B
+    ws = pkv.alloc_attention_workspace(sum(prompts), Hq, Hkv, D)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    i32 = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+    for step, (new, kind) in enumerate([(prompts, "window"), ([1] * B, "decode"), ([20] * B, "tree"), ([1] * B, "decode"),
+                                        ([3, 0, 1, 7], "window"), ([4] * B, "tree")]):
+        lens = [a + n for a, n in zip(lens, new)]
+        T = sum(new)
+        q, k, v, qw, kw = inputs(T, Hq, Hkv, D, step)
+        v.clamp_(-4, 4)
+        pos = np.concatenate([np.arange(L - n, L) for L, n in zip(lens, new)])
+        seq = np.repeat(np.arange(B), new)
+        slots = bt.cpu().numpy()[seq, pos // bs].astype(np.int64) * bs + pos % bs
+        qd = torch.empty(T, Hq, D, dtype=torch.bfloat16, device="cuda")
+        pkv.qk_norm_rope_store(q, k, v, qw, kw, 1e-6, i32(pos), inv, i32(slots), qd, kc, vc, err_word=err)
+        cu, ld = i32(np.concatenate([[0], np.cumsum(new)])), i32(lens)
+        out = torch.full_like(qd, float("nan"))
+        if kind == "decode":
+            pkv.paged_decode_window(qd, kc, vc, bt, ld, D ** -0.5, window, sinks, out, ws, err_word=err)
+        elif kind == "window":
+            pkv.paged_attention_window(qd, kc, vc, bt, cu, ld, D ** -0.5, window, sinks, out, ws, err_word=err)
+        if kind != "tree":
+            sees = [window_sees(L, n, window, sinks) for L, n in zip(lens, new)]
+        else:
+            masks = random_trees(new, 1, np.random.default_rng(step))
+            pkv.paged_attention_tree(qd, kc, vc, bt, None, ld, torch.from_numpy(masks).cuda(), D ** -0.5, out, ws,
+                                     err_word=err, new_per_seq=new[0])
+            sees = [tree_sees(L, n, masks[n * b:n * b + n]) for b, (L, n) in enumerate(zip(lens, new))]
+        assert err.item() == 0
+        r = 0
+        for b, s in enumerate(sees):
+            n, L = s.shape
+            rows = lambda c: c[bt[b].long()].reshape(-1, Hkv, D)[:L].double()
+            x = torch.einsum("nhgd,lhd->hgnl", qd[r:r + n].double().view(n, Hkv, Hq // Hkv, D), rows(kc)) * D ** -0.5
+            w = torch.softmax(x.masked_fill(~torch.from_numpy(s).cuda(), float("-inf")), -1)
+            want = torch.einsum("hgnl,lhd->nhgd", w, rows(vc)).reshape(n, Hq, D)
+            mag = torch.einsum("hgnl,lhd->nhgd", w, rows(vc).abs()).reshape(n, Hq, D)
+            # bf16 caches: weights 2^-8 on the tile, scores 2^-12 at magnitudes below 2^6 (see test_gpu_masks.py)
+            off = (out[r:r + n].double() - want).abs() - (2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -11) * mag)
+            assert n == 0 or off.max() <= 0, (step, kind, off.max().item())
+            r += n
