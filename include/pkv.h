@@ -611,7 +611,9 @@ PKV_API pkv_status pkv_paged_attention_window_i8(
  *   tree_mask   [num_rows, mask_words] int32, bit t of a row is bit t % 32 of
  *               word t / 32; bits of later nodes (t > i) are ignored.  A node
  *               sees itself only if its own bit is set.
- * A row that sees no key (L = n and an empty mask) gives zeros.  The mask of a
+ * A row that sees no key (L = n and an empty mask) gives zeros; K, V and scales
+ * of a node that no row sees (a place that a smaller tree leaves unused) may
+ * hold anything.  The mask of a
  * chain is its lower triangle: the results of pkv_paged_attention (to rounding,
  * where another kernel runs).
  * mask_words >= 1; a sequence has at most 32 * mask_words nodes (new_per_seq

@@ -423,7 +423,8 @@ __device__ __forceinline__ uint32_t row_sees(const DecodeParams &p, int32_t tok0
     return v;
 }
 
-// Which of the 32 tokens from tok0 on some query of the entry sees (or, a drafted one, may see).
+// Which of the 32 tokens from tok0 on some query of the entry sees (or, a drafted one, may see: whether one does, its
+// queries' masks tell).
 __device__ __forceinline__ uint32_t entry_sees(const DecodeParams &p, int32_t tok0, int32_t L, int32_t cnt)
 {
     return low_bits(L - tok0) & (~low_bits(window_start(p, L, cnt) - tok0) | low_bits(p.sinks - tok0));
@@ -2442,7 +2443,7 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
         // tokens of the tile (masked calls: a bit for each that some query of the entry sees)
         constexpr int kAll = MASK ? int(0xffffffffu >> (32 - TC::TW)) : TC::TW;
         const bool whole = MASK && (mt.flags & kWhole) != 0;
-        const int valid = !MASK ? min(TC::TW, mt.L - tok0) : whole ? kAll : int(entry_sees(p, tok0, mt.L, mt.cnt)) & kAll;
+        int valid = !MASK ? min(TC::TW, mt.L - tok0) : whole ? kAll : int(entry_sees(p, tok0, mt.L, mt.cnt)) & kAll;
         if ((MASK ? valid != 0 : valid > 0) && nvh > 0) {
             const uint32_t kb = stage_addr + uint32_t(s) * lay.stage_bytes;
             if constexpr (!QS && CT != kI8) {
@@ -2486,6 +2487,13 @@ __global__ void __launch_bounds__(TC5 ? (tc5_consumers(CT) + 1) * 32 : (team_war
                                                                   : nullptr))
                                             : 0;
                     }
+                }
+                // drafted tokens: those that some row sees (the warp's rows are all the entry's)
+                if (!all && p.tree && tok0 + TC::TW > mt.base) {
+                    int any = lim[0];
+#pragma unroll
+                    for (int hr = 1; hr < HR; ++hr) any |= lim[hr];
+                    valid = int(__reduce_or_sync(kFull, uint32_t(any))) & kAll;
                 }
             } else {
 #pragma unroll

@@ -471,6 +471,35 @@ __device__ __forceinline__ void mt_merge(const TileParams &tp, const int32_t *bo
     }
 }
 
+// Which of the 64 tokens from tok0 on, drafted ones among them, query qi of the entry sees (x, y; none: qi >= cnt), and
+// which some query does (z, w).  The rows of one warp are a part of the queries, so a warp looks at all of them, a lane
+// at every 32nd, and a row takes its own from the lane that has it: one trip for the masks (a second one for the
+// entry's: 256 short sequences of 1 to 4 nodes 58.4 us, so 50.0).
+__device__ __forceinline__ uint4 mt_tree_sees(const DecodeParams &p, int32_t tok0, int32_t L, int32_t cnt, int32_t row0,
+                                              int32_t base, int qi, int lane)
+{
+    uint4 s = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+    for (int i0 = 0; i0 < cnt; i0 += 32) {
+        uint32_t a = 0u, b = 0u;
+        if (i0 + lane < cnt) {
+            const uint32_t *mask = p.tree + (long long)(row0 + i0 + lane) * p.tree_words;
+            a = row_sees(p, tok0, L - cnt + i0 + lane, base, mask);
+            b = row_sees(p, tok0 + 32, L - cnt + i0 + lane, base, mask);
+        }
+        const uint32_t x = __shfl_sync(kFull, a, qi & 31), y = __shfl_sync(kFull, b, qi & 31);
+        if (qi >> 5 == i0 >> 5) {
+            s.x = x;
+            s.y = y;
+        }
+        s.z |= a;
+        s.w |= b;
+    }
+    s.z = __reduce_or_sync(kFull, s.z);
+    s.w = __reduce_or_sync(kFull, s.w);
+    return s;
+}
+
 // The softmax warps (see the head of the file).
 template <int D, bool MERGE>
 __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const MtSmem &m, uint8_t *ring, uint8_t *qop,
@@ -512,7 +541,6 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
         const SeenUnits su = seen_units(p, L, cnt);
         const bool row_ok = qi < cnt;
         const int32_t pos = L - cnt + qi;  // the row's query
-        const uint32_t *mask = p.tree && row_ok ? p.tree + (long long)(row0 + qi) * p.tree_words : nullptr;
         // token units that every query sees whole
         const int32_t all0 = (max(L - p.window, 0) + kMtKeys - 1) / kMtKeys;
         const int32_t all1 = (p.tree ? min(L - cnt + 1, base) : L - cnt + 1) / kMtKeys;
@@ -522,12 +550,20 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
         for (int i = 0; i < len; ++i, ++k) {
             const int32_t tu = su.token_unit(u0 + i), tok0 = tu * kMtKeys;
             const bool all = tu >= all0 && tu < all1;
-            uint32_t v0 = 0xffffffffu, v1 = 0xffffffffu, e0 = v0, e1 = v0;  // the keys that the row sees, that any row does
+            uint32_t v0 = 0xffffffffu, v1 = 0xffffffffu, e0 = v0, e1 = v0;  // the keys that the row sees, that any query does
             if (!all) {
-                v0 = row_ok ? row_sees(p, tok0, pos, base, mask) : 0u;
-                v1 = row_ok ? row_sees(p, tok0 + 32, pos, base, mask) : 0u;
-                e0 = entry_sees(p, tok0, L, cnt);
-                e1 = entry_sees(p, tok0 + 32, L, cnt);
+                if (p.tree && tok0 + kMtKeys > base) {
+                    const uint4 s = mt_tree_sees(p, tok0, L, cnt, row0, base, qi, lane);
+                    v0 = s.x;
+                    v1 = s.y;
+                    e0 = s.z;
+                    e1 = s.w;
+                } else {
+                    v0 = row_ok ? row_sees(p, tok0, pos, base, nullptr) : 0u;
+                    v1 = row_ok ? row_sees(p, tok0 + 32, pos, base, nullptr) : 0u;
+                    e0 = entry_sees(p, tok0, L, cnt);
+                    e1 = entry_sees(p, tok0 + 32, L, cnt);
+                }
             }
             if (!wait(&m.sfull[k & 1u], (k >> 1) & 1u)) return;
             tc_fence_after();
