@@ -26,6 +26,7 @@ static int64_t unit_bound(int ct, bool qs, int G, int32_t num_kv_heads, int64_t 
 
 // What a masked call adds (see DecodeParams): a window and sinks, or a tree over the sequences' new tokens.
 struct MaskArgs {
+    bool new_tokens = false;  // an attention call: each query needs a key of its own, one query too
     int32_t window = INT32_MAX, sinks = 0;
     const uint32_t *tree = nullptr;
     int32_t tree_words = 0, tree_n = 0;
@@ -132,6 +133,7 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
     p.NB = num_blocks;
     p.max_blocks = max_blocks_per_seq;
     p.len_limit = int32_t(len_limit);
+    p.min_len = !row_cnt && (qn > 1 || (mask && mask->new_tokens)) ? qn : 0;
     // query-split entries of 128 rows run on the tensor-memory CTAs where they can
     const bool tc5 = qs && (i8 || tc5_eligible(head_dim, G, gq, block_size, num_seqs, dev.max_smem_optin));
     p.hg = qs ? 1 : head_group(num_kv_heads, G);
@@ -735,6 +737,7 @@ extern "C" pkv_status pkv_paged_attention_window(
     int32_t *err_word, pkv_stream_t stream)
 {
     MaskArgs m;
+    m.new_tokens = true;
     m.window = window;
     m.sinks = sinks;
     if (const pkv_status st = check_mask(m, false); st != PKV_OK) return st;
@@ -753,6 +756,7 @@ extern "C" pkv_status pkv_paged_attention_window_i8(
     int32_t *err_word, pkv_stream_t stream)
 {
     MaskArgs m;
+    m.new_tokens = true;
     m.window = window;
     m.sinks = sinks;
     if (const pkv_status st = check_mask(m, false); st != PKV_OK) return st;
@@ -771,6 +775,7 @@ extern "C" pkv_status pkv_paged_attention_tree(
 {
     if (num_rows > 0 && !tree_mask) return PKV_EINVAL;
     MaskArgs m;
+    m.new_tokens = true;
     m.tree = reinterpret_cast<const uint32_t *>(tree_mask);
     m.tree_words = mask_words;
     m.tree_n = new_per_seq;
@@ -793,6 +798,7 @@ extern "C" pkv_status pkv_paged_attention_tree_i8(
 {
     if (num_rows > 0 && !tree_mask) return PKV_EINVAL;
     MaskArgs m;
+    m.new_tokens = true;
     m.tree = reinterpret_cast<const uint32_t *>(tree_mask);
     m.tree_words = mask_words;
     m.tree_n = new_per_seq;

@@ -170,6 +170,8 @@ struct DecodeParams {
     BalanceState *ws_bal;
     int32_t *err;
     int32_t B, Hq, Hkv, bs, log2_bs, NB, max_blocks, len_limit;
+    int32_t min_len;  // shortest context length: a key for each of a sequence's new tokens (0: a decode, or entries made
+                      // by a call's own expansion)
     int32_t hg, nhg, sub, toks;  // kv heads per group, groups, warp slices per head, tokens per unit
     int32_t boxtok, nbox;        // tokens per TMA box (min(toks, bs)) and boxes per unit
     int32_t nst, cons, lg_nbox;  // ring stages, consumer warps (hg * sub), log2(nbox)
@@ -507,9 +509,7 @@ static __device__ void unit_prefix_scan(const DecodeParams &p, int32_t *scan, in
         for (int k = 0; k < kScanBatch; ++k) {
             if (i0 + k >= hi) break;
             int32_t n = 0;
-            // several queries of a sequence sharing a stream need at least one key each (the row
-            // arrays of a chunked call are built that way; a same-n call can break it)
-            if (len[k] < 0 || len[k] > p.len_limit || (!p.row_cnt && p.qn > 1 && len[k] < p.qn)) {
+            if (len[k] < p.min_len || len[k] > p.len_limit) {
                 if (blockIdx.x == 0) flag_error(p.err, PKV_ERR_CONTEXT_RANGE);
             } else {
                 if constexpr (MASK)

@@ -1,10 +1,11 @@
-"""GPU tests of windowed and tree calls at their edges: drafted nodes that nobody sees.  Bounds as in test_gpu_masks.py.
+"""GPU tests of windowed and tree calls at their edges: drafted nodes that nobody sees, lengths that do not fit.  Bounds
+as in test_gpu_masks.py.
 """
 import numpy as np
 import pytest
 import torch
 
-from mask_reference import Problem, random_trees, tree_sees
+from mask_reference import Problem, random_trees, tree_sees, window_sees
 from paged_kv_cache_62_gb300 import pkv
 from test_gpu_masks import attend, check
 
@@ -18,6 +19,17 @@ def _built():
     import __graft_entry__
     __graft_entry__.build()
     torch.cuda.set_device(0)
+
+
+def only(prob, keep):
+    """The problem of some sequences of another one, over the same cache, and the rows of theirs."""
+    part = object.__new__(Problem)
+    part.__dict__.update(prob.__dict__)
+    cu = np.concatenate([[0], np.cumsum(prob.new)])
+    rows = np.concatenate([np.arange(cu[b], cu[b + 1]) for b in keep]) if keep else np.zeros(0, int)
+    part.sees, part.bt = [prob.sees[b] for b in keep], prob.bt[keep]
+    part.lens, part.new, part.q = [prob.lens[b] for b in keep], [prob.new[b] for b in keep], prob.q[rows]
+    return part, rows
 
 
 # ------------------------------------------------------------------------------------------ nodes that nobody sees
@@ -46,3 +58,44 @@ def test_nodes_that_nobody_sees_may_hold_anything(cache, Hq, Hkv, D, bs, n, pad)
     for workers, uniform in ((0, n), (0, 0), (40, n), (40, 0)):
         out = attend(prob, (md,), "tree", uniform=uniform, workers=workers, dev=dev)
         check(out, prob, f"uniform {uniform} workers {workers}", long_runs=True)
+
+
+# ------------------------------------------------------------------------------------------ lengths
+@pytest.mark.parametrize("kind", ["window", "tree"])
+@pytest.mark.parametrize("cache", ["bf16", "int8"])
+@pytest.mark.parametrize("n", [1, 3, 30])
+@pytest.mark.parametrize("bad", [0, -1, 1 << 20, -(1 << 31)])
+def test_lengths_that_do_not_fit(kind, cache, n, bad):
+    """Fewer keys than new tokens, negative lengths and lengths beyond the table: flagged, zeros, the others unharmed;
+    the same with a fixed number of new tokens and with offsets."""
+    lens, wrong = [40, 300, 77, 64], [1, 3]
+    if kind == "window":
+        prob = Problem(cache, [window_sees(L, n, 50, 3) for L in lens], 16, 8, 64, 16, seed=n)
+        args = (50, 3)
+    else:
+        masks = random_trees([n] * 4, 1, np.random.default_rng(n))
+        prob = Problem(cache, [tree_sees(L, n, masks[b * n:b * n + n]) for b, L in enumerate(lens)], 16, 8, 64, 16, seed=n)
+        args = (torch.from_numpy(masks).cuda(),)
+    q, c, bt, ld, cu = prob.cuda()
+    ld[wrong] = bad
+    good, rows = only(prob, [0, 2])
+    for uniform in (n, 0):
+        out = attend(prob, args, kind, uniform=uniform, err_is=pkv.ERR_CONTEXT_RANGE, dev=(q, c, bt, ld, cu))
+        for b in wrong:
+            assert not out[b * n:b * n + n].any(), uniform
+        check(out[rows], good, f"uniform {uniform}", long_runs=True)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("bad", [-1, 1 << 20, -(1 << 31)])
+def test_decode_lengths_that_do_not_fit(cache, bad):
+    prob = Problem(cache, [window_sees(L, 1, 50, 3) for L in (40, 300, 77, 64)], 16, 8, 64, 16, seed=1)
+    q, c, bt, ld, _ = prob.cuda()
+    ld[1] = bad
+    out, err = torch.full_like(q, float("nan")), torch.zeros(1, dtype=torch.int32, device="cuda")
+    name = {"bf16": "", "fp8": "_fp8", "int8": "_i8"}[cache]
+    getattr(pkv, "paged_decode_window" + name)(q, *c, bt, ld, prob.scale, 50, 3, out, pkv.alloc_workspace(4, 16, 8, 64),
+                                               err_word=err)
+    assert err.item() == pkv.ERR_CONTEXT_RANGE and not out[1].any()
+    good, rows = only(prob, [0, 2, 3])
+    check(out[rows], good, "others")
