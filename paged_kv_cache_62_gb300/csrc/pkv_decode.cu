@@ -14,16 +14,6 @@ extern "C" size_t pkv_paged_decode_workspace_size(int32_t num_seqs, int32_t num_
     return ws_layout(num_seqs, num_q_heads / num_kv_heads, num_kv_heads, head_dim).total;
 }
 
-// The units of a call's list at most (`entries` of them hold work): unit counts and positions in the list are kept in
-// 32 bits.  int8 calls count the units of the CTA that runs them, the others 8 tokens of a kv head.
-static int64_t unit_bound(int ct, bool qs, int G, int32_t num_kv_heads, int64_t entries, int64_t len_limit)
-{
-    if (ct != kI8) return int64_t(num_kv_heads) * entries * ((len_limit + 7) / 8);
-    const int hg = qs ? 1 : head_group(num_kv_heads, G);
-    const int toks = warp_tokens(G, true, qs, qs) * (qs ? 1 : warp_slices(G, hg));
-    return num_kv_heads / hg * entries * ((len_limit + toks - 1) / toks);
-}
-
 // What a masked call adds (see DecodeParams): a window and sinks, or a tree over the sequences' new tokens.
 struct MaskArgs {
     bool new_tokens = false;  // an attention call: each query needs a key of its own, one query too
@@ -63,6 +53,20 @@ static int64_t seen_bound(const MaskArgs *m, int64_t len_limit, int64_t n)
     return m ? std::min<int64_t>(len_limit, int64_t(m->window) + m->sinks + n - 1) : len_limit;
 }
 
+// The units of a call's list at most (`entries` of them hold work, up to `queries` queries each): unit counts and
+// positions in the list are kept in 32 bits.  int8 calls count the units of the CTA that runs them, the others 8 tokens of
+// a kv head.  A masked call's list has what its queries see (a window that begins inside a unit, or sinks that end
+// inside one: a unit more each).
+static int64_t unit_bound(int ct, bool qs, int G, int32_t num_kv_heads, int64_t entries, int64_t len_limit,
+                          const MaskArgs *mask, int64_t queries)
+{
+    const int hg = ct != kI8 || qs ? 1 : head_group(num_kv_heads, G);
+    const int toks = ct != kI8 ? 8 : warp_tokens(G, true, qs, qs) * (qs ? 1 : warp_slices(G, hg));
+    int64_t units = (len_limit + toks - 1) / toks;
+    if (mask) units = std::min(units, (seen_bound(mask, len_limit, queries) + toks - 1) / toks + 2);
+    return num_kv_heads / hg * entries * units;
+}
+
 // Shared by the entry points of all cache types (ct; k_scale / v_scale: the
 // per-kv-head scales of E4M3 caches, scales: those of int8 ones, device arrays).  qn > 1: entry b holds up to qn
 // queries that share its K/V stream as qn * G virtual heads of a kv head --
@@ -100,7 +104,9 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
     if (ct == kI8 && (!scales || (reinterpret_cast<uintptr_t>(scales) & 7u))) return PKV_EINVAL;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return PKV_EINVAL;
     const int64_t len_limit = std::min<int64_t>(max_context_len, int64_t(max_blocks_per_seq) * block_size);
-    if (unit_bound(ct, qs, G, num_kv_heads, live < 0 ? num_seqs : live, len_limit) > INT32_MAX) return PKV_EBOUNDS;
+    const int64_t queries = qs ? 128 / gq : qn;  // of an entry at most
+    if (unit_bound(ct, qs, G, num_kv_heads, live < 0 ? num_seqs : live, len_limit, mask, queries) > INT32_MAX)
+        return PKV_EBOUNDS;
     if (mask && len_limit > kMaskMaxLen) return PKV_EBOUNDS;
     if (qs && (ct == kE4m3 || !row_cnt || (i8 && !row0))) return PKV_EINVAL;  // query-split entries are chunks of bf16 or int8 calls
     if ((k_new || v_new) && (qs || ct == kI8 || qn != 1 || row_seq || !k_new || !v_new || !aligned16(k_new) ||
@@ -179,8 +185,7 @@ static pkv_status decode_call(int ct, bool qs, int32_t qn, const uint16_t *q, co
         // (a window that begins inside a unit, or sinks that end inside one: a unit more each)
         int64_t per_seg = (len_limit + p.toks - 1) / p.toks;
         if (mask)
-            per_seg = std::min(per_seg, (seen_bound(mask, len_limit, int64_t(qn) * (qs ? team_warps(G) : 1)) +
-                                         p.toks - 1) / p.toks + 2);
+            per_seg = std::min(per_seg, (seen_bound(mask, len_limit, queries) + p.toks - 1) / p.toks + 2);
         const int64_t units_max = int64_t(num_seqs) * p.nhg * per_seg;
         if (units_max < dev.sm_count) {
             if ((!qs || i8) && per_seg <= kSegmentUnits && int64_t(num_seqs) * p.nhg <= kMaxSlots) {
@@ -572,7 +577,7 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
         if (mask && qs && ct == kBf16) {  // (a segment's list counts a few units more there)
             if (live * num_kv_heads * ((seen_bound(mask, len_max, tile) + kMtKeys - 1) / kMtKeys + 8) > INT32_MAX)
                 return PKV_EBOUNDS;
-        } else if (unit_bound(ct, qs, G, num_kv_heads, live, len_max) > INT32_MAX) {
+        } else if (unit_bound(ct, qs, G, num_kv_heads, live, len_max, mask, chunk) > INT32_MAX) {
             return PKV_EBOUNDS;
         }
         DeviceInfo dev;

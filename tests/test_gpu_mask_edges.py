@@ -1,5 +1,5 @@
-"""GPU tests of windowed and tree calls at their edges: drafted nodes that nobody sees, lengths that do not fit.  Bounds
-as in test_gpu_masks.py.
+"""GPU tests of windowed and tree calls at their edges: drafted nodes that nobody sees, lengths that do not fit, long
+tables.  Bounds as in test_gpu_masks.py.
 """
 import numpy as np
 import pytest
@@ -7,7 +7,7 @@ import torch
 
 from mask_reference import Problem, random_trees, tree_sees, window_sees
 from paged_kv_cache_62_gb300 import pkv
-from test_gpu_masks import attend, check
+from test_gpu_masks import attend, check, decode
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +99,25 @@ def test_decode_lengths_that_do_not_fit(cache, bad):
     assert err.item() == pkv.ERR_CONTEXT_RANGE and not out[1].any()
     good, rows = only(prob, [0, 2, 3])
     check(out[rows], good, "others")
+
+
+# ------------------------------------------------------------------------------------------ long tables
+@pytest.mark.parametrize("cache,n", [("bf16", 1), ("fp8", 1), ("int8", 1), ("bf16", 3), ("int8", 3), ("bf16", 20),
+                                     ("int8", 20)])
+def test_short_windows_at_the_end_of_long_tables(cache, n):
+    """256 sequences of up to 9.6 million tokens, of which a window's are there: the list has what is seen."""
+    B, bs, mb = 256, 16, 600_000
+    rng = np.random.default_rng(n)
+    lens = [int(L) for L in rng.integers(n, 200, B)]
+    prob = Problem(cache, [window_sees(L, n, 50, 0) for L in lens], 16, 8, 64, bs, seed=n)
+    q, c, bt, ld, cu = prob.cuda()
+    shift = torch.from_numpy(rng.integers(0, mb - bt.shape[1], B)).int().cuda()
+    shift[0] = mb - bt.shape[1]
+    shift[[b for b in range(B) if lens[b] < 50 + n]] = 0  # (their windows begin at the sequence's start)
+    table = torch.full((B, mb), -1, dtype=torch.int32, device="cuda")
+    table.scatter_(1, (shift[:, None] + torch.arange(bt.shape[1], device="cuda")).long(), bt)
+    dev = (q, c, table, ld + shift * bs, cu)
+    if n == 1:
+        check(decode(prob, 50, 0, dev=dev), prob, "decode")
+    for uniform in (n, 0) if cache != "fp8" else ():
+        check(attend(prob, (50, 0), uniform=uniform, dev=dev), prob, f"uniform {uniform}", long_runs=True)
