@@ -563,11 +563,14 @@ PKV_API pkv_status pkv_paged_attention_i8(const uint16_t *q, const int8_t *k_cac
  * and errors as the calls without window; max_context_len at most 2^30 (PKV_EBOUNDS).  Where a
  * call's queries share a pass, K and V of a key that one of them sees should be finite: an
  * infinity or NaN there may reach the others.
- * Several new tokens over bf16 caches: with new_per_seq n, n * num_q_heads / num_kv_heads
- * <= 16, as pkv_paged_attention's single pass.  Else in tiles of 128 / (num_q_heads /
- * num_kv_heads) queries on the tensor cores, the softmax's weights rounded to bf16 (2^-8 of a
- * weight at most); num_workers then counts eighths of a CTA of the tile kernel, and 0 takes
- * two CTAs an SM.
+ * Several new tokens over bf16 caches: with new_per_seq = n <= q (q as there), as
+ * pkv_paged_attention's single pass.  Else in tiles of 128 / (num_q_heads /
+ * num_kv_heads) queries on the tensor cores; num_workers then counts eighths of
+ * a CTA of the tile kernel, and 0 takes two CTAs an SM.  The softmax's weights
+ * enter the product with V as two bf16 parts (2^-16 of a weight at most) in
+ * calls of at most 2q new tokens per sequence on average, whichever way the
+ * call says how many there are, and rounded to one (2^-8 of a weight at most)
+ * in longer ones.
  */
 PKV_API pkv_status pkv_paged_decode_window(
     const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,

@@ -549,10 +549,12 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
     // (Query-split int8 entries, and those of masked calls, fill the tensor-memory tile: as many whole queries as 128
     // rows hold.)
     const int32_t tile = 128 / std::min(num_q_heads / num_kv_heads, 128);
-    // (Masked calls over bf16 caches: mask_tile_kernel reads the keys once, at any number of new tokens.  64 sequences of
-    // 512-4096, 16 / 8 heads of 128: 12 nodes each 114 us against 224 on regular CTAs, 1 to 4 nodes 105 against 112; two
-    // sequences of 9 nodes 24 against 159; 256 sequences of 50-300 with 1 to 4 nodes 53 against 54.)
-    bool qs = (mask && ct == kBf16) || int64_t(num_rows) > 2 * int64_t(qg) * num_seqs;
+    // (Masked calls over bf16 caches: mask_tile_kernel reads the keys once, at any number of new tokens, and its results
+    // repeat bit for bit.  With two parts to a weight, 64 sequences of 512-4096, 16 / 8 heads of 128: 12 nodes each 120 us
+    // against 224 on regular CTAs, 1 to 4 nodes 116 against 118, under a window of 1024 60 against 65; two sequences of 9
+    // nodes 26 against 159; but 256 sequences of 50-300 with 1 to 4 nodes 63 against 55.)
+    const bool few = int64_t(num_rows) <= 2 * int64_t(qg) * num_seqs;
+    bool qs = (mask && ct == kBf16) || !few;
     if (ct == kI8 && !qs && int64_t(num_rows) > int64_t(qg) * num_seqs) {
         // Between one and two chunks a sequence: regular CTAs read the keys twice, but take larger calls as fast; in
         // calls of few tiles their list, one entry a row, most of them empty, costs more (16 new tokens, 16 / 8 heads
@@ -606,8 +608,11 @@ static pkv_status attention_call(int ct, const uint16_t *q, const void *k_cache,
             p.scale_log2 = float(double(scale) * 1.4426950408889634);
             p.toks = kMtKeys;
             set_mask(p, *mask);
-            return mask_tile_call(p, k_cache, v_cache, cu_seqlens_q, num_seqs, num_rows, new_per_seq, max_new, head_dim,
-                                  wsb, num_workers, reinterpret_cast<cudaStream_t>(stream));
+            // (few new tokens: two parts to a weight, as on the regular CTAs that take such calls without masks.  One part:
+            // 12 nodes each 115 us, so 120; 1 to 4 nodes 112, so 116, under a window 55, so 60; 256 short sequences 50, so
+            // 63.  Long runs with two parts: 32-node trees 106 us, so 110; 64-token chunks 61, so 67; prompts 50, so 59.)
+            return mask_tile_call(p, k_cache, v_cache, cu_seqlens_q, num_seqs, num_rows, new_per_seq, max_new, few,
+                                  head_dim, wsb, num_workers, reinterpret_cast<cudaStream_t>(stream));
         }
     }
     if (ct == kI8 && qs) {

@@ -2946,8 +2946,8 @@ constexpr int kMtKeys = 64;
 int32_t mask_tile_entries(int32_t num_seqs, int32_t num_rows, int32_t per_seq, int32_t tile);
 bool mask_tile_fits(int D, int32_t entries, bool ragged, int max_smem);
 pkv_status mask_tile_call(DecodeParams &p, const void *k_cache, const void *v_cache, const int32_t *cu, int32_t num_seqs,
-                          int32_t num_rows, int32_t per_seq, int32_t max_new, int32_t head_dim, uint8_t *workspace,
-                          int32_t num_workers, cudaStream_t stream);
+                          int32_t num_rows, int32_t per_seq, int32_t max_new, bool two_parts, int32_t head_dim,
+                          uint8_t *workspace, int32_t num_workers, cudaStream_t stream);
 
 // Whether a query-split call can run on the tensor-memory CTAs: bf16 caches, entries of 128 rows
 // (16 virtual heads per block: the query heads of a kv head a power of two), 128-key tiles within one

@@ -7,8 +7,10 @@
 // list leaves out what no query of the entry sees (seen_units).  Per unit
 //     S = Q K^T  (128 x 64, fp32 in tensor memory),   P = 2^(c S - m),   O += P V  (128 x D, fp32 in tensor memory)
 // with m the row's running max, moved only when a score passes it by kRescaleSlack (O is then scaled in place), and
-// out = O / l at the segment's end, l the fp32 sum of the weights.  P enters the product as bf16, the operand type of V
-// (2^-8 of a weight at most; a second product for the rest would double the output product's time).
+// out = O / l at the segment's end, l the fp32 sum of the weights.  P enters the product as bf16, the operand type of V:
+// in calls of few new tokens as two parts (TWO), bf16(p) and bf16 of what that leaves, in the columns that the scores had
+// (2^-16 of a weight at most, as the decode kernel's); in longer ones as one (2^-8), as the tensor-memory CTAs take it in
+// calls without masks (see attention_call).
 //
 // Why this shape: one unit's chain of copy, product, softmax and product has far more latency than work, so two CTAs
 // share an SM, each with its own segments, half the tensor memory (two score buffers of 64 columns and the output: 256
@@ -76,6 +78,7 @@ struct TileParams {
     int32_t max_new;
     int32_t snap;         // see kMtSnap, kMtWhole
     bool ctr_by_row;      // arrival counters by the entry's first row, not by entry
+    bool two;             // weights as two bf16 parts, not one (see the head of the file)
     int32_t merge;        // 1: the CTA that completes a segment merges it; 2: a second kernel does; 0: nothing to merge
 };
 
@@ -501,7 +504,7 @@ __device__ __forceinline__ uint4 mt_tree_sees(const DecodeParams &p, int32_t tok
 }
 
 // The softmax warps (see the head of the file).
-template <int D, bool MERGE>
+template <int D, bool MERGE, bool TWO>
 __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const MtSmem &m, uint8_t *ring, uint8_t *qop,
                            uint32_t tmem, int32_t *bound, int *sh, const MtSlices &sl, uint32_t gen)
 {
@@ -623,7 +626,7 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
             uint64_t ps[2] = {0ull, 0ull};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {  // 32 keys at a time: the first half's output product runs beside the second
-                uint32_t w[kMtKeys / 4];
+                uint32_t w[kMtKeys / 4], rest[TWO ? kMtKeys / 4 : 1];
 #pragma unroll
                 for (int j = 0; j < kMtKeys / 4; ++j) {
                     const int e = 32 * h + 2 * j;
@@ -632,6 +635,8 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
                     const float p0 = ex2(x.x), p1 = ex2(x.y);
                     ps[j & 1] = mt_add2(ps[j & 1], mt_two(p0, p1));
                     w[j] = pack_bf16x2(p0, p1);
+                    if constexpr (TWO)
+                        rest[j] = pack_bf16x2(p0 - __uint_as_float(w[j] << 16), p1 - __uint_as_float(w[j] & 0xffff0000u));
                 }
                 if (h == 0 && (e0 & e1) != 0xffffffffu) {
                     // V rows that no query sees may hold anything, and 0 * NaN is NaN: zeros there, once they have landed.
@@ -649,6 +654,7 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
                     fence_proxy_async_smem();  // for the tensor core
                 }
                 tmem_st16(sbuf + uint32_t(16 * h), w);
+                if constexpr (TWO) tmem_st16(sbuf + uint32_t(kMtKeys / 2 + 16 * h), rest);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -723,7 +729,7 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
 
 // The issuing warp, lane 0.  One thread's chain of instructions per unit, so addresses and descriptors are kept and
 // moved on, not made anew (made anew, with a division for the slots: 3100 cycles a unit, the CTA's longest chain).
-template <int D>
+template <int D, bool TWO>
 __device__ void mt_products(const DecodeParams &p, const MtSmem &m, uint32_t ring, uint32_t qop, uint32_t tmem)
 {
     constexpr uint32_t IS = idesc_bf16_f32(128, kMtKeys, false), IP = idesc_bf16_f32(128, D, true);
@@ -772,6 +778,8 @@ __device__ void mt_products(const DecodeParams &p, const MtSmem &m, uint32_t rin
                 tc_fence_after();
             }
             tc_mma_bf16_ta(d, pa + uint32_t(8 * i), vd + uint32_t(i) * (2048 / 16), IP, i > 0 || !first);
+            if constexpr (TWO)
+                tc_mma_bf16_ta(d, pa + uint32_t(kMtKeys / 2 + 8 * i), vd + uint32_t(i) * (2048 / 16), IP, true);
         }
         tc_commit_at(odone + 8 * b);
         tc_commit_at(empty + 8 * vs);
@@ -1035,7 +1043,7 @@ __device__ __forceinline__ void mt_setup(const TileParams &tp, int32_t *scan, ui
     __syncthreads();
 }
 
-template <int D, bool MERGE>
+template <int D, bool MERGE, bool TWO>
 __global__ void __launch_bounds__(kMtThreads, 2)
     mask_tile_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TileParams tp)
@@ -1106,9 +1114,9 @@ __global__ void __launch_bounds__(kMtThreads, 2)
     uint8_t *qop = smem + lay.off_q;
     if (int(blockIdx.x) < sl.nsl) {
         if (warp < kMtSoftmaxWarps) {
-            mt_softmax<D, MERGE>(tp, &qmap, m, smem, qop, tmem, bound, sh, sl, gen);
+            mt_softmax<D, MERGE, TWO>(tp, &qmap, m, smem, qop, tmem, bound, sh, sl, gen);
         } else if (warp == kMtSoftmaxWarps) {
-            if (lane == 0) mt_products<D>(p, m, smem_u32(smem), smem_u32(qop), tmem);
+            if (lane == 0) mt_products<D, TWO>(p, m, smem_u32(smem), smem_u32(qop), tmem);
             __syncwarp();
             if (!mbar_wait_bounded(m.drain, 0u) && lane == 0) flag_error(p.err, PKV_ERR_WAIT_TIMEOUT);
         } else {
@@ -1227,6 +1235,20 @@ static bool encode_q_map(CUtensorMap *map, const TileParams &tp, int D)
     return false;
 }
 
+template <int D, bool MERGE, bool TWO>
+static pkv_status launch_kernel(const TileParams &tp, const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                int device, int grid, uint32_t smem, cudaStream_t stream)
+{
+    auto kern = mask_tile_kernel<D, MERGE, TWO>;
+    if (!ensure_smem_attribute<D, MERGE, kBf16, TWO, true, true>(kern, device, smem)) return PKV_ECUDA;
+    const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kMtThreads), smem, stream, qmap, kmap, vmap, tp);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return cuda_fail("mask_tile_kernel launch", e);
+    }
+    return launch_status("mask_tile_kernel launch");
+}
+
 template <int D>
 static pkv_status launch_tile(TileParams &tp, const void *k_cache, const void *v_cache, const DeviceInfo &dev,
                               int32_t num_workers, cudaStream_t stream)
@@ -1257,16 +1279,9 @@ static pkv_status launch_tile(TileParams &tp, const void *k_cache, const void *v
         !cached_cache_map(&kmap, dev.device, k_cache, false, D, p.Hkv, rows, 1, p.boxtok, 1) ||
         !cached_cache_map(&vmap, dev.device, v_cache, false, D, p.Hkv, rows, 1, p.boxtok, 1))
         return PKV_ECUDA;
-    auto kern = tp.merge == 1 ? mask_tile_kernel<D, true> : mask_tile_kernel<D, false>;
-    if (!(tp.merge == 1 ? ensure_smem_attribute<D, 16, kBf16, true, true, true>(kern, dev.device, total)
-                        : ensure_smem_attribute<D, 15, kBf16, true, true, true>(kern, dev.device, total)))
-        return PKV_ECUDA;
-    const cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kMtThreads), total, stream, qmap, kmap, vmap, tp);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return cuda_fail("mask_tile_kernel launch", e);
-    }
-    const pkv_status st = launch_status("mask_tile_kernel launch");
+    auto fn = tp.merge == 1 ? (tp.two ? launch_kernel<D, true, true> : launch_kernel<D, true, false>)
+                            : (tp.two ? launch_kernel<D, false, true> : launch_kernel<D, false, false>);
+    const pkv_status st = fn(tp, qmap, kmap, vmap, dev.device, grid, total, stream);
     if (st != PKV_OK || tp.merge != 2) return st;
     const size_t bytes = size_t(8 + kMaxSlots + 1 + p.B + 1) * 4 + size_t(p.B) * 2;  // (few segments: a few KiB)
     const cudaError_t em = launch_pdl(mask_merge_kernel<D>, dim3(D / 4, unsigned(p.B * p.nhg)), dim3(kMtMergeThreads), bytes,
@@ -1290,8 +1305,8 @@ bool mask_tile_fits(int D, int32_t entries, bool ragged, int max_smem)
 }
 
 pkv_status mask_tile_call(DecodeParams &p, const void *k_cache, const void *v_cache, const int32_t *cu, int32_t num_seqs,
-                          int32_t num_rows, int32_t per_seq, int32_t max_new, int32_t head_dim, uint8_t *workspace,
-                          int32_t num_workers, cudaStream_t stream)
+                          int32_t num_rows, int32_t per_seq, int32_t max_new, bool two_parts, int32_t head_dim,
+                          uint8_t *workspace, int32_t num_workers, cudaStream_t stream)
 {
     DeviceInfo dev;
     if (!current_device_info(&dev)) return PKV_ECUDA;
@@ -1303,6 +1318,7 @@ pkv_status mask_tile_call(DecodeParams &p, const void *k_cache, const void *v_ca
     tp.tile = 128 / p.gq;
     tp.per_entry = per_seq > 0 ? (per_seq + tp.tile - 1) / tp.tile : 0;
     tp.max_new = max_new;
+    tp.two = two_parts;
     p.B = mask_tile_entries(num_seqs, num_rows, per_seq, tp.tile);
     const WsLayout ws = ws_layout(num_rows, 16, p.Hkv, head_dim, true);  // (see mt_piece)
     p.ws_ml = reinterpret_cast<float *>(workspace + ws.ml_off);

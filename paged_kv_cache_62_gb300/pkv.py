@@ -675,7 +675,9 @@ def paged_attention_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
                            num_workers: int = 0, err_word: torch.Tensor | None = None, stream=None,
                            new_per_seq: int = 0) -> None:
     """paged_attention in which each new token sees the last `window` keys up to its own and the sequence's first
-    `sinks`; table entries of blocks that no new token sees are not read."""
+    `sinks`; table entries of blocks that no new token sees are not read.  Softmax weights enter the product with V as
+    two bf16 parts (2^-16) in calls of up to 2 * (16 // (Hq // Hkv)) new tokens per sequence on average, rounded to one
+    (2^-8) in longer ones."""
     st = _native().paged_attention_mask(q, k_cache, v_cache, None, block_tables, cu_seqlens_q, context_lens, None, window,
                                         sinks, scale, out, workspace, max_context_len, num_workers, err_word, stream,
                                         new_per_seq)
@@ -704,7 +706,8 @@ def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
                          num_workers: int = 0, err_word: torch.Tensor | None = None, stream=None,
                          new_per_seq: int = 0) -> None:
     """paged_attention of drafted trees: a sequence's n new tokens are nodes, parents first, and node i sees the keys
-    before the draft and the nodes t <= i whose bit is set in its row of tree_mask (int32 [rows, words])."""
+    before the draft and the nodes t <= i whose bit is set in its row of tree_mask (int32 [rows, words]).  Softmax
+    weights as paged_attention_window's."""
     if tree_mask is None:
         raise ValueError("paged_attention_tree: tree_mask is needed")
     st = _native().paged_attention_mask(q, k_cache, v_cache, None, block_tables, cu_seqlens_q, context_lens, tree_mask, 0,

@@ -1,5 +1,5 @@
 """GPU tests of windowed and tree calls at their edges: drafted nodes that nobody sees, lengths that do not fit, long
-tables.  Bounds as in test_gpu_masks.py.
+tables, the weights' precision when few new tokens come by offsets.  Bounds as in test_gpu_masks.py.
 """
 import numpy as np
 import pytest
@@ -121,3 +121,48 @@ def test_short_windows_at_the_end_of_long_tables(cache, n):
         check(decode(prob, 50, 0, dev=dev), prob, "decode")
     for uniform in (n, 0) if cache != "fp8" else ():
         check(attend(prob, (50, 0), uniform=uniform, dev=dev), prob, f"uniform {uniform}", long_runs=True)
+
+
+# ------------------------------------------------------------------------------------------ the weights' precision
+def one_part(prob):
+    """The result with each softmax weight rounded to one bf16 part, the sum of weights taken before that (64 bits on
+    the CPU)."""
+    out, r, G = torch.zeros(prob.q.shape, dtype=torch.float64), 0, prob.Hq // prob.Hkv
+    for b, s in enumerate(prob.sees):
+        n, L = s.shape
+        if n:
+            at = torch.arange(L)
+            page, row = torch.from_numpy(prob.bt[b].astype(np.int64))[at // prob.bs], at % prob.bs
+            k, v = (torch.nan_to_num(t[page, row]) for t in (prob.kd, prob.vd))
+            x = torch.einsum("nhgd,lhd->hgnl", prob.q[r:r + n].double().view(n, prob.Hkv, G, prob.D), k) * prob.scale
+            x = x.masked_fill(torch.from_numpy(~s), float("-inf"))
+            p = torch.exp(x - x.amax(-1, keepdim=True))
+            o = torch.einsum("hgnl,lhd->nhgd", p.bfloat16().double(), v) / p.sum(-1).permute(2, 0, 1)[..., None]
+            out[r:r + n] = o.reshape(n, prob.Hq, prob.D)
+        r += n
+    return out
+
+
+@pytest.mark.parametrize("kind", ["window", "tree"])
+@pytest.mark.parametrize("Hq,Hkv,D,bs,most", [(16, 8, 128, 16, 16), (8, 8, 64, 64, 32), (16, 2, 64, 256, 4),
+                                              (15, 5, 128, 32, 10)])
+def test_few_new_tokens_keep_their_weights(kind, Hq, Hkv, D, bs, most):
+    """Up to twice the tokens of one pass on average, by offsets or all alike: the weights' parts are those of the plain
+    attention of as many (2^-16), whichever way the call says how many there are."""
+    rng = np.random.default_rng(most)
+    for new in ([1] * 24, [1, 3, 2, 1] * 6, [most] * 6, [most + 3, 1, most - 1, most - 3]):
+        lens = [n + int(rng.integers(1, 6)) for n in new]
+        if kind == "window":
+            sees, args = [window_sees(L, n, 5, 1) for L, n in zip(lens, new)], (5, 1)
+        else:
+            masks = random_trees(new, 2, rng, noise=False)
+            cu = np.concatenate([[0], np.cumsum(new)])
+            sees, args = [tree_sees(L, n, masks[a:a + n]) for L, n, a in zip(lens, new, cu)], None
+        prob = Problem("bf16", sees, Hq, Hkv, D, bs, seed=len(new))
+        want, mag = prob.want()
+        over = (one_part(prob) - want).abs() - (2.0 ** -8 * want.abs() + 2.0 ** -11 * mag)
+        assert over.max() > 0  # one part would show
+        args = args or (torch.from_numpy(masks).cuda(),)
+        check(attend(prob, args, kind), prob, f"offsets, {new}")
+        if len(set(new)) == 1:
+            check(attend(prob, args, kind, uniform=new[0]), prob, f"uniform, {new}")
