@@ -1,11 +1,12 @@
-"""GPU tests of windowed and tree calls at their edges: drafted nodes that nobody sees, lengths that do not fit, long
-tables, the weights' precision when few new tokens come by offsets.  Bounds as in test_gpu_masks.py.
+"""GPU tests of windowed and tree calls at their edges: drafted nodes that nobody sees, lengths and table entries that do
+not fit, scale blocks of zeros and of no numbers, keys that are not finite, long tables, and the weights' precision when
+few new tokens come by offsets.  Bounds as in test_gpu_masks.py.
 """
 import numpy as np
 import pytest
 import torch
 
-from mask_reference import Problem, random_trees, tree_sees, window_sees
+from mask_reference import SB, Problem, random_trees, tree_sees, window_sees
 from paged_kv_cache_62_gb300 import pkv
 from test_gpu_masks import attend, check, decode
 
@@ -99,6 +100,154 @@ def test_decode_lengths_that_do_not_fit(cache, bad):
     assert err.item() == pkv.ERR_CONTEXT_RANGE and not out[1].any()
     good, rows = only(prob, [0, 2, 3])
     check(out[rows], good, "others")
+
+
+# ------------------------------------------------------------------------------------------ table entries
+@pytest.mark.parametrize("cache", ["bf16", "int8"])
+@pytest.mark.parametrize("kind", ["window", "tree"])
+@pytest.mark.parametrize("n", [1, 4, 33, 90])
+@pytest.mark.parametrize("Hq,Hkv,D,bs", [(16, 8, 64, 16), (6, 2, 128, 128)])
+def test_table_entries_out_of_range(cache, kind, n, Hq, Hkv, D, bs):
+    """An entry that names no block is flagged where a query needs it, at any place of the sequence, and not looked at
+    elsewhere; the other sequences get what they get without it."""
+    lens, masks = [400, 300, 500, 277], None
+    if kind == "window":
+        sees, args = [window_sees(L, n, 60, 3) for L in lens], (60, 3)
+    else:
+        masks = random_trees([n] * 4, 3, np.random.default_rng(n))
+        sees = [tree_sees(L, n, masks[b * n:b * n + n]) for b, L in enumerate(lens)]
+        args = (torch.from_numpy(masks).cuda(),)
+    prob = Problem(cache, sees, Hq, Hkv, D, bs, seed=n + bs)
+    q, c, bt, ld, cu = prob.cuda()
+    NB = c[0].shape[0]
+    good, rows = only(prob, [0, 1, 3])
+    needed = [p for p in range(-(-lens[2] // bs)) if prob.bt[2, p] >= 0]
+    spare = [p for p in range(prob.bt.shape[1]) if prob.bt[2, p] < 0]
+    for uniform in (n, 0):
+        for page, entry in zip((needed[0], needed[-1], needed[len(needed) // 2]), (NB, -1, 2 ** 31 - 1)):
+            t = bt.clone()
+            t[2, page] = entry
+            out = attend(prob, args, kind, uniform=uniform, err_is=pkv.ERR_BLOCK_RANGE, dev=(q, c, t, ld, cu))
+            check(out[rows], good, f"uniform {uniform} page {page}", long_runs=True)
+        t = bt.clone()
+        t[2, spare] = 2 ** 31 - 1
+        check(attend(prob, args, kind, uniform=uniform, dev=(q, c, t, ld, cu)), prob, "spare", long_runs=True)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8", "int8"])
+def test_decode_table_entries_out_of_range(cache):
+    prob = Problem(cache, [window_sees(L, 1, 60, 3) for L in (400, 300, 500, 277)], 16, 8, 64, 16, seed=1)
+    q, c, bt, ld, _ = prob.cuda()
+    NB, good = c[0].shape[0], only(prob, [0, 1, 3])
+    name = {"bf16": "", "fp8": "_fp8", "int8": "_i8"}[cache]
+    ws = pkv.alloc_workspace(4, 16, 8, 64)
+    for page, entry, flag in ((0, NB, 1), (31, -1, 1), (29, 2 ** 31 - 1, 1), (10, 2 ** 31 - 1, 0)):
+        t = bt.clone()
+        t[2, page] = entry
+        out, err = torch.full_like(q, float("nan")), torch.zeros(1, dtype=torch.int32, device="cuda")
+        getattr(pkv, "paged_decode_window" + name)(q, *c, t, ld, prob.scale, 60, 3, out, ws, err_word=err)
+        assert err.item() == (pkv.ERR_BLOCK_RANGE if flag else 0)
+        check(out[good[1]], good[0], f"page {page}")
+        if not flag:
+            check(out, prob, "spare")
+
+
+# ------------------------------------------------------------------------------------------ scale blocks
+def scale_problem(kind, n, Hq, Hkv, D, bs, change, seed):
+    """An int8 problem whose scales `change` alters; the 64-bit values follow."""
+    lens = [max(n, 90), 300 + n, 517]
+    if kind == "window":
+        sees, args = [window_sees(L, n, 130, 20) for L in lens], (130, 20)
+    else:
+        masks = random_trees([n] * 3, 3, np.random.default_rng(n), noise=False)
+        sees = [tree_sees(L, n, masks[b * n:b * n + n]) for b, L in enumerate(lens)]
+        args = (torch.from_numpy(masks).cuda(),)
+    prob = Problem("int8", sees, Hq, Hkv, D, bs, seed)
+    change(prob)
+    wide = prob.sc.double()
+    wide = torch.where(wide.abs() < 2.0 ** -104, 0.0, wide).repeat_interleave(SB, 1)  # smaller V scales count as zero
+    prob.kd, prob.vd = prob.kc.double() * wide[..., 0:1], prob.vc.double() * wide[..., 1:2]
+    return prob, args
+
+
+@pytest.mark.parametrize("kind", ["window", "tree"])
+@pytest.mark.parametrize("n", [1, 6, 40, 90])
+@pytest.mark.parametrize("Hq,Hkv,D,bs", [(16, 8, 128, 16), (8, 1, 64, 64)])
+@pytest.mark.parametrize("which", [(0,), (1,), (0, 1)])
+def test_scale_blocks_of_zeros_under_a_mask(kind, n, Hq, Hkv, D, bs, which):
+    """K blocks of zeros score zero, V blocks of zeros (or of scales that count as zero) add weight and no values.
+
+    A code enters the 16-row tiles' output product 1152 too large and a second product takes that off again: two
+    roundings at 1152 times the weights, 2^-23 of it each where an accumulator truncates, leave less than 2^-11 of a
+    code.  Beside codes of ordinary blocks the bound's other terms cover that; a row that sees blocks of zeros alone
+    has nothing else, so the largest V scale's 2^-11 is added."""
+    rng = np.random.default_rng(n)
+
+    def change(prob):
+        for i in which:
+            hit = torch.from_numpy(rng.random(prob.sc.shape[:3]) < 0.4)
+            small = torch.from_numpy(rng.random(hit.shape) < 0.3) & bool(i)
+            old = prob.sc[..., i]
+            prob.sc[..., i] = torch.where(hit & ~old.isnan(), torch.where(small, 2.0 ** -110, 0.0), old)
+
+    prob, args = scale_problem(kind, n, Hq, Hkv, D, bs, change, n + Hq)
+    want, mag = prob.want()
+    bound = 2.0 ** -8 * want.abs() + 2.0 ** -10 * mag + 2.0 ** -11 * prob.sc[..., 1].nan_to_num().max().item()
+    dev = prob.cuda()
+    outs = [attend(prob, args, kind, uniform=uniform, dev=dev) for uniform in (n, 0)]
+    if n == 1 and kind == "window":
+        outs.append(decode(prob, *args, dev=dev))
+    for out in outs:
+        off = (out.cpu().double() - want).abs() - bound
+        assert off.max() <= 0, off.max().item()
+
+
+@pytest.mark.parametrize("kind", ["window", "tree"])
+@pytest.mark.parametrize("n", [1, 6, 40, 90])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+@pytest.mark.parametrize("i", [0, 1])
+def test_a_scale_block_that_is_no_number_spoils_its_readers_alone(kind, n, what, i):
+    """The block of a sequence's first keys (a sink's) and one kv head: the queries of that head give no numbers, the
+    other heads and sequences what they give without it."""
+    clean, args = scale_problem(kind, n, 16, 4, 64, 16, lambda prob: None, n)
+    dirty, _ = scale_problem(kind, n, 16, 4, 64, 16, lambda prob: None, n)
+    dirty.sc[dirty.bt[1, 0], 0, 2, i] = what
+    for uniform in (n, 0):
+        out = attend(dirty, args, kind, uniform=uniform)
+        assert torch.isnan(out[n:2 * n, 8:12]).all(), uniform
+        out[n:2 * n, 8:12] = attend(clean, args, kind, uniform=uniform)[n:2 * n, 8:12]
+        check(out, clean, f"uniform {uniform}")
+
+
+# ------------------------------------------------------------------------------------------ keys that are not finite
+@pytest.mark.parametrize("kind,n", [("decode", 1)] + [(k, n) for k in ("window", "tree") for n in (1, 4, 33, 90)])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("where", ["k", "v"])
+def test_a_key_that_is_not_finite_stays_with_its_sequence_and_head(kind, n, what, where):
+    """A key that every query of a sequence sees: other sequences and kv heads are as without it, and a NaN reaches those
+    who see it."""
+    lens = [n + 30, 300 + n, 517]
+    if kind != "tree":
+        sees, args = [window_sees(L, n, 130, 20) for L in lens], (130, 20)
+    else:
+        masks = random_trees([n] * 3, 3, np.random.default_rng(n), noise=False)
+        sees = [tree_sees(L, n, masks[b * n:b * n + n]) for b, L in enumerate(lens)]
+        args = (torch.from_numpy(masks).cuda(),)
+    prob = Problem("bf16", sees, 16, 4, 64, 32, seed=n)
+    q, c, bt, ld, cu = prob.cuda()
+    spoilt = [t.clone() for t in c]
+    spoilt[where == "v"][bt[1, 0].item(), 7, 2, 5] = what
+    for uniform in (n, 0) if kind != "decode" else (None,):
+        give = lambda cache: (decode(prob, *args, dev=(q, cache, bt, ld, cu)) if kind == "decode" else
+                              attend(prob, args, kind, uniform=uniform, dev=(q, cache, bt, ld, cu)))
+        out = give(spoilt)
+        hit = out[n:2 * n, 8:12]
+        if what != what:
+            assert torch.isnan(hit if where == "k" else hit[..., 5]).all()
+        if where == "v":
+            assert not torch.isfinite(hit[..., 5]).any()
+        out[n:2 * n, 8:12] = give(c)[n:2 * n, 8:12]
+        check(out, prob, f"uniform {uniform}", long_runs=True)
 
 
 # ------------------------------------------------------------------------------------------ long tables
