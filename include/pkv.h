@@ -573,10 +573,11 @@ PKV_API pkv_status pkv_paged_attention_i8(const uint16_t *q, const int8_t *k_cac
  * in longer ones.
  */
 PKV_API pkv_status pkv_paged_decode_window(
-    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
-    int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
-    int32_t num_blocks, int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out,
-    void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream);
+    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables,
+    int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads,
+    int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len,
+    float scale, int32_t window, int32_t sinks, uint16_t *out, void *workspace, size_t workspace_bytes,
+    int32_t num_workers, int32_t *err_word, pkv_stream_t stream);
 PKV_API pkv_status pkv_paged_decode_window_fp8(
     const uint16_t *q, const uint8_t *k_cache, const uint8_t *v_cache, const float *k_scale,
     const float *v_scale, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
@@ -585,23 +586,24 @@ PKV_API pkv_status pkv_paged_decode_window_fp8(
     void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream);
 PKV_API pkv_status pkv_paged_decode_window_i8(
     const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache, const float *scales,
-    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
-    int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
-    int32_t num_blocks, int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out,
-    void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream);
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
+    int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out, void *workspace,
+    size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream);
 PKV_API pkv_status pkv_paged_attention_window(
-    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
-    const int32_t *context_lens, int32_t num_seqs, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
-    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, int32_t window,
-    int32_t sinks, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
-    int32_t *err_word, pkv_stream_t stream);
+    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables,
+    int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q, const int32_t *context_lens, int32_t num_seqs,
+    int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+    int32_t num_blocks, int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out,
+    int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word,
+    pkv_stream_t stream);
 PKV_API pkv_status pkv_paged_attention_window_i8(
     const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache, const float *scales,
     const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
     const int32_t *context_lens, int32_t num_seqs, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
-    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, int32_t window,
-    int32_t sinks, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
-    int32_t *err_word, pkv_stream_t stream);
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale,
+    int32_t window, int32_t sinks, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes,
+    int32_t num_workers, int32_t *err_word, pkv_stream_t stream);
 
 /*
  * pkv_paged_attention_tree, pkv_paged_attention_tree_i8 -- attention of a
@@ -627,18 +629,19 @@ PKV_API pkv_status pkv_paged_attention_window_i8(
  * max_context_len at most 2^30 (PKV_EBOUNDS).  (The pages have no counterpart.)
  */
 PKV_API pkv_status pkv_paged_attention_tree(
-    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
-    const int32_t *context_lens, int32_t num_seqs, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
-    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, const int32_t *tree_mask,
-    int32_t mask_words, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
+    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables,
+    int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q, const int32_t *context_lens, int32_t num_seqs,
+    int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+    int32_t num_blocks, int32_t max_context_len, float scale, const int32_t *tree_mask, int32_t mask_words,
+    uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
     int32_t *err_word, pkv_stream_t stream);
 PKV_API pkv_status pkv_paged_attention_tree_i8(
     const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache, const float *scales,
     const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
     const int32_t *context_lens, int32_t num_seqs, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
-    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, const int32_t *tree_mask,
-    int32_t mask_words, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
-    int32_t *err_word, pkv_stream_t stream);
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale,
+    const int32_t *tree_mask, int32_t mask_words, uint16_t *out, int32_t new_per_seq, void *workspace,
+    size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream);
 
 /*
  * pkv_copy_blocks_i8 -- pkv_copy_blocks for int8 caches: block dst of both

@@ -690,10 +690,11 @@ extern "C" pkv_status pkv_paged_attention_i8(const uint16_t *q, const int8_t *k_
 
 // ------------------------------------------------------------------ sliding windows with sinks, trees
 extern "C" pkv_status pkv_paged_decode_window(
-    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
-    int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
-    int32_t num_blocks, int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out,
-    void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream)
+    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables,
+    int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads,
+    int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len,
+    float scale, int32_t window, int32_t sinks, uint16_t *out, void *workspace, size_t workspace_bytes,
+    int32_t num_workers, int32_t *err_word, pkv_stream_t stream)
 {
     MaskArgs m;
     m.window = window;
@@ -706,11 +707,11 @@ extern "C" pkv_status pkv_paged_decode_window(
 }
 
 extern "C" pkv_status pkv_paged_decode_window_fp8(
-    const uint16_t *q, const uint8_t *k_cache, const uint8_t *v_cache, const float *k_scale,
-    const float *v_scale, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
-    int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
-    int32_t num_blocks, int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out,
-    void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream)
+    const uint16_t *q, const uint8_t *k_cache, const uint8_t *v_cache, const float *k_scale, const float *v_scale,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
+    int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out, void *workspace,
+    size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream)
 {
     MaskArgs m;
     m.window = window;
@@ -724,10 +725,10 @@ extern "C" pkv_status pkv_paged_decode_window_fp8(
 
 extern "C" pkv_status pkv_paged_decode_window_i8(
     const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache, const float *scales,
-    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
-    int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
-    int32_t num_blocks, int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out,
-    void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream)
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
+    int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out, void *workspace,
+    size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream)
 {
     MaskArgs m;
     m.window = window;
@@ -740,11 +741,12 @@ extern "C" pkv_status pkv_paged_decode_window_i8(
 }
 
 extern "C" pkv_status pkv_paged_attention_window(
-    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
-    const int32_t *context_lens, int32_t num_seqs, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
-    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, int32_t window,
-    int32_t sinks, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
-    int32_t *err_word, pkv_stream_t stream)
+    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables,
+    int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q, const int32_t *context_lens, int32_t num_seqs,
+    int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+    int32_t num_blocks, int32_t max_context_len, float scale, int32_t window, int32_t sinks, uint16_t *out,
+    int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *err_word,
+    pkv_stream_t stream)
 {
     MaskArgs m;
     m.new_tokens = true;
@@ -777,10 +779,11 @@ extern "C" pkv_status pkv_paged_attention_window_i8(
 }
 
 extern "C" pkv_status pkv_paged_attention_tree(
-    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
-    const int32_t *context_lens, int32_t num_seqs, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
-    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, const int32_t *tree_mask,
-    int32_t mask_words, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
+    const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache, const int32_t *block_tables,
+    int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q, const int32_t *context_lens, int32_t num_seqs,
+    int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+    int32_t num_blocks, int32_t max_context_len, float scale, const int32_t *tree_mask, int32_t mask_words,
+    uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
     int32_t *err_word, pkv_stream_t stream)
 {
     if (num_rows > 0 && !tree_mask) return PKV_EINVAL;
@@ -802,9 +805,9 @@ extern "C" pkv_status pkv_paged_attention_tree_i8(
     const uint16_t *q, const int8_t *k_cache, const int8_t *v_cache, const float *scales,
     const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *cu_seqlens_q,
     const int32_t *context_lens, int32_t num_seqs, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
-    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, const int32_t *tree_mask,
-    int32_t mask_words, uint16_t *out, int32_t new_per_seq, void *workspace, size_t workspace_bytes, int32_t num_workers,
-    int32_t *err_word, pkv_stream_t stream)
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale,
+    const int32_t *tree_mask, int32_t mask_words, uint16_t *out, int32_t new_per_seq, void *workspace,
+    size_t workspace_bytes, int32_t num_workers, int32_t *err_word, pkv_stream_t stream)
 {
     if (num_rows > 0 && !tree_mask) return PKV_EINVAL;
     MaskArgs m;

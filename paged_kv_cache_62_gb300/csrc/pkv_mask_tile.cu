@@ -293,35 +293,7 @@ __device__ __forceinline__ int mt_slice_of(const int32_t *bound, int nsl, int s,
     return lo;
 }
 
-// Two fp32 values an instruction, and the largest of three.
-__device__ __forceinline__ uint64_t mt_two(float lo, float hi)
-{
-    uint64_t v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
-    return v;
-}
-
-__device__ __forceinline__ float2 mt_parts(uint64_t v)
-{
-    float2 p;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(p.x), "=f"(p.y) : "l"(v));
-    return p;
-}
-
-__device__ __forceinline__ uint64_t mt_fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t mt_add2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
+// The largest of three.
 __device__ __forceinline__ float mt_max3(float a, float b, float c)
 {
     float r;
@@ -622,7 +594,7 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
                 }
             }
             const float mneg = mrun == -INFINITY ? 0.f : -mrun;
-            const uint64_t c2 = mt_two(c, c), m2 = mt_two(mneg, mneg);
+            const uint64_t c2 = f32x2(c, c), m2 = f32x2(mneg, mneg);
             uint64_t ps[2] = {0ull, 0ull};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {  // 32 keys at a time: the first half's output product runs beside the second
@@ -631,9 +603,9 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
                 for (int j = 0; j < kMtKeys / 4; ++j) {
                     const int e = 32 * h + 2 * j;
                     const float2 x =
-                        mt_parts(mt_fma2(mt_two(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2, m2));
+                        f32x2_parts(fma2(f32x2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2, m2));
                     const float p0 = ex2(x.x), p1 = ex2(x.y);
-                    ps[j & 1] = mt_add2(ps[j & 1], mt_two(p0, p1));
+                    ps[j & 1] = add2(ps[j & 1], f32x2(p0, p1));
                     w[j] = pack_bf16x2(p0, p1);
                     if constexpr (TWO)
                         rest[j] = pack_bf16x2(p0 - __uint_as_float(w[j] << 16), p1 - __uint_as_float(w[j] & 0xffff0000u));
@@ -660,7 +632,7 @@ __device__ void mt_softmax(const TileParams &tp, const CUtensorMap *qmap, const 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&m.pfull[2 * (k & 1u) + h]);
             }
-            const float2 pa = mt_parts(ps[0]), pb = mt_parts(ps[1]);
+            const float2 pa = f32x2_parts(ps[0]), pb = f32x2_parts(ps[1]);
             lrun += (pa.x + pa.y) + (pb.x + pb.y);
         }
         // The segment's part here ends, with the last output product.

@@ -201,31 +201,6 @@ constexpr int kNormPieces = 2;  // pieces of a lane in flight (1: 48.8-50.4 us, 
 // neighbours and unusual head sizes take more registers (1531 rows of 14 + 2 heads of 80: 5.9 us, with 12 7.7 us).
 __host__ __device__ constexpr int norm_ctas(bool adj, int per) { return adj || per == 0 ? 8 : 12; }
 
-// Two floats in one register pair.
-__device__ __forceinline__ uint64_t f32x2(float lo, float hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 f32x2_parts(uint64_t v)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ void unpack8(uint4 v, uint64_t (&x)[4])
 {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};

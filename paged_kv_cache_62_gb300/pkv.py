@@ -62,20 +62,22 @@ SIGNATURES = {
                                 _P, _I64, _P, _P]),
     "pkv_rope_store": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _I32, _P, _P, _P, _I32, _I32, _I32, _I32,
                                       _I32, _I32, _P, _I64, _P, _P, _I32, _I32, _P, _P]),
-    "pkv_paged_decode_window": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32, _I32, _I32,
-        _P, _P, _SZ, _I32, _P, _P]),
-    "pkv_paged_decode_window_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32, _I32, _I32,
-        _P, _P, _SZ, _I32, _P, _P]),
-    "pkv_paged_decode_window_i8": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32, _I32, _I32,
-        _P, _P, _SZ, _I32, _P, _P]),
-    "pkv_paged_attention_window": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32,
-        _I32, _I32, _P, _I32, _P, _SZ, _I32, _P, _P]),
-    "pkv_paged_attention_window_i8": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32,
-        _I32, _I32, _P, _I32, _P, _SZ, _I32, _P, _P]),
-    "pkv_paged_attention_tree": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32,
-        _P, _I32, _P, _I32, _P, _SZ, _I32, _P, _P]),
-    "pkv_paged_attention_tree_i8": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _F32,
-        _P, _I32, _P, _I32, _P, _SZ, _I32, _P, _P]),
+    "pkv_paged_decode_window": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                                               _F32, _I32, _I32, _P, _P, _SZ, _I32, _P, _P]),
+    "pkv_paged_decode_window_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32,
+                                                   _I32, _I32, _F32, _I32, _I32, _P, _P, _SZ, _I32, _P, _P]),
+    "pkv_paged_decode_window_i8": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32,
+                                                  _I32, _F32, _I32, _I32, _P, _P, _SZ, _I32, _P, _P]),
+    "pkv_paged_attention_window": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32,
+                                                  _I32, _I32, _F32, _I32, _I32, _P, _I32, _P, _SZ, _I32, _P, _P]),
+    "pkv_paged_attention_window_i8": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32,
+                                                     _I32, _I32, _I32, _F32, _I32, _I32, _P, _I32, _P, _SZ, _I32, _P,
+                                                     _P]),
+    "pkv_paged_attention_tree": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32,
+                                                _I32, _I32, _F32, _P, _I32, _P, _I32, _P, _SZ, _I32, _P, _P]),
+    "pkv_paged_attention_tree_i8": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32,
+                                                   _I32, _I32, _I32, _F32, _P, _I32, _P, _I32, _P, _SZ, _I32, _P,
+                                                   _P]),
     "pkv_qk_norm_rope": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _F32, _P, _I32, _P, _P, _I32, _I32, _I32, _I32,
                                         _I32, _I32, _P, _I64, _P, _I64, _P, _P]),
     "pkv_qk_norm_rope_store": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _F32, _P, _I32, _P, _P, _P, _I32,
