@@ -24,9 +24,9 @@
 // odone[k % 2] and the V slot free; a segment's Q landed -> qready (its copy is issued once the last scores that read
 // the one before are in).  S(k) is issued when P(k - 2) V is done, P(k - 1) V after S(k), or before it where unit k
 // opens a segment.  The weights go out 32 keys at a time, so that the first half's product runs beside the second
-// half's exponentials (32-node trees of 64 sequences 106.4 us, so 104.7).  Every barrier's next phase needs its waiter's
-// own next step, so none runs two phases ahead; the softmax warps, which see only some V tiles, look at their barrier
-// after the unit's scores, which come behind the slot's item before.
+// half's exponentials (32-node trees of 64 sequences, one call after another on the same inputs, 106.4 us, so 104.7).
+// Every barrier's next phase needs its waiter's own next step, so none runs two phases ahead; the softmax warps, which
+// see only some V tiles, look at their barrier after the unit's scores, which come behind the slot's item before.
 //
 // The list is cut into equal slices, one a CTA.  Slices, and with them the sums' order, depend on the list and the grid
 // alone: the results repeat bit for bit.  Pieces of a segment that lies in several slices are merged
@@ -40,12 +40,15 @@
 // and hands each segment to the others in shared memory (MtDesc), the next one before it copies the last unit of this
 // one.
 //
-// What bounds it (64 sequences of 512-4096, 16 / 8 heads of 128, 1.95 GHz): 32-node trees, 596 MB, 110 us of 87.7 at the
-// copy rate; 64-token chunks under a window of 1024, 63 us of 45; whole prompts of 1-2048 tokens under a window of 512,
-// 55 us of 15 at the products' rate.  A unit takes a CTA 2000-2200 cycles: softmax 1000, a wait of 500-900 for the next
-// scores, which share one tensor pipe with the other CTA's products and wait for the output product that reads the
-// same columns, masks and instruction fetch 400.  Tensor memory holds no third score buffer at head_dim 128.  A
-// segment's end costs 5000 to 7000 cycles: its last product, 128 rows of 256 bytes, the first unit's masks.
+// What bounds it (64 sequences of 512-4096, 16 / 8 heads of 128, 1.95 GHz; calls whose inputs come from memory; the steps
+// above and at the constants are from calls at other stages): 32-node trees, 596 MB, 110 us of 87.7 at the copy rate;
+// 64-token chunks under a window of 1024, 62.7 us of 45; whole prompts of 1-2048 tokens under a window of 512, 54 us of
+// 15 at the products' rate.  A unit takes a CTA 2000-2200 cycles: softmax 1000, a wait of 500-900 for the next scores,
+// which share one tensor pipe with the other CTA's products and wait for the output product that reads the same columns,
+// masks and instruction fetch 400.  Tensor memory holds no third score buffer at head_dim 128.  A segment's end costs
+// 5000 to 7000 cycles: its last product, 128 rows of 256 bytes, the first unit's masks.  Where segments are not cut,
+// slices are uneven: a bound moves to its segment's start, and the fullest of 304 CTAs has 51 to 57 places of the list in
+// the chunks (mean 36.8) and 52 to 54 in the prompts (mean 41.9).
 #include "pkv_decode_kernel.cuh"
 
 namespace pkv {
