@@ -618,9 +618,9 @@ PKV_API pkv_status pkv_paged_attention_window_i8(
  *               sees itself only if its own bit is set.
  * A row that sees no key (L = n and an empty mask) gives zeros; K, V and scales
  * of a node that no row sees (a place that a smaller tree leaves unused) may
- * hold anything.  The mask of a
- * chain is its lower triangle: the results of pkv_paged_attention (to rounding,
- * where another kernel runs).
+ * hold anything, but its table entry has to name a block.  The mask of a chain
+ * is its lower triangle: the results of pkv_paged_attention (to rounding, where
+ * another kernel runs).
  * mask_words >= 1; a sequence has at most 32 * mask_words nodes (new_per_seq
  * beyond: PKV_EINVAL; offsets beyond: zeros and PKV_ERR_CONTEXT_RANGE).
  * Tiles and roundings over bf16 caches as pkv_paged_attention_window.
